@@ -28,12 +28,15 @@ STATUS_NAMES = {0: "CDG_OK", 1: "CDG_ERR_INVALID_ARG", 2: "CDG_ERR_UNSUPPORTED",
 ERR_INVALID_ARG = 1
 ERR_SCRATCH_TOO_SMALL = 8
 NOALLOC_MAX_WEIGHT_BYTES = 8 << 20
-F16, BF16 = 0, 1
+F16, BF16, F32 = 0, 1, 2
 EPI_RELU_BWD, EPI_OUT_F32, EPI_RELU_BWD_BITS, EPI_SUM, EPI_SUM_X = 1, 2, 4, 8, 16
 EPI_GELU_BWD, EPI_SILU_BWD = 32, 64
 FUSED_WRITE_G = 256
 ACT_FLAGS = {"relu": EPI_RELU_BWD, "gelu": EPI_GELU_BWD, "silu": EPI_SILU_BWD}
 DTYPES = {"f16": F16, "bf16": BF16}
+ANY_DTYPES = {"f16": F16, "bf16": BF16, "f32": F32}  # the token operators and the weight update
+MAX_TOP = 32
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 EXPORTS = ("cdg_plan", "cdg_plan_host", "cdg_destroy", "cdg_get_output_dims", "cdg_packed_weight_bytes",
            "cdg_plan_get_info", "cdg_prepack_weights", "cdg_dgrad", "cdg_device_status", "cdg_status_string",
@@ -42,7 +45,11 @@ EXPORTS = ("cdg_plan", "cdg_plan_host", "cdg_destroy", "cdg_get_output_dims", "c
            "cdg_fused_plan", "cdg_fused_plan_host", "cdg_fused_destroy", "cdg_fused_packed_weight_bytes",
            "cdg_fused_prepack_weights", "cdg_dgrad_fused", "cdg_fused_get_info", "cdg_fused_device_status", "cdg_pack_relu_mask", "cdg_relu_mask_bytes",
            "cdg_wgrad_plan", "cdg_wgrad_plan_host", "cdg_wgrad_destroy", "cdg_wgrad_workspace_bytes",
-           "cdg_wgrad_get_info", "cdg_wgrad", "cdg_wgrad_device_status")
+           "cdg_wgrad_get_info", "cdg_wgrad", "cdg_wgrad_device_status",
+           "cdg_token_logprobs", "cdg_token_logprobs_grad", "cdg_embed", "cdg_embed_grad",
+           "cdg_embed_grad_workspace_bytes", "cdg_muon_plan", "cdg_muon_plan_host", "cdg_muon_destroy",
+           "cdg_muon_workspace_bytes", "cdg_muon_get_info", "cdg_muon_orthogonalize", "cdg_muon_step",
+           "cdg_muon_device_status")
 
 
 class CdgError(RuntimeError):
@@ -151,6 +158,33 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.cdg_wgrad.restype = i
     lib.cdg_wgrad_device_status.argtypes = [hp, vp]
     lib.cdg_wgrad_device_status.restype = i
+    ll, f, sz = ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+    lib.cdg_token_logprobs.argtypes = [vp, ll, vp, i, ll, i, i, f, i, vp, vp, vp, vp, vp, vp]
+    lib.cdg_token_logprobs.restype = i
+    lib.cdg_token_logprobs_grad.argtypes = [vp, ll, vp, i, ll, i, i, f, vp, vp, vp, vp, vp, ll, vp]
+    lib.cdg_token_logprobs_grad.restype = i
+    lib.cdg_embed.argtypes = [vp, ll, vp, i, ll, i, i, i, f, vp, ll, vp]
+    lib.cdg_embed.restype = i
+    lib.cdg_embed_grad.argtypes = [vp, ll, vp, i, ll, i, i, i, f, vp, ll, i, i, vp, vp]
+    lib.cdg_embed_grad.restype = i
+    lib.cdg_embed_grad_workspace_bytes.argtypes = [ll, i, i]
+    lib.cdg_embed_grad_workspace_bytes.restype = sz
+    lib.cdg_muon_plan.argtypes = [i] * 5 + [f] * 4 + [ctypes.POINTER(hp)]
+    lib.cdg_muon_plan.restype = i
+    lib.cdg_muon_plan_host.argtypes = [i] * 5 + [f] * 4 + [i, ctypes.POINTER(hp)]
+    lib.cdg_muon_plan_host.restype = i
+    lib.cdg_muon_destroy.argtypes = [hp]
+    lib.cdg_muon_destroy.restype = None
+    lib.cdg_muon_workspace_bytes.argtypes = [hp]
+    lib.cdg_muon_workspace_bytes.restype = sz
+    lib.cdg_muon_get_info.argtypes = [hp, ctypes.POINTER(MuonInfo)]
+    lib.cdg_muon_get_info.restype = i
+    lib.cdg_muon_orthogonalize.argtypes = [hp, vp, vp, vp, vp]
+    lib.cdg_muon_orthogonalize.restype = i
+    lib.cdg_muon_step.argtypes = [hp, vp, vp, vp, vp, vp, f, f, f, f, i, vp, vp]
+    lib.cdg_muon_step.restype = i
+    lib.cdg_muon_device_status.argtypes = [hp, vp]
+    lib.cdg_muon_device_status.restype = i
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -549,3 +583,228 @@ def plan_host(N, H, W, C, K, R, S, stride=1, pad=0, dil=1, dtype="bf16", relu=Fa
               num_sms=148, relu_bits=False, sums: int = 0, act: str = "relu") -> Plan:
     return Plan(N, H, W, C, K, R, S, stride, pad, dil, dtype, relu, out_f32, host_sms=num_sms, relu_bits=relu_bits,
                 sums=sums, act=act)
+
+
+# ---- token operators: log probabilities, embedding, and their gradients
+
+
+def _dtype(dtype) -> int:
+    return ANY_DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+
+
+def _esize(dtype) -> int:
+    return 4 if _dtype(dtype) == F32 else 2
+
+
+def _dense(t, n: int, esize: int, what: str) -> int | None:
+    """Address of a dense argument of n elements of esize bytes (None stays None)."""
+    if t is None or isinstance(t, int):
+        return t
+    _check_buffer(t, n * esize, what)
+    if t.element_size() != esize:
+        raise ValueError(f"{what} has elements of {t.element_size()} bytes; {esize} are needed")
+    return t.data_ptr()
+
+
+def _matrix(t, rows: int, cols: int, esize: int, ld: int | None, what: str) -> tuple[int | None, int]:
+    """Address and row stride of a rows x cols argument.  A 2-D tensor may have
+    any row stride with unit column stride (a slice of a wider one); any other
+    tensor is taken as dense; a raw address has row stride ld, or cols."""
+    if t is None or isinstance(t, int):
+        return t, int(ld if ld is not None else cols)
+    if getattr(t, "dim", lambda: 1)() == 2 and not t.is_contiguous():
+        if tuple(t.shape) != (rows, cols):
+            raise ValueError(f"{what} is {tuple(t.shape)}; the call needs {(rows, cols)}")
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what} must have unit column stride")
+        if rows > 1 and t.stride(0) < cols:
+            raise ValueError(f"{what} has overlapping rows (row stride {t.stride(0)} for {cols} columns)")
+        if rows == 0:
+            return t.data_ptr(), cols
+        _check_buffer(t[0, :], cols * esize, what)
+        own = t.stride(0) if rows > 1 else cols
+    else:
+        _check_buffer(t, rows * cols * esize, what)
+        own = cols
+    if t.element_size() != esize:
+        raise ValueError(f"{what} has elements of {t.element_size()} bytes; {esize} are needed")
+    if ld is not None and int(ld) != own:
+        raise ValueError(f"{what} has row stride {own}, not {ld}")
+    return t.data_ptr(), int(own)
+
+
+def _tokens(t, n: int, what: str) -> tuple[int | None, int]:
+    """Address and bytes per number of a token list (int32 or int64; a raw address is int64)."""
+    if t is None or isinstance(t, int):
+        return t, 8
+    size = t.element_size()
+    if size not in (4, 8) or t.is_floating_point():
+        raise ValueError(f"{what} must hold int32 or int64 token numbers")
+    _check_buffer(t, n * size, what)
+    return t.data_ptr(), size
+
+
+def token_logprobs(logits, targets, logp, lse, rows: int, vocab: int, dtype="bf16", scale: float = 1.0,
+                   entropy=None, top: int = 0, top_ids=None, top_logp=None, ld: int | None = None,
+                   stream=None) -> None:
+    """Log probabilities of given tokens under softmax(scale * logits)
+    (cdg_token_logprobs): logp[i] of targets[i] (0 where a target names no
+    token), lse[i], and on request the row's entropy and its `top` largest
+    entries with their log probabilities.  Outputs fp32 (top_ids int32); a
+    target list or output that is not wanted is None."""
+    rows, vocab, top = int(rows), int(vocab), int(top)
+    lg, ld = _matrix(logits, rows, vocab, _esize(dtype), ld, "logits")
+    tg, ib = _tokens(targets, rows, "targets")
+    rc = load_library().cdg_token_logprobs(
+        lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), top, _dense(logp, rows, 4, "logp"),
+        _dense(lse, rows, 4, "lse"), _dense(entropy, rows, 4, "entropy"), _dense(top_ids, rows * top, 4, "top_ids"),
+        _dense(top_logp, rows * top, 4, "top_logp"), _stream(stream))
+    if rc != OK:
+        raise CdgError(rc, "cdg_token_logprobs")
+
+
+def token_logprobs_grad(logits, targets, lse, entropy, g_logp, g_entropy, dlogits, rows: int, vocab: int,
+                        dtype="bf16", scale: float = 1.0, ld: int | None = None, ld_d: int | None = None,
+                        stream=None) -> None:
+    """The gradient of token_logprobs (cdg_token_logprobs_grad) for the row
+    gradients g_logp and g_entropy (None: no entropy term) into dlogits, which
+    may be the logits themselves."""
+    rows, vocab = int(rows), int(vocab)
+    lg, ld = _matrix(logits, rows, vocab, _esize(dtype), ld, "logits")
+    dl, ld_d = _matrix(dlogits, rows, vocab, _esize(dtype), ld_d, "dlogits")
+    tg, ib = _tokens(targets, rows, "targets")
+    rc = load_library().cdg_token_logprobs_grad(
+        lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), _dense(lse, rows, 4, "lse"),
+        _dense(entropy, rows, 4, "entropy"), _dense(g_logp, rows, 4, "g_logp"),
+        _dense(g_entropy, rows, 4, "g_entropy"), dl, ld_d, _stream(stream))
+    if rc != OK:
+        raise CdgError(rc, "cdg_token_logprobs_grad")
+
+
+def embed(table, tokens, out, count: int, vocab: int, dim: int, dtype="bf16", scale: float = 1.0,
+          ld_table: int | None = None, ld_out: int | None = None, stream=None) -> None:
+    """out[i] = scale * table[tokens[i]], zeros where there is no token (cdg_embed)."""
+    count, vocab, dim = int(count), int(vocab), int(dim)
+    tb, ld_table = _matrix(table, vocab, dim, _esize(dtype), ld_table, "table")
+    ou, ld_out = _matrix(out, count, dim, _esize(dtype), ld_out, "out")
+    tk, ib = _tokens(tokens, count, "tokens")
+    rc = load_library().cdg_embed(tb, ld_table, tk, ib, count, vocab, dim, _dtype(dtype), float(scale), ou, ld_out,
+                                  _stream(stream))
+    if rc != OK:
+        raise CdgError(rc, "cdg_embed")
+
+
+def embed_grad_workspace_bytes(count: int, vocab: int, dim: int) -> int:
+    """Bytes of embed_grad's workspace (cdg_embed_grad_workspace_bytes)."""
+    n = int(load_library().cdg_embed_grad_workspace_bytes(int(count), int(vocab), int(dim)))
+    if n == 0:
+        raise CdgError(ERR_INVALID_ARG, "cdg_embed_grad_workspace_bytes")
+    return n
+
+
+def embed_grad(dout, tokens, dtable, workspace, count: int, vocab: int, dim: int, dtype="bf16", scale: float = 1.0,
+               out_f32: bool = False, accumulate: bool = False, ld_dout: int | None = None,
+               ld_dtable: int | None = None, stream=None) -> None:
+    """dtable[v] = scale * the sum of dout[i] over the i with tokens[i] = v
+    (cdg_embed_grad); accumulate=True adds to the rows that tokens point to."""
+    count, vocab, dim = int(count), int(vocab), int(dim)
+    do, ld_dout = _matrix(dout, count, dim, _esize(dtype), ld_dout, "dout")
+    dt, ld_dtable = _matrix(dtable, vocab, dim, 4 if out_f32 else _esize(dtype), ld_dtable, "dtable")
+    tk, ib = _tokens(tokens, count, "tokens")
+    if workspace is not None and not isinstance(workspace, int):
+        _check_buffer(workspace, embed_grad_workspace_bytes(count, vocab, dim), "workspace")
+    rc = load_library().cdg_embed_grad(do, ld_dout, tk, ib, count, vocab, dim, _dtype(dtype), float(scale), dt,
+                                       ld_dtable, int(bool(out_f32)), int(bool(accumulate)), _addr(workspace),
+                                       _stream(stream))
+    if rc != OK:
+        raise CdgError(rc, "cdg_embed_grad")
+
+
+# ---- the weight update from an orthogonalised gradient
+
+
+class MuonInfo(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int), ("n", ctypes.c_int), ("transposed", ctypes.c_int), ("tile_m", ctypes.c_int),
+                ("tile_n", ctypes.c_int), ("launches", ctypes.c_int)]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class MuonPlan:
+    """One planned shape of the orthogonalised weight update (a ``cdg_muon_t``):
+    a batch of rows x cols matrices, e.g. filters stored KRSC as K x (R*S*C)."""
+
+    def __init__(self, rows, cols, batch=1, dtype="bf16", steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7,
+                 host_sms: int | None = None):
+        self.lib = load_library()
+        self.shape = dict(batch=int(batch), rows=int(rows), cols=int(cols))
+        self.dtype = dtype
+        a, b, c = coefficients
+        h = ctypes.c_void_p()
+        args = (batch, rows, cols, _dtype(dtype), steps, a, b, c, eps)
+        if host_sms is None:
+            rc = self.lib.cdg_muon_plan(*args, ctypes.byref(h))
+        else:
+            rc = self.lib.cdg_muon_plan_host(*args, host_sms, ctypes.byref(h))
+        if rc != OK:
+            raise CdgError(rc, "cdg_muon_plan")
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            self.lib.cdg_muon_destroy(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        self.close()
+
+    @property
+    def workspace_bytes(self) -> int:
+        return int(self.lib.cdg_muon_workspace_bytes(self.handle))
+
+    def info(self) -> dict:
+        inf = MuonInfo()
+        rc = self.lib.cdg_muon_get_info(self.handle, ctypes.byref(inf))
+        if rc != OK:
+            raise CdgError(rc, "cdg_muon_get_info")
+        return inf.as_dict()
+
+    def _elements(self) -> int:
+        d = self.shape
+        return d["batch"] * d["rows"] * d["cols"]
+
+    def orthogonalize(self, U, O, workspace, stream=None) -> None:
+        """O = the Newton-Schulz orthogonalisation of every matrix of U (cdg_muon_orthogonalize)."""
+        n, es = self._elements(), _esize(self.dtype)
+        _check_buffer(workspace, self.workspace_bytes, "workspace")
+        rc = self.lib.cdg_muon_orthogonalize(self.handle, _dense(U, n, es, "U"), _dense(O, n, es, "O"),
+                                             _addr(workspace), _stream(stream))
+        if rc != OK:
+            raise CdgError(rc, "cdg_muon_orthogonalize")
+
+    def step(self, W, G, M, W_out, M_out, workspace, lr: float, momentum: float = 0.95, weight_decay: float = 0.0,
+             update_scale: float = 1.0, nesterov: bool = True, stream=None) -> None:
+        """The weight update (cdg_muon_step): M_out = momentum * M + G, W_out =
+        (1 - lr * weight_decay) * W - lr * update_scale * orthogonalize(U).
+        W_out may be W and M_out may be M."""
+        n = self._elements()
+        _check_buffer(workspace, self.workspace_bytes, "workspace")
+        rc = self.lib.cdg_muon_step(
+            self.handle, _dense(W, n, 4, "W"), _dense(G, n, _esize(self.dtype), "G"), _dense(M, n, 4, "M"),
+            _dense(W_out, n, 4, "W_out"), _dense(M_out, n, 4, "M_out"), float(lr), float(momentum),
+            float(weight_decay), float(update_scale), int(bool(nesterov)), _addr(workspace), _stream(stream))
+        if rc != OK:
+            raise CdgError(rc, "cdg_muon_step")
+
+    def device_status(self, stream=None) -> int:
+        return int(self.lib.cdg_muon_device_status(self.handle, _stream(stream)))
+
+
+def muon_plan(rows, cols, batch=1, dtype="bf16", steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7) -> MuonPlan:
+    return MuonPlan(rows, cols, batch, dtype, steps, coefficients, eps)
+
+
+def muon_plan_host(rows, cols, batch=1, dtype="bf16", steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7,
+                   num_sms=148) -> MuonPlan:
+    return MuonPlan(rows, cols, batch, dtype, steps, coefficients, eps, host_sms=num_sms)

@@ -1,0 +1,631 @@
+// Token log probabilities for sm_103a, and their gradient: kernels and C entry
+// points.
+//
+// Forward.  With c = scale * log2(e), every element of a row is read once:
+//
+//   ref >= 0-th order: a running reference, the largest z_j c seen so far
+//   s = sum 2^(z_j c - ref),   e = sum 2^(z_j c - ref) (z_j c - ref)
+//
+// and when a thread's group of vectors holds a larger value, s and e move to
+// the new reference: with r = 2^(ref - ref'), s' = s r and
+// e' = r (e + (ref - ref') s).  The reference is the rounded product itself,
+// so it drops out exactly: lse = ln2 (ref + log2 s), and the entropy is
+// ln2 (log2 s - e / s).  Threads, warps and the CTAs of a cluster are joined by
+// the same rule, in a fixed order.
+//
+// The largest logits: each thread keeps the maximum of its elements (the
+// running maximum above, needed anyway).  The k-th largest of some thread
+// maxima is at most the k-th largest element, so only threads whose maximum
+// reaches that bound read their elements again (from L2) and list those that
+// reach it: a few dozen, ranked by counting larger 64-bit keys (ordered value,
+// then lowest number).  If more than kCand reach it (many equal values) each
+// warp instead keeps an exact sorted list of its k largest keys in one scan.
+#include <cmath>
+
+#include "ptx.cuh"
+#include "token_device.cuh"
+
+namespace cdg {
+namespace {
+
+constexpr int kMaxTop = 32;
+constexpr int kMaxVocab = 1 << 30;  // element numbers stay in 32 bits
+constexpr int kCand = 1024;       // candidate keys a CTA ranks
+constexpr int kMaxCluster = 8;    // CTAs that share a row
+constexpr int kUnroll = 4;        // 16-byte loads in flight per thread
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kFloor = -1000.0f;  // 2^-1000 is 0 in fp32: exponents are clamped here so that 0 * -inf does not arise
+
+struct LogprobArgs {
+    const void *logits, *targets;
+    long long ld;
+    int index_bytes, vocab, top, cluster;
+    float scale, c;  // c = scale * log2(e)
+    float *logp, *lse, *entropy, *top_logp;
+    int *top_ids;
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// max that keeps a NaN operand (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Running sums about a reference (see the head of the file), and the largest
+// logit itself.
+struct Sums {
+    float ref, s, e, zmax;
+};
+
+__device__ __forceinline__ Sums join(const Sums &a, const Sums &b)
+{
+    Sums r;
+    r.ref = fmaxf(a.ref, b.ref);
+    const bool none = r.ref == -INFINITY;  // both empty: s = e = 0
+    const float da = none ? 0.0f : fmaxf(a.ref - r.ref, kFloor), db = none ? 0.0f : fmaxf(b.ref - r.ref, kFloor);
+    const float ra = exp2_fast(da), rb = exp2_fast(db);
+    r.s = a.s * ra + b.s * rb;
+    r.e = ra * fmaf(da, a.s, a.e) + rb * fmaf(db, b.s, b.e);
+    r.zmax = fmaxf(a.zmax, b.zmax);
+    return r;
+}
+
+// Float order as unsigned order (-0 and +0 equal); 0 is below every number.
+__device__ __forceinline__ uint32_t ordered(float f)
+{
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u)
+{
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+// Larger key = larger value, then lower element number.  Never 0.
+__device__ __forceinline__ unsigned long long make_key(float z, int j)
+{
+    return (static_cast<unsigned long long>(ordered(z)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(j));
+}
+__device__ __forceinline__ int key_index(unsigned long long k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
+
+// Largest of a 16-byte vector's elements (NaN elements may be dropped).
+template <typename T>
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t max_words<float>(uint32_t a, uint32_t b)
+{
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+template <>
+__device__ __forceinline__ uint32_t max_words<__half>(uint32_t a, uint32_t b)
+{
+    const __half2 r = __hmax2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t max_words<__nv_bfloat16>(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <typename T>
+__device__ __forceinline__ float max_word(uint32_t w)
+{
+    float f[2];
+    widen<T>(w, f);
+    return sizeof(T) == 4 ? f[0] : fmaxf(f[0], f[1]);
+}
+
+// The part of a row that this CTA reads: 16-byte vectors from an aligned
+// address, and up to one vector's worth of single elements before the first
+// (CTA 0 of the row) and after the last (its last CTA).
+template <typename T>
+struct Slice {
+    const T *row;
+    int v0, nv;      // vectors: element numbers v0 + i * kPerVec
+    int head, tail0, tail;
+
+    __device__ __forceinline__ Slice(const T *r, int vocab, int rank, int nrank) : row(r)
+    {
+        constexpr int E = kPerVec<T>;
+        const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+        const int h = min(mis ? E - mis : 0, vocab);
+        const int all = (vocab - h) / E;
+        const int a = static_cast<int>(static_cast<long long>(all) * rank / nrank);
+        const int b = static_cast<int>(static_cast<long long>(all) * (rank + 1) / nrank);
+        v0 = h + a * E;
+        nv = b - a;
+        head = rank == 0 ? h : 0;
+        tail0 = h + all * E;
+        tail = rank == nrank - 1 ? vocab - tail0 : 0;
+    }
+    __device__ __forceinline__ uint4 vec(int i) const
+    {
+        return __ldg(reinterpret_cast<const uint4 *>(row + v0) + i);
+    }
+    // number of the single element thread t holds, or -1
+    __device__ __forceinline__ int single(int t) const
+    {
+        if (t < head) return t;
+        t -= kPerVec<T>;
+        return t >= 0 && t < tail ? tail0 + t : -1;
+    }
+};
+
+// One value or one group of vectors into the running sums.
+__device__ __forceinline__ void raise(Sums &a, float gmax_c)
+{
+    if (gmax_c > a.ref) {
+        const float d = fmaxf(a.ref - gmax_c, kFloor), r = exp2_fast(d);
+        a.e = r * fmaf(d, a.s, a.e);
+        a.s *= r;
+        a.ref = gmax_c;
+    }
+}
+__device__ __forceinline__ void add(Sums &a, float z, float c, float shift)
+{
+    const float u = max_nan(fmaf(z, c, -shift), kFloor);
+    const float p = exp2_fast(u);
+    a.s += p;
+    a.e = fmaf(p, u, a.e);
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void add_group(Sums &a, const uint4 (&v)[N], float c)
+{
+    uint32_t w = max_words<T>(max_words<T>(v[0].x, v[0].y), max_words<T>(v[0].z, v[0].w));
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        w = max_words<T>(w, max_words<T>(max_words<T>(v[i].x, v[i].y), max_words<T>(v[i].z, v[i].w)));
+    const float g = max_word<T>(w);
+    a.zmax = fmaxf(a.zmax, g);
+    raise(a, g * c);
+    const float shift = a.ref == -INFINITY ? 0.0f : a.ref;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float f[kPerVec<T>];
+        widen_vec<T>(v[i], f);
+#pragma unroll
+        for (int j = 0; j < kPerVec<T>; ++j) add(a, f[j], c, shift);
+    }
+}
+
+// Insert warp-uniform key x into the warp's descending list (lane l holds its
+// l-th largest key).
+__device__ __forceinline__ void list_insert(unsigned long long &mine, unsigned long long x, int lane)
+{
+    const unsigned larger = __ballot_sync(0xFFFFFFFFu, mine > x);
+    const int pos = __popc(larger);
+    const unsigned long long up = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
+    if (lane == pos) mine = x;
+    else if (lane > pos) mine = up;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// keys[0..n) -> the min(n, k) largest in out, descending.  Returns that count.
+template <int THREADS>
+__device__ __forceinline__ int rank_keys(const unsigned long long *keys, int n, int k, unsigned long long *out)
+{
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const unsigned long long x = keys[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += keys[j] > x;
+        if (rank < k) out[rank] = x;
+    }
+    return min(n, k);
+}
+
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const LogprobArgs p)
+{
+    constexpr int W = THREADS / 32, PER_WARP = kMaxTop / W;  // thread maxima each warp offers
+    __shared__ Sums part[W];
+    __shared__ Sums mine;
+    __shared__ unsigned long long cand[kCand], best[kMaxTop];
+    __shared__ uint32_t offer[kMaxTop];
+    __shared__ int ncand, nbest;
+
+    const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const long long i = blockIdx.x / p.cluster;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const Slice<T> sl(static_cast<const T *>(p.logits) + i * p.ld, p.vocab, rank, p.cluster);
+
+    // ---- one pass: sums and the thread's maximum
+    Sums a{-INFINITY, 0.0f, 0.0f, -INFINITY};
+    const int single = sl.single(tid);
+    if (single >= 0) {
+        const float z = Elem<T>::get(sl.row[single]);
+        a.zmax = fmaxf(a.zmax, z);
+        raise(a, z * p.c);
+        add(a, z, p.c, a.ref == -INFINITY ? 0.0f : a.ref);
+    }
+    int v = 0;
+    for (; v + kUnroll * THREADS <= sl.nv; v += kUnroll * THREADS) {
+        uint4 x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) x[u] = sl.vec(v + u * THREADS + tid);
+        add_group<T, kUnroll>(a, x, p.c);
+    }
+    for (v += tid; v < sl.nv; v += THREADS) {
+        const uint4 x[1] = {sl.vec(v)};
+        add_group<T, 1>(a, x, p.c);
+    }
+    // no element at all in this thread: below every element
+    const uint32_t omax = single >= 0 || tid < sl.nv ? ordered(a.zmax) : 0u;
+
+    // ---- join the CTA
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const Sums b{__shfl_xor_sync(0xFFFFFFFFu, a.ref, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+                     __shfl_xor_sync(0xFFFFFFFFu, a.e, o), __shfl_xor_sync(0xFFFFFFFFu, a.zmax, o)};
+        a = join(a, b);
+    }
+    if (lane == 0) part[warp] = a;
+    if (p.top) {
+        uint32_t m = omax;
+#pragma unroll
+        for (int r = 0; r < PER_WARP; ++r) {
+            const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, m);
+            const unsigned holders = __ballot_sync(0xFFFFFFFFu, m == g);
+            if (lane == 0) offer[warp * PER_WARP + r] = g;
+            if (lane == __ffs(holders) - 1) m = 0u;
+        }
+        if (tid == 0) ncand = 0;
+    }
+    __syncthreads();
+    Sums all = part[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) all = join(all, part[w]);
+
+    // ---- the CTA's largest logits
+    if (p.top) {
+        const uint32_t mo = offer[lane];
+        int larger = 0;
+#pragma unroll
+        for (int l = 0; l < 32; ++l) {
+            const uint32_t o = __shfl_sync(0xFFFFFFFFu, mo, l);
+            larger += o > mo || (o == mo && l < lane);
+        }
+        const int at = __ffs(__ballot_sync(0xFFFFFFFFu, larger == p.top - 1)) - 1;
+        const uint32_t bound = __shfl_sync(0xFFFFFFFFu, mo, at);
+        if (omax >= bound && omax) {
+            auto offer_one = [&](float z, int j) {
+                if (ordered(z) >= bound) {
+                    const int n = atomicAdd(&ncand, 1);
+                    if (n < kCand) cand[n] = make_key(z, j);
+                }
+            };
+            if (single >= 0) offer_one(Elem<T>::get(sl.row[single]), single);
+            const volatile int *listed = &ncand;
+#pragma unroll 4
+            for (int u = tid; u < sl.nv && *listed <= kCand; u += THREADS) {
+                float f[kPerVec<T>];
+                widen_vec<T>(sl.vec(u), f);
+#pragma unroll
+                for (int e = 0; e < kPerVec<T>; ++e) offer_one(f[e], sl.v0 + u * kPerVec<T> + e);
+            }
+        }
+        __syncthreads();
+        int n = ncand;
+        if (n > kCand) {
+            // many equal values: exact lists, one per warp (keys start at 0: below every key)
+            __syncthreads();
+            unsigned long long list = 0;
+            auto offer_all = [&](unsigned long long x) {
+                unsigned b = __ballot_sync(0xFFFFFFFFu, x > __shfl_sync(0xFFFFFFFFu, list, p.top - 1));
+                while (b) {
+                    const int l = __ffs(b) - 1;
+                    b &= b - 1;
+                    const unsigned long long y = __shfl_sync(0xFFFFFFFFu, x, l);
+                    if (y > __shfl_sync(0xFFFFFFFFu, list, p.top - 1)) list_insert(list, y, lane);
+                }
+            };
+            offer_all(single >= 0 ? make_key(Elem<T>::get(sl.row[single]), single) : 0ull);
+            for (int u0 = warp * 32; u0 < sl.nv; u0 += THREADS) {
+                const int u = u0 + lane;
+                float f[kPerVec<T>];
+                const bool real = u < sl.nv;
+                widen_vec<T>(real ? sl.vec(u) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+                for (int e = 0; e < kPerVec<T>; ++e)
+                    offer_all(real ? make_key(f[e], sl.v0 + u * kPerVec<T> + e) : 0ull);
+            }
+            if (lane < p.top) cand[warp * p.top + lane] = list;
+            n = W * p.top;
+            __syncthreads();
+        }
+        const int k = rank_keys<THREADS>(cand, n, p.top, best);
+        if (tid == 0) nbest = k;
+    }
+
+    // ---- join the row's CTAs: CTA 0 reads the others' sums and keys
+    if (p.cluster > 1) {
+        if (tid == 0) mine = all;
+        cluster_sync();
+        if (rank == 0) {
+            const uint32_t own = smem_u32(&mine);
+            for (int r = 1; r < p.cluster; ++r) {
+                const uint32_t q = mapa_shared(own, r);
+                const Sums b{__uint_as_float(ld_cluster_u32(q)), __uint_as_float(ld_cluster_u32(q + 4)),
+                             __uint_as_float(ld_cluster_u32(q + 8)), __uint_as_float(ld_cluster_u32(q + 12))};
+                all = join(all, b);
+            }
+            if (p.top) {
+                const uint32_t at = smem_u32(best), cnt = smem_u32(&nbest);
+                for (int x = tid; x < p.cluster * kMaxTop; x += THREADS) {
+                    const int r = x / kMaxTop, j = x % kMaxTop;
+                    const bool have = j < static_cast<int>(ld_cluster_u32(mapa_shared(cnt, r)));
+                    const uint32_t q = mapa_shared(at, r) + 8u * j;
+                    const uint32_t lo = have ? ld_cluster_u32(q) : 0u, hi = have ? ld_cluster_u32(q + 4) : 0u;
+                    cand[x] = (static_cast<unsigned long long>(hi) << 32) | lo;
+                }
+                __syncthreads();
+                rank_keys<THREADS>(cand, p.cluster * kMaxTop, p.top, best);
+            }
+        }
+        cluster_sync();  // the others' shared memory has been read
+        if (rank) return;
+    }
+    if (p.top) __syncthreads();
+
+    // The largest logit is finite, its product with c is not (logits near the
+    // type's limits, e.g. a row masked with its lowest value): sums about the
+    // logit itself, in a second pass by this CTA alone.
+    const bool extreme = fabsf(all.zmax) < INFINITY && !(fabsf(all.zmax * p.c) < INFINITY);
+    if (extreme) {
+        const float zmax = all.zmax;
+        float s = 0.0f, e = 0.0f;
+        for (int j = tid; j < p.vocab; j += THREADS) {
+            const float u = max_nan((Elem<T>::get(sl.row[j]) - zmax) * p.c, kFloor), w = exp2_fast(u);
+            s += w;
+            e = fmaf(w, u, e);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
+        }
+        if (lane == 0) part[warp] = Sums{0.0f, s, e, zmax};
+        __syncthreads();
+        all.s = all.e = 0.0f;
+        for (int w = 0; w < W; ++w) {
+            all.s += part[w].s;
+            all.e += part[w].e;
+        }
+    }
+
+    const float logs = log2f(all.s);
+    const bool none = all.zmax == -INFINITY && all.s == 0.0f;  // nothing but -inf
+    const bool bad = isnan(all.s);
+    auto logp_of = [&](float z) {
+        if (none) return -INFINITY;
+        return kLn2 * ((extreme ? (z - all.zmax) * p.c : fmaf(z, p.c, -all.ref)) - logs);
+    };
+    if (tid == 0) {
+        if (p.lse) p.lse[i] = none ? -INFINITY : extreme ? fmaf(all.zmax, p.scale, kLn2 * logs) : kLn2 * (all.ref + logs);
+        if (p.entropy) p.entropy[i] = none ? 0.0f : kLn2 * (logs - all.e / all.s);
+        if (p.logp) {
+            const int t = token_at(p.targets, p.index_bytes, i, p.vocab);
+            p.logp[i] = t >= 0 ? logp_of(Elem<T>::get(sl.row[t])) : 0.0f;
+        }
+    }
+    if (tid < p.top) {
+        const unsigned long long x = best[tid];
+        const float z = unordered(static_cast<uint32_t>(x >> 32));
+        p.top_ids[i * p.top + tid] = bad ? -1 : key_index(x);
+        p.top_logp[i * p.top + tid] = bad ? NAN : logp_of(z);
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+struct LogprobGradArgs {
+    const void *logits, *targets;
+    long long ld, ld_d;
+    int index_bytes, vocab, chunks;
+    float scale;
+    const float *lse, *entropy, *g_logp, *g_entropy;
+    void *dlogits;
+};
+
+// One element: t = scale z - lse (= log p), q = scale z - (lse - H) (= log p +
+// H, which cancel where p is largest: lse - H as a sum of two floats),
+// d = -scale (g + h q) p, and + scale g at the target.
+struct GradRow {
+    float scale, lse, lse_h, lse_h_lo, h, g;  // lse - H = lse_h + lse_h_lo
+    __device__ __forceinline__ float operator()(float z) const
+    {
+        const float t = max_nan(fmaf(z, scale, -lse), kFloor);  // p = 0 there, and its weight stays finite
+        const float q = fmaxf(fmaf(z, scale, -lse_h) - lse_h_lo, kFloor);
+        const float p = exp2_fast(t * 1.44269504088896341f);
+        return -scale * fmaf(h, q, g) * p;
+    }
+};
+
+constexpr int kGradThreads = 256;
+
+// A CTA takes one chunk of a row: kGradThreads * kUnroll vectors.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogprobGradArgs p)
+{
+    constexpr int E = kPerVec<T>;
+    const long long i = blockIdx.x / p.chunks;
+    const int chunk = static_cast<int>(blockIdx.x - i * p.chunks), tid = threadIdx.x;
+    const T *z = static_cast<const T *>(p.logits) + i * p.ld;
+    T *d = static_cast<T *>(p.dlogits) + i * p.ld_d;
+    const int t = token_at(p.targets, p.index_bytes, i, p.vocab);
+    const float lse = __ldg(p.lse + i);
+    const bool none = lse == -INFINITY;  // a row of -inf: zero gradient
+    const float g = t >= 0 && !none ? __ldg(p.g_logp + i) : 0.0f;
+    const float h = p.g_entropy && !none ? __ldg(p.g_entropy + i) : 0.0f;
+    const float H = p.g_entropy && !none ? __ldg(p.entropy + i) : 0.0f;
+    // two-sum of lse and -H (Knuth): the rounding error of lse - H, exactly
+    const float lh = lse - H, back = lh - lse, lo = (lse - (lh - back)) + (-H - back);
+    const GradRow f{p.scale, none ? 0.0f : lse, none ? 0.0f : lh, none ? 0.0f : lo, h, g};
+    auto one = [&](int j) {
+        float r = f(Elem<T>::get(z[j]));
+        if (j == t) r = fmaf(p.scale, g, r);
+        d[j] = Elem<T>::put(r);
+    };
+
+    const uint32_t za = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z)) & 15u;
+    const uint32_t da = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(d)) & 15u;
+    if (za != da) {  // the two rows never align together: element by element
+        const int j0 = chunk * kGradThreads * kUnroll * E;
+#pragma unroll 4
+        for (int j = j0 + tid; j < min(j0 + kGradThreads * kUnroll * E, p.vocab); j += kGradThreads) one(j);
+        return;
+    }
+    const int head = min(za ? static_cast<int>((16u - za) / sizeof(T)) : 0, p.vocab);
+    const int nv = (p.vocab - head) / E;
+    if (chunk == 0) {
+        const int rest = head + nv * E;
+        if (tid < head) one(tid);
+        else if (tid >= 32 && tid - 32 < p.vocab - rest) one(rest + tid - 32);
+    }
+    const uint4 *zv = reinterpret_cast<const uint4 *>(z + head);
+    uint4 *dv = reinterpret_cast<uint4 *>(d + head);
+    const int v0 = chunk * kGradThreads * kUnroll + tid;
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        if (v0 + u * kGradThreads < nv) x[u] = zv[v0 + u * kGradThreads];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const int v = v0 + u * kGradThreads;
+        if (v >= nv) break;
+        float y[E];
+        widen_vec<T>(x[u], y);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = f(y[e]);
+        const int at = t - head - v * E;
+        if (t >= 0 && at >= 0 && at < E) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (e == at) y[e] = fmaf(p.scale, g, y[e]);
+        }
+        dv[v] = narrow_vec<T>(y);
+    }
+}
+
+template <typename T, int THREADS>
+cudaError_t launch_logprobs(const LogprobArgs &a, long long rows, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * a.cluster));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a);
+}
+
+template <typename T>
+cudaError_t launch_logprobs(const LogprobArgs &a, long long rows, cudaStream_t s)
+{
+    return a.vocab <= 8192 ? launch_logprobs<T, 128>(a, rows, s) : launch_logprobs<T, 512>(a, rows, s);
+}
+
+bool bad_common(const void *logits, long long ld, int index_bytes, long long rows, int vocab, int dtype, float scale)
+{
+    return rows < 0 || vocab < 1 || ld < vocab || (dtype != CDG_F16 && dtype != CDG_BF16 && dtype != CDG_F32) ||
+           (index_bytes != 4 && index_bytes != 8) || !(scale > 0.0f) || !std::isfinite(scale) || (rows > 0 && !logits);
+}
+
+}  // namespace
+}  // namespace cdg
+
+extern "C" {
+
+int cdg_token_logprobs(const void *logits, long long ld, const void *targets, int index_bytes, long long rows,
+                       int vocab, int dtype, float scale, int top, float *logp, float *lse, float *entropy,
+                       int *top_ids, float *top_logp, cdg_stream_t stream)
+{
+    using namespace cdg;
+    if (bad_common(logits, ld, index_bytes, rows, vocab, dtype, scale) || top < 0 || top > kMaxTop || top > vocab)
+        return CDG_ERR_INVALID_ARG;
+    if (rows == 0) return CDG_OK;
+    if (!targets != !logp || (top > 0) != (top_ids != nullptr) || (top > 0) != (top_logp != nullptr) ||
+        (!logp && !lse && !entropy && !top))
+        return CDG_ERR_INVALID_ARG;
+    if (rows > (1ll << 31) / kMaxCluster - 1 || vocab > kMaxVocab) return CDG_ERR_UNSUPPORTED;
+    const int es = dtype_bytes(dtype);
+    if (!aligned_to(logits, es) || !aligned_to(targets, index_bytes) || !aligned_to(logp, 4) || !aligned_to(lse, 4) ||
+        !aligned_to(entropy, 4) || !aligned_to(top_ids, 4) || !aligned_to(top_logp, 4))
+        return CDG_ERR_ALIGNMENT;
+    const size_t n = static_cast<size_t>(rows);
+    const Extent in[2] = {extent(logits, matrix_bytes(rows, vocab, ld, es)), extent(targets, n * index_bytes)};
+    const Extent out[5] = {extent(logp, n * 4), extent(lse, n * 4), extent(entropy, n * 4), extent(top_ids, n * top * 4),
+                           extent(top_logp, n * top * 4)};
+    for (int i = 0; i < 5; ++i) {
+        for (const Extent &e : in)
+            if (overlap(out[i], e)) return CDG_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return CDG_ERR_ALIAS;
+    }
+    const int sms = sm_count();
+    if (sms < 1) return CDG_ERR_CUDA;
+    LogprobArgs a{logits, targets, ld, index_bytes, vocab, top, 1, scale,
+                  static_cast<float>(static_cast<double>(scale) * 1.4426950408889634), logp, lse, entropy, top_logp,
+                  top_ids};
+    // CTAs a row: while there are fewer rows than SMs, split a row over a cluster
+    while (a.cluster < kMaxCluster && rows * a.cluster * 2 <= 2ll * sms && vocab / (2 * a.cluster) >= 4096) a.cluster *= 2;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == CDG_F32   ? launch_logprobs<float>(a, rows, s)
+                          : dtype == CDG_F16 ? launch_logprobs<__half>(a, rows, s)
+                                             : launch_logprobs<__nv_bfloat16>(a, rows, s);
+    return e == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
+}
+
+int cdg_token_logprobs_grad(const void *logits, long long ld, const void *targets, int index_bytes, long long rows,
+                            int vocab, int dtype, float scale, const float *lse, const float *entropy,
+                            const float *g_logp, const float *g_entropy, void *dlogits, long long ld_d,
+                            cdg_stream_t stream)
+{
+    using namespace cdg;
+    if (bad_common(logits, ld, index_bytes, rows, vocab, dtype, scale) || ld_d < vocab) return CDG_ERR_INVALID_ARG;
+    if (rows == 0) return CDG_OK;
+    if (!targets || !lse || !g_logp || !dlogits || (g_entropy && !entropy)) return CDG_ERR_INVALID_ARG;
+    const int es = dtype_bytes(dtype);
+    const int per = kGradThreads * kUnroll * (16 / es);
+    const int chunks = (vocab - 1) / per + 1;
+    if (rows > ((1ll << 31) - 1) / chunks || vocab > kMaxVocab) return CDG_ERR_UNSUPPORTED;
+    if (!aligned_to(logits, es) || !aligned_to(targets, index_bytes) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) ||
+        !aligned_to(g_logp, 4) || !aligned_to(g_entropy, 4) || !aligned_to(dlogits, es))
+        return CDG_ERR_ALIGNMENT;
+    const size_t n = static_cast<size_t>(rows);
+    const Extent out = extent(dlogits, matrix_bytes(rows, vocab, ld_d, es));
+    const Extent in[5] = {extent(targets, n * index_bytes), extent(lse, n * 4), extent(entropy, n * 4),
+                          extent(g_logp, n * 4), extent(g_entropy, n * 4)};
+    for (const Extent &e : in)
+        if (overlap(out, e)) return CDG_ERR_ALIAS;
+    if (!(dlogits == logits && ld == ld_d) && overlap(out, extent(logits, matrix_bytes(rows, vocab, ld, es))))
+        return CDG_ERR_ALIAS;
+    const LogprobGradArgs a{logits, targets, ld, ld_d, index_bytes, vocab, chunks, scale, lse, entropy, g_logp,
+                            g_entropy, dlogits};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = static_cast<unsigned>(rows * chunks);
+    if (dtype == CDG_F32) logprobs_grad_kernel<float><<<grid, kGradThreads, 0, s>>>(a);
+    else if (dtype == CDG_F16) logprobs_grad_kernel<__half><<<grid, kGradThreads, 0, s>>>(a);
+    else logprobs_grad_kernel<__nv_bfloat16><<<grid, kGradThreads, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,75 @@
+// Launch parameters shared by the host side (muon_api.cu) and the sm_103a
+// kernels (muon_sm103.cu) of the orthogonalised weight update.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cdg_params.h"
+
+// Fixed-point-like scales (powers of two) of the fp16 operands: X, A = X X^T
+// and B = b A + c A^2 are stored times 1024, so that values of norm about 1
+// keep their 11 bits down to 6e-8 of it.
+#define CMU_SCALE 1024.0f
+#define CMU_MAX_PARTIALS 512  // partial sums of squares a matrix
+#define CMU_BM 128
+#define CMU_BN 128
+#define CMU_BK 64
+#define CMU_STAGES 6
+// Two-part products move their sums from tensor memory to registers after this
+// many K blocks (see gemm_kernel); one-part products once.
+#define CMU_CHAIN 2
+#define CMU_STAGE_BYTES ((CMU_BM + CMU_BN) * CMU_BK * 2)
+
+// One batched product C[b] = opA[b] opB[b]^T over K, fp32 sums, and what its
+// epilogue makes of it.
+enum CmuMode {
+    CMU_GRAM = 0,    // A = X X^T (symmetric)
+    CMU_POLY = 1,    // B = b A + c A A^T (symmetric), its diagonal apart
+    CMU_UPDATE = 2,  // X' = (a + diag B) X + (B - diag B) X
+    CMU_FINAL = 3    // the last update: O, or W
+};
+
+struct CmuGemm {
+    // high and low parts of the operands: {k, rows, batch}, boxes {64, 128, 1};
+    // tmB of an update: {n, k, batch}, boxes {64, 64, 1}
+    CUtensorMap tmA[2], tmB[2];
+    int mode;
+    int parts;        // 1: high parts; 3: high x high + high x low + low x high
+    int M, N, K, batch;
+    int first;        // X is still times xs[b] instead of CMU_SCALE
+    int has_lo;       // X has a low part
+    int pitch_x, pitch_a;  // row pitches of X (n) and of A, B (m), elements
+    const float *xs;
+    const uint16_t *x_hi, *x_lo;  // X before the step
+    uint16_t *y_hi, *y_lo;        // X after it
+    uint16_t *mat, *mat_lo;       // A (written by GRAM, read by POLY); low parts with parts = 3
+    uint16_t *poly, *poly_lo;     // B without its diagonal (written by POLY)
+    float *diag;                  // diagonal of B
+    float a, b, c;
+    // FINAL: O (dtype) or W_out; transposed: element (i, j) of X is element (j, i) of O
+    int out_type, transposed, rows, cols;
+    void *out;
+    const float *w_in;
+    float w_keep, w_step;  // W_out = w_keep W - w_step O
+    int *status;
+};
+
+struct CmuPrepare {
+    int batch, rows, cols, dtype, transposed, partials;
+    int nesterov;         // -1: U itself; 0, 1: momentum
+    float momentum, eps;
+    const void *u;        // U or G
+    const float *m_in;
+    float *m_out;
+    float *partial;       // [batch][CMU_MAX_PARTIALS]
+    float *xs;            // [batch]
+    uint16_t *x_hi, *x_lo;
+    int pitch_x, has_lo;
+};
+
+cudaError_t cmu_prepare_kernels();
+cudaError_t cmu_launch_norm(const CmuPrepare &p, cudaStream_t stream);
+cudaError_t cmu_launch_split(const CmuPrepare &p, cudaStream_t stream);
+cudaError_t cmu_launch_gemm(const CmuGemm &p, cudaStream_t stream);

@@ -64,7 +64,8 @@ typedef enum {
                                   /* CDG_NOALLOC_MAX_WEIGHT_BYTES                 */
 } cdg_status_t;
 
-typedef enum { CDG_F16 = 0, CDG_BF16 = 1 } cdg_dtype_t;
+/* CDG_F32 is taken by the token operators and the weight update (below) only. */
+typedef enum { CDG_F16 = 0, CDG_BF16 = 1, CDG_F32 = 2 } cdg_dtype_t;
 
 /* Epilogue flags (bit set). */
 enum {
@@ -477,6 +478,156 @@ int cdg_wgrad(cdg_wgrad_t h, const void *dY, const void *x, void *dW, void *work
 
 /* Synchronise stream, then read and clear the plan's device status word. */
 int cdg_wgrad_device_status(cdg_wgrad_t h, cdg_stream_t stream);
+
+/*
+ * Token operators: the two ends of a training step whose layers' gradients
+ * cdg_dgrad and cdg_wgrad compute -- the log probabilities of given tokens
+ * with the gradient of the logits (the first dY), and the embedding lookup
+ * with its gradient -- and the forms that serving takes them in.
+ *
+ * None of these needs a plan or synchronises; every call is asynchronous on
+ * stream and allocates nothing.  Sizes of zero rows or tokens launch nothing.
+ * Matrices have unit column stride and a row stride `ld` in elements (at least
+ * the row length); rows may start at any element (pointers aligned to the
+ * element; no 16-byte rule).  dtype is CDG_F16, CDG_BF16 or CDG_F32.  Token
+ * numbers are int32 (index_bytes = 4) or int64 (8); a number outside
+ * [0, vocab) -- -1, -100 -- names no token.  Results do not depend on
+ * scheduling: repeated calls give the same bits.
+ *
+ * cdg_token_logprobs: with z = scale * logits[i], p = softmax(z),
+ *
+ *     lse[i]     = log sum over j of exp(z_j)
+ *     logp[i]    = z_t - lse[i], t = targets[i]; 0 where there is no token
+ *     entropy[i] = - sum over j of p_j log p_j   (p_j = 0 adds nothing)
+ *     top_ids[i][0..top), top_logp[i][0..top):
+ *                  the `top` largest logits, largest first, equal ones by
+ *                  lowest number, and their log probabilities
+ *
+ * Sums are fp32.  Logits of -inf (masked tokens) have probability 0.  A row of
+ * -inf alone has lse = logp = top_logp = -inf, entropy 0 and top_ids 0, 1, ...
+ * A row that holds NaN or +inf answers NaN everywhere, and top_ids -1.
+ *   scale       > 0, finite (1 / temperature)
+ *   vocab       at most 2^30
+ *   top         0 .. 32, at most vocab
+ *   targets and logp may both be NULL; lse and entropy may be NULL; top_ids and
+ *   top_logp are NULL exactly when top = 0.  fp32 outputs, int32 top_ids,
+ *   dense, none overlapping another or the logits (CDG_ERR_ALIAS).
+ */
+int cdg_token_logprobs(const void *logits, long long ld, const void *targets, int index_bytes, long long rows,
+                       int vocab, int dtype, float scale, int top, float *logp, float *lse, float *entropy,
+                       int *top_ids, float *top_logp, cdg_stream_t stream);
+
+/*
+ * The gradient of cdg_token_logprobs: for the row gradients g = g_logp[i] and
+ * h = g_entropy[i] of logp and entropy,
+ *
+ *     dlogits[i][j] = scale * (g (1[j = t] - p_j) - h p_j (log p_j + entropy[i]))
+ *
+ * with log p_j = z_j - lse[i]; lse and entropy as cdg_token_logprobs wrote
+ * them.  A row without a token has g = 0; a row of -inf alone gets zeros.
+ * g_entropy may be NULL (h = 0; entropy may then be NULL too).  dlogits has
+ * the logits' dtype and may be the logits themselves (same pointer, same
+ * stride); any other overlap is CDG_ERR_ALIAS.
+ */
+int cdg_token_logprobs_grad(const void *logits, long long ld, const void *targets, int index_bytes, long long rows,
+                            int vocab, int dtype, float scale, const float *lse, const float *entropy,
+                            const float *g_logp, const float *g_entropy, void *dlogits, long long ld_d,
+                            cdg_stream_t stream);
+
+/*
+ * cdg_embed: out[i][:] = scale * table[tokens[i]][:], rounded once; a row of
+ * zeros where there is no token.  table is vocab x dim, out count x dim, both
+ * dtype.  out must not overlap the table or the tokens.  dim at most 2^24.
+ */
+int cdg_embed(const void *table, long long ld_table, const void *tokens, int index_bytes, long long count, int vocab,
+              int dim, int dtype, float scale, void *out, long long ld_out, cdg_stream_t stream);
+
+/*
+ * The gradient of cdg_embed with respect to the table:
+ *
+ *     dtable[v][:] = scale * (sum of dout[i][:] over the i with tokens[i] = v)
+ *
+ * added in ascending order of i within parts of a fixed size, the parts in
+ * order, in fp32, and rounded once to dtype, or kept fp32 with out_f32 = 1.  accumulate = 0
+ * writes every row of dtable (zeros where no token points); accumulate = 1
+ * adds the sums to the rows that tokens point to and leaves the others alone
+ * (a table tied to an output layer already holds that layer's gradient).
+ *   workspace   device, cdg_embed_grad_workspace_bytes(count, vocab, dim)
+ *               bytes, 16-byte aligned, overwritten
+ * dtable and workspace overlap each other and the inputs nowhere
+ * (CDG_ERR_ALIAS).  count below 2^30, dim at most 2^24.
+ */
+int cdg_embed_grad(const void *dout, long long ld_dout, const void *tokens, int index_bytes, long long count,
+                   int vocab, int dim, int dtype, float scale, void *dtable, long long ld_dtable, int out_f32,
+                   int accumulate, void *workspace, cdg_stream_t stream);
+
+/* Bytes of cdg_embed_grad's workspace; 0 for sizes it refuses.  Host only. */
+size_t cdg_embed_grad_workspace_bytes(long long count, int vocab, int dim);
+
+/*
+ * The weight update from an orthogonalised gradient (the Muon optimiser's
+ * step): what consumes cdg_wgrad's dW, a K x (R*S*C) matrix as it is stored.
+ *
+ * cdg_muon_orthogonalize: for every rows x cols matrix U of a batch, `steps`
+ * Newton-Schulz products with the quintic (a, b, c),
+ *
+ *     X = U / (|U|_F + eps)
+ *     steps times:  A = X X^T,  X = a X + (b A + c A^2) X
+ *
+ * on the smaller side (X^T X for rows > cols), which drives the singular
+ * values of U towards 1 and keeps its singular vectors.  U and O are dtype
+ * (CDG_F16, CDG_BF16 or CDG_F32), dense, batch x rows x cols; O may not
+ * overlap U.  Products run on the tensor cores on fp16 operands with fp32
+ * sums; X is held as a high and a low fp16 part and the diagonal of b A + c A^2
+ * in fp32, so that O is within about 1e-3 of the iteration in exact arithmetic
+ * (relative, Frobenius).  CDG_F32 plans, and plans whose smaller side is at
+ * most 128, take every operand as two fp16 parts, at three products for one:
+ * O is then within about 1e-5.  |U|_F must be representable: its square is summed in
+ * fp32.  A zero U gives a zero O; a U with a NaN or an infinity gives NaN.
+ *
+ * cdg_muon_step: the whole update of fp32 weights W from a gradient G (dtype)
+ * and its momentum M (fp32), all batch x rows x cols, dense:
+ *
+ *     M_out = momentum * M + G
+ *     U     = G + momentum * M_out  (nesterov = 1),  M_out (nesterov = 0)
+ *     W_out = (1 - lr * weight_decay) * W - lr * update_scale * orthogonalize(U)
+ *
+ * M_out may be M, and W_out may be W; no other overlap (CDG_ERR_ALIAS).
+ *
+ * A plan holds one shape.  Calls on one plan must not overlap on the GPU if
+ * they share the workspace (device, cdg_muon_workspace_bytes bytes, 256-byte
+ * aligned, overwritten).  Pointers of U, O, G, M and W are 16-byte aligned.
+ * A device-side pipeline timeout (which a correct launch never hits) is
+ * reported by cdg_muon_device_status.
+ */
+typedef struct cdg_muon_st *cdg_muon_t;
+
+/* batch, rows, cols >= 1; steps 1 .. 32; eps >= 0.  (a, b, c) must keep
+ * [0, 1] bounded over the steps: every iterate of the scalar map
+ * x -> a x + b x^3 + c x^5 within 4, and |b x^2 + c x^4| <= 60
+ * (CDG_ERR_INVALID_ARG otherwise). */
+int cdg_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a, float b, float c, float eps,
+                  cdg_muon_t *out);
+/* The same planning without a device (num_sms stands in for the SM count). */
+int cdg_muon_plan_host(int batch, int rows, int cols, int dtype, int steps, float a, float b, float c, float eps,
+                       int num_sms, cdg_muon_t *out);
+void cdg_muon_destroy(cdg_muon_t h);
+size_t cdg_muon_workspace_bytes(cdg_muon_t h);
+
+typedef struct {
+    int m, n;             /* the smaller and the larger side                      */
+    int transposed;       /* 1: rows > cols, the kernels hold U^T                 */
+    int tile_m, tile_n;   /* output tile of the products                          */
+    int launches;         /* kernel launches of one cdg_muon_orthogonalize        */
+} cdg_muon_info_t;
+int cdg_muon_get_info(cdg_muon_t h, cdg_muon_info_t *info);
+
+int cdg_muon_orthogonalize(cdg_muon_t h, const void *U, void *O, void *workspace, cdg_stream_t stream);
+int cdg_muon_step(cdg_muon_t h, const float *W, const void *G, const float *M, float *W_out, float *M_out, float lr,
+                  float momentum, float weight_decay, float update_scale, int nesterov, void *workspace,
+                  cdg_stream_t stream);
+/* Synchronise stream, then read and clear the plan's device status word. */
+int cdg_muon_device_status(cdg_muon_t h, cdg_stream_t stream);
 
 #ifdef __cplusplus
 }
