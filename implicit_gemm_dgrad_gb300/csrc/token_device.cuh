@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/cdg.h"
 
 namespace cdg {
@@ -124,12 +126,16 @@ static inline size_t matrix_bytes(long long rows, long long cols, long long ld, 
     return rows > 0 ? static_cast<size_t>((rows - 1) * ld + cols) * static_cast<size_t>(esize) : 0;
 }
 
+// SM count of the current device (0 on an error); the runtime's own query takes
+// a fifth of a launch, so the answer is kept per device.
 static inline int sm_count()
 {
+    static std::atomic<int> known[64];
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
