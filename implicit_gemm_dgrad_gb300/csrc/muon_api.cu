@@ -53,13 +53,15 @@ bool iteration_bounded(int steps, double a, double b, double c)
 // Up to this smaller side every plan takes two-part operands (see the head of
 // muon_sm103.cu): the products are launch-bound there.
 constexpr int kSmallSide = 128;
+// From this smaller side one-part products run in CTA pairs on 256 x 256 tiles.
+constexpr int kPairSide = 1024;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
 struct cdg_muon_st {
-    int batch, rows, cols, dtype, steps, transposed, m, n, pitch_x, pitch_a, partials, parts;
+    int batch, rows, cols, dtype, steps, transposed, m, n, pitch_x, pitch_a, partials, parts, pair, sms;
     float a, b, c, eps;
     bool host_only;
     int *d_status;
@@ -67,7 +69,7 @@ struct cdg_muon_st {
     // byte offsets in the workspace
     size_t x[2][2], mat[2], poly[2], diag, partial, xs;  // x[buffer][part], mat[part], poly[part]
     const void *cached_ws;
-    CUtensorMap x_rows[2][2], x_cols[2][2], mat_rows[2], poly_rows[2];
+    CUtensorMap x_rows[2][2], x_cols[2][2], mat_rows[2], poly_rows[2], mat_cols[2], poly_cols[2];
     cdg_muon_info_t info;
 };
 
@@ -106,6 +108,8 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     const size_t nb = static_cast<size_t>(batch);
     const size_t xb = nb * m * h->pitch_x * 2, ab = nb * m * h->pitch_a * 2;
     h->parts = dtype == CDG_F32 || m <= kSmallSide ? 3 : 1;
+    h->pair = h->parts == 1 && m >= kPairSide;
+    h->sms = num_sms;
     for (int i = 0; i < 2; ++i)
         for (int q = 0; q < 2; ++q) h->x[i][q] = take(xb);
     for (int q = 0; q < 2; ++q) {
@@ -119,8 +123,7 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     h->info.m = m;
     h->info.n = n;
     h->info.transposed = h->transposed;
-    h->info.tile_m = CMU_BM;
-    h->info.tile_n = CMU_BN;
+    h->info.tile_m = h->info.tile_n = h->pair ? 256 : 128;
     h->info.launches = 2 + 3 * steps;
     if (!host_only) {
         if (cmu_prepare_kernels() != cudaSuccess || cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess ||
@@ -160,6 +163,8 @@ int encode_maps(cdg_muon_st *h, void *workspace)
         }
         ok = ok && encode(&h->mat_rows[q], ws + h->mat[q], h->m, h->m, h->batch, h->pitch_a, 128);
         ok = ok && encode(&h->poly_rows[q], ws + h->poly[q], h->m, h->m, h->batch, h->pitch_a, 128);
+        ok = ok && encode(&h->mat_cols[q], ws + h->mat[q], h->m, h->m, h->batch, h->pitch_a, 64);
+        ok = ok && encode(&h->poly_cols[q], ws + h->poly[q], h->m, h->m, h->batch, h->pitch_a, 64);
     }
     if (!ok) return CDG_ERR_CUDA;
     h->cached_ws = workspace;
@@ -193,14 +198,9 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
     CmuGemm g;
     std::memset(&g, 0, sizeof g);
     g.batch = h->batch;
-    g.pitch_x = h->pitch_x;
-    g.pitch_a = h->pitch_a;
     g.xs = p.xs;
     g.parts = h->parts;
-    g.mat = at16(h->mat[0]);
-    g.mat_lo = at16(h->mat[1]);
-    g.poly = at16(h->poly[0]);
-    g.poly_lo = at16(h->poly[1]);
+    g.pair = h->pair;
     g.diag = reinterpret_cast<float *>(ws + h->diag);
     g.a = h->a; g.b = h->b; g.c = h->c;
     g.out = f.out; g.out_type = f.out_type; g.w_in = f.w_in; g.w_keep = f.w_keep; g.w_step = f.w_step;
@@ -210,26 +210,32 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
         const int cur = k & 1;
         g.first = k == 0;
         g.has_lo = k > 0 || p.has_lo;
-        g.x_hi = at16(h->x[cur][0]);
-        g.x_lo = at16(h->x[cur][1]);
-        g.y_hi = at16(h->x[cur ^ 1][0]);
-        g.y_lo = at16(h->x[cur ^ 1][1]);
         g.mode = CMU_GRAM;
         g.M = g.N = h->m;
         g.K = h->n;
-        for (int q = 0; q < 2; ++q) g.tmA[q] = g.tmB[q] = h->x_rows[cur][q];
-        if (cmu_launch_gemm(g, s) != cudaSuccess) return CDG_ERR_CUDA;
+        for (int q = 0; q < 2; ++q) {
+            g.tmA[q] = g.tmB[q] = h->x_rows[cur][q];
+            g.tmY[q] = h->mat_rows[q];
+            g.tmT[q] = h->mat_cols[q];
+        }
+        if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
         g.mode = CMU_POLY;
         g.K = h->m;
-        for (int q = 0; q < 2; ++q) g.tmA[q] = g.tmB[q] = h->mat_rows[q];
-        if (cmu_launch_gemm(g, s) != cudaSuccess) return CDG_ERR_CUDA;
+        for (int q = 0; q < 2; ++q) {
+            g.tmA[q] = g.tmB[q] = g.tmE[q] = h->mat_rows[q];
+            g.tmY[q] = h->poly_rows[q];
+            g.tmT[q] = h->poly_cols[q];
+        }
+        if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
         g.mode = k == h->steps - 1 ? CMU_FINAL : CMU_UPDATE;
         g.N = h->n;
         for (int q = 0; q < 2; ++q) {
             g.tmA[q] = h->poly_rows[q];
             g.tmB[q] = h->x_cols[cur][q];
+            g.tmE[q] = h->x_rows[cur][q];
+            g.tmY[q] = h->x_rows[cur ^ 1][q];
         }
-        if (cmu_launch_gemm(g, s) != cudaSuccess) return CDG_ERR_CUDA;
+        if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
     }
     return CDG_OK;
 }

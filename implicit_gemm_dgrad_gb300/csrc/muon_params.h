@@ -13,14 +13,16 @@
 // keep their 11 bits down to 6e-8 of it.
 #define CMU_SCALE 1024.0f
 #define CMU_MAX_PARTIALS 512  // partial sums of squares a matrix
-#define CMU_BM 128
-#define CMU_BN 128
+// A CTA's share of a stage: 128 rows of A and 128 rows (or columns) of B, 64 of K.
 #define CMU_BK 64
-#define CMU_STAGES 6
+#define CMU_STAGES 5
+#define CMU_HALF_BYTES (128 * CMU_BK * 2)
+#define CMU_STAGE_BYTES (2 * CMU_HALF_BYTES)
+#define CMU_STAGING_BYTES (2 * CMU_HALF_BYTES)  // per group of four epilogue warps: 128 x 64 fp16, twice
+#define CMU_BAR_BYTES 512
 // Two-part products move their sums from tensor memory to registers after this
 // many K blocks (see gemm_kernel); one-part products once.
 #define CMU_CHAIN 2
-#define CMU_STAGE_BYTES ((CMU_BM + CMU_BN) * CMU_BK * 2)
 
 // One batched product C[b] = opA[b] opB[b]^T over K, fp32 sums, and what its
 // epilogue makes of it.
@@ -32,21 +34,20 @@ enum CmuMode {
 };
 
 struct CmuGemm {
-    // high and low parts of the operands: {k, rows, batch}, boxes {64, 128, 1};
-    // tmB of an update: {n, k, batch}, boxes {64, 64, 1}
-    CUtensorMap tmA[2], tmB[2];
+    // High and low parts of: the operands ({k, rows, batch}, boxes {64, 128, 1};
+    // tmB of an update {n, k, batch}, boxes {64, 64, 1}), the epilogue's input
+    // and its output (boxes {64, 128, 1}), and the output's mirror image
+    // (symmetric products, boxes {64, 64, 1}).
+    CUtensorMap tmA[2], tmB[2], tmE[2], tmY[2], tmT[2];
     int mode;
+    int pair;         // CTA pairs on 256 x 256 tiles (one-part products), else 128 x 128 tiles
+    int tiles_m, tiles;  // tiles along M; tiles a matrix
     int parts;        // 1: high parts; 3: high x high + high x low + low x high
     int M, N, K, batch;
     int first;        // X is still times xs[b] instead of CMU_SCALE
     int has_lo;       // X has a low part
-    int pitch_x, pitch_a;  // row pitches of X (n) and of A, B (m), elements
     const float *xs;
-    const uint16_t *x_hi, *x_lo;  // X before the step
-    uint16_t *y_hi, *y_lo;        // X after it
-    uint16_t *mat, *mat_lo;       // A (written by GRAM, read by POLY); low parts with parts = 3
-    uint16_t *poly, *poly_lo;     // B without its diagonal (written by POLY)
-    float *diag;                  // diagonal of B
+    float *diag;      // diagonal of B, [batch][M]
     float a, b, c;
     // FINAL: O (dtype) or W_out; transposed: element (i, j) of X is element (j, i) of O
     int out_type, transposed, rows, cols;
@@ -72,4 +73,4 @@ struct CmuPrepare {
 cudaError_t cmu_prepare_kernels();
 cudaError_t cmu_launch_norm(const CmuPrepare &p, cudaStream_t stream);
 cudaError_t cmu_launch_split(const CmuPrepare &p, cudaStream_t stream);
-cudaError_t cmu_launch_gemm(const CmuGemm &p, cudaStream_t stream);
+cudaError_t cmu_launch_gemm(const CmuGemm &p, int sms, cudaStream_t stream);

@@ -24,6 +24,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <climits>
+
 #include "muon_params.h"
 #include "token_device.cuh"
 #include "wait.cuh"
@@ -127,233 +130,568 @@ __global__ void __launch_bounds__(256) split_kernel(const CmuPrepare p)
 }
 
 // ---------------------------------------------------------------- products
-struct Epilogue {
-    const CmuGemm &p;
-    int b, i;         // matrix, row of the output
-    float xs;         // scale of X
-    bool mirror;      // symmetric, off the diagonal: write the transpose too
+__device__ __forceinline__ void tma_load_3d_to(bool pair, uint32_t dst, const CUtensorMap &map, uint32_t bar, int x, int y,
+                                               int z)
+{
+    if (pair) tma_load_3d_pair(dst, reinterpret_cast<uint64_t>(&map), bar, x, y, z);
+    else tma_load_3d(dst, reinterpret_cast<uint64_t>(&map), bar, x, y, z);
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v)
+{
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
 
-    // Columns [j, j + 32) of row i: acc holds the sums.
-    __device__ __forceinline__ void chunk(int j0, const float *acc) const
+// Output tile t: matrix b, tile row tm, tile column tn.  Symmetric products
+// have only tn <= tm.
+struct Tile {
+    int b, tm, tn;
+    __device__ __forceinline__ Tile(const CmuGemm &p, bool sym, int t)
     {
-        if (p.mode == CMU_GRAM) {
-            const float f = (CMU_SCALE / xs) / xs;
-            float v[32];
-#pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = acc[q] * f;
-            symmetric(p.mat, p.mat_lo, j0, v);
-        } else if (p.mode == CMU_POLY) {
-            const long long row = (static_cast<long long>(b) * p.M + i) * p.pitch_a + j0;
-            float v[32];
-#pragma unroll
-            for (int q = 0; q < 32; ++q) {
-                float a = 0.0f;
-                if (i < p.M && j0 + q < p.N) {
-                    a = half_bits(p.mat[row + q]);
-                    if (p.parts == 3) a += half_bits(p.mat_lo[row + q]);
-                }
-                v[q] = fmaf(p.b, a, p.c * (acc[q] * (1.0f / CMU_SCALE)));
-                if (j0 + q == i && i < p.M) {
-                    p.diag[static_cast<long long>(b) * p.M + i] = v[q] * (1.0f / CMU_SCALE);
-                    v[q] = 0.0f;
-                }
-            }
-            symmetric(p.poly, p.poly_lo, j0, v);
+        b = t / p.tiles;
+        const int r = t - b * p.tiles;
+        if (sym) {
+            tm = static_cast<int>((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
+            while ((tm + 1) * (tm + 2) / 2 <= r) ++tm;
+            while (tm * (tm + 1) / 2 > r) --tm;
+            tn = r - tm * (tm + 1) / 2;
         } else {
-            if (i >= p.M) return;
-            const long long at = (static_cast<long long>(b) * p.M + i) * p.pitch_x + j0;
-            const float f = 1.0f / xs, lin = (p.a + p.diag[static_cast<long long>(b) * p.M + i]) * f;
-#pragma unroll
-            for (int q = 0; q < 32; ++q) {
-                const int j = j0 + q;
-                if (j >= p.N) break;
-                float x = half_bits(p.x_hi[at + q]);
-                if (p.has_lo) x += half_bits(p.x_lo[at + q]);
-                const float y = fmaf(lin, x, acc[q] * (f / CMU_SCALE));
-                if (p.mode == CMU_UPDATE) {
-                    const float s = y * CMU_SCALE;
-                    const uint16_t hi = to_half_bits(s);
-                    p.y_hi[at + q] = hi;
-                    p.y_lo[at + q] = to_half_bits(s - half_bits(hi));
-                } else {
-                    const long long o = static_cast<long long>(b) * p.rows * p.cols +
-                                        (p.transposed ? static_cast<long long>(j) * p.cols + i
-                                                      : static_cast<long long>(i) * p.cols + j);
-                    if (p.w_in) static_cast<float *>(p.out)[o] = fmaf(p.w_keep, p.w_in[o], -p.w_step * y);
-                    else if (p.out_type == CDG_T_F32) static_cast<float *>(p.out)[o] = y;
-                    else if (p.out_type == CDG_T_BF16) static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(y);
-                    else static_cast<__half *>(p.out)[o] = __float2half_rn(y);
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void symmetric(uint16_t *out, uint16_t *out_lo, int j0, const float (&v)[32]) const
-    {
-        if (i >= p.M) return;
-        const long long base = static_cast<long long>(b) * p.M * p.pitch_a;
-#pragma unroll
-        for (int q = 0; q < 32; ++q) {
-            if (j0 + q >= p.N) break;
-            const long long at = base + static_cast<long long>(i) * p.pitch_a + j0 + q;
-            const long long to = base + static_cast<long long>(j0 + q) * p.pitch_a + i;
-            const uint16_t hi = to_half_bits(v[q]);
-            out[at] = hi;
-            if (mirror) out[to] = hi;
-            if (p.parts == 3) {
-                const uint16_t lo = to_half_bits(v[q] - half_bits(hi));
-                out_lo[at] = lo;
-                if (mirror) out_lo[to] = lo;
-            }
+            tn = r / p.tiles_m;
+            tm = r - tn * p.tiles_m;
         }
     }
 };
 
-// One 128 x 128 output tile a CTA: warp 0 loads, warp 1 issues the MMAs, warps
-// 4-7 read the accumulator.  Symmetric products compute the tiles on and below
-// the diagonal and write the others as their transposes.
+// Shared memory: the operand ring, the epilogue's staging (a 128 x 64 fp16
+// block in 128-byte-swizzled rows, twice, for each group of four warps),
+// mbarriers.
+template <bool PAIR>
+struct Layout {
+    static constexpr int kGroups = PAIR ? 2 : 1;             // of epilogue warps, 128 columns each
+    static constexpr int kThreads = 128 + 128 * kGroups;
+    static constexpr int kTile = PAIR ? 256 : 128;
+    static constexpr int kCols = 128 * kGroups;              // TMEM columns an accumulator
+    static constexpr int kSmem = 1024 + CMU_STAGES * CMU_STAGE_BYTES + kGroups * CMU_STAGING_BYTES + CMU_BAR_BYTES;
+    static_assert(kSmem <= CDG_MAX_DYN_SMEM, "shared memory");
+    uint32_t s0, staging, full0, empty0, acc_full0, acc_empty0, drain, epi0;
+    __device__ __forceinline__ explicit Layout(uint32_t base)
+    {
+        s0 = base;
+        staging = base + CMU_STAGES * CMU_STAGE_BYTES;
+        full0 = staging + kGroups * CMU_STAGING_BYTES;
+        empty0 = full0 + 8u * CMU_STAGES;
+        acc_full0 = empty0 + 8u * CMU_STAGES;
+        acc_empty0 = acc_full0 + 16u;
+        drain = acc_empty0 + 16u;
+        epi0 = drain + 8u;
+    }
+    static constexpr int kWords = 8 * (2 * CMU_STAGES + 2 + 2 + 1 + kGroups);  // after the mbarriers
+};
+
+// Epilogue of one group of four warps: thread = row of the CTA's 128, 64
+// columns at a time.
+template <bool PAIR>
+struct Epilogue {
+    const CmuGemm &p;
+    const Layout<PAIR> &L;
+    Ctl ctl;
+    int group, warp_in_group, lane, row;  // row: of the CTA's 128
+    bool elected, sym;
+    uint32_t buf0, buf1, bar, phase, sw;
+
+    __device__ __forceinline__ Epilogue(const CmuGemm &p_, const Layout<PAIR> &L_, Ctl c, bool sym_)
+        : p(p_), L(L_), ctl(c), sym(sym_)
+    {
+        const int warp = threadIdx.x / 32 - CDG_EPI_WARP0;
+        lane = threadIdx.x % 32;
+        group = warp / 4;
+        warp_in_group = warp % 4;
+        row = warp_in_group * 32 + lane;
+        elected = elect_one_sync() && warp_in_group == 0;
+        buf0 = L.staging + group * CMU_STAGING_BYTES;
+        buf1 = buf0 + CMU_HALF_BYTES;
+        bar = L.epi0 + 8u * group;
+        phase = 0;
+        sw = row & 7;
+    }
+    __device__ __forceinline__ void sync() const { named_bar_sync(1 + group, 128); }
+    // 16-byte piece q (8 columns) of this thread's row in a staging buffer
+    __device__ __forceinline__ uint32_t piece(uint32_t buf, int q) const
+    {
+        return buf + static_cast<uint32_t>(row) * 128u + ((static_cast<uint32_t>(q) ^ sw) << 4);
+    }
+    // The block of the epilogue's input that a later chunk() needs.
+    __device__ __forceinline__ void fetch(int b, int i0, int j0) const
+    {
+        if (elected) {
+            const bool lo = p.mode == CMU_POLY ? p.parts == 3 : p.has_lo != 0;
+            bulk_wait_group_read<0>();
+            mbar_arrive_expect_tx(bar, lo ? 2 * CMU_HALF_BYTES : CMU_HALF_BYTES);
+            tma_load_3d(buf0, reinterpret_cast<uint64_t>(&p.tmE[0]), bar, j0, i0, b);
+            if (lo) tma_load_3d(buf1, reinterpret_cast<uint64_t>(&p.tmE[1]), bar, j0, i0, b);
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool fetched()
+    {
+        const bool ok = wait_bar(bar, phase, ctl);
+        phase ^= 1u;
+        return !named_bar_red_or(1 + group, 128, !ok);
+    }
+    // Eight values of the input block: high parts, and low parts where there are any.
+    __device__ __forceinline__ void input(int q, bool lo, float (&x)[8]) const
+    {
+        uint32_t w[4];
+        ld_shared_v4(piece(buf0, q), w);
+        widen_vec<__half>(make_uint4(w[0], w[1], w[2], w[3]), x);
+        if (lo) {
+            float y[8];
+            ld_shared_v4(piece(buf1, q), w);
+            widen_vec<__half>(make_uint4(w[0], w[1], w[2], w[3]), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += y[e];
+        }
+    }
+    __device__ __forceinline__ void put(uint32_t buf, int q, const float (&x)[8]) const
+    {
+        const uint4 w = narrow_vec<__half>(x);
+        st_shared_v4(piece(buf, q), w.x, w.y, w.z, w.w);
+    }
+    __device__ __forceinline__ static void low_part(float (&x)[8])
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] -= __half2float(__float2half_rn(x[e]));
+    }
+
+    // v: the sums of columns [j0, j0 + 64) of row i0 + row; j0 < N and i0 < M.
+    // False when the launch is giving up.
+    __device__ __forceinline__ bool chunk(int b, int i0, int j0, bool mirror, float xs, float (&v)[64])
+    {
+        const int i = i0 + row;
+        if (p.mode == CMU_GRAM) {
+            const float f = (CMU_SCALE / xs) / xs;
+#pragma unroll
+            for (int q = 0; q < 64; ++q) v[q] *= f;
+            symmetric(b, i0, j0, mirror, v);
+            return true;
+        }
+        if (!fetched()) return false;
+        if (p.mode == CMU_POLY) {
+            float d = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float a[8];
+                input(q, p.parts == 3, a);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float &x = v[8 * q + e];
+                    x = fmaf(p.b, a[e], p.c * (x * (1.0f / CMU_SCALE)));
+                    if (j0 + 8 * q + e == i) {
+                        d = x;
+                        x = 0.0f;
+                    }
+                }
+            }
+            if (i >= j0 && i < j0 + 64 && i < p.M) p.diag[static_cast<long long>(b) * p.M + i] = d * (1.0f / CMU_SCALE);
+            symmetric(b, i0, j0, mirror, v);
+            return true;
+        }
+        const float f = 1.0f / xs, g = f / CMU_SCALE;
+        const float lin = (p.a + (i < p.M ? p.diag[static_cast<long long>(b) * p.M + i] : 0.0f)) * f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float x[8];
+            input(q, p.has_lo, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[8 * q + e] = fmaf(lin, x[e], v[8 * q + e] * g);
+            if (p.mode == CMU_UPDATE) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = v[8 * q + e] * CMU_SCALE;
+                put(buf0, q, x);
+                low_part(x);
+                put(buf1, q, x);
+            }
+        }
+        if (p.mode == CMU_UPDATE) {
+            fence_proxy_async_smem();
+            sync();
+            if (elected) {
+                tma_store_3d(reinterpret_cast<uint64_t>(&p.tmY[0]), buf0, j0, i0, b);
+                tma_store_3d(reinterpret_cast<uint64_t>(&p.tmY[1]), buf1, j0, i0, b);
+                bulk_commit_group();
+            }
+        } else {
+            result(b, i0, j0, v);
+            fence_proxy_async_smem();  // the block has been read: the next fetch may overwrite it
+            sync();
+        }
+        return true;
+    }
+    // A block of A or B and, off the diagonal, its transpose; high parts, then low parts.
+    __device__ __forceinline__ void symmetric(int b, int i0, int j0, bool mirror, float (&v)[64]) const
+    {
+        for (int part = 0; part < (p.parts == 3 ? 2 : 1); ++part) {
+            if (elected) bulk_wait_group_read<0>();
+            sync();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = v[8 * q + e];
+                put(buf0, q, x);
+                if (mirror) {
+                    // column j of this row -> row j, column `row` of two 64-column blocks
+                    const uint32_t at = buf1 + static_cast<uint32_t>(row / 64) * 8192u + (row & 7) * 2u;
+                    const uint32_t c = (row & 63) >> 3;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) st_shared_u16(at + (8 * q + e) * 128u + ((c ^ e) << 4), to_half_bits(x[e]));
+                }
+                low_part(x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * q + e] = x[e];
+            }
+            fence_proxy_async_smem();
+            sync();
+            if (elected) {
+                tma_store_3d(reinterpret_cast<uint64_t>(&p.tmY[part]), buf0, j0, i0, b);
+                if (mirror) {
+                    tma_store_3d(reinterpret_cast<uint64_t>(&p.tmT[part]), buf1, i0, j0, b);
+                    if (i0 + 64 < p.M) tma_store_3d(reinterpret_cast<uint64_t>(&p.tmT[part]), buf1 + 8192u, i0 + 64, j0, b);
+                }
+                bulk_commit_group();
+            }
+        }
+    }
+    __device__ __forceinline__ void write(long long o, float y) const
+    {
+        if (p.w_in) static_cast<float *>(p.out)[o] = fmaf(p.w_keep, p.w_in[o], -p.w_step * y);
+        else if (p.out_type == CDG_T_F32) static_cast<float *>(p.out)[o] = y;
+        else if (p.out_type == CDG_T_BF16) static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(y);
+        else static_cast<__half *>(p.out)[o] = __float2half_rn(y);
+    }
+    // O or W: lanes along the output's rows either way.
+    __device__ __forceinline__ void result(int b, int i0, int j0, const float (&v)[64]) const
+    {
+        const long long base = static_cast<long long>(b) * p.rows * p.cols;
+        const int n = min(64, p.N - j0);
+        if (p.transposed) {
+            const int i = i0 + row;
+            if (i < p.M) {
+                const long long at = base + static_cast<long long>(j0) * p.cols + i;
+#pragma unroll
+                for (int q = 0; q < 64; ++q)
+                    if (q < n) write(at + static_cast<long long>(q) * p.cols, v[q]);
+            }
+            return;
+        }
+        // through the staging: a warp's 32 rows x 64 columns of fp32, column c of row r at (c + r) % 64
+        sync();  // every row's input has been read
+        const uint32_t w0 = buf0 + warp_in_group * 8192u;
+#pragma unroll
+        for (int q = 0; q < 64; ++q) st_shared_f32(w0 + lane * 256u + ((q + lane) & 63) * 4u, v[q]);
+        __syncwarp();
+        const int r0 = i0 + warp_in_group * 32, rows = min(32, p.M - r0);
+        long long at = base + static_cast<long long>(r0) * p.cols + j0 + lane;
+        for (int r = 0; r < rows; ++r, at += p.cols) {
+            if (lane < n) write(at, ld_shared_f32(w0 + r * 256u + ((lane + r) & 63) * 4u));
+            if (lane + 32 < n) write(at + 32, ld_shared_f32(w0 + r * 256u + ((lane + 32 + r) & 63) * 4u));
+        }
+    }
+
+    // One output tile whose sums are in registers or tensor memory: get(c, v)
+    // fills v with 64-column chunk c of this group.
+    __device__ __forceinline__ int chunks(int i0, int j0) const { return i0 < p.M ? max(0, min(2, (p.N - j0 + 63) / 64)) : 0; }
+};
+
+__device__ __forceinline__ void tmem_ld_64(uint32_t at, float (&v)[64])
+{
+    uint32_t (&r)[64] = reinterpret_cast<uint32_t(&)[64]>(v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x16(at + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * q]));
+    tmem_ld_wait();
+}
+
+// Persistent: every CTA (or CTA pair) walks the output tiles.  Warps 0 and 2
+// load stages in turn, warp 1 issues the MMAs, warps 4.. run the epilogue,
+// which overlaps the next tile's products (two accumulators).  Symmetric
+// products compute the tiles on and below the diagonal and store the others as
+// their transposes.
+//
+// One-part products of large matrices run in CTA pairs: 256 x 256 tiles, each
+// CTA holding half of the rows of A and of B.  Others take 128 x 128 tiles.
 //
 // The tensor core rounds every addition to its fp32 sum towards zero, so long
 // chains drift (a Gaussian 3000 x 4608 fp32 U: 5e-5 in the result).  Two-part
-// products therefore take CMU_CHAIN blocks at a time into one of two
-// accumulators, and the epilogue warps add them up in registers.
-__global__ void __launch_bounds__(CDG_THREADS, 1) gemm_kernel(const __grid_constant__ CmuGemm p)
+// products therefore take CMU_CHAIN blocks at a time into one accumulator
+// after the other, and the epilogue warps add them up in registers.
+template <bool PAIR>
+__global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const __grid_constant__ CmuGemm p)
 {
+    using Lay = Layout<PAIR>;
     extern __shared__ uint8_t smem_raw[];
-    const bool sym = p.mode <= CMU_POLY;
-    const int tm = blockIdx.y, tn = blockIdx.x, b = blockIdx.z;
-    if (sym && tn > tm) return;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    const uint32_t bars = base + CMU_STAGES * CMU_STAGE_BYTES;
-    const uint32_t full0 = bars, empty0 = bars + 8u * CMU_STAGES, acc_full0 = bars + 16u * CMU_STAGES,
-                   acc_empty0 = acc_full0 + 16u, drain_bar = acc_full0 + 32u;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(smem_raw + (bars - raw) + 16 * CMU_STAGES + 40);
-    volatile uint32_t *abort_flag = slot + 1;
+    const Lay L(base);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(smem_raw + (L.full0 - raw) + Lay::kWords);
+    volatile uint32_t *abort_flag = slot + 1, *used = slot + 2;  // used[stage]: parity of its last load, + 2
+    static_assert(Lay::kWords + 8 + 4 * CMU_STAGES <= CMU_BAR_BYTES, "barrier area");
+    const bool sym = p.mode <= CMU_POLY;
     const int warp = threadIdx.x / 32;
+    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+    const int total = p.tiles * p.batch;
+    const int kblocks = (p.K + CMU_BK - 1) / CMU_BK, blocks = p.parts * kblocks;
+    const int chain = p.parts == 3 ? CMU_CHAIN : blocks;
+    grid_dep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < CMU_STAGES; ++s) {
-            mbar_init(full0 + 8u * s, 1);
-            mbar_init(empty0 + 8u * s, 1);
+            mbar_init(L.full0 + 8u * s, 1);
+            mbar_init(L.empty0 + 8u * s, 1);
+            used[s] = 0u;
         }
         for (int a = 0; a < 2; ++a) {
-            mbar_init(acc_full0 + 8u * a, 1);
-            mbar_init(acc_empty0 + 8u * a, 4);  // one arrival per epilogue warp
+            mbar_init(L.acc_full0 + 8u * a, 1);
+            mbar_init(L.acc_empty0 + 8u * a, PAIR ? 16 : 4);  // one arrival per epilogue warp (of both CTAs)
         }
-        mbar_init(drain_bar, 1);
+        mbar_init(L.drain, 1);
+        for (int g = 0; g < Lay::kGroups; ++g) mbar_init(L.epi0 + 8u * g, 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    grid_dep_wait();
     if (warp == 1) {
-        tmem_alloc(smem_u32(slot), 2 * CMU_BN);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(smem_u32(slot), 2 * Lay::kCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(slot), 2 * Lay::kCols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers exist before anything crosses over
     tc_fence_after();
     const uint32_t tmem = *slot;
     const Ctl ctl{abort_flag, p.status};
-    const int kblocks = (p.K + CMU_BK - 1) / CMU_BK, blocks = p.parts * kblocks;
-    const int chain = p.parts == 3 ? CMU_CHAIN : blocks;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
         const bool leader = elect_one_sync();
-        uint32_t loaded = 0;
-        for (int k = 0; k < blocks; ++k) {
-            const int s = k % CMU_STAGES;
-            if (!wait_bar(empty0 + 8u * s, ((k / CMU_STAGES) & 1u) ^ 1u, ctl)) break;
-            if (leader) {
-                const uint32_t sa = base + s * CMU_STAGE_BYTES, sb = sa + CMU_BM * CMU_BK * 2, bar = full0 + 8u * s;
-                // low x high, high x low, then high x high: the tensor core rounds every
-                // addition towards zero, and the small parts go in while the sum is small
-                const int part = k / kblocks, k0 = (k - part * kblocks) * CMU_BK;
-                const uint64_t mapA = reinterpret_cast<uint64_t>(&p.tmA[p.parts == 3 && part == 0]);
-                const uint64_t mapB = reinterpret_cast<uint64_t>(&p.tmB[p.parts == 3 && part == 1]);
-                mbar_arrive_expect_tx(bar, CMU_STAGE_BYTES);
-                tma_load_3d(sa, mapA, bar, k0, tm * CMU_BM, b);
-                if (sym) {
-                    tma_load_3d(sb, mapB, bar, k0, tn * CMU_BN, b);
-                } else {
-                    for (int q = 0; q < CMU_BN / 64; ++q)
-                        tma_load_3d(sb + q * 8192, mapB, bar, tn * CMU_BN + q * 64, k0, b);
+        const uint32_t lead_full0 = PAIR ? mapa_shared(L.full0, 0) : L.full0;
+        int s = 0, turn = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int t = first; ok && t < total; t += step) {
+            const Tile tile(p, sym, t);
+            const int row0 = tile.tm * Lay::kTile + rank * 128, col0 = tile.tn * Lay::kTile + rank * 128;
+            for (int k = 0; k < blocks; ++k) {
+                if (turn == warp) {
+                    if (!wait_bar(L.empty0 + 8u * s, parity ^ 1u, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) {
+                        used[s] = parity | 2u;
+                        const uint32_t sa = L.s0 + s * CMU_STAGE_BYTES, sb = sa + CMU_HALF_BYTES;
+                        const uint32_t bar = lead_full0 + 8u * s;
+                        // low x high, high x low, then high x high: the tensor core rounds every
+                        // addition towards zero, and the small parts go in while the sum is small
+                        const int part = k / kblocks, k0 = (k - part * kblocks) * CMU_BK;
+                        const CUtensorMap &ma = p.tmA[p.parts == 3 && part == 0], &mb = p.tmB[p.parts == 3 && part == 1];
+                        if (rank == 0) mbar_arrive_expect_tx(L.full0 + 8u * s, (PAIR ? 2 : 1) * CMU_STAGE_BYTES);
+                        tma_load_3d_to(PAIR, sa, ma, bar, k0, row0, tile.b);
+                        if (sym) {
+                            tma_load_3d_to(PAIR, sb, mb, bar, k0, col0, tile.b);
+                        } else {
+                            tma_load_3d_to(PAIR, sb, mb, bar, col0, k0, tile.b);
+                            tma_load_3d_to(PAIR, sb + 8192u, mb, bar, col0 + 64, k0, tile.b);
+                        }
+                    }
+                    __syncwarp();
+                }
+                turn ^= 2;
+                if (++s == CMU_STAGES) {
+                    s = 0;
+                    parity ^= 1u;
                 }
             }
-            __syncwarp();
-            loaded = k + 1;
-        }
-        // on an abort, let the loads in flight land before the CTA exits
-        if (*abort_flag) {
-            volatile uint32_t no_abort = 0;
-            const Ctl drain{&no_abort, p.status};
-            for (uint32_t k = loaded > CMU_STAGES ? loaded - CMU_STAGES : 0; k < loaded; ++k)
-                wait_bar(full0 + 8u * (k % CMU_STAGES), (k / CMU_STAGES) & 1u, drain);
         }
     } else if (warp == 1) {
-        const bool leader = elect_one_sync();
-        const uint32_t idesc = (1u << 4) | (sym ? 0u : 1u << 16) | (static_cast<uint32_t>(CMU_BN >> 3) << 17) |
-                               (static_cast<uint32_t>(CMU_BM >> 4) << 24);
-        for (int k = 0; k < blocks; ++k) {
-            const int s = k % CMU_STAGES, link = k / chain, in_chain = k - link * chain;
-            const uint32_t acc = link & 1;
-            if (in_chain == 0 && !wait_bar(acc_empty0 + 8u * acc, ((link >> 1) & 1u) ^ 1u, ctl)) break;
-            if (!wait_bar(full0 + 8u * s, (k / CMU_STAGES) & 1u, ctl)) break;
-            tc_fence_after();
-            if (leader) {
-                const uint32_t sa = base + s * CMU_STAGE_BYTES, sb = sa + CMU_BM * CMU_BK * 2;
-                const uint64_t ad = sdesc_k128_sw128(sa);
-                const uint64_t bd = sym ? sdesc_k128_sw128(sb) : desc_mn_sw128(sb, 8192);
-                const uint32_t bstep = sym ? 2u : 128u;
+        volatile uint32_t no_abort = 0;
+        if (rank == 0) {
+            const bool leader = elect_one_sync();
+            const uint32_t idesc = (1u << 4) | (sym ? 0u : 1u << 16) | (static_cast<uint32_t>(Lay::kCols >> 3) << 17) |
+                                   (static_cast<uint32_t>(Lay::kTile >> 4) << 24);
+            int s = 0;
+            uint32_t parity = 0, link = 0;
+            bool ok = true;
+            for (int t = first; ok && t < total; t += step) {
+                for (int k = 0, in_chain = 0; k < blocks; ++k) {
+                    const uint32_t acc = link & 1u;
+                    if ((in_chain == 0 && !wait_bar(L.acc_empty0 + 8u * acc, ((link >> 1) & 1u) ^ 1u, ctl)) ||
+                        !wait_bar(L.full0 + 8u * s, parity, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const bool last = in_chain == chain - 1 || k == blocks - 1;
+                    if (leader) {
+                        const uint32_t sa = L.s0 + s * CMU_STAGE_BYTES, sb = sa + CMU_HALF_BYTES;
+                        const uint64_t ad = sdesc_k128_sw128(sa);
+                        const uint64_t bd = sym ? sdesc_k128_sw128(sb) : desc_mn_sw128(sb, 8192);
+                        const uint32_t bstep = sym ? 2u : 128u, d = tmem + acc * Lay::kCols;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    umma_f16(tmem + acc * CMU_BN, ad + 2u * q, bd + bstep * q, idesc, (in_chain | q) != 0);
-                umma_commit(empty0 + 8u * s);
-                if (in_chain == chain - 1 || k == blocks - 1) umma_commit(acc_full0 + 8u * acc);
+                        for (int q = 0; q < 4; ++q) {
+                            if (PAIR) umma_f16_pair(d, ad + 2u * q, bd + bstep * q, idesc, (in_chain | q) != 0);
+                            else umma_f16(d, ad + 2u * q, bd + bstep * q, idesc, (in_chain | q) != 0);
+                        }
+                        if (PAIR) {
+                            umma_commit_pair(L.empty0 + 8u * s);
+                            if (last) umma_commit_pair(L.acc_full0 + 8u * acc);
+                        } else {
+                            umma_commit(L.empty0 + 8u * s);
+                            if (last) umma_commit(L.acc_full0 + 8u * acc);
+                        }
+                    }
+                    __syncwarp();
+                    ++in_chain;
+                    if (last) {
+                        in_chain = 0;
+                        ++link;
+                    }
+                    if (++s == CMU_STAGES) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
+                }
+            }
+            if (leader) {
+                if (PAIR) umma_commit_pair(L.drain);
+                else umma_commit(L.drain);
             }
             __syncwarp();
         }
         // tensor memory is freed only after the MMAs in flight
-        if (leader) umma_commit(drain_bar);
-        __syncwarp();
-        volatile uint32_t no_abort = 0;
-        wait_bar(drain_bar, 0, Ctl{&no_abort, p.status});
+        wait_bar(L.drain, 0, Ctl{&no_abort, p.status});
     } else if (warp >= CDG_EPI_WARP0) {
-        const int quad = warp & 3, lane = threadIdx.x % 32;
-        float sum[CMU_BN];
+        Epilogue<PAIR> e(p, L, ctl, sym);
+        const uint32_t lane_base = static_cast<uint32_t>(e.warp_in_group * 32) << 16;
+        uint32_t link = 0;
         bool ok = true;
-        for (int link = 0; link * chain < blocks; ++link) {
-            const uint32_t acc = link & 1;
-            if (!wait_bar(acc_full0 + 8u * acc, (link >> 1) & 1u, ctl)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int cc = 0; cc < CMU_BN; cc += 32) {
-                uint32_t r[32];
-                const uint32_t at = tmem + acc * CMU_BN + cc + (static_cast<uint32_t>(quad * 32) << 16);
-                tmem_ld_32x32b_x16(at, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-                tmem_ld_32x32b_x16(at + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 32; ++q) sum[cc + q] = link ? sum[cc + q] + __uint_as_float(r[q]) : __uint_as_float(r[q]);
-            }
+        auto hand_back = [&](uint32_t acc) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty0 + 8u * acc);
-        }
-        if (ok) {
-            const Epilogue e{p, b, tm * CMU_BM + quad * 32 + lane, p.first ? p.xs[b] : CMU_SCALE, sym && tn < tm};
+            if (e.lane == 0) {
+                if (PAIR && rank != 0) mbar_arrive_cluster(mapa_shared(L.acc_empty0 + 8u * acc, 0));
+                else mbar_arrive(L.acc_empty0 + 8u * acc);
+            }
+        };
+        for (int t = first; ok && t < total; t += step) {
+            const Tile tile(p, sym, t);
+            const int i0 = tile.tm * Lay::kTile + rank * 128, j0 = tile.tn * Lay::kTile + e.group * 128;
+            const int n = e.chunks(i0, j0);
+            const bool mirror = sym && tile.tn < tile.tm;
+            const float xs = p.first ? p.xs[tile.b] : CMU_SCALE;
+            if (n > 0 && p.mode != CMU_GRAM) e.fetch(tile.b, i0, j0);
+            if constexpr (PAIR) {
+                const uint32_t acc = link & 1u;
+                ok = wait_bar(L.acc_full0 + 8u * acc, (link >> 1) & 1u, ctl);
+                if (named_bar_red_or(1 + e.group, 128, !ok)) break;
+                ++link;
+                tc_fence_after();
+                for (int c = 0; c < n; ++c) {
+                    float v[64];
+                    tmem_ld_64(tmem + acc * Lay::kCols + e.group * 128 + c * 64 + lane_base, v);
+                    if (c == n - 1) hand_back(acc);
+                    if (!(ok = e.chunk(tile.b, i0, j0 + 64 * c, mirror, xs, v))) break;
+                    if (c + 1 < n && p.mode != CMU_GRAM) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
+                }
+                if (n == 0) hand_back(acc);
+            } else {
+                float sum[2][64];
+                for (int k = 0; ok && k < blocks; k += chain, ++link) {
+                    const uint32_t acc = link & 1u;
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(L.acc_full0 + 8u * acc, (link >> 1) & 1u, ctl));
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-            for (int cc = 0; cc < CMU_BN; cc += 32)
-                if (tn * CMU_BN + cc < p.N) e.chunk(tn * CMU_BN + cc, sum + cc);
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(tmem + acc * Lay::kCols + c * 16 + lane_base, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            float &x = sum[c / 4][c % 4 * 16 + q];
+                            x = k ? x + __uint_as_float(r[q]) : __uint_as_float(r[q]);
+                        }
+                    }
+                    hand_back(acc);
+                }
+                if (named_bar_red_or(1, 128, !ok)) break;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (c >= n) break;
+                    if (!(ok = e.chunk(tile.b, i0, j0 + 64 * c, mirror, xs, sum[c]))) break;
+                    if (c + 1 < n && p.mode != CMU_GRAM) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
+                }
+            }
+        }
+        if (e.elected) bulk_wait_group_all();
+    }
+
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) {
+        // copies in flight land before the CTA exits
+        volatile uint32_t no_abort = 0;
+        const Ctl drain{&no_abort, p.status};
+        if (rank == 0) {
+            for (int s = 0; s < CMU_STAGES; ++s)
+                if (used[s] & 2u) wait_bar(L.full0 + 8u * s, used[s] & 1u, drain);
+        }
+        const uint64_t t0 = global_timer_ns();  // the peer's barrier, and the epilogue's blocks
+        while (global_timer_ns() - t0 < 200000ull) {
         }
     }
+    tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // neither CTA leaves while the other may still signal it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * CMU_BN);
+        if (PAIR) tmem_dealloc_pair(tmem, 2 * Lay::kCols);
+        else tmem_dealloc(tmem, 2 * Lay::kCols);
     }
 }
 
-constexpr int kSmem = 1024 + CMU_STAGES * CMU_STAGE_BYTES + 256;
+template <bool PAIR>
+cudaError_t launch_gemm(CmuGemm p, int sms, cudaStream_t s)
+{
+    using Lay = Layout<PAIR>;
+    p.tiles_m = (p.M + Lay::kTile - 1) / Lay::kTile;
+    const int tiles_n = (p.N + Lay::kTile - 1) / Lay::kTile;
+    p.tiles = p.mode <= CMU_POLY ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * tiles_n;
+    const long long total = static_cast<long long>(p.tiles) * p.batch;
+    if (total > INT_MAX / 2) return cudaErrorInvalidConfiguration;
+    const int width = PAIR ? 2 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(width * std::min<long long>(total, std::max(1, sms / width))));
+    cfg.blockDim = dim3(Lay::kThreads);
+    cfg.dynamicSmemBytes = Lay::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = width;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<PAIR>, p);
+}
 
 template <typename T>
 void launch_norm(const CmuPrepare &p, cudaStream_t s)
@@ -372,7 +710,11 @@ void launch_split(const CmuPrepare &p, cudaStream_t s)
 
 cudaError_t cmu_prepare_kernels()
 {
-    return cudaFuncSetAttribute(cdg::gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cdg::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(cdg::gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               cdg::Layout<false>::kSmem);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(cdg::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   cdg::Layout<true>::kSmem);
 }
 
 cudaError_t cmu_launch_norm(const CmuPrepare &p, cudaStream_t s)
@@ -391,9 +733,7 @@ cudaError_t cmu_launch_split(const CmuPrepare &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
-cudaError_t cmu_launch_gemm(const CmuGemm &p, cudaStream_t s)
+cudaError_t cmu_launch_gemm(const CmuGemm &p, int sms, cudaStream_t s)
 {
-    const dim3 grid((p.N + CMU_BN - 1) / CMU_BN, (p.M + CMU_BM - 1) / CMU_BM, p.batch);
-    cdg::gemm_kernel<<<grid, CDG_THREADS, cdg::kSmem, s>>>(p);
-    return cudaGetLastError();
+    return p.pair ? cdg::launch_gemm<true>(p, sms, s) : cdg::launch_gemm<false>(p, sms, s);
 }
