@@ -34,40 +34,49 @@ EncodeTiledFn encode_tiled()
     return fn;
 }
 
-// [0, 1] stays bounded: see cdg_muon_plan.
-bool iteration_bounded(int steps, double a, double b, double c)
+// What the iteration does to a singular value x in [0, 1] (a grid of them):
+// whether it stays within the bounds of cdg_muon_plan, and within those of the
+// Gram form's fp16 operands (see iterate_kernel: A, Q and T times 1024, P times
+// 32; P's size is also what multiplies the rounding of A).
+struct Bounds {
+    bool iteration, gram;
+};
+Bounds iteration_bounds(int steps, double a, double b, double c)
 {
+    Bounds ok{true, true};
     const int kPoints = 8192;
     for (int i = 0; i <= kPoints; ++i) {
-        double x = static_cast<double>(i) / kPoints;
+        double x = static_cast<double>(i) / kPoints, p = 1.0;
         for (int s = 0; s < steps; ++s) {
-            const double x2 = x * x, poly = b * x2 + c * x2 * x2;
-            if (!(std::fabs(poly) <= 60.0)) return false;
-            x *= a + poly;
-            if (!(std::fabs(x) <= 4.0)) return false;
+            const double x2 = x * x, poly = b * x2 + c * x2 * x2, q = a + poly;
+            if (!(std::fabs(poly) <= 60.0)) ok.iteration = false;
+            x *= q;
+            p *= q;
+            if (!(std::fabs(x) <= 4.0)) ok.iteration = false;
+            if (!ok.iteration) return Bounds{false, false};
+            if (std::fabs(q) > 32.0 || std::fabs(q) * x2 > 32.0 || std::fabs(p) > 1000.0) ok.gram = false;
         }
     }
-    return true;
+    return ok;
 }
 
-// Up to this smaller side every plan takes two-part operands (see the head of
-// muon_sm103.cu): the products are launch-bound there.
-constexpr int kSmallSide = 128;
 // From this smaller side one-part products run in CTA pairs on 256 x 256 tiles.
 constexpr int kPairSide = 1024;
+// Ranges of K the Gram form's X X^T is cut into, at most.
+constexpr int kMaxSplits = 8;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
 struct cdg_muon_st {
-    int batch, rows, cols, dtype, steps, transposed, m, n, pitch_x, pitch_a, partials, parts, pair, sms;
+    int batch, rows, cols, dtype, steps, transposed, m, n, pitch_x, pitch_a, partials, gram, splits, sms;
     float a, b, c, eps;
     bool host_only;
     int *d_status;
     size_t ws_bytes;
     // byte offsets in the workspace
-    size_t x[2][2], mat[2], poly[2], diag, partial, xs;  // x[buffer][part], mat[part], poly[part]
+    size_t x[2][2], mat[2], poly[2], diag, partial, sums, xs;  // x[buffer][part], mat[part], poly[part]
     const void *cached_ws;
     CUtensorMap x_rows[2][2], x_cols[2][2], mat_rows[2], poly_rows[2], mat_cols[2], poly_cols[2];
     cdg_muon_info_t info;
@@ -82,8 +91,10 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     *out = nullptr;
     if (batch < 1 || rows < 1 || cols < 1 || (dtype != CDG_F16 && dtype != CDG_BF16 && dtype != CDG_F32) || steps < 1 ||
         steps > 32 || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !std::isfinite(eps) ||
-        eps < 0.0f || num_sms < 1 || !iteration_bounded(steps, a, b, c))
+        eps < 0.0f || num_sms < 1)
         return CDG_ERR_INVALID_ARG;
+    const Bounds bounds = iteration_bounds(steps, a, b, c);
+    if (!bounds.iteration) return CDG_ERR_INVALID_ARG;
     const int m = std::min(rows, cols), n = std::max(rows, cols);
     if (batch > 65535 || m > 32768 || n > (1 << 21)) return CDG_ERR_UNSUPPORTED;
     cdg_muon_st *h = new (std::nothrow) cdg_muon_st();
@@ -107,24 +118,29 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     };
     const size_t nb = static_cast<size_t>(batch);
     const size_t xb = nb * m * h->pitch_x * 2, ab = nb * m * h->pitch_a * 2;
-    h->parts = dtype == CDG_F32 || m <= kSmallSide ? 3 : 1;
-    h->pair = h->parts == 1 && m >= kPairSide;
+    h->gram = m <= CMU_SIDE && bounds.gram;
+    h->splits = std::min((n + CMU_BK - 1) / CMU_BK, kMaxSplits);
     h->sms = num_sms;
+    // low parts of A and B: three products for one (fp32 updates, and small matrices without the Gram form), or P's
+    const bool low = dtype == CDG_F32 || m <= CMU_SIDE;
     for (int i = 0; i < 2; ++i)
         for (int q = 0; q < 2; ++q) h->x[i][q] = take(xb);
     for (int q = 0; q < 2; ++q) {
-        h->mat[q] = q == 0 || h->parts == 3 ? take(ab) : h->mat[0];
-        h->poly[q] = q == 0 || h->parts == 3 ? take(ab) : h->poly[0];
+        h->mat[q] = q == 0 || low ? take(ab) : h->mat[0];
+        h->poly[q] = q == 0 || low ? take(ab) : h->poly[0];
     }
     h->diag = take(nb * m * 4);
     h->partial = take(nb * CMU_MAX_PARTIALS * 4);
     h->xs = take(nb * 4);
+    h->sums = h->gram ? take(nb * h->splits * CMU_SIDE * CMU_SIDE * 4) : 0;
     h->ws_bytes = at;
     h->info.m = m;
     h->info.n = n;
     h->info.transposed = h->transposed;
-    h->info.tile_m = h->info.tile_n = h->pair ? 256 : 128;
-    h->info.launches = 2 + 3 * steps;
+    const bool precise = dtype == CDG_F32;
+    h->info.tile_m = h->info.tile_n = !precise && m >= kPairSide ? 256 : 128;
+    h->info.gram = h->gram && !precise;
+    h->info.launches = h->info.gram ? 5 : 2 + 3 * steps;
     if (!host_only) {
         if (cmu_prepare_kernels() != cudaSuccess || cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess ||
             cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) {
@@ -193,19 +209,53 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
     p.x_hi = at16(h->x[0][0]);
     p.x_lo = at16(h->x[0][1]);
     p.pitch_x = h->pitch_x;
-    p.has_lo = p.nesterov >= 0 || h->parts == 3;
+    // an fp32 update keeps fp32 accuracy; a step's is scaled by the learning rate
+    const bool precise = p.nesterov < 0 && h->dtype == CDG_F32, gram = h->gram && !precise;
+    const int parts = precise || h->m <= CMU_SIDE ? 3 : 1;
+    p.has_lo = p.nesterov >= 0 || precise || (parts == 3 && !gram);
     if (cmu_launch_norm(p, s) != cudaSuccess || cmu_launch_split(p, s) != cudaSuccess) return CDG_ERR_CUDA;
     CmuGemm g;
     std::memset(&g, 0, sizeof g);
     g.batch = h->batch;
     g.xs = p.xs;
-    g.parts = h->parts;
-    g.pair = h->pair;
+    g.parts = parts;
+    g.pair = parts == 1 && h->m >= kPairSide;
+    g.poly_scale = CMU_SCALE;
     g.diag = reinterpret_cast<float *>(ws + h->diag);
     g.a = h->a; g.b = h->b; g.c = h->c;
     g.out = f.out; g.out_type = f.out_type; g.w_in = f.w_in; g.w_keep = f.w_keep; g.w_step = f.w_step;
     g.transposed = h->transposed; g.rows = h->rows; g.cols = h->cols;
     g.status = h->d_status;
+    if (gram) {
+        g.first = 1;
+        g.has_lo = p.has_lo;
+        g.M = g.N = h->m;
+        g.K = h->n;
+        g.mode = CMU_PARTIAL;
+        g.parts = p.has_lo ? 3 : 1;
+        g.tiles = h->splits;
+        g.partial = reinterpret_cast<float *>(ws + h->sums);
+        for (int q = 0; q < 2; ++q) {
+            g.tmA[q] = g.tmB[q] = g.tmE[q] = h->x_rows[0][q];
+            g.tmY[q] = h->x_rows[1][q];
+            g.tmT[q] = h->mat_cols[q];
+        }
+        if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
+        const CmuIterate it{h->batch, h->m, h->steps, h->splits, h->pitch_a, h->a, h->b, h->c, g.partial, g.xs,
+                            at16(h->poly[0]), at16(h->poly[1]), g.diag, h->d_status};
+        if (cmu_launch_iterate(it, s) != cudaSuccess) return CDG_ERR_CUDA;
+        g.mode = CMU_FINAL;
+        g.parts = p.has_lo ? 3 : 2;
+        g.a = 0.0f;
+        g.poly_scale = CMU_POLY_SCALE;
+        g.N = h->n;
+        g.K = h->m;
+        for (int q = 0; q < 2; ++q) {
+            g.tmA[q] = h->poly_rows[q];
+            g.tmB[q] = h->x_cols[0][q];
+        }
+        return cmu_launch_gemm(g, h->sms, s) == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
+    }
     for (int k = 0; k < h->steps; ++k) {
         const int cur = k & 1;
         g.first = k == 0;

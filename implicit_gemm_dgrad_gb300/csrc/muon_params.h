@@ -30,7 +30,22 @@ enum CmuMode {
     CMU_GRAM = 0,    // A = X X^T (symmetric)
     CMU_POLY = 1,    // B = b A + c A A^T (symmetric), its diagonal apart
     CMU_UPDATE = 2,  // X' = (a + diag B) X + (B - diag B) X
-    CMU_FINAL = 3    // the last update: O, or W
+    CMU_FINAL = 3,   // the last update: O, or W
+    CMU_PARTIAL = 4  // fp32 partial sums of X X^T over one of several ranges of K (one tile a matrix)
+};
+
+// The whole iteration of a matrix of up to 128 rows on its Gram matrix: see
+// iterate_kernel.
+#define CMU_SIDE 128
+#define CMU_POLY_SCALE 32.0f  // P, whose eigenvalues reach a^steps, is stored times 32
+struct CmuIterate {
+    int batch, m, steps, splits, pitch_a;
+    float a, b, c;
+    const float *partial;  // [batch][splits][128][128]: X X^T, X times xs
+    const float *xs;
+    uint16_t *poly, *poly_lo;
+    float *diag;
+    int *status;
 };
 
 struct CmuGemm {
@@ -41,14 +56,15 @@ struct CmuGemm {
     CUtensorMap tmA[2], tmB[2], tmE[2], tmY[2], tmT[2];
     int mode;
     int pair;         // CTA pairs on 256 x 256 tiles (one-part products), else 128 x 128 tiles
-    int tiles_m, tiles;  // tiles along M; tiles a matrix
-    int parts;        // 1: high parts; 3: high x high + high x low + low x high
+    int tiles_m, tiles;  // tiles along M; tiles (PARTIAL: ranges of K) a matrix
+    int parts;        // 1: high x high; 2: and low x high before it; 3: and high x low between
     int M, N, K, batch;
     int first;        // X is still times xs[b] instead of CMU_SCALE
     int has_lo;       // X has a low part
     const float *xs;
     float *diag;      // diagonal of B, [batch][M]
-    float a, b, c;
+    float *partial;   // PARTIAL: [batch][tiles][128][128]
+    float a, b, c, poly_scale;  // poly_scale: B is stored times it
     // FINAL: O (dtype) or W_out; transposed: element (i, j) of X is element (j, i) of O
     int out_type, transposed, rows, cols;
     void *out;
@@ -73,4 +89,5 @@ struct CmuPrepare {
 cudaError_t cmu_prepare_kernels();
 cudaError_t cmu_launch_norm(const CmuPrepare &p, cudaStream_t stream);
 cudaError_t cmu_launch_split(const CmuPrepare &p, cudaStream_t stream);
+cudaError_t cmu_launch_iterate(const CmuIterate &p, cudaStream_t stream);
 cudaError_t cmu_launch_gemm(const CmuGemm &p, int sms, cudaStream_t stream);

@@ -148,15 +148,21 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v)
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
-// Output tile t: matrix b, tile row tm, tile column tn.  Symmetric products
-// have only tn <= tm.
+// Output tile t: matrix b, tile row tm, tile column tn, blocks [k0, k0 + kn) of
+// K.  Symmetric products have only tn <= tm.
 struct Tile {
-    int b, tm, tn;
+    int b, tm, tn, k0, kn;
     __device__ __forceinline__ Tile(const CmuGemm &p, bool sym, int t)
     {
         b = t / p.tiles;
-        const int r = t - b * p.tiles;
-        if (sym) {
+        const int r = t - b * p.tiles, kblocks = (p.K + CMU_BK - 1) / CMU_BK;
+        k0 = 0;
+        kn = kblocks;
+        if (p.mode == CMU_PARTIAL) {
+            tm = tn = 0;
+            k0 = static_cast<int>(static_cast<long long>(kblocks) * r / p.tiles);
+            kn = static_cast<int>(static_cast<long long>(kblocks) * (r + 1) / p.tiles) - k0;
+        } else if (sym) {
             tm = static_cast<int>((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
             while ((tm + 1) * (tm + 2) / 2 <= r) ++tm;
             while (tm * (tm + 1) / 2 > r) --tm;
@@ -302,7 +308,7 @@ struct Epilogue {
             symmetric(b, i0, j0, mirror, v);
             return true;
         }
-        const float f = 1.0f / xs, g = f / CMU_SCALE;
+        const float f = 1.0f / xs, g = f / p.poly_scale;
         const float lin = (p.a + (i < p.M ? p.diag[static_cast<long long>(b) * p.M + i] : 0.0f)) * f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -440,13 +446,12 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
     uint32_t *slot = reinterpret_cast<uint32_t *>(smem_raw + (L.full0 - raw) + Lay::kWords);
     volatile uint32_t *abort_flag = slot + 1, *used = slot + 2;  // used[stage]: parity of its last load, + 2
     static_assert(Lay::kWords + 8 + 4 * CMU_STAGES <= CMU_BAR_BYTES, "barrier area");
-    const bool sym = p.mode <= CMU_POLY;
+    const bool sym = p.mode <= CMU_POLY || p.mode == CMU_PARTIAL;  // B is K-major, as A
     const int warp = threadIdx.x / 32;
     const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
     const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
     const int total = p.tiles * p.batch;
-    const int kblocks = (p.K + CMU_BK - 1) / CMU_BK, blocks = p.parts * kblocks;
-    const int chain = p.parts == 3 ? CMU_CHAIN : blocks;
+    const int chain = p.parts > 1 || p.mode == CMU_PARTIAL ? CMU_CHAIN : INT_MAX;
     grid_dep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < CMU_STAGES; ++s) {
@@ -489,6 +494,7 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
         for (int t = first; ok && t < total; t += step) {
             const Tile tile(p, sym, t);
             const int row0 = tile.tm * Lay::kTile + rank * 128, col0 = tile.tn * Lay::kTile + rank * 128;
+            const int blocks = p.parts * tile.kn;
             for (int k = 0; k < blocks; ++k) {
                 if (turn == warp) {
                     if (!wait_bar(L.empty0 + 8u * s, parity ^ 1u, ctl)) {
@@ -501,8 +507,8 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                         const uint32_t bar = lead_full0 + 8u * s;
                         // low x high, high x low, then high x high: the tensor core rounds every
                         // addition towards zero, and the small parts go in while the sum is small
-                        const int part = k / kblocks, k0 = (k - part * kblocks) * CMU_BK;
-                        const CUtensorMap &ma = p.tmA[p.parts == 3 && part == 0], &mb = p.tmB[p.parts == 3 && part == 1];
+                        const int part = k / tile.kn, k0 = (tile.k0 + k - part * tile.kn) * CMU_BK;
+                        const CUtensorMap &ma = p.tmA[p.parts > 1 && part == 0], &mb = p.tmB[p.parts == 3 && part == 1];
                         if (rank == 0) mbar_arrive_expect_tx(L.full0 + 8u * s, (PAIR ? 2 : 1) * CMU_STAGE_BYTES);
                         tma_load_3d_to(PAIR, sa, ma, bar, k0, row0, tile.b);
                         if (sym) {
@@ -531,6 +537,7 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
             uint32_t parity = 0, link = 0;
             bool ok = true;
             for (int t = first; ok && t < total; t += step) {
+                const int blocks = p.parts * Tile(p, sym, t).kn;
                 for (int k = 0, in_chain = 0; k < blocks; ++k) {
                     const uint32_t acc = link & 1u;
                     if ((in_chain == 0 && !wait_bar(L.acc_empty0 + 8u * acc, ((link >> 1) & 1u) ^ 1u, ctl)) ||
@@ -597,7 +604,8 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
             const int n = e.chunks(i0, j0);
             const bool mirror = sym && tile.tn < tile.tm;
             const float xs = p.first ? p.xs[tile.b] : CMU_SCALE;
-            if (n > 0 && p.mode != CMU_GRAM) e.fetch(tile.b, i0, j0);
+            const bool fetches = p.mode != CMU_GRAM && p.mode != CMU_PARTIAL;
+            if (n > 0 && fetches) e.fetch(tile.b, i0, j0);
             if constexpr (PAIR) {
                 const uint32_t acc = link & 1u;
                 ok = wait_bar(L.acc_full0 + 8u * acc, (link >> 1) & 1u, ctl);
@@ -609,12 +617,13 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                     tmem_ld_64(tmem + acc * Lay::kCols + e.group * 128 + c * 64 + lane_base, v);
                     if (c == n - 1) hand_back(acc);
                     if (!(ok = e.chunk(tile.b, i0, j0 + 64 * c, mirror, xs, v))) break;
-                    if (c + 1 < n && p.mode != CMU_GRAM) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
+                    if (c + 1 < n && fetches) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
                 }
                 if (n == 0) hand_back(acc);
             } else {
                 float sum[2][64];
-                for (int k = 0; ok && k < blocks; k += chain, ++link) {
+                const int links = (p.parts * tile.kn - 1) / chain + 1;
+                for (int k = 0; ok && k < links; ++k, ++link) {
                     const uint32_t acc = link & 1u;
                     ok = __all_sync(0xFFFFFFFFu, wait_bar(L.acc_full0 + 8u * acc, (link >> 1) & 1u, ctl));
                     if (!ok) break;
@@ -633,11 +642,24 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                     hand_back(acc);
                 }
                 if (named_bar_red_or(1, 128, !ok)) break;
+                if (p.mode == CMU_PARTIAL) {
+                    // rows and columns below M, 16 bytes at a time (pads up to a multiple of 4 are sums of zeros)
+                    float *out = p.partial + static_cast<long long>(t) * (CMU_SIDE * CMU_SIDE) + e.row * CMU_SIDE;
+                    if (e.row < p.M)
+#pragma unroll
+                        for (int q = 0; q < 128; q += 4)
+                            if (q < p.N)
+                                *reinterpret_cast<float4 *>(out + q) =
+                                    make_float4(sum[q / 64][q % 64], sum[q / 64][q % 64 + 1], sum[q / 64][q % 64 + 2],
+                                                sum[q / 64][q % 64 + 3]);
+                    __syncwarp();
+                    continue;
+                }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if (c >= n) break;
                     if (!(ok = e.chunk(tile.b, i0, j0 + 64 * c, mirror, xs, sum[c]))) break;
-                    if (c + 1 < n && p.mode != CMU_GRAM) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
+                    if (c + 1 < n && fetches) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
                 }
             }
         }
@@ -673,7 +695,8 @@ cudaError_t launch_gemm(CmuGemm p, int sms, cudaStream_t s)
     using Lay = Layout<PAIR>;
     p.tiles_m = (p.M + Lay::kTile - 1) / Lay::kTile;
     const int tiles_n = (p.N + Lay::kTile - 1) / Lay::kTile;
-    p.tiles = p.mode <= CMU_POLY ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * tiles_n;
+    if (p.mode != CMU_PARTIAL)
+        p.tiles = p.mode <= CMU_POLY ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * tiles_n;
     const long long total = static_cast<long long>(p.tiles) * p.batch;
     if (total > INT_MAX / 2) return cudaErrorInvalidConfiguration;
     const int width = PAIR ? 2 : 1;
@@ -691,6 +714,269 @@ cudaError_t launch_gemm(CmuGemm p, int sms, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, gemm_kernel<PAIR>, p);
+}
+
+// ---------------------------------------------------------------- small matrices
+// Up to 128 rows, the iteration runs on the m x m Gram matrix alone, one CTA a
+// matrix, every operand in shared memory:
+//
+//   A = X X^T;  steps times:  Q = a I + b A + c A^2,  P <- Q P,  A <- Q A Q
+//
+// (all polynomials of A: symmetric, and they commute), and the result is P X,
+// one more product.  Against the three products a step over all of X this is
+// 14 dependent products of 128 x 128 instead of 15 launches.  Operands are two
+// fp16 parts (22 bits): a small singular value s enters A as s^2, and the
+// factor P on it, up to a^steps = 485, comes out within 1e-4 to 1e-3 of the
+// iteration on X (64-bit simulation; spectra over four decades).
+//
+// 256 threads: thread t holds row t % 128, columns 64 (t / 128) .. + 63 of the
+// accumulators.
+constexpr int kItThreads = 256;
+constexpr uint32_t kMatBytes = 4 * CMU_HALF_BYTES;  // high parts of columns 0-63, 64-127; then low parts
+constexpr int kItSmem = 1024 + 3 * static_cast<int>(kMatBytes) + 256;
+
+__global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t mA = base, mQ = base + kMatBytes, mP = base + 2 * kMatBytes, bar0 = base + 3 * kMatBytes;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(smem_raw + (bar0 - raw) + 16);
+    volatile uint32_t *abort_flag = slot + 1;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int row = tid % 128, half = tid / 128, b = blockIdx.x;
+    grid_dep_launch_dependents();
+    if (tid == 0) {
+        mbar_init(bar0, 1);
+        mbar_init(bar0 + 8, 1);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    grid_dep_wait();
+    if (warp == 0) {
+        tmem_alloc(smem_u32(slot), 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    const Ctl ctl{abort_flag, p.status};
+    const bool leader = warp == 0 && elect_one_sync();
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+
+    // the ranges' partial sums, in order, to A = sum / xs^2 (fp32, in Q's and P's place)
+    {
+        const float f = (1.0f / p.xs[b]) / p.xs[b];
+        const float *src = p.partial + static_cast<long long>(b) * p.splits * (CMU_SIDE * CMU_SIDE);
+        const int n4 = (p.m + 3) / 4;
+        for (int x = tid; x < p.m * n4; x += kItThreads) {
+            const int r = x / n4, c = x - r * n4;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = 0; k < p.splits; ++k) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + static_cast<long long>(k) * (CMU_SIDE * CMU_SIDE) +
+                                                                         r * CMU_SIDE) + c);
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+            st_shared_v4(mQ + r * 512u + ((static_cast<uint32_t>(c) ^ (r & 31)) << 4), __float_as_uint(s.x * f),
+                         __float_as_uint(s.y * f), __float_as_uint(s.z * f), __float_as_uint(s.w * f));
+        }
+        __syncthreads();
+    }
+
+    // piece q (8 columns) of this thread's row half in matrix `mat`, part 0 or 1
+    auto piece = [&](uint32_t mat, int part, int q) {
+        return mat + static_cast<uint32_t>(2 * part + half) * CMU_HALF_BYTES + static_cast<uint32_t>(row) * 128u +
+               ((static_cast<uint32_t>(q) ^ (row & 7)) << 4);
+    };
+    auto put = [&](uint32_t mat, int q, const float (&x)[8]) {
+        uint4 w = narrow_vec<__half>(x);
+        st_shared_v4(piece(mat, 0, q), w.x, w.y, w.z, w.w);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[e] - __half2float(__float2half_rn(x[e]));
+        w = narrow_vec<__half>(y);
+        st_shared_v4(piece(mat, 1, q), w.x, w.y, w.z, w.w);
+    };
+    auto get = [&](uint32_t mat, int q, float (&x)[8]) {
+        uint32_t w[4];
+        float y[8];
+        ld_shared_v4(piece(mat, 0, q), w);
+        widen_vec<__half>(make_uint4(w[0], w[1], w[2], w[3]), x);
+        ld_shared_v4(piece(mat, 1, q), w);
+        widen_vec<__half>(make_uint4(w[0], w[1], w[2], w[3]), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += y[e];
+    };
+    // accumulator d <- X Y: low x high, high x low, high x high
+    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(128 >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+    auto multiply = [&](uint32_t d, uint32_t x, uint32_t y) {
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint64_t ad = sdesc_k128_sw128(x + (2u * (part == 0) + s) * CMU_HALF_BYTES);
+                const uint64_t bd = sdesc_k128_sw128(y + (2u * (part == 1) + s) * CMU_HALF_BYTES);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) umma_f16(tmem + 128 * d, ad + 2u * q, bd + 2u * q, idesc, (part | s | q) != 0);
+            }
+        umma_commit(bar0 + 8 * d);
+    };
+    // everything written to shared memory is seen by the products issued next
+    auto ready = [&]() {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    uint32_t phase[2] = {0u, 0u};
+    auto wait = [&](int d) {
+        const bool ok = wait_bar(bar0 + 8u * d, phase[d], ctl);
+        phase[d] ^= 1u;
+        tc_fence_after();
+        return __syncthreads_and(ok) != 0;
+    };
+    auto load = [&](int d, int q, float (&v)[16]) {  // 16 columns of accumulator d
+        uint32_t(&r)[16] = reinterpret_cast<uint32_t(&)[16]>(v);
+        tmem_ld_32x32b_x16(tmem + 128 * d + half * 64 + 16 * q + lane_base, r);
+        tmem_ld_wait();
+    };
+
+    // A to its two parts
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        float x[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t c = half * 16u + 2u * q + h;
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (row < p.m && static_cast<int>(4 * c) < p.m) ld_shared_v4(mQ + row * 512u + ((c ^ (row & 31)) << 4), w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * h + e] = CMU_SCALE * __uint_as_float(w[e]);
+        }
+        put(mA, q, x);
+    }
+    ready();
+    constexpr float kInv = 1.0f / CMU_SCALE;
+    bool ok = true;
+    for (int k = 0; k < p.steps; ++k) {
+        // Q = a I + b A + c A A
+        if (leader) multiply(0, mA, mA);
+        __syncwarp();
+        if (!(ok = wait(0))) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v[16];
+            load(0, q, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[8];
+                get(mA, 2 * q + h, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = fmaf(p.b, x[e], p.c * (v[8 * h + e] * kInv));
+                    if (half * 64 + 16 * q + 8 * h + e == row) x[e] += p.a * CMU_SCALE;
+                }
+                put(mQ, 2 * q + h, x);
+                if (k == 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= CMU_POLY_SCALE * kInv;
+                    put(mP, 2 * q + h, x);
+                }
+            }
+        }
+        ready();
+        const bool last = k == p.steps - 1;
+        if (leader) {
+            if (!last) multiply(0, mQ, mA);
+            if (k > 0) multiply(1, mQ, mP);
+        }
+        __syncwarp();
+        if (!last) {  // T = Q A, in A's place
+            if (!(ok = wait(0))) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                load(0, q, v);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = v[8 * h + e] * kInv;
+                    put(mA, 2 * q + h, x);
+                }
+            }
+            ready();
+            if (leader) multiply(0, mA, mQ);  // A <- T Q
+            __syncwarp();
+        }
+        if (k > 0) {  // P <- Q P
+            if (!(ok = wait(1))) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                load(1, q, v);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = v[8 * h + e] * kInv;
+                    put(mP, 2 * q + h, x);
+                }
+            }
+        }
+        if (!last) {
+            if (!(ok = wait(0))) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                load(0, q, v);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = v[8 * h + e] * kInv;
+                    put(mA, 2 * q + h, x);
+                }
+            }
+            ready();
+        }
+    }
+    // P without its diagonal, and the diagonal
+    if (ok && row < p.m) {
+        const long long at = (static_cast<long long>(b) * p.m + row) * p.pitch_a + half * 64;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int j = half * 64 + 8 * q;
+            if (j >= p.m) break;
+            float x[8], y[8];
+            get(mP, q, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (j + e == row) {
+                    p.diag[static_cast<long long>(b) * p.m + row] = x[e] * (1.0f / CMU_POLY_SCALE);
+                    x[e] = 0.0f;
+                }
+                y[e] = x[e] - __half2float(__float2half_rn(x[e]));
+            }
+            *reinterpret_cast<uint4 *>(p.poly + at + 8 * q) = narrow_vec<__half>(x);
+            *reinterpret_cast<uint4 *>(p.poly_lo + at + 8 * q) = narrow_vec<__half>(y);
+        }
+    }
+    if (!ok) {  // giving up: what is in flight ends before tensor memory is freed
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
 }
 
 template <typename T>
@@ -712,7 +998,9 @@ cudaError_t cmu_prepare_kernels()
 {
     const cudaError_t e = cudaFuncSetAttribute(cdg::gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                cdg::Layout<false>::kSmem);
-    return e != cudaSuccess ? e
+    if (e != cudaSuccess) return e;
+    const cudaError_t i = cudaFuncSetAttribute(cdg::iterate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cdg::kItSmem);
+    return i != cudaSuccess ? i
                             : cudaFuncSetAttribute(cdg::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    cdg::Layout<true>::kSmem);
 }
@@ -731,6 +1019,21 @@ cudaError_t cmu_launch_split(const CmuPrepare &p, cudaStream_t s)
     else if (p.dtype == CDG_F16) cdg::launch_split<__half>(p, s);
     else cdg::launch_split<__nv_bfloat16>(p, s);
     return cudaGetLastError();
+}
+
+cudaError_t cmu_launch_iterate(const CmuIterate &p, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch));
+    cfg.blockDim = dim3(cdg::kItThreads);
+    cfg.dynamicSmemBytes = cdg::kItSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cdg::iterate_kernel, p);
 }
 
 cudaError_t cmu_launch_gemm(const CmuGemm &p, int sms, cudaStream_t s)

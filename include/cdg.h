@@ -580,9 +580,8 @@ size_t cdg_embed_grad_workspace_bytes(long long count, int vocab, int dim);
  * overlap U.  Products run on the tensor cores on fp16 operands with fp32
  * sums; X is held as a high and a low fp16 part and the diagonal of b A + c A^2
  * in fp32, so that O is within about 1e-3 of the iteration in exact arithmetic
- * (relative, Frobenius).  CDG_F32 plans, and plans whose smaller side is at
- * most 128, take every operand as two fp16 parts, at three products for one:
- * O is then within about 1e-5.  |U|_F must be representable: its square is summed in
+ * (relative, Frobenius).  With CDG_F32 every operand is two fp16 parts, at
+ * three products for one, and O is within about 1e-5.  |U|_F must be representable: its square is summed in
  * fp32.  A zero U gives a zero O; a U with a NaN or an infinity gives NaN.
  *
  * cdg_muon_step: the whole update of fp32 weights W from a gradient G (dtype)
@@ -592,6 +591,8 @@ size_t cdg_embed_grad_workspace_bytes(long long count, int vocab, int dim);
  *     U     = G + momentum * M_out  (nesterov = 1),  M_out (nesterov = 0)
  *     W_out = (1 - lr * weight_decay) * W - lr * update_scale * orthogonalize(U)
  *
+ * M_out and the sum for W_out are fp32; the orthogonalised update is within
+ * about 1e-3 whatever the dtype of G.
  * M_out may be M, and W_out may be W; no other overlap (CDG_ERR_ALIAS).
  *
  * A plan holds one shape.  Calls on one plan must not overlap on the GPU if
@@ -618,6 +619,7 @@ typedef struct {
     int m, n;             /* the smaller and the larger side                      */
     int transposed;       /* 1: rows > cols, the kernels hold U^T                 */
     int tile_m, tile_n;   /* output tile of the products                          */
+    int gram;             /* 1: the steps run on X X^T alone, on one SM a matrix    */
     int launches;         /* kernel launches of one cdg_muon_orthogonalize        */
 } cdg_muon_info_t;
 int cdg_muon_get_info(cdg_muon_t h, cdg_muon_info_t *info);

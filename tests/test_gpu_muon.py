@@ -211,3 +211,20 @@ def test_plans_workspaces_and_streams():
     assert_near(O1, iterate(U1), "bf16")
     assert_near(O2, iterate(U2), "bf16")
     assert torch.equal(O1, O3)
+
+
+@pytest.mark.parametrize("coefficients,steps,gram", [((A, B, C), 5, 1), ((A, B, C), 8, 0), ((1.875, -1.25, 0.375), 8, 1)])
+@pytest.mark.parametrize("rows,cols", [(48, 700), (128, 128), (90, 31)])
+def test_small_matrices_on_both_paths(rows, cols, coefficients, steps, gram):
+    """Up to 128 rows the steps run on X X^T where the amplification of small
+    singular values stays within 1000 (a^5 = 485; a^8 = 19818 does not), else on X."""
+    import torch
+    p = cdg.muon_plan(rows, cols, batch=2, dtype="bf16", steps=steps, coefficients=coefficients)
+    assert p.info()["gram"] == gram
+    for kind in ("gauss", "lowrank"):
+        U = make(2, rows, cols, kind, 12).bfloat16()
+        O = torch.empty_like(U)
+        p.orthogonalize(U, O, workspace(p))
+        torch.cuda.synchronize()
+        assert p.device_status() == 0
+        assert_near(O, iterate(U, steps, coefficients=coefficients), "bf16", kind)
