@@ -64,6 +64,9 @@ Bounds iteration_bounds(int steps, double a, double b, double c)
 constexpr int kPairSide = 1024;
 // Ranges of K the Gram form's X X^T is cut into, at most.
 constexpr int kMaxSplits = 8;
+// Blocks of K a split tile's CTA takes at least (512 x 4608: 207 us with 4, 196 us with
+// 16, 232 us unsplit; 256 x 1024: 127 us with 4, 112 us unsplit).
+constexpr int kMinRange = 16;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -188,6 +191,22 @@ int encode_maps(cdg_muon_st *h, void *workspace)
 }
 
 // The products after the norm and the first X; the last one writes `out`.
+// The form of a product of M x N outputs over K (maps of 128-row and of 64-row
+// boxes of the B operand for both): pairs where the matrix is large; else square
+// tiles, or narrow ones where square tiles would occupy at most half of the SMs,
+// and then with K split until all SMs work or a range is down to kMinRange blocks.
+void choose_form(CmuGemm &g, bool pair, int sms, const CUtensorMap *b128, const CUtensorMap *b64)
+{
+    const bool sym = g.mode <= CMU_POLY;
+    const long long tm = (g.M + 127) / 128, tn = (g.N + 127) / 128, tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
+    g.form = pair ? CMU_PAIR : 2 * tiles <= sms ? CMU_NARROW : CMU_SQUARE;
+    g.split = 1;
+    const int blocks = (g.K + CMU_BK - 1) / CMU_BK;
+    if (g.form == CMU_NARROW)
+        while (g.split < 8 && 2 * tiles * g.split * 2 <= sms && blocks / (2 * g.split) >= kMinRange) g.split *= 2;
+    for (int q = 0; q < 2; ++q) g.tmB[q] = g.form == CMU_NARROW ? b64[q] : b128[q];
+}
+
 struct Final {
     void *out;
     int out_type;
@@ -219,7 +238,7 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
     g.batch = h->batch;
     g.xs = p.xs;
     g.parts = parts;
-    g.pair = parts == 1 && h->m >= kPairSide;
+    const bool pair = parts == 1 && h->m >= kPairSide;
     g.poly_scale = CMU_SCALE;
     g.diag = reinterpret_cast<float *>(ws + h->diag);
     g.a = h->a; g.b = h->b; g.c = h->c;
@@ -232,6 +251,8 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
         g.M = g.N = h->m;
         g.K = h->n;
         g.mode = CMU_PARTIAL;
+        g.form = CMU_SQUARE;
+        g.split = 1;
         g.parts = p.has_lo ? 3 : 1;
         g.tiles = h->splits;
         g.partial = reinterpret_cast<float *>(ws + h->sums);
@@ -250,10 +271,8 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
         g.poly_scale = CMU_POLY_SCALE;
         g.N = h->n;
         g.K = h->m;
-        for (int q = 0; q < 2; ++q) {
-            g.tmA[q] = h->poly_rows[q];
-            g.tmB[q] = h->x_cols[0][q];
-        }
+        for (int q = 0; q < 2; ++q) g.tmA[q] = h->poly_rows[q];
+        choose_form(g, false, h->sms, h->x_cols[0], h->x_cols[0]);
         return cmu_launch_gemm(g, h->sms, s) == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
     }
     for (int k = 0; k < h->steps; ++k) {
@@ -264,27 +283,29 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
         g.M = g.N = h->m;
         g.K = h->n;
         for (int q = 0; q < 2; ++q) {
-            g.tmA[q] = g.tmB[q] = h->x_rows[cur][q];
+            g.tmA[q] = g.tmE[q] = h->x_rows[cur][q];
             g.tmY[q] = h->mat_rows[q];
             g.tmT[q] = h->mat_cols[q];
         }
+        choose_form(g, pair, h->sms, h->x_rows[cur], h->x_cols[cur]);
         if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
         g.mode = CMU_POLY;
         g.K = h->m;
         for (int q = 0; q < 2; ++q) {
-            g.tmA[q] = g.tmB[q] = g.tmE[q] = h->mat_rows[q];
+            g.tmA[q] = g.tmE[q] = h->mat_rows[q];
             g.tmY[q] = h->poly_rows[q];
             g.tmT[q] = h->poly_cols[q];
         }
+        choose_form(g, pair, h->sms, h->mat_rows, h->mat_cols);
         if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
         g.mode = k == h->steps - 1 ? CMU_FINAL : CMU_UPDATE;
         g.N = h->n;
         for (int q = 0; q < 2; ++q) {
             g.tmA[q] = h->poly_rows[q];
-            g.tmB[q] = h->x_cols[cur][q];
             g.tmE[q] = h->x_rows[cur][q];
             g.tmY[q] = h->x_rows[cur ^ 1][q];
         }
+        choose_form(g, pair, h->sms, h->x_cols[cur], h->x_cols[cur]);
         if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
     }
     return CDG_OK;

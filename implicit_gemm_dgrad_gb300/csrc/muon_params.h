@@ -34,6 +34,10 @@ enum CmuMode {
     CMU_PARTIAL = 4  // fp32 partial sums of X X^T over one of several ranges of K (one tile a matrix)
 };
 
+// Output tiles of a product: 256 x 256 by CTA pairs, 128 x 128, or 128 x 64
+// with K split over the CTAs of a cluster.
+enum CmuForm { CMU_PAIR = 0, CMU_SQUARE = 1, CMU_NARROW = 2 };
+
 // The whole iteration of a matrix of up to 128 rows on its Gram matrix: see
 // iterate_kernel.
 #define CMU_SIDE 128
@@ -55,7 +59,8 @@ struct CmuGemm {
     // (symmetric products, boxes {64, 64, 1}).
     CUtensorMap tmA[2], tmB[2], tmE[2], tmY[2], tmT[2];
     int mode;
-    int pair;         // CTA pairs on 256 x 256 tiles (one-part products), else 128 x 128 tiles
+    int form;         // CMU_PAIR, CMU_SQUARE, CMU_NARROW
+    int split;        // NARROW: CTAs of a cluster that share a tile's K
     int tiles_m, tiles;  // tiles along M; tiles (PARTIAL: ranges of K) a matrix
     int parts;        // 1: high x high; 2: and low x high before it; 3: and high x low between
     int M, N, K, batch;

@@ -48,30 +48,83 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t slice
     return d;
 }
 
-__device__ __forceinline__ float half_bits(uint16_t v) { return __half2float(__ushort_as_half(v)); }
 __device__ __forceinline__ uint16_t to_half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 
 // ---------------------------------------------------------------- norm and first X
-// U at element e of matrix b: U itself, or from G and the new momentum.
-template <typename T>
-__device__ __forceinline__ float update_at(const CmuPrepare &p, long long e)
+// Eight consecutive values of U, from element e (a multiple of 8): U itself,
+// or from G and the momentum.  FIRST: the momentum is updated on the way.
+template <typename T, bool FIRST>
+__device__ __forceinline__ void update_8(const CmuPrepare &p, long long e, float (&u)[8])
+{
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.u) + e);
+    if constexpr (sizeof(T) == 4) {
+        float lo[4], hi[4];
+        widen_vec<T>(src[0], lo);
+        widen_vec<T>(src[1], hi);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            u[q] = lo[q];
+            u[4 + q] = hi[q];
+        }
+    } else {
+        widen_vec<T>(src[0], u);
+    }
+    if (p.nesterov < 0) return;
+    float m[8];
+    const float4 *mi = reinterpret_cast<const float4 *>((FIRST ? p.m_in : p.m_out) + e);
+    float4 *mo = reinterpret_cast<float4 *>(p.m_out + e);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float4 v = mi[h];
+        if (FIRST) {
+            v = make_float4(fmaf(p.momentum, v.x, u[4 * h]), fmaf(p.momentum, v.y, u[4 * h + 1]),
+                            fmaf(p.momentum, v.z, u[4 * h + 2]), fmaf(p.momentum, v.w, u[4 * h + 3]));
+            mo[h] = v;
+        }
+        m[4 * h] = v.x;
+        m[4 * h + 1] = v.y;
+        m[4 * h + 2] = v.z;
+        m[4 * h + 3] = v.w;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) u[q] = p.nesterov ? fmaf(p.momentum, m[q], u[q]) : m[q];
+}
+template <typename T, bool FIRST>
+__device__ __forceinline__ float update_1(const CmuPrepare &p, long long e)
 {
     const float g = Elem<T>::get(static_cast<const T *>(p.u)[e]);
     if (p.nesterov < 0) return g;
-    const float m = p.m_out[e];
+    float m = (FIRST ? p.m_in : p.m_out)[e];
+    if (FIRST) p.m_out[e] = m = fmaf(p.momentum, m, g);
     return p.nesterov ? fmaf(p.momentum, m, g) : m;
 }
 
+constexpr int kPrepareThreads = 256;
+
+// The momentum, and partial sums of squares of U.  A matrix's elements in
+// groups of eight from a multiple of eight, single ones at its ends.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_kernel(const CmuPrepare p)
+__global__ void __launch_bounds__(kPrepareThreads) norm_kernel(const CmuPrepare p)
 {
-    __shared__ float part[8];
-    const long long per = static_cast<long long>(p.rows) * p.cols, base = blockIdx.y * per;
+    __shared__ float part[kPrepareThreads / 32];
+    const long long per = static_cast<long long>(p.rows) * p.cols, a = blockIdx.y * per, b = a + per;
+    const long long a8 = min((a + 7) / 8 * 8, b), b8 = max(a8, b / 8 * 8);
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     float s = 0.0f;
-    for (long long e = blockIdx.x * 256ll + threadIdx.x; e < per; e += gridDim.x * 256ll) {
-        if (p.nesterov >= 0)
-            p.m_out[base + e] = fmaf(p.momentum, p.m_in[base + e], Elem<T>::get(static_cast<const T *>(p.u)[base + e]));
-        const float u = update_at<T>(p, base + e);
+    const long long first = blockIdx.x * static_cast<long long>(kPrepareThreads) + threadIdx.x;
+#pragma unroll 2
+    for (long long g = a8 / 8 + first; g < b8 / 8; g += static_cast<long long>(gridDim.x) * kPrepareThreads) {
+        float u[8];
+        update_8<T, true>(p, 8 * g, u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s = fmaf(u[q], u[q], s);
+    }
+    if (first < a8 - a) {
+        const float u = update_1<T, true>(p, a + first);
+        s = fmaf(u, u, s);
+    } else if (first >= 8 && first - 8 < b - b8) {
+        const float u = update_1<T, true>(p, b8 + first - 8);
         s = fmaf(u, u, s);
     }
 #pragma unroll
@@ -80,19 +133,17 @@ __global__ void __launch_bounds__(256) norm_kernel(const CmuPrepare p)
     __syncthreads();
     if (threadIdx.x == 0) {
         float t = 0.0f;
-        for (int w = 0; w < 8; ++w) t += part[w];
+        for (int w = 0; w < kPrepareThreads / 32; ++w) t += part[w];
         p.partial[blockIdx.y * CMU_MAX_PARTIALS + blockIdx.x] = t;
     }
 }
 
 // X = U 2^k with 2^k |U|_F in [1024, 2048), as a high and a low fp16 part, and
-// xs = 2^k (|U|_F + eps): X / xs is the normalised U.
-template <typename T>
-__global__ void __launch_bounds__(256) split_kernel(const CmuPrepare p)
+// xs = 2^k (|U|_F + eps): X / xs is the normalised U.  The factor 2^k of matrix
+// b, by every CTA.
+__device__ __forceinline__ float first_scale(const CmuPrepare &p, int b, bool write)
 {
-    __shared__ float tile[32][33];
     __shared__ float pw2;
-    const int b = blockIdx.z;
     if (threadIdx.x < 32) {
         float s = 0.0f;
         for (int i = threadIdx.x; i < p.partials; i += 32) s += p.partial[b * CMU_MAX_PARTIALS + i];
@@ -104,28 +155,76 @@ __global__ void __launch_bounds__(256) split_kernel(const CmuPrepare p)
             const int k = norm > 0.0f && finite ? max(-100, min(100, 10 - ilogbf(norm))) : 0;
             const float f = ldexpf(1.0f, k);
             pw2 = finite ? f : NAN;  // an infinity or NaN in U: X is NaN
-            if (blockIdx.x == 0 && blockIdx.y == 0) p.xs[b] = f * (norm + p.eps);
+            if (write) p.xs[b] = f * (norm + p.eps);
         }
     }
     __syncthreads();
-    const float f = pw2;
+    return pw2;
+}
+
+__device__ __forceinline__ void put_parts(const CmuPrepare &p, long long at, const float (&x)[8])
+{
+    *reinterpret_cast<uint4 *>(p.x_hi + at) = narrow_vec<__half>(x);
+    if (p.has_lo) {
+        float y[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y[q] = x[q] - __half2float(__float2half_rn(x[q]));
+        *reinterpret_cast<uint4 *>(p.x_lo + at) = narrow_vec<__half>(y);
+    }
+}
+
+// Rows of a multiple of eight columns, not transposed: X has U's layout.
+template <typename T>
+__global__ void __launch_bounds__(kPrepareThreads) split_flat_kernel(const CmuPrepare p)
+{
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const long long groups = static_cast<long long>(p.rows) * p.cols / 8;
+    const float f = first_scale(p, blockIdx.y, blockIdx.x == 0);
+#pragma unroll 2
+    for (long long g = blockIdx.x * static_cast<long long>(kPrepareThreads) + threadIdx.x; g < groups;
+         g += static_cast<long long>(gridDim.x) * kPrepareThreads) {
+        const long long e = 8 * (blockIdx.y * groups + g);
+        float u[8];
+        update_8<T, false>(p, e, u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) u[q] *= f;
+        put_parts(p, e, u);
+    }
+}
+
+// Any other shape: 64 x 64 blocks of X through shared memory, read along U's
+// rows and written eight columns at a time (the pitch is a multiple of eight).
+template <typename T>
+__global__ void __launch_bounds__(kPrepareThreads) split_kernel(const CmuPrepare p)
+{
+    __shared__ float tile[64][65];
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int b = blockIdx.z, tid = threadIdx.x;
+    const float f = first_scale(p, b, blockIdx.x == 0 && blockIdx.y == 0);
     const int m = p.transposed ? p.cols : p.rows, n = p.transposed ? p.rows : p.cols;
     const long long base = static_cast<long long>(b) * p.rows * p.cols;
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-    const int i0 = blockIdx.y * 32, j0 = blockIdx.x * 32;
-    if (p.transposed) {
-        for (int r = ty; r < 32; r += 8)
-            if (j0 + r < n && i0 + tx < m) tile[tx][r] = update_at<T>(p, base + static_cast<long long>(j0 + r) * p.cols + i0 + tx);
-        __syncthreads();
+    const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+    const int x = tid % 64, y = tid / 64;  // x along U's rows
+    const int u_row0 = p.transposed ? j0 : i0, u_col = (p.transposed ? i0 : j0) + x;
+#pragma unroll 8
+    for (int r = y; r < 64; r += kPrepareThreads / 64) {
+        const float v = u_row0 + r < p.rows && u_col < p.cols
+                            ? f * update_1<T, false>(p, base + static_cast<long long>(u_row0 + r) * p.cols + u_col)
+                            : 0.0f;
+        if (p.transposed) tile[x][r] = v;
+        else tile[r][x] = v;
     }
-    for (int r = ty; r < 32; r += 8) {
-        const int i = i0 + r, j = j0 + tx;
+    __syncthreads();
+#pragma unroll
+    for (int g = tid; g < 64 * 8; g += kPrepareThreads) {
+        const int i = i0 + g / 8, j = j0 + g % 8 * 8;
         if (i >= m || j >= n) continue;
-        const float u = f * (p.transposed ? tile[r][tx] : update_at<T>(p, base + static_cast<long long>(i) * p.cols + j));
-        const long long at = (static_cast<long long>(b) * m + i) * p.pitch_x + j;
-        const uint16_t hi = to_half_bits(u);
-        p.x_hi[at] = hi;
-        if (p.has_lo) p.x_lo[at] = to_half_bits(u - half_bits(hi));
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = tile[g / 8][g % 8 * 8 + q];
+        put_parts(p, (static_cast<long long>(b) * m + i) * p.pitch_x + j, v);
     }
 }
 
@@ -143,53 +242,77 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4])
                  : "r"(addr)
                  : "memory");
 }
+// All threads of the cluster; shared memory written before arriving is seen after waiting.
+__device__ __forceinline__ void cluster_barrier_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_barrier_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v)
 {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
 // Output tile t: matrix b, tile row tm, tile column tn, blocks [k0, k0 + kn) of
-// K.  Symmetric products have only tn <= tm.
+// K.  Symmetric products have only the tiles that reach the diagonal or lie
+// below it; `mirror`: wholly below it.
+template <int FORM>
 struct Tile {
     int b, tm, tn, k0, kn;
-    __device__ __forceinline__ Tile(const CmuGemm &p, bool sym, int t)
+    bool mirror;
+    __device__ __forceinline__ Tile(const CmuGemm &p, bool sym, int t, int rank)
     {
         b = t / p.tiles;
         const int r = t - b * p.tiles, kblocks = (p.K + CMU_BK - 1) / CMU_BK;
-        k0 = 0;
-        kn = kblocks;
+        int part = 0, parts = 1;
+        mirror = false;
         if (p.mode == CMU_PARTIAL) {
             tm = tn = 0;
-            k0 = static_cast<int>(static_cast<long long>(kblocks) * r / p.tiles);
-            kn = static_cast<int>(static_cast<long long>(kblocks) * (r + 1) / p.tiles) - k0;
+            part = r;
+            parts = p.tiles;
         } else if (sym) {
-            tm = static_cast<int>((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
-            while ((tm + 1) * (tm + 2) / 2 <= r) ++tm;
-            while (tm * (tm + 1) / 2 > r) --tm;
-            tn = r - tm * (tm + 1) / 2;
+            // tile rows before tm hold tm (tm + 1) / 2 square tiles, or twice as many narrow ones
+            const int h = FORM == CMU_NARROW ? r / 2 : r;
+            tm = static_cast<int>((sqrtf(8.0f * h + 1.0f) - 1.0f) * 0.5f);
+            while ((tm + 1) * (tm + 2) / 2 <= h) ++tm;
+            while (tm * (tm + 1) / 2 > h) --tm;
+            tn = r - (FORM == CMU_NARROW ? 2 : 1) * (tm * (tm + 1) / 2);
+            mirror = (FORM == CMU_NARROW ? tn / 2 : tn) < tm;
         } else {
             tn = r / p.tiles_m;
             tm = r - tn * p.tiles_m;
         }
+        if (FORM == CMU_NARROW) {
+            part = rank;
+            parts = p.split;
+        }
+        k0 = static_cast<int>(static_cast<long long>(kblocks) * part / parts);
+        kn = static_cast<int>(static_cast<long long>(kblocks) * (part + 1) / parts) - k0;
     }
 };
 
 // Shared memory: the operand ring, the epilogue's staging (a 128 x 64 fp16
 // block in 128-byte-swizzled rows, twice, for each group of four warps),
 // mbarriers.
-template <bool PAIR>
+template <int FORM>
 struct Layout {
-    static constexpr int kGroups = PAIR ? 2 : 1;             // of epilogue warps, 128 columns each
+    static constexpr bool kPair = FORM == CMU_PAIR;
+    static constexpr int kGroups = kPair ? 2 : 1;            // of epilogue warps, 128 columns each (NARROW: 64)
     static constexpr int kThreads = 128 + 128 * kGroups;
-    static constexpr int kTile = PAIR ? 256 : 128;
-    static constexpr int kCols = 128 * kGroups;              // TMEM columns an accumulator
-    static constexpr int kSmem = 1024 + CMU_STAGES * CMU_STAGE_BYTES + kGroups * CMU_STAGING_BYTES + CMU_BAR_BYTES;
+    static constexpr int kTileM = kPair ? 256 : 128, kTileN = kPair ? 256 : FORM == CMU_SQUARE ? 128 : 64;
+    static constexpr int kCols = kTileN;                     // TMEM columns an accumulator
+    static constexpr uint32_t kBBytes = FORM == CMU_NARROW ? CMU_HALF_BYTES / 2 : CMU_HALF_BYTES;
+    static constexpr uint32_t kStage = CMU_HALF_BYTES + kBBytes;
+    static constexpr int kSmem = 1024 + CMU_STAGES * static_cast<int>(kStage) + kGroups * CMU_STAGING_BYTES + CMU_BAR_BYTES;
     static_assert(kSmem <= CDG_MAX_DYN_SMEM, "shared memory");
     uint32_t s0, staging, full0, empty0, acc_full0, acc_empty0, drain, epi0;
     __device__ __forceinline__ explicit Layout(uint32_t base)
     {
         s0 = base;
-        staging = base + CMU_STAGES * CMU_STAGE_BYTES;
+        staging = base + CMU_STAGES * kStage;
         full0 = staging + kGroups * CMU_STAGING_BYTES;
         empty0 = full0 + 8u * CMU_STAGES;
         acc_full0 = empty0 + 8u * CMU_STAGES;
@@ -202,16 +325,16 @@ struct Layout {
 
 // Epilogue of one group of four warps: thread = row of the CTA's 128, 64
 // columns at a time.
-template <bool PAIR>
+template <int FORM>
 struct Epilogue {
     const CmuGemm &p;
-    const Layout<PAIR> &L;
+    const Layout<FORM> &L;
     Ctl ctl;
     int group, warp_in_group, lane, row;  // row: of the CTA's 128
     bool elected, sym;
     uint32_t buf0, buf1, bar, phase, sw;
 
-    __device__ __forceinline__ Epilogue(const CmuGemm &p_, const Layout<PAIR> &L_, Ctl c, bool sym_)
+    __device__ __forceinline__ Epilogue(const CmuGemm &p_, const Layout<FORM> &L_, Ctl c, bool sym_)
         : p(p_), L(L_), ctl(c), sym(sym_)
     {
         const int warp = threadIdx.x / 32 - CDG_EPI_WARP0;
@@ -410,9 +533,11 @@ struct Epilogue {
         }
     }
 
-    // One output tile whose sums are in registers or tensor memory: get(c, v)
-    // fills v with 64-column chunk c of this group.
-    __device__ __forceinline__ int chunks(int i0, int j0) const { return i0 < p.M ? max(0, min(2, (p.N - j0 + 63) / 64)) : 0; }
+    // 64-column chunks of this group in the tile at (i0, j0)
+    __device__ __forceinline__ int chunks(int i0, int j0) const
+    {
+        return i0 < p.M ? max(0, min(FORM == CMU_NARROW ? 1 : 2, (p.N - j0 + 63) / 64)) : 0;
+    }
 };
 
 __device__ __forceinline__ void tmem_ld_64(uint32_t at, float (&v)[64])
@@ -430,16 +555,20 @@ __device__ __forceinline__ void tmem_ld_64(uint32_t at, float (&v)[64])
 // their transposes.
 //
 // One-part products of large matrices run in CTA pairs: 256 x 256 tiles, each
-// CTA holding half of the rows of A and of B.  Others take 128 x 128 tiles.
+// CTA holding half of the rows of A and of B.  Others take 128 x 128 tiles, or,
+// where those would leave most SMs idle, 128 x 64 tiles by clusters that split K:
+// each CTA sums its range, the others leave their sums in shared memory, and
+// the first adds them in order and runs the epilogue.
 //
 // The tensor core rounds every addition to its fp32 sum towards zero, so long
 // chains drift (a Gaussian 3000 x 4608 fp32 U: 5e-5 in the result).  Two-part
 // products therefore take CMU_CHAIN blocks at a time into one accumulator
 // after the other, and the epilogue warps add them up in registers.
-template <bool PAIR>
-__global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const __grid_constant__ CmuGemm p)
+template <int FORM>
+__global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const __grid_constant__ CmuGemm p)
 {
-    using Lay = Layout<PAIR>;
+    using Lay = Layout<FORM>;
+    constexpr bool PAIR = Lay::kPair, NARROW = FORM == CMU_NARROW;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     const Lay L(base);
@@ -448,11 +577,15 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
     static_assert(Lay::kWords + 8 + 4 * CMU_STAGES <= CMU_BAR_BYTES, "barrier area");
     const bool sym = p.mode <= CMU_POLY || p.mode == CMU_PARTIAL;  // B is K-major, as A
     const int warp = threadIdx.x / 32;
-    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-    const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+    const int width = PAIR ? 2 : NARROW ? p.split : 1;  // CTAs a tile
+    const int rank = width > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int half = PAIR ? rank : 0;                   // of the pair's rows
+    const int first = blockIdx.x / width, step = gridDim.x / width;
     const int total = p.tiles * p.batch;
     const int chain = p.parts > 1 || p.mode == CMU_PARTIAL ? CMU_CHAIN : INT_MAX;
     grid_dep_launch_dependents();
+    if (threadIdx.x < 10)  // the tensor maps (five pairs, one after the other), fetched while the launch waits
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(p.tmA + threadIdx.x)) : "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < CMU_STAGES; ++s) {
             mbar_init(L.full0 + 8u * s, 1);
@@ -485,6 +618,7 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
     const uint32_t tmem = *slot;
     const Ctl ctl{abort_flag, p.status};
 
+    bool at_barrier = false;  // this thread has been at the barrier of a split K
     if (warp == 0 || warp == 2) {
         const bool leader = elect_one_sync();
         const uint32_t lead_full0 = PAIR ? mapa_shared(L.full0, 0) : L.full0;
@@ -492,8 +626,8 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
         uint32_t parity = 0;
         bool ok = true;
         for (int t = first; ok && t < total; t += step) {
-            const Tile tile(p, sym, t);
-            const int row0 = tile.tm * Lay::kTile + rank * 128, col0 = tile.tn * Lay::kTile + rank * 128;
+            const Tile<FORM> tile(p, sym, t, rank);
+            const int row0 = tile.tm * Lay::kTileM + half * 128, col0 = tile.tn * Lay::kTileN + half * 128;
             const int blocks = p.parts * tile.kn;
             for (int k = 0; k < blocks; ++k) {
                 if (turn == warp) {
@@ -503,19 +637,19 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                     }
                     if (leader) {
                         used[s] = parity | 2u;
-                        const uint32_t sa = L.s0 + s * CMU_STAGE_BYTES, sb = sa + CMU_HALF_BYTES;
+                        const uint32_t sa = L.s0 + s * Lay::kStage, sb = sa + CMU_HALF_BYTES;
                         const uint32_t bar = lead_full0 + 8u * s;
                         // low x high, high x low, then high x high: the tensor core rounds every
                         // addition towards zero, and the small parts go in while the sum is small
                         const int part = k / tile.kn, k0 = (tile.k0 + k - part * tile.kn) * CMU_BK;
                         const CUtensorMap &ma = p.tmA[p.parts > 1 && part == 0], &mb = p.tmB[p.parts == 3 && part == 1];
-                        if (rank == 0) mbar_arrive_expect_tx(L.full0 + 8u * s, (PAIR ? 2 : 1) * CMU_STAGE_BYTES);
+                        if (half == 0) mbar_arrive_expect_tx(L.full0 + 8u * s, (PAIR ? 2 : 1) * Lay::kStage);
                         tma_load_3d_to(PAIR, sa, ma, bar, k0, row0, tile.b);
                         if (sym) {
                             tma_load_3d_to(PAIR, sb, mb, bar, k0, col0, tile.b);
                         } else {
                             tma_load_3d_to(PAIR, sb, mb, bar, col0, k0, tile.b);
-                            tma_load_3d_to(PAIR, sb + 8192u, mb, bar, col0 + 64, k0, tile.b);
+                            if (!NARROW) tma_load_3d_to(PAIR, sb + 8192u, mb, bar, col0 + 64, k0, tile.b);
                         }
                     }
                     __syncwarp();
@@ -529,15 +663,15 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
         }
     } else if (warp == 1) {
         volatile uint32_t no_abort = 0;
-        if (rank == 0) {
+        if (half == 0) {
             const bool leader = elect_one_sync();
             const uint32_t idesc = (1u << 4) | (sym ? 0u : 1u << 16) | (static_cast<uint32_t>(Lay::kCols >> 3) << 17) |
-                                   (static_cast<uint32_t>(Lay::kTile >> 4) << 24);
+                                   (static_cast<uint32_t>(Lay::kTileM >> 4) << 24);
             int s = 0;
             uint32_t parity = 0, link = 0;
             bool ok = true;
             for (int t = first; ok && t < total; t += step) {
-                const int blocks = p.parts * Tile(p, sym, t).kn;
+                const int blocks = p.parts * Tile<FORM>(p, sym, t, rank).kn;
                 for (int k = 0, in_chain = 0; k < blocks; ++k) {
                     const uint32_t acc = link & 1u;
                     if ((in_chain == 0 && !wait_bar(L.acc_empty0 + 8u * acc, ((link >> 1) & 1u) ^ 1u, ctl)) ||
@@ -548,7 +682,7 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                     tc_fence_after();
                     const bool last = in_chain == chain - 1 || k == blocks - 1;
                     if (leader) {
-                        const uint32_t sa = L.s0 + s * CMU_STAGE_BYTES, sb = sa + CMU_HALF_BYTES;
+                        const uint32_t sa = L.s0 + s * Lay::kStage, sb = sa + CMU_HALF_BYTES;
                         const uint64_t ad = sdesc_k128_sw128(sa);
                         const uint64_t bd = sym ? sdesc_k128_sw128(sb) : desc_mn_sw128(sb, 8192);
                         const uint32_t bstep = sym ? 2u : 128u, d = tmem + acc * Lay::kCols;
@@ -586,7 +720,7 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
         // tensor memory is freed only after the MMAs in flight
         wait_bar(L.drain, 0, Ctl{&no_abort, p.status});
     } else if (warp >= CDG_EPI_WARP0) {
-        Epilogue<PAIR> e(p, L, ctl, sym);
+        Epilogue<FORM> e(p, L, ctl, sym);
         const uint32_t lane_base = static_cast<uint32_t>(e.warp_in_group * 32) << 16;
         uint32_t link = 0;
         bool ok = true;
@@ -599,10 +733,10 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
             }
         };
         for (int t = first; ok && t < total; t += step) {
-            const Tile tile(p, sym, t);
-            const int i0 = tile.tm * Lay::kTile + rank * 128, j0 = tile.tn * Lay::kTile + e.group * 128;
-            const int n = e.chunks(i0, j0);
-            const bool mirror = sym && tile.tn < tile.tm;
+            const Tile<FORM> tile(p, sym, t, rank);
+            const int i0 = tile.tm * Lay::kTileM + half * 128, j0 = tile.tn * Lay::kTileN + e.group * 128;
+            const int n = NARROW && rank ? 0 : e.chunks(i0, j0);
+            const bool mirror = tile.mirror;
             const float xs = p.first ? p.xs[tile.b] : CMU_SCALE;
             const bool fetches = p.mode != CMU_GRAM && p.mode != CMU_PARTIAL;
             if (n > 0 && fetches) e.fetch(tile.b, i0, j0);
@@ -621,7 +755,8 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                 }
                 if (n == 0) hand_back(acc);
             } else {
-                float sum[2][64];
+                constexpr int CHUNKS = Lay::kTileN / 64;
+                float sum[CHUNKS][64];
                 const int links = (p.parts * tile.kn - 1) / chain + 1;
                 for (int k = 0; ok && k < links; ++k, ++link) {
                     const uint32_t acc = link & 1u;
@@ -629,7 +764,7 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < 4 * CHUNKS; ++c) {
                         uint32_t r[16];
                         tmem_ld_32x32b_x16(tmem + acc * Lay::kCols + c * 16 + lane_base, r);
                         tmem_ld_wait();
@@ -642,7 +777,43 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                     hand_back(acc);
                 }
                 if (named_bar_red_or(1, 128, !ok)) break;
-                if (p.mode == CMU_PARTIAL) {
+                if (NARROW && p.split > 1) {
+                    // the other CTAs' sums in their ring (all of it read: the range is done), columns 4 c .. + 3 of row r
+                    // in 16-byte piece (c + r) % 16; the first CTA adds them in rank order
+                    const uint32_t own = e.row * 256u;
+                    if (rank) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            st_shared_v4(L.s0 + own + ((c + e.lane) & 15) * 16u, __float_as_uint(sum[0][4 * c]),
+                                         __float_as_uint(sum[0][4 * c + 1]), __float_as_uint(sum[0][4 * c + 2]),
+                                         __float_as_uint(sum[0][4 * c + 3]));
+                    }
+                    __syncwarp();
+                    cluster_barrier_arrive();
+                    cluster_barrier_wait();
+                    at_barrier = true;
+                    if (rank == 0 && n > 0) {
+                        for (int r = 1; r < p.split; ++r) {
+                            const uint32_t at = mapa_shared(L.s0, r) + own;
+                            // all loads of a half before its additions: a load takes hundreds of cycles
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float4 x[8];
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) x[c] = ld_cluster_f32x4(at + ((8 * h + c + e.lane) & 15) * 16u);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    float *y = sum[0] + 32 * h + 4 * c;
+                                    y[0] += x[c].x;
+                                    y[1] += x[c].y;
+                                    y[2] += x[c].z;
+                                    y[3] += x[c].w;
+                                }
+                            }
+                        }
+                    }
+                }
+                if (FORM == CMU_SQUARE && p.mode == CMU_PARTIAL) {
                     // rows and columns below M, 16 bytes at a time (pads up to a multiple of 4 are sums of zeros)
                     float *out = p.partial + static_cast<long long>(t) * (CMU_SIDE * CMU_SIDE) + e.row * CMU_SIDE;
                     if (e.row < p.M)
@@ -650,13 +821,13 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
                         for (int q = 0; q < 128; q += 4)
                             if (q < p.N)
                                 *reinterpret_cast<float4 *>(out + q) =
-                                    make_float4(sum[q / 64][q % 64], sum[q / 64][q % 64 + 1], sum[q / 64][q % 64 + 2],
-                                                sum[q / 64][q % 64 + 3]);
+                                    make_float4(sum[q / 64 % CHUNKS][q % 64], sum[q / 64 % CHUNKS][q % 64 + 1],
+                                                sum[q / 64 % CHUNKS][q % 64 + 2], sum[q / 64 % CHUNKS][q % 64 + 3]);
                     __syncwarp();
                     continue;
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < CHUNKS; ++c) {
                     if (c >= n) break;
                     if (!(ok = e.chunk(tile.b, i0, j0 + 64 * c, mirror, xs, sum[c]))) break;
                     if (c + 1 < n && fetches) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
@@ -665,13 +836,21 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
         }
         if (e.elected) bulk_wait_group_all();
     }
+    if (NARROW && p.split > 1) {
+        // the loaders and the MMA warp stand at the cluster's barrier too (the epilogue warps have passed it, unless
+        // the launch is giving up before they came there)
+        if (warp < CDG_EPI_WARP0 || !at_barrier) {
+            cluster_barrier_arrive();
+            cluster_barrier_wait();
+        }
+    }
 
     __syncthreads();
     if (*abort_flag && threadIdx.x == 0) {
         // copies in flight land before the CTA exits
         volatile uint32_t no_abort = 0;
         const Ctl drain{&no_abort, p.status};
-        if (rank == 0) {
+        if (half == 0) {
             for (int s = 0; s < CMU_STAGES; ++s)
                 if (used[s] & 2u) wait_bar(L.full0 + 8u * s, used[s] & 1u, drain);
         }
@@ -681,7 +860,7 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();  // neither CTA leaves while the other may still signal it
+    if (width > 1) cluster_sync();  // no CTA leaves while another may still signal it or read its shared memory
     if (warp == 1) {
         tc_fence_after();
         if (PAIR) tmem_dealloc_pair(tmem, 2 * Lay::kCols);
@@ -689,19 +868,31 @@ __global__ void __launch_bounds__(Layout<PAIR>::kThreads, 1) gemm_kernel(const _
     }
 }
 
-template <bool PAIR>
+// Tiles of a matrix in one form.
+template <int FORM>
+void count_tiles(CmuGemm &p)
+{
+    using Lay = Layout<FORM>;
+    p.tiles_m = (p.M + Lay::kTileM - 1) / Lay::kTileM;
+    const int tiles_n = (p.N + Lay::kTileN - 1) / Lay::kTileN;
+    if (p.mode == CMU_PARTIAL) return;  // the caller's ranges of K
+    if (p.mode > CMU_POLY) p.tiles = p.tiles_m * tiles_n;
+    else if (FORM == CMU_NARROW) p.tiles = p.tiles_m * (p.tiles_m + 1) - (tiles_n < 2 * p.tiles_m);  // its last row may lack a tile
+    else p.tiles = p.tiles_m * (p.tiles_m + 1) / 2;
+}
+
+template <int FORM>
 cudaError_t launch_gemm(CmuGemm p, int sms, cudaStream_t s)
 {
-    using Lay = Layout<PAIR>;
-    p.tiles_m = (p.M + Lay::kTile - 1) / Lay::kTile;
-    const int tiles_n = (p.N + Lay::kTile - 1) / Lay::kTile;
-    if (p.mode != CMU_PARTIAL)
-        p.tiles = p.mode <= CMU_POLY ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * tiles_n;
+    using Lay = Layout<FORM>;
+    count_tiles<FORM>(p);
     const long long total = static_cast<long long>(p.tiles) * p.batch;
-    if (total > INT_MAX / 2) return cudaErrorInvalidConfiguration;
-    const int width = PAIR ? 2 : 1;
+    if (total > INT_MAX / 16) return cudaErrorInvalidConfiguration;
+    const int width = Lay::kPair ? 2 : FORM == CMU_NARROW ? p.split : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(width * std::min<long long>(total, std::max(1, sms / width))));
+    // persistent, but for tiles whose K is split (their ring holds the sums at the end)
+    const long long at_once = FORM == CMU_NARROW ? total : std::min<long long>(total, std::max(1, sms / width));
+    cfg.gridDim = dim3(static_cast<unsigned>(width * at_once));
     cfg.blockDim = dim3(Lay::kThreads);
     cfg.dynamicSmemBytes = Lay::kSmem;
     cfg.stream = s;
@@ -712,8 +903,8 @@ cudaError_t launch_gemm(CmuGemm p, int sms, cudaStream_t s)
     attr[1].val.clusterDim.x = width;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_kernel<PAIR>, p);
+    cfg.numAttrs = width > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<FORM>, p);
 }
 
 // ---------------------------------------------------------------- small matrices
@@ -729,9 +920,10 @@ cudaError_t launch_gemm(CmuGemm p, int sms, cudaStream_t s)
 // factor P on it, up to a^steps = 485, comes out within 1e-4 to 1e-3 of the
 // iteration on X (64-bit simulation; spectra over four decades).
 //
-// 256 threads: thread t holds row t % 128, columns 64 (t / 128) .. + 63 of the
-// accumulators.
-constexpr int kItThreads = 256;
+// 512 threads: thread t holds row t % 128 and, of the accumulators' columns,
+// the 16 from 16 (t / 128) and the 16 from 64 + 16 (t / 128).  Only the first
+// m rows and columns, rounded up to 16, are multiplied and read.
+constexpr int kItThreads = 512;
 constexpr uint32_t kMatBytes = 4 * CMU_HALF_BYTES;  // high parts of columns 0-63, 64-127; then low parts
 constexpr int kItSmem = 1024 + 3 * static_cast<int>(kMatBytes) + 256;
 
@@ -742,8 +934,9 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
     const uint32_t mA = base, mQ = base + kMatBytes, mP = base + 2 * kMatBytes, bar0 = base + 3 * kMatBytes;
     uint32_t *slot = reinterpret_cast<uint32_t *>(smem_raw + (bar0 - raw) + 16);
     volatile uint32_t *abort_flag = slot + 1;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int row = tid % 128, half = tid / 128, b = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid / 32;
+    const int row = tid % 128, group = tid / 128, b = blockIdx.x;
+    const int used = (p.m + 15) / 16 * 16;
     grid_dep_launch_dependents();
     if (tid == 0) {
         mbar_init(bar0, 1);
@@ -763,8 +956,11 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
     const Ctl ctl{abort_flag, p.status};
     const bool leader = warp == 0 && elect_one_sync();
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // this thread's chunks of 16 columns: from 16 group, and 64 + 16 group
+    const bool rows = (warp & 3) * 32 < used;  // warp-uniform
+    const int chunks = !rows ? 0 : 64 + 16 * group < used ? 2 : 16 * group < used ? 1 : 0;
 
-    // the ranges' partial sums, in order, to A = sum / xs^2 (fp32, in Q's and P's place)
+    // the ranges' partial sums, in order, to A = sum / xs^2 (fp32, in Q's place)
     {
         const float f = (1.0f / p.xs[b]) / p.xs[b];
         const float *src = p.partial + static_cast<long long>(b) * p.splits * (CMU_SIDE * CMU_SIDE);
@@ -772,7 +968,7 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
         for (int x = tid; x < p.m * n4; x += kItThreads) {
             const int r = x / n4, c = x - r * n4;
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
             for (int k = 0; k < p.splits; ++k) {
                 const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + static_cast<long long>(k) * (CMU_SIDE * CMU_SIDE) +
                                                                          r * CMU_SIDE) + c);
@@ -787,41 +983,46 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
         __syncthreads();
     }
 
-    // piece q (8 columns) of this thread's row half in matrix `mat`, part 0 or 1
-    auto piece = [&](uint32_t mat, int part, int q) {
-        return mat + static_cast<uint32_t>(2 * part + half) * CMU_HALF_BYTES + static_cast<uint32_t>(row) * 128u +
+    // columns 64 s + 8 q .. + 7 of this thread's row in matrix `mat`, part 0 or 1
+    auto piece = [&](uint32_t mat, int part, int s, int q) {
+        return mat + static_cast<uint32_t>(2 * part + s) * CMU_HALF_BYTES + static_cast<uint32_t>(row) * 128u +
                ((static_cast<uint32_t>(q) ^ (row & 7)) << 4);
     };
-    auto put = [&](uint32_t mat, int q, const float (&x)[8]) {
-        uint4 w = narrow_vec<__half>(x);
-        st_shared_v4(piece(mat, 0, q), w.x, w.y, w.z, w.w);
-        float y[8];
+    auto put = [&](uint32_t mat, int s, int q, const float *x) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e] - __half2float(__float2half_rn(x[e]));
-        w = narrow_vec<__half>(y);
-        st_shared_v4(piece(mat, 1, q), w.x, w.y, w.z, w.w);
+        for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+            const float2 w = __half22float2(h);
+            const __half2 l = __floats2half2_rn(x[2 * e] - w.x, x[2 * e + 1] - w.y);
+            hi[e] = *reinterpret_cast<const uint32_t *>(&h);
+            lo[e] = *reinterpret_cast<const uint32_t *>(&l);
+        }
+        st_shared_v4(piece(mat, 0, s, q), hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(piece(mat, 1, s, q), lo[0], lo[1], lo[2], lo[3]);
     };
-    auto get = [&](uint32_t mat, int q, float (&x)[8]) {
+    auto get = [&](uint32_t mat, int s, int q, float (&x)[8]) {
         uint32_t w[4];
         float y[8];
-        ld_shared_v4(piece(mat, 0, q), w);
+        ld_shared_v4(piece(mat, 0, s, q), w);
         widen_vec<__half>(make_uint4(w[0], w[1], w[2], w[3]), x);
-        ld_shared_v4(piece(mat, 1, q), w);
+        ld_shared_v4(piece(mat, 1, s, q), w);
         widen_vec<__half>(make_uint4(w[0], w[1], w[2], w[3]), y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += y[e];
     };
     // accumulator d <- X Y: low x high, high x low, high x high
-    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(128 >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(used >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
     auto multiply = [&](uint32_t d, uint32_t x, uint32_t y) {
+        uint32_t more = 0;
 #pragma unroll
         for (int part = 0; part < 3; ++part)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int k = 0; k < used; k += 16) {
+                const uint32_t s = k / 64, q = k % 64 / 16;
                 const uint64_t ad = sdesc_k128_sw128(x + (2u * (part == 0) + s) * CMU_HALF_BYTES);
                 const uint64_t bd = sdesc_k128_sw128(y + (2u * (part == 1) + s) * CMU_HALF_BYTES);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) umma_f16(tmem + 128 * d, ad + 2u * q, bd + 2u * q, idesc, (part | s | q) != 0);
+                umma_f16(tmem + 128 * d, ad + 2u * q, bd + 2u * q, idesc, more);
+                more = 1;
             }
         umma_commit(bar0 + 8 * d);
     };
@@ -839,25 +1040,44 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
         tc_fence_after();
         return __syncthreads_and(ok) != 0;
     };
-    auto load = [&](int d, int q, float (&v)[16]) {  // 16 columns of accumulator d
-        uint32_t(&r)[16] = reinterpret_cast<uint32_t(&)[16]>(v);
-        tmem_ld_32x32b_x16(tmem + 128 * d + half * 64 + 16 * q + lane_base, r);
-        tmem_ld_wait();
+    // accumulator d times f into matrix `mat`, after `also` has seen or changed each
+    // piece: also(values, slice, piece)
+    auto store = [&](int d, float f, uint32_t mat, auto also) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (c >= chunks) break;
+            float v[16];
+            tmem_ld_32x32b_x16(tmem + 128 * d + 64 * c + 16 * group + lane_base, reinterpret_cast<uint32_t(&)[16]>(v));
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * h + e] *= f;
+                also(v + 8 * h, c, 2 * group + h);
+                put(mat, c, 2 * group + h, v + 8 * h);
+            }
+            __syncwarp();
+        }
     };
+    auto nothing = [](float *, int, int) {};
 
     // A to its two parts
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        float x[8];
+    for (int c = 0; c < 2; ++c) {
+        if (c >= chunks) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t c = half * 16u + 2u * q + h;
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-            if (row < p.m && static_cast<int>(4 * c) < p.m) ld_shared_v4(mQ + row * 512u + ((c ^ (row & 31)) << 4), w);
+            float x[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * h + e] = CMU_SCALE * __uint_as_float(w[e]);
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t at = 16u * c + 4u * group + 2u * h + g;  // of the row's 16-byte pieces of fp32
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (row < p.m && static_cast<int>(4 * at) < p.m) ld_shared_v4(mQ + row * 512u + ((at ^ (row & 31)) << 4), w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[4 * g + e] = CMU_SCALE * __uint_as_float(w[e]);
+            }
+            put(mA, c, 2 * group + h, x);
         }
-        put(mA, q, x);
     }
     ready();
     constexpr float kInv = 1.0f / CMU_SCALE;
@@ -867,27 +1087,20 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
         if (leader) multiply(0, mA, mA);
         __syncwarp();
         if (!(ok = wait(0))) break;
+        store(0, p.c * kInv, mQ, [&](float *v, int s, int q) {
+            float x[8];
+            get(mA, s, q, x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float v[16];
-            load(0, q, v);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[8];
-                get(mA, 2 * q + h, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = fmaf(p.b, x[e], p.c * (v[8 * h + e] * kInv));
-                    if (half * 64 + 16 * q + 8 * h + e == row) x[e] += p.a * CMU_SCALE;
-                }
-                put(mQ, 2 * q + h, x);
-                if (k == 0) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= CMU_POLY_SCALE * kInv;
-                    put(mP, 2 * q + h, x);
-                }
+            for (int e = 0; e < 8; ++e) {
+                v[e] = fmaf(p.b, x[e], v[e]);
+                if (64 * s + 8 * q + e == row) v[e] += p.a * CMU_SCALE;
             }
-        }
+            if (k == 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = v[e] * (CMU_POLY_SCALE * kInv);
+                put(mP, s, q, x);
+            }
+        });
         ready();
         const bool last = k == p.steps - 1;
         if (leader) {
@@ -897,74 +1110,43 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
         __syncwarp();
         if (!last) {  // T = Q A, in A's place
             if (!(ok = wait(0))) break;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[16];
-                load(0, q, v);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = v[8 * h + e] * kInv;
-                    put(mA, 2 * q + h, x);
-                }
-            }
+            store(0, kInv, mA, nothing);
             ready();
             if (leader) multiply(0, mA, mQ);  // A <- T Q
             __syncwarp();
         }
         if (k > 0) {  // P <- Q P
             if (!(ok = wait(1))) break;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[16];
-                load(1, q, v);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = v[8 * h + e] * kInv;
-                    put(mP, 2 * q + h, x);
-                }
-            }
+            store(1, kInv, mP, nothing);
         }
         if (!last) {
             if (!(ok = wait(0))) break;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[16];
-                load(0, q, v);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = v[8 * h + e] * kInv;
-                    put(mA, 2 * q + h, x);
-                }
-            }
+            store(0, kInv, mA, nothing);
             ready();
         }
     }
     // P without its diagonal, and the diagonal
     if (ok && row < p.m) {
-        const long long at = (static_cast<long long>(b) * p.m + row) * p.pitch_a + half * 64;
+        const long long at = (static_cast<long long>(b) * p.m + row) * p.pitch_a;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int j = half * 64 + 8 * q;
-            if (j >= p.m) break;
-            float x[8], y[8];
-            get(mP, q, x);
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (j + e == row) {
-                    p.diag[static_cast<long long>(b) * p.m + row] = x[e] * (1.0f / CMU_POLY_SCALE);
-                    x[e] = 0.0f;
+            for (int h = 0; h < 2; ++h) {
+                const int j = 64 * c + 16 * group + 8 * h;
+                if (c >= chunks || j >= p.m) continue;
+                float x[8], y[8];
+                get(mP, c, 2 * group + h, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (j + e == row) {
+                        p.diag[static_cast<long long>(b) * p.m + row] = x[e] * (1.0f / CMU_POLY_SCALE);
+                        x[e] = 0.0f;
+                    }
+                    y[e] = x[e] - __half2float(__float2half_rn(x[e]));
                 }
-                y[e] = x[e] - __half2float(__float2half_rn(x[e]));
+                *reinterpret_cast<uint4 *>(p.poly + at + j) = narrow_vec<__half>(x);
+                *reinterpret_cast<uint4 *>(p.poly_lo + at + j) = narrow_vec<__half>(y);
             }
-            *reinterpret_cast<uint4 *>(p.poly + at + 8 * q) = narrow_vec<__half>(x);
-            *reinterpret_cast<uint4 *>(p.poly_lo + at + 8 * q) = narrow_vec<__half>(y);
-        }
     }
     if (!ok) {  // giving up: what is in flight ends before tensor memory is freed
         const uint64_t t0 = global_timer_ns();
@@ -979,16 +1161,35 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
     }
 }
 
-template <typename T>
-void launch_norm(const CmuPrepare &p, cudaStream_t s)
+// A launch that may begin while the one before it ends (its kernel waits).
+template <typename... A>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t s, const A &...args)
 {
-    norm_kernel<T><<<dim3(p.partials, p.batch), 256, 0, s>>>(p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T>
+cudaError_t launch_norm(const CmuPrepare &p, cudaStream_t s)
+{
+    return launch_early(norm_kernel<T>, dim3(p.partials, p.batch), kPrepareThreads, 0, s, p);
 }
 template <typename T>
-void launch_split(const CmuPrepare &p, cudaStream_t s)
+cudaError_t launch_split(const CmuPrepare &p, cudaStream_t s)
 {
+    if (!p.transposed && p.cols % 8 == 0)
+        return launch_early(split_flat_kernel<T>, dim3(p.partials, p.batch), kPrepareThreads, 0, s, p);
     const int m = p.transposed ? p.cols : p.rows, n = p.transposed ? p.rows : p.cols;
-    split_kernel<T><<<dim3((n + 31) / 32, (m + 31) / 32, p.batch), 256, 0, s>>>(p);
+    return launch_early(split_kernel<T>, dim3((n + 63) / 64, (m + 63) / 64, p.batch), kPrepareThreads, 0, s, p);
 }
 
 }  // namespace
@@ -996,47 +1197,37 @@ void launch_split(const CmuPrepare &p, cudaStream_t s)
 
 cudaError_t cmu_prepare_kernels()
 {
-    const cudaError_t e = cudaFuncSetAttribute(cdg::gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               cdg::Layout<false>::kSmem);
-    if (e != cudaSuccess) return e;
-    const cudaError_t i = cudaFuncSetAttribute(cdg::iterate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cdg::kItSmem);
-    return i != cudaSuccess ? i
-                            : cudaFuncSetAttribute(cdg::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   cdg::Layout<true>::kSmem);
+    using namespace cdg;
+    const auto raise = [](const void *f, int bytes) {
+        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    cudaError_t e = raise(reinterpret_cast<const void *>(gemm_kernel<CMU_PAIR>), Layout<CMU_PAIR>::kSmem);
+    if (e == cudaSuccess) e = raise(reinterpret_cast<const void *>(gemm_kernel<CMU_SQUARE>), Layout<CMU_SQUARE>::kSmem);
+    if (e == cudaSuccess) e = raise(reinterpret_cast<const void *>(gemm_kernel<CMU_NARROW>), Layout<CMU_NARROW>::kSmem);
+    if (e == cudaSuccess) e = raise(reinterpret_cast<const void *>(iterate_kernel), kItSmem);
+    return e;
 }
 
 cudaError_t cmu_launch_norm(const CmuPrepare &p, cudaStream_t s)
 {
-    if (p.dtype == CDG_F32) cdg::launch_norm<float>(p, s);
-    else if (p.dtype == CDG_F16) cdg::launch_norm<__half>(p, s);
-    else cdg::launch_norm<__nv_bfloat16>(p, s);
-    return cudaGetLastError();
+    return p.dtype == CDG_F32 ? cdg::launch_norm<float>(p, s)
+                              : p.dtype == CDG_F16 ? cdg::launch_norm<__half>(p, s) : cdg::launch_norm<__nv_bfloat16>(p, s);
 }
 
 cudaError_t cmu_launch_split(const CmuPrepare &p, cudaStream_t s)
 {
-    if (p.dtype == CDG_F32) cdg::launch_split<float>(p, s);
-    else if (p.dtype == CDG_F16) cdg::launch_split<__half>(p, s);
-    else cdg::launch_split<__nv_bfloat16>(p, s);
-    return cudaGetLastError();
+    return p.dtype == CDG_F32 ? cdg::launch_split<float>(p, s)
+                              : p.dtype == CDG_F16 ? cdg::launch_split<__half>(p, s) : cdg::launch_split<__nv_bfloat16>(p, s);
 }
 
 cudaError_t cmu_launch_iterate(const CmuIterate &p, cudaStream_t s)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.batch));
-    cfg.blockDim = dim3(cdg::kItThreads);
-    cfg.dynamicSmemBytes = cdg::kItSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cdg::iterate_kernel, p);
+    return cdg::launch_early(cdg::iterate_kernel, dim3(p.batch), cdg::kItThreads, cdg::kItSmem, s, p);
 }
 
 cudaError_t cmu_launch_gemm(const CmuGemm &p, int sms, cudaStream_t s)
 {
-    return p.pair ? cdg::launch_gemm<true>(p, sms, s) : cdg::launch_gemm<false>(p, sms, s);
+    if (p.form == CMU_PAIR) return cdg::launch_gemm<CMU_PAIR>(p, sms, s);
+    if (p.form == CMU_NARROW) return cdg::launch_gemm<CMU_NARROW>(p, sms, s);
+    return cdg::launch_gemm<CMU_SQUARE>(p, sms, s);
 }
