@@ -30,15 +30,16 @@ namespace {
 
 constexpr int kMaxTop = 32;
 constexpr int kMaxVocab = 1 << 30;  // element numbers stay in 32 bits
-constexpr int kCand = 1024;       // candidate keys a CTA ranks
-constexpr int kMaxCluster = 8;    // CTAs that share a row
-constexpr int kUnroll = 4;        // 16-byte loads in flight per thread
+constexpr int kThreads = 256;
+constexpr int kCand = 1024;         // candidate keys a CTA ranks
+constexpr int kMaxCluster = 8;      // CTAs that share a row
+constexpr int kUnroll = 4;          // 16-byte loads in flight per thread, and as many ahead
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1000.0f;  // 2^-1000 is 0 in fp32: exponents are clamped here so that 0 * -inf does not arise
 
 struct LogprobArgs {
     const void *logits, *targets;
-    long long ld;
+    long long ld, rows;
     int index_bytes, vocab, top, cluster;
     float scale, c;  // c = scale * log2(e)
     float *logp, *lse, *entropy, *top_logp;
@@ -60,6 +61,34 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
+// Two fp32 numbers in one register pair: one instruction for both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Running sums about a reference (see the head of the file), and the largest
 // logit itself.
 struct Sums {
@@ -77,6 +106,16 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b)
     r.e = ra * fmaf(da, a.s, a.e) + rb * fmaf(db, b.s, b.e);
     r.zmax = fmaxf(a.zmax, b.zmax);
     return r;
+}
+__device__ __forceinline__ Sums join_lanes(Sums a)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const Sums b{__shfl_xor_sync(0xFFFFFFFFu, a.ref, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+                     __shfl_xor_sync(0xFFFFFFFFu, a.e, o), __shfl_xor_sync(0xFFFFFFFFu, a.zmax, o)};
+        a = join(a, b);
+    }
+    return a;
 }
 
 // Float order as unsigned order (-0 and +0 equal); 0 is below every number.
@@ -96,32 +135,56 @@ __device__ __forceinline__ unsigned long long make_key(float z, int j)
 }
 __device__ __forceinline__ int key_index(unsigned long long k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
 
-// Largest of a 16-byte vector's elements (NaN elements may be dropped).
+// Element-wise largest and smallest of two words (NaN elements may be dropped).
 template <typename T>
-__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b);
+struct Words;
 template <>
-__device__ __forceinline__ uint32_t max_words<float>(uint32_t a, uint32_t b)
-{
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-}
+struct Words<float> {
+    static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }
+    static __device__ __forceinline__ uint32_t min(uint32_t a, uint32_t b) { return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b))); }
+    static constexpr uint32_t kLowest = 0xFF800000u;  // -inf in every element
+};
 template <>
-__device__ __forceinline__ uint32_t max_words<__half>(uint32_t a, uint32_t b)
-{
-    const __half2 r = __hmax2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
+struct Words<__half> {
+    static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b)
+    {
+        const __half2 r = __hmax2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static __device__ __forceinline__ uint32_t min(uint32_t a, uint32_t b)
+    {
+        const __half2 r = __hmin2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static constexpr uint32_t kLowest = 0xFC00FC00u;
+};
 template <>
-__device__ __forceinline__ uint32_t max_words<__nv_bfloat16>(uint32_t a, uint32_t b)
-{
-    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
+struct Words<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b)
+    {
+        const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static __device__ __forceinline__ uint32_t min(uint32_t a, uint32_t b)
+    {
+        const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static constexpr uint32_t kLowest = 0xFF80FF80u;
+};
 template <typename T>
 __device__ __forceinline__ float max_word(uint32_t w)
 {
     float f[2];
     widen<T>(w, f);
     return sizeof(T) == 4 ? f[0] : fmaxf(f[0], f[1]);
+}
+template <typename T>
+__device__ __forceinline__ float min_word(uint32_t w)
+{
+    float f[2];
+    widen<T>(w, f);
+    return sizeof(T) == 4 ? f[0] : fminf(f[0], f[1]);
 }
 
 // The part of a row that this CTA reads: 16-byte vectors from an aligned
@@ -160,42 +223,74 @@ struct Slice {
     }
 };
 
-// One value or one group of vectors into the running sums.
-__device__ __forceinline__ void raise(Sums &a, float gmax_c)
+// A thread's running sums while it reads: s and e as two numbers each (even
+// and odd elements).
+struct Run {
+    float ref, zmax;
+    f32x2 s, e;
+};
+
+// The reference moves up to y.
+__device__ __forceinline__ void raise(Run &a, float y)
 {
-    if (gmax_c > a.ref) {
-        const float d = fmaxf(a.ref - gmax_c, kFloor), r = exp2_fast(d);
-        a.e = r * fmaf(d, a.s, a.e);
-        a.s *= r;
-        a.ref = gmax_c;
+    if (y > a.ref) {
+        const float d = fmaxf(a.ref - y, kFloor), r = exp2_fast(d);
+        const f32x2 rr = pack2(r, r);
+        a.e = mul2(rr, fma2(pack2(d, d), a.s, a.e));
+        a.s = mul2(rr, a.s);
+        a.ref = y;
     }
 }
-__device__ __forceinline__ void add(Sums &a, float z, float c, float shift)
+// Two logits.  CLAMP: one may lie far below the reference, or be -inf.
+template <bool CLAMP>
+__device__ __forceinline__ void add(Run &a, float z0, float z1, f32x2 c, f32x2 minus_ref)
 {
-    const float u = max_nan(fmaf(z, c, -shift), kFloor);
-    const float p = exp2_fast(u);
-    a.s += p;
-    a.e = fmaf(p, u, a.e);
+    f32x2 u = fma2(pack2(z0, z1), c, minus_ref);
+    float u0, u1;
+    unpack2(u, u0, u1);
+    if (CLAMP) {
+        u0 = max_nan(u0, kFloor);
+        u1 = max_nan(u1, kFloor);
+        u = pack2(u0, u1);
+    }
+    const f32x2 w = pack2(exp2_fast(u0), exp2_fast(u1));
+    a.s = add2(a.s, w);
+    a.e = fma2(w, u, a.e);
 }
-
-template <typename T, int N>
-__device__ __forceinline__ void add_group(Sums &a, const uint4 (&v)[N], float c)
+template <typename T, bool CLAMP, int N>
+__device__ __forceinline__ void add_all(Run &a, const uint4 (&v)[N], float c)
 {
-    uint32_t w = max_words<T>(max_words<T>(v[0].x, v[0].y), max_words<T>(v[0].z, v[0].w));
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-        w = max_words<T>(w, max_words<T>(max_words<T>(v[i].x, v[i].y), max_words<T>(v[i].z, v[i].w)));
-    const float g = max_word<T>(w);
-    a.zmax = fmaxf(a.zmax, g);
-    raise(a, g * c);
-    const float shift = a.ref == -INFINITY ? 0.0f : a.ref;
+    const float ref = a.ref == -INFINITY ? 0.0f : a.ref;
+    const f32x2 cc = pack2(c, c), minus = pack2(-ref, -ref);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float f[kPerVec<T>];
         widen_vec<T>(v[i], f);
 #pragma unroll
-        for (int j = 0; j < kPerVec<T>; ++j) add(a, f[j], c, shift);
+        for (int j = 0; j < kPerVec<T>; j += 2) add<CLAMP>(a, f[j], f[j + 1], cc, minus);
     }
+}
+template <typename T, int N>
+__device__ __forceinline__ void add_group(Run &a, const uint4 (&v)[N], float c)
+{
+    using W = Words<T>;
+    uint32_t hi = W::max(W::max(v[0].x, v[0].y), W::max(v[0].z, v[0].w));
+#pragma unroll
+    for (int i = 1; i < N; ++i) hi = W::max(hi, W::max(W::max(v[i].x, v[i].y), W::max(v[i].z, v[i].w)));
+    const float g = max_word<T>(hi);
+    a.zmax = fmaxf(a.zmax, g);
+    raise(a, g * c);
+    if constexpr (sizeof(T) == 2) {
+        // the smallest of the group costs half an instruction an element, the clamp a whole one
+        uint32_t lo = W::min(W::min(v[0].x, v[0].y), W::min(v[0].z, v[0].w));
+#pragma unroll
+        for (int i = 1; i < N; ++i) lo = W::min(lo, W::min(W::min(v[i].x, v[i].y), W::min(v[i].z, v[i].w)));
+        if (fmaf(min_word<T>(lo), c, -a.ref) > kFloor) {
+            add_all<T, false>(a, v, c);
+            return;
+        }
+    }
+    add_all<T, true>(a, v, c);
 }
 
 // Insert warp-uniform key x into the warp's descending list (lane l holds its
@@ -209,91 +304,122 @@ __device__ __forceinline__ void list_insert(unsigned long long &mine, unsigned l
     else if (lane > pos) mine = up;
 }
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // keys[0..n) -> the min(n, k) largest in out, descending.  Returns that count.
-template <int THREADS>
-__device__ __forceinline__ int rank_keys(const unsigned long long *keys, int n, int k, unsigned long long *out)
+template <int TEAM>
+__device__ __forceinline__ int rank_keys(const unsigned long long *keys, int n, int k, unsigned long long *out, int tid)
 {
-    for (int i = threadIdx.x; i < n; i += THREADS) {
+    for (int i = tid; i < n; i += TEAM) {
         const unsigned long long x = keys[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) rank += keys[j] > x;
         if (rank < k) out[rank] = x;
     }
     return min(n, k);
 }
 
-template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const LogprobArgs p)
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v)
 {
-    constexpr int W = THREADS / 32, PER_WARP = kMaxTop / W;  // thread maxima each warp offers
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// TEAM threads a row: a warp each of eight rows, or the CTA, which a cluster of
+// CTAs may share the row with.
+template <typename T, int TEAM>
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs p)
+{
+    constexpr bool WARP = TEAM == 32;
+    constexpr int W = TEAM / 32, TEAMS = kThreads / TEAM, CAND = kCand / TEAMS;
+    constexpr int PER_WARP = kMaxTop / W;  // thread maxima each warp offers
     __shared__ Sums part[W];
-    __shared__ Sums mine;
-    __shared__ unsigned long long cand[kCand], best[kMaxTop];
+    __shared__ unsigned long long s_cand[TEAMS][CAND], s_best[TEAMS][kMaxTop];
     __shared__ uint32_t offer[kMaxTop];
-    __shared__ int ncand, nbest;
+    __shared__ int s_ncand[TEAMS];
+    // what the cluster's other CTAs leave with the first one
+    __shared__ Sums from_sums[kMaxCluster];
+    __shared__ unsigned long long from_keys[kMaxCluster][kMaxTop];
+    __shared__ int from_count[kMaxCluster];
 
-    const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const long long i = blockIdx.x / p.cluster;
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const Slice<T> sl(static_cast<const T *>(p.logits) + i * p.ld, p.vocab, rank, p.cluster);
+    const int lane = threadIdx.x % 32, tid = threadIdx.x % TEAM, warp = tid / 32, team = threadIdx.x / TEAM;
+    const int rank = !WARP && p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const long long i = WARP ? static_cast<long long>(blockIdx.x) * TEAMS + team : blockIdx.x / p.cluster;
+    if (!WARP && p.cluster > 1) cluster_arrive();  // every CTA of the cluster has started before one writes to the first
+    if (WARP && i >= p.rows) return;
+    auto sync = [] {
+        if (WARP) __syncwarp();
+        else __syncthreads();
+    };
+    unsigned long long *const cand = s_cand[team], *const best = s_best[team];
+    int *const ncand = s_ncand + team;
+    const Slice<T> sl(static_cast<const T *>(p.logits) + i * p.ld, p.vocab, rank, WARP ? 1 : p.cluster);
 
-    // ---- one pass: sums and the thread's maximum
-    Sums a{-INFINITY, 0.0f, 0.0f, -INFINITY};
+    // ---- one pass: sums and the thread's maximum; the next group is on its way while one is added
+    Run run{-INFINITY, -INFINITY, 0ull, 0ull};
     const int single = sl.single(tid);
+    const uint4 lowest = make_uint4(Words<T>::kLowest, Words<T>::kLowest, Words<T>::kLowest, Words<T>::kLowest);
+    auto fetch = [&](int v, uint4 (&x)[kUnroll]) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) x[u] = v + u * TEAM + tid < sl.nv ? sl.vec(v + u * TEAM + tid) : lowest;
+    };
+    uint4 x[kUnroll];
+    fetch(0, x);
     if (single >= 0) {
         const float z = Elem<T>::get(sl.row[single]);
-        a.zmax = fmaxf(a.zmax, z);
-        raise(a, z * p.c);
-        add(a, z, p.c, a.ref == -INFINITY ? 0.0f : a.ref);
+        run.zmax = z == z ? z : -INFINITY;
+        raise(run, z * p.c);
+        const float ref = run.ref == -INFINITY ? 0.0f : run.ref;
+        add<true>(run, z, -INFINITY, pack2(p.c, p.c), pack2(-ref, -ref));
     }
-    int v = 0;
-    for (; v + kUnroll * THREADS <= sl.nv; v += kUnroll * THREADS) {
-        uint4 x[kUnroll];
+    for (int v = 0; v < sl.nv; v += kUnroll * TEAM) {
+        uint4 next[kUnroll];
+        const bool more = v + kUnroll * TEAM < sl.nv;
+        if (more) fetch(v + kUnroll * TEAM, next);
+        add_group<T, kUnroll>(run, x, p.c);
+        if (more) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) x[u] = sl.vec(v + u * THREADS + tid);
-        add_group<T, kUnroll>(a, x, p.c);
-    }
-    for (v += tid; v < sl.nv; v += THREADS) {
-        const uint4 x[1] = {sl.vec(v)};
-        add_group<T, 1>(a, x, p.c);
+            for (int u = 0; u < kUnroll; ++u) x[u] = next[u];
+        }
     }
     // no element at all in this thread: below every element
-    const uint32_t omax = single >= 0 || tid < sl.nv ? ordered(a.zmax) : 0u;
+    const uint32_t omax = single >= 0 || tid < sl.nv ? ordered(run.zmax) : 0u;
 
-    // ---- join the CTA
+    // ---- join the team
+    float s0, s1, e0, e1;
+    unpack2(run.s, s0, s1);
+    unpack2(run.e, e0, e1);
+    Sums all = join_lanes(Sums{run.ref, s0 + s1, e0 + e1, run.zmax});
+    uint32_t mo = omax;  // lane l: one of 32 thread maxima
+    if (p.top && tid == 0) *ncand = 0;
+    if (!WARP) {
+        if (lane == 0) part[warp] = all;
+        if (p.top) {
+            uint32_t m = omax;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const Sums b{__shfl_xor_sync(0xFFFFFFFFu, a.ref, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
-                     __shfl_xor_sync(0xFFFFFFFFu, a.e, o), __shfl_xor_sync(0xFFFFFFFFu, a.zmax, o)};
-        a = join(a, b);
-    }
-    if (lane == 0) part[warp] = a;
-    if (p.top) {
-        uint32_t m = omax;
-#pragma unroll
-        for (int r = 0; r < PER_WARP; ++r) {
-            const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, m);
-            const unsigned holders = __ballot_sync(0xFFFFFFFFu, m == g);
-            if (lane == 0) offer[warp * PER_WARP + r] = g;
-            if (lane == __ffs(holders) - 1) m = 0u;
+            for (int r = 0; r < PER_WARP; ++r) {
+                const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, m);
+                const unsigned holders = __ballot_sync(0xFFFFFFFFu, m == g);
+                if (lane == 0) offer[warp * PER_WARP + r] = g;
+                if (lane == __ffs(holders) - 1) m = 0u;
+            }
         }
-        if (tid == 0) ncand = 0;
-    }
-    __syncthreads();
-    Sums all = part[0];
+        __syncthreads();
+        all = part[0];
 #pragma unroll
-    for (int w = 1; w < W; ++w) all = join(all, part[w]);
+        for (int w = 1; w < W; ++w) all = join(all, part[w]);
+        if (p.top) mo = offer[lane];
+    } else if (p.top) {
+        __syncwarp();
+    }
 
-    // ---- the CTA's largest logits
+    // ---- the team's largest logits
+    int nbest = 0;
     if (p.top) {
-        const uint32_t mo = offer[lane];
         int larger = 0;
 #pragma unroll
         for (int l = 0; l < 32; ++l) {
@@ -305,91 +431,103 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         if (omax >= bound && omax) {
             auto offer_one = [&](float z, int j) {
                 if (ordered(z) >= bound) {
-                    const int n = atomicAdd(&ncand, 1);
-                    if (n < kCand) cand[n] = make_key(z, j);
+                    const int n = atomicAdd(ncand, 1);
+                    if (n < CAND) cand[n] = make_key(z, j);
                 }
             };
             if (single >= 0) offer_one(Elem<T>::get(sl.row[single]), single);
-            const volatile int *listed = &ncand;
-#pragma unroll 4
-            for (int u = tid; u < sl.nv && *listed <= kCand; u += THREADS) {
-                float f[kPerVec<T>];
-                widen_vec<T>(sl.vec(u), f);
+            const volatile int *listed = ncand;
+            for (int v = 0; v < sl.nv && *listed <= CAND; v += kUnroll * TEAM) {
+                fetch(v, x);
 #pragma unroll
-                for (int e = 0; e < kPerVec<T>; ++e) offer_one(f[e], sl.v0 + u * kPerVec<T> + e);
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int q = v + u * TEAM + tid;
+                    if (q >= sl.nv) break;
+                    const uint32_t hi = Words<T>::max(Words<T>::max(x[u].x, x[u].y), Words<T>::max(x[u].z, x[u].w));
+                    if (ordered(max_word<T>(hi)) < bound) continue;
+                    float f[kPerVec<T>];
+                    widen_vec<T>(x[u], f);
+#pragma unroll
+                    for (int e = 0; e < kPerVec<T>; ++e) offer_one(f[e], sl.v0 + q * kPerVec<T> + e);
+                }
             }
         }
-        __syncthreads();
-        int n = ncand;
-        if (n > kCand) {
+        sync();
+        int n = *ncand;
+        if (n > CAND) {
             // many equal values: exact lists, one per warp (keys start at 0: below every key)
-            __syncthreads();
+            sync();
             unsigned long long list = 0;
-            auto offer_all = [&](unsigned long long x) {
-                unsigned b = __ballot_sync(0xFFFFFFFFu, x > __shfl_sync(0xFFFFFFFFu, list, p.top - 1));
+            auto offer_all = [&](unsigned long long key) {
+                unsigned b = __ballot_sync(0xFFFFFFFFu, key > __shfl_sync(0xFFFFFFFFu, list, p.top - 1));
                 while (b) {
                     const int l = __ffs(b) - 1;
                     b &= b - 1;
-                    const unsigned long long y = __shfl_sync(0xFFFFFFFFu, x, l);
+                    const unsigned long long y = __shfl_sync(0xFFFFFFFFu, key, l);
                     if (y > __shfl_sync(0xFFFFFFFFu, list, p.top - 1)) list_insert(list, y, lane);
                 }
             };
             offer_all(single >= 0 ? make_key(Elem<T>::get(sl.row[single]), single) : 0ull);
-            for (int u0 = warp * 32; u0 < sl.nv; u0 += THREADS) {
+            for (int u0 = warp * 32; u0 < sl.nv; u0 += TEAM) {
                 const int u = u0 + lane;
                 float f[kPerVec<T>];
                 const bool real = u < sl.nv;
-                widen_vec<T>(real ? sl.vec(u) : make_uint4(0, 0, 0, 0), f);
+                widen_vec<T>(real ? sl.vec(u) : lowest, f);
 #pragma unroll
                 for (int e = 0; e < kPerVec<T>; ++e)
                     offer_all(real ? make_key(f[e], sl.v0 + u * kPerVec<T> + e) : 0ull);
             }
             if (lane < p.top) cand[warp * p.top + lane] = list;
             n = W * p.top;
-            __syncthreads();
+            sync();
         }
-        const int k = rank_keys<THREADS>(cand, n, p.top, best);
-        if (tid == 0) nbest = k;
+        nbest = rank_keys<TEAM>(cand, n, p.top, best, tid);
+        sync();
     }
 
-    // ---- join the row's CTAs: CTA 0 reads the others' sums and keys
-    if (p.cluster > 1) {
-        if (tid == 0) mine = all;
-        cluster_sync();
-        if (rank == 0) {
-            const uint32_t own = smem_u32(&mine);
-            for (int r = 1; r < p.cluster; ++r) {
-                const uint32_t q = mapa_shared(own, r);
-                const Sums b{__uint_as_float(ld_cluster_u32(q)), __uint_as_float(ld_cluster_u32(q + 4)),
-                             __uint_as_float(ld_cluster_u32(q + 8)), __uint_as_float(ld_cluster_u32(q + 12))};
-                all = join(all, b);
+    // ---- join the row's CTAs: the others leave their sums and keys with the first
+    if (!WARP && p.cluster > 1) {
+        cluster_wait();
+        if (rank) {
+            if (tid == 0) {
+                const uint32_t to = mapa_shared(smem_u32(&from_sums[rank]), 0);
+                st_cluster_u32(to, __float_as_uint(all.ref));
+                st_cluster_u32(to + 4, __float_as_uint(all.s));
+                st_cluster_u32(to + 8, __float_as_uint(all.e));
+                st_cluster_u32(to + 12, __float_as_uint(all.zmax));
+                st_cluster_u32(mapa_shared(smem_u32(&from_count[rank]), 0), static_cast<uint32_t>(nbest));
             }
-            if (p.top) {
-                const uint32_t at = smem_u32(best), cnt = smem_u32(&nbest);
-                for (int x = tid; x < p.cluster * kMaxTop; x += THREADS) {
-                    const int r = x / kMaxTop, j = x % kMaxTop;
-                    const bool have = j < static_cast<int>(ld_cluster_u32(mapa_shared(cnt, r)));
-                    const uint32_t q = mapa_shared(at, r) + 8u * j;
-                    const uint32_t lo = have ? ld_cluster_u32(q) : 0u, hi = have ? ld_cluster_u32(q + 4) : 0u;
-                    cand[x] = (static_cast<unsigned long long>(hi) << 32) | lo;
-                }
-                __syncthreads();
-                rank_keys<THREADS>(cand, p.cluster * kMaxTop, p.top, best);
-            }
+            if (tid < nbest) st_cluster_u64(mapa_shared(smem_u32(&from_keys[rank][tid]), 0), best[tid]);
+            __syncwarp();
+            cluster_arrive();
+            return;
         }
-        cluster_sync();  // the others' shared memory has been read
-        if (rank) return;
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        for (int r = 1; r < p.cluster; ++r) all = join(all, from_sums[r]);
+        if (p.top) {
+            int n = nbest;
+            if (tid < nbest) cand[tid] = best[tid];
+            for (int r = 1; r < p.cluster; ++r) {
+                const int k = from_count[r];
+                if (tid < k) cand[n + tid] = from_keys[r][tid];
+                n += k;
+            }
+            __syncthreads();
+            rank_keys<TEAM>(cand, n, p.top, best, tid);
+            __syncthreads();
+        }
     }
-    if (p.top) __syncthreads();
 
     // The largest logit is finite, its product with c is not (logits near the
     // type's limits, e.g. a row masked with its lowest value): sums about the
-    // logit itself, in a second pass by this CTA alone.
+    // logit itself, in a second pass by this team alone.
     const bool extreme = fabsf(all.zmax) < INFINITY && !(fabsf(all.zmax * p.c) < INFINITY);
     if (extreme) {
         const float zmax = all.zmax;
         float s = 0.0f, e = 0.0f;
-        for (int j = tid; j < p.vocab; j += THREADS) {
+        for (int j = tid; j < p.vocab; j += TEAM) {
             const float u = max_nan((Elem<T>::get(sl.row[j]) - zmax) * p.c, kFloor), w = exp2_fast(u);
             s += w;
             e = fmaf(w, u, e);
@@ -399,13 +537,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
         }
-        if (lane == 0) part[warp] = Sums{0.0f, s, e, zmax};
-        __syncthreads();
-        all.s = all.e = 0.0f;
-        for (int w = 0; w < W; ++w) {
-            all.s += part[w].s;
-            all.e += part[w].e;
+        if (!WARP) {
+            __syncthreads();
+            if (lane == 0) part[warp] = Sums{0.0f, s, e, zmax};
+            __syncthreads();
+            s = e = 0.0f;
+            for (int w = 0; w < W; ++w) {
+                s += part[w].s;
+                e += part[w].e;
+            }
         }
+        all.s = s;
+        all.e = e;
     }
 
     const float logs = log2f(all.s);
@@ -424,9 +567,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         }
     }
     if (tid < p.top) {
-        const unsigned long long x = best[tid];
-        const float z = unordered(static_cast<uint32_t>(x >> 32));
-        p.top_ids[i * p.top + tid] = bad ? -1 : key_index(x);
+        const unsigned long long key = best[tid];
+        const float z = unordered(static_cast<uint32_t>(key >> 32));
+        p.top_ids[i * p.top + tid] = bad ? -1 : key_index(key);
         p.top_logp[i * p.top + tid] = bad ? NAN : logp_of(z);
     }
 }
@@ -521,26 +664,27 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
     }
 }
 
-template <typename T, int THREADS>
-cudaError_t launch_logprobs(const LogprobArgs &a, long long rows, cudaStream_t s)
+// Up to this vocabulary a warp takes a row.
+constexpr int kWarpVocab = 4096;
+
+template <typename T>
+cudaError_t launch_logprobs(const LogprobArgs &a, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * a.cluster));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
+    if (a.vocab <= kWarpVocab) {
+        cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kThreads / 32 - 1) / (kThreads / 32)));
+        return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 32>, a);
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(a.rows * a.cluster));
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = a.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a);
-}
-
-template <typename T>
-cudaError_t launch_logprobs(const LogprobArgs &a, long long rows, cudaStream_t s)
-{
-    return a.vocab <= 8192 ? launch_logprobs<T, 128>(a, rows, s) : launch_logprobs<T, 512>(a, rows, s);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads>, a);
 }
 
 bool bad_common(const void *logits, long long ld, int index_bytes, long long rows, int vocab, int dtype, float scale)
@@ -582,15 +726,15 @@ int cdg_token_logprobs(const void *logits, long long ld, const void *targets, in
     }
     const int sms = sm_count();
     if (sms < 1) return CDG_ERR_CUDA;
-    LogprobArgs a{logits, targets, ld, index_bytes, vocab, top, 1, scale,
+    LogprobArgs a{logits, targets, ld, rows, index_bytes, vocab, top, 1, scale,
                   static_cast<float>(static_cast<double>(scale) * 1.4426950408889634), logp, lse, entropy, top_logp,
                   top_ids};
     // CTAs a row: while there are fewer rows than SMs, split a row over a cluster
     while (a.cluster < kMaxCluster && rows * a.cluster * 2 <= 2ll * sms && vocab / (2 * a.cluster) >= 4096) a.cluster *= 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == CDG_F32   ? launch_logprobs<float>(a, rows, s)
-                          : dtype == CDG_F16 ? launch_logprobs<__half>(a, rows, s)
-                                             : launch_logprobs<__nv_bfloat16>(a, rows, s);
+    const cudaError_t e = dtype == CDG_F32   ? launch_logprobs<float>(a, s)
+                          : dtype == CDG_F16 ? launch_logprobs<__half>(a, s)
+                                             : launch_logprobs<__nv_bfloat16>(a, s);
     return e == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
 }
 
