@@ -33,7 +33,8 @@ constexpr int kMaxVocab = 1 << 30;  // element numbers stay in 32 bits
 constexpr int kThreads = 256;
 constexpr int kCand = 1024;         // candidate keys a CTA ranks
 constexpr int kMaxCluster = 8;      // CTAs that share a row
-constexpr int kUnroll = 4;          // 16-byte loads in flight per thread, and as many ahead
+constexpr int kUnroll = 4;          // 16-byte loads in flight per thread
+constexpr int kCtasPerSm = 6;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1000.0f;  // 2^-1000 is 0 in fp32: exponents are clamped here so that 0 * -inf does not arise
 
@@ -89,33 +90,21 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
     return r;
 }
 
-// Running sums about a reference (see the head of the file), and the largest
-// logit itself.
+// A row's sums about the reference zmax c (rounded), zmax the largest logit of
+// those summed.
 struct Sums {
-    float ref, s, e, zmax;
+    float zmax, s, e;
 };
+__device__ __forceinline__ float reference(float zmax, float c) { return zmax == -INFINITY ? 0.0f : zmax * c; }
 
-__device__ __forceinline__ Sums join(const Sums &a, const Sums &b)
+// Sums moved to a larger largest logit.
+__device__ __forceinline__ void move_to(Sums &a, float zmax, float c)
 {
-    Sums r;
-    r.ref = fmaxf(a.ref, b.ref);
-    const bool none = r.ref == -INFINITY;  // both empty: s = e = 0
-    const float da = none ? 0.0f : fmaxf(a.ref - r.ref, kFloor), db = none ? 0.0f : fmaxf(b.ref - r.ref, kFloor);
-    const float ra = exp2_fast(da), rb = exp2_fast(db);
-    r.s = a.s * ra + b.s * rb;
-    r.e = ra * fmaf(da, a.s, a.e) + rb * fmaf(db, b.s, b.e);
-    r.zmax = fmaxf(a.zmax, b.zmax);
-    return r;
-}
-__device__ __forceinline__ Sums join_lanes(Sums a)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const Sums b{__shfl_xor_sync(0xFFFFFFFFu, a.ref, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
-                     __shfl_xor_sync(0xFFFFFFFFu, a.e, o), __shfl_xor_sync(0xFFFFFFFFu, a.zmax, o)};
-        a = join(a, b);
-    }
-    return a;
+    const float d = a.zmax == -INFINITY ? 0.0f : fmaxf(a.zmax * c - zmax * c, kFloor);  // none yet: s = e = 0
+    const float r = exp2_fast(d);
+    a.e = r * fmaf(d, a.s, a.e);
+    a.s *= r;
+    a.zmax = zmax;
 }
 
 // Float order as unsigned order (-0 and +0 equal); 0 is below every number.
@@ -127,6 +116,19 @@ __device__ __forceinline__ uint32_t ordered(float f)
 __device__ __forceinline__ float unordered(uint32_t u)
 {
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+// Largest of the warp's (NaN stays out: it never enters a zmax).
+__device__ __forceinline__ float warp_max(float z) { return unordered(__reduce_max_sync(0xFFFFFFFFu, ordered(z))); }
+// The warp's sums, in every lane.
+__device__ __forceinline__ Sums join_lanes(Sums a, float c)
+{
+    move_to(a, warp_max(a.zmax), c);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+        a.e += __shfl_xor_sync(0xFFFFFFFFu, a.e, o);
+    }
+    return a;
 }
 // Larger key = larger value, then lower element number.  Never 0.
 __device__ __forceinline__ unsigned long long make_key(float z, int j)
@@ -142,7 +144,6 @@ template <>
 struct Words<float> {
     static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }
     static __device__ __forceinline__ uint32_t min(uint32_t a, uint32_t b) { return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b))); }
-    static constexpr uint32_t kLowest = 0xFF800000u;  // -inf in every element
 };
 template <>
 struct Words<__half> {
@@ -156,7 +157,6 @@ struct Words<__half> {
         const __half2 r = __hmin2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&r);
     }
-    static constexpr uint32_t kLowest = 0xFC00FC00u;
 };
 template <>
 struct Words<__nv_bfloat16> {
@@ -170,7 +170,6 @@ struct Words<__nv_bfloat16> {
         const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&r);
     }
-    static constexpr uint32_t kLowest = 0xFF80FF80u;
 };
 template <typename T>
 __device__ __forceinline__ float max_word(uint32_t w)
@@ -332,7 +331,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // TEAM threads a row: a warp each of eight rows, or the CTA, which a cluster of
 // CTAs may share the row with.
 template <typename T, int TEAM>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs p)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const LogprobArgs p)
 {
     constexpr bool WARP = TEAM == 32;
     constexpr int W = TEAM / 32, TEAMS = kThreads / TEAM, CAND = kCand / TEAMS;
@@ -359,41 +358,42 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     int *const ncand = s_ncand + team;
     const Slice<T> sl(static_cast<const T *>(p.logits) + i * p.ld, p.vocab, rank, WARP ? 1 : p.cluster);
 
-    // ---- one pass: sums and the thread's maximum; the next group is on its way while one is added
-    Run run{-INFINITY, -INFINITY, 0ull, 0ull};
     const int single = sl.single(tid);
-    const uint4 lowest = make_uint4(Words<T>::kLowest, Words<T>::kLowest, Words<T>::kLowest, Words<T>::kLowest);
-    auto fetch = [&](int v, uint4 (&x)[kUnroll]) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) x[u] = v + u * TEAM + tid < sl.nv ? sl.vec(v + u * TEAM + tid) : lowest;
-    };
+    const auto vec_at = [&](int v) { return sl.vec(v + tid); };
+
+    // ---- one pass: sums and the thread's maximum
+    Run run{-INFINITY, -INFINITY, 0ull, 0ull};
     uint4 x[kUnroll];
-    fetch(0, x);
+    int v = 0;
+    for (; v + kUnroll * TEAM <= sl.nv; v += kUnroll * TEAM) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) x[u] = vec_at(v + u * TEAM);
+        add_group<T, kUnroll>(run, x, p.c);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        if (v + u * TEAM + tid < sl.nv) x[u] = vec_at(v + u * TEAM);
     if (single >= 0) {
         const float z = Elem<T>::get(sl.row[single]);
-        run.zmax = z == z ? z : -INFINITY;
+        run.zmax = fmaxf(run.zmax, z);
         raise(run, z * p.c);
         const float ref = run.ref == -INFINITY ? 0.0f : run.ref;
         add<true>(run, z, -INFINITY, pack2(p.c, p.c), pack2(-ref, -ref));
     }
-    for (int v = 0; v < sl.nv; v += kUnroll * TEAM) {
-        uint4 next[kUnroll];
-        const bool more = v + kUnroll * TEAM < sl.nv;
-        if (more) fetch(v + kUnroll * TEAM, next);
-        add_group<T, kUnroll>(run, x, p.c);
-        if (more) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) x[u] = next[u];
+    for (int u = 0; u < kUnroll; ++u)
+        if (v + u * TEAM + tid < sl.nv) {
+            const uint4 y[1] = {x[u]};
+            add_group<T, 1>(run, y, p.c);
         }
-    }
     // no element at all in this thread: below every element
     const uint32_t omax = single >= 0 || tid < sl.nv ? ordered(run.zmax) : 0u;
 
-    // ---- join the team
+    // ---- join the team: the CTA's sums end in its first warp
     float s0, s1, e0, e1;
     unpack2(run.s, s0, s1);
     unpack2(run.e, e0, e1);
-    Sums all = join_lanes(Sums{run.ref, s0 + s1, e0 + e1, run.zmax});
+    Sums all = join_lanes(Sums{run.zmax, s0 + s1, e0 + e1}, p.c);
     uint32_t mo = omax;  // lane l: one of 32 thread maxima
     if (p.top && tid == 0) *ncand = 0;
     if (!WARP) {
@@ -409,9 +409,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             }
         }
         __syncthreads();
-        all = part[0];
-#pragma unroll
-        for (int w = 1; w < W; ++w) all = join(all, part[w]);
+        if (warp == 0) all = join_lanes(lane < W ? part[lane] : Sums{-INFINITY, 0.0f, 0.0f}, p.c);
         if (p.top) mo = offer[lane];
     } else if (p.top) {
         __syncwarp();
@@ -437,11 +435,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             };
             if (single >= 0) offer_one(Elem<T>::get(sl.row[single]), single);
             const volatile int *listed = ncand;
-            for (int v = 0; v < sl.nv && *listed <= CAND; v += kUnroll * TEAM) {
-                fetch(v, x);
+            // (a row of less than a full group is still in x)
+            for (int w = 0; w < sl.nv && *listed <= CAND; w += kUnroll * TEAM) {
+                if (sl.nv >= kUnroll * TEAM) {
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u)
+                        if (w + u * TEAM + tid < sl.nv) x[u] = vec_at(w + u * TEAM);
+                }
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int q = v + u * TEAM + tid;
+                    const int q = w + u * TEAM + tid;
                     if (q >= sl.nv) break;
                     const uint32_t hi = Words<T>::max(Words<T>::max(x[u].x, x[u].y), Words<T>::max(x[u].z, x[u].w));
                     if (ordered(max_word<T>(hi)) < bound) continue;
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
                 const int u = u0 + lane;
                 float f[kPerVec<T>];
                 const bool real = u < sl.nv;
-                widen_vec<T>(real ? sl.vec(u) : lowest, f);
+                widen_vec<T>(real ? sl.vec(u) : make_uint4(0u, 0u, 0u, 0u), f);
 #pragma unroll
                 for (int e = 0; e < kPerVec<T>; ++e)
                     offer_all(real ? make_key(f[e], sl.v0 + u * kPerVec<T> + e) : 0ull);
@@ -491,10 +494,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
         if (rank) {
             if (tid == 0) {
                 const uint32_t to = mapa_shared(smem_u32(&from_sums[rank]), 0);
-                st_cluster_u32(to, __float_as_uint(all.ref));
+                st_cluster_u32(to, __float_as_uint(all.zmax));
                 st_cluster_u32(to + 4, __float_as_uint(all.s));
                 st_cluster_u32(to + 8, __float_as_uint(all.e));
-                st_cluster_u32(to + 12, __float_as_uint(all.zmax));
                 st_cluster_u32(mapa_shared(smem_u32(&from_count[rank]), 0), static_cast<uint32_t>(nbest));
             }
             if (tid < nbest) st_cluster_u64(mapa_shared(smem_u32(&from_keys[rank][tid]), 0), best[tid]);
@@ -502,10 +504,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             cluster_arrive();
             return;
         }
+        if (tid == 0) from_sums[0] = all;
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        for (int r = 1; r < p.cluster; ++r) all = join(all, from_sums[r]);
+        if (warp == 0) all = join_lanes(lane < p.cluster ? from_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, p.c);
         if (p.top) {
             int n = nbest;
             if (tid < nbest) cand[tid] = best[tid];
@@ -520,46 +523,36 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
         }
     }
 
+    if (warp != 0) return;  // the first warp of the team has the sums and writes the row's answers
+
     // The largest logit is finite, its product with c is not (logits near the
     // type's limits, e.g. a row masked with its lowest value): sums about the
-    // logit itself, in a second pass by this team alone.
+    // logit itself, in a second pass by this warp alone.
     const bool extreme = fabsf(all.zmax) < INFINITY && !(fabsf(all.zmax * p.c) < INFINITY);
     if (extreme) {
-        const float zmax = all.zmax;
-        float s = 0.0f, e = 0.0f;
-        for (int j = tid; j < p.vocab; j += TEAM) {
-            const float u = max_nan((Elem<T>::get(sl.row[j]) - zmax) * p.c, kFloor), w = exp2_fast(u);
-            s += w;
-            e = fmaf(w, u, e);
+        all.s = all.e = 0.0f;
+        for (int j = lane; j < p.vocab; j += 32) {
+            const float u = max_nan((Elem<T>::get(sl.row[j]) - all.zmax) * p.c, kFloor), w = exp2_fast(u);
+            all.s += w;
+            all.e = fmaf(w, u, all.e);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
+            all.s += __shfl_xor_sync(0xFFFFFFFFu, all.s, o);
+            all.e += __shfl_xor_sync(0xFFFFFFFFu, all.e, o);
         }
-        if (!WARP) {
-            __syncthreads();
-            if (lane == 0) part[warp] = Sums{0.0f, s, e, zmax};
-            __syncthreads();
-            s = e = 0.0f;
-            for (int w = 0; w < W; ++w) {
-                s += part[w].s;
-                e += part[w].e;
-            }
-        }
-        all.s = s;
-        all.e = e;
     }
+    const float ref = reference(all.zmax, p.c);
 
     const float logs = log2f(all.s);
     const bool none = all.zmax == -INFINITY && all.s == 0.0f;  // nothing but -inf
     const bool bad = isnan(all.s);
     auto logp_of = [&](float z) {
         if (none) return -INFINITY;
-        return kLn2 * ((extreme ? (z - all.zmax) * p.c : fmaf(z, p.c, -all.ref)) - logs);
+        return kLn2 * ((extreme ? (z - all.zmax) * p.c : fmaf(z, p.c, -ref)) - logs);
     };
     if (tid == 0) {
-        if (p.lse) p.lse[i] = none ? -INFINITY : extreme ? fmaf(all.zmax, p.scale, kLn2 * logs) : kLn2 * (all.ref + logs);
+        if (p.lse) p.lse[i] = none ? -INFINITY : extreme ? fmaf(all.zmax, p.scale, kLn2 * logs) : kLn2 * (ref + logs);
         if (p.entropy) p.entropy[i] = none ? 0.0f : kLn2 * (logs - all.e / all.s);
         if (p.logp) {
             const int t = token_at(p.targets, p.index_bytes, i, p.vocab);
@@ -664,16 +657,18 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
     }
 }
 
-// Up to this vocabulary a warp takes a row.
+// Up to this vocabulary a warp takes a row, if there are more rows than run at
+// once with a CTA each; fewer rows end sooner that way (256 x 1000 with 5
+// alternatives: 4.2 us against 8.9; 65536 rows: 242 us against 154).
 constexpr int kWarpVocab = 4096;
 
 template <typename T>
-cudaError_t launch_logprobs(const LogprobArgs &a, cudaStream_t s)
+cudaError_t launch_logprobs(const LogprobArgs &a, int sms, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    if (a.vocab <= kWarpVocab) {
+    if (a.vocab <= kWarpVocab && a.rows > static_cast<long long>(kCtasPerSm) * sms) {
         cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kThreads / 32 - 1) / (kThreads / 32)));
         return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 32>, a);
     }
@@ -732,9 +727,9 @@ int cdg_token_logprobs(const void *logits, long long ld, const void *targets, in
     // CTAs a row: while there are fewer rows than SMs, split a row over a cluster
     while (a.cluster < kMaxCluster && rows * a.cluster * 2 <= 2ll * sms && vocab / (2 * a.cluster) >= 4096) a.cluster *= 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == CDG_F32   ? launch_logprobs<float>(a, s)
-                          : dtype == CDG_F16 ? launch_logprobs<__half>(a, s)
-                                             : launch_logprobs<__nv_bfloat16>(a, s);
+    const cudaError_t e = dtype == CDG_F32   ? launch_logprobs<float>(a, sms, s)
+                          : dtype == CDG_F16 ? launch_logprobs<__half>(a, sms, s)
+                                             : launch_logprobs<__nv_bfloat16>(a, sms, s);
     return e == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
 }
 
