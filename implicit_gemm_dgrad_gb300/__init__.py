@@ -614,11 +614,20 @@ def _esize(dtype) -> int:
     return 4 if _dtype(dtype) == F32 else 2
 
 
+_tensor = _cuda_device = None  # torch.Tensor and the current device's number, once a torch tensor has been seen
+
+
 def _bytes_of(t, n: int, esize: int, what: str) -> int:
     """Address of a dense CUDA tensor of at least n elements of esize bytes."""
+    if type(t) is _tensor and t.itemsize == esize and t.nbytes >= n * esize and t.is_contiguous() and \
+            t.get_device() == _cuda_device():
+        return t.data_ptr()  # what the checks below find, without their cost
     if t.element_size() != esize:
         raise ValueError(f"{what} has elements of {t.element_size()} bytes; {esize} are needed")
     _check_buffer(t, n * esize, what)
+    if _tensor is None and type(t).__module__ == "torch":
+        import torch
+        globals().update(_tensor=torch.Tensor, _cuda_device=getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     return t.data_ptr()
 
 

@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
 struct LogprobGradArgs {
     const void *logits, *targets;
     long long ld, ld_d;
+    long long rows;
     int index_bytes, vocab, chunks;
     float scale;
     const float *lse, *entropy, *g_logp, *g_entropy;
@@ -593,13 +594,16 @@ struct GradRow {
 
 constexpr int kGradThreads = 256;
 
-// A CTA takes one chunk of a row: kGradThreads * kUnroll vectors.
-template <typename T>
+// TX threads take one chunk of a row, TX * kUnroll vectors; a CTA several rows
+// where a row is short.
+template <typename T, int TX>
 __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogprobGradArgs p)
 {
     constexpr int E = kPerVec<T>;
-    const long long i = blockIdx.x / p.chunks;
-    const int chunk = static_cast<int>(blockIdx.x - i * p.chunks), tid = threadIdx.x;
+    const int tid = threadIdx.x % TX;
+    const long long group = blockIdx.x / p.chunks, i = group * (kGradThreads / TX) + threadIdx.x / TX;
+    const int chunk = static_cast<int>(blockIdx.x - group * p.chunks);
+    if (i >= p.rows) return;
     const T *z = static_cast<const T *>(p.logits) + i * p.ld;
     T *d = static_cast<T *>(p.dlogits) + i * p.ld_d;
     const int t = token_at(p.targets, p.index_bytes, i, p.vocab);
@@ -620,9 +624,9 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
     const uint32_t za = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z)) & 15u;
     const uint32_t da = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(d)) & 15u;
     if (za != da) {  // the two rows never align together: element by element
-        const int j0 = chunk * kGradThreads * kUnroll * E;
+        const int n = TX * kUnroll * E, j0 = chunk * n;
 #pragma unroll 4
-        for (int j = j0 + tid; j < min(j0 + kGradThreads * kUnroll * E, p.vocab); j += kGradThreads) one(j);
+        for (int j = j0 + tid; j < min(j0 + n, p.vocab); j += TX) one(j);
         return;
     }
     const int head = min(za ? static_cast<int>((16u - za) / sizeof(T)) : 0, p.vocab);
@@ -630,18 +634,18 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
     if (chunk == 0) {
         const int rest = head + nv * E;
         if (tid < head) one(tid);
-        else if (tid >= 32 && tid - 32 < p.vocab - rest) one(rest + tid - 32);
+        else if (tid >= 8 && tid - 8 < p.vocab - rest) one(rest + tid - 8);
     }
     const uint4 *zv = reinterpret_cast<const uint4 *>(z + head);
     uint4 *dv = reinterpret_cast<uint4 *>(d + head);
-    const int v0 = chunk * kGradThreads * kUnroll + tid;
+    const int v0 = chunk * TX * kUnroll + tid;
     uint4 x[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-        if (v0 + u * kGradThreads < nv) x[u] = zv[v0 + u * kGradThreads];
+        if (v0 + u * TX < nv) x[u] = zv[v0 + u * TX];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        const int v = v0 + u * kGradThreads;
+        const int v = v0 + u * TX;
         if (v >= nv) break;
         float y[E];
         widen_vec<T>(x[u], y);
@@ -680,6 +684,15 @@ cudaError_t launch_logprobs(const LogprobArgs &a, int sms, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads>, a);
+}
+
+template <typename T>
+void launch_grad(const LogprobGradArgs &a, int tx, unsigned grid, cudaStream_t s)
+{
+    if (tx == 32) logprobs_grad_kernel<T, 32><<<grid, kGradThreads, 0, s>>>(a);
+    else if (tx == 64) logprobs_grad_kernel<T, 64><<<grid, kGradThreads, 0, s>>>(a);
+    else if (tx == 128) logprobs_grad_kernel<T, 128><<<grid, kGradThreads, 0, s>>>(a);
+    else logprobs_grad_kernel<T, kGradThreads><<<grid, kGradThreads, 0, s>>>(a);
 }
 
 bool bad_common(const void *logits, long long ld, int index_bytes, long long rows, int vocab, int dtype, float scale)
@@ -743,8 +756,11 @@ int cdg_token_logprobs_grad(const void *logits, long long ld, const void *target
     if (rows == 0) return CDG_OK;
     if (!targets || !lse || !g_logp || !dlogits || (g_entropy && !entropy)) return CDG_ERR_INVALID_ARG;
     const int es = dtype_bytes(dtype);
-    const int per = kGradThreads * kUnroll * (16 / es);
+    int tx = 32;
+    while (tx < kGradThreads && static_cast<long long>(tx) * kUnroll * (16 / es) < vocab) tx *= 2;
+    const int per = tx * kUnroll * (16 / es), ty = kGradThreads / tx;
     const int chunks = (vocab - 1) / per + 1;
+    const long long groups = (rows - 1) / ty + 1;
     if (rows > ((1ll << 31) - 1) / chunks || vocab > kMaxVocab) return CDG_ERR_UNSUPPORTED;
     if (!aligned_to(logits, es) || !aligned_to(targets, index_bytes) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) ||
         !aligned_to(g_logp, 4) || !aligned_to(g_entropy, 4) || !aligned_to(dlogits, es))
@@ -757,13 +773,13 @@ int cdg_token_logprobs_grad(const void *logits, long long ld, const void *target
         if (overlap(out, e)) return CDG_ERR_ALIAS;
     if (!(dlogits == logits && ld == ld_d) && overlap(out, extent(logits, matrix_bytes(rows, vocab, ld, es))))
         return CDG_ERR_ALIAS;
-    const LogprobGradArgs a{logits, targets, ld, ld_d, index_bytes, vocab, chunks, scale, lse, entropy, g_logp,
+    const LogprobGradArgs a{logits, targets, ld, ld_d, rows, index_bytes, vocab, chunks, scale, lse, entropy, g_logp,
                             g_entropy, dlogits};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = static_cast<unsigned>(rows * chunks);
-    if (dtype == CDG_F32) logprobs_grad_kernel<float><<<grid, kGradThreads, 0, s>>>(a);
-    else if (dtype == CDG_F16) logprobs_grad_kernel<__half><<<grid, kGradThreads, 0, s>>>(a);
-    else logprobs_grad_kernel<__nv_bfloat16><<<grid, kGradThreads, 0, s>>>(a);
+    const unsigned grid = static_cast<unsigned>(groups * chunks);
+    if (dtype == CDG_F32) launch_grad<float>(a, tx, grid, s);
+    else if (dtype == CDG_F16) launch_grad<__half>(a, tx, grid, s);
+    else launch_grad<__nv_bfloat16>(a, tx, grid, s);
     return cudaGetLastError() == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
 }
 
