@@ -16,113 +16,126 @@ namespace {
 
 constexpr int kMaxDim = 1 << 24;
 
+// Where a matrix's rows lie in 16-byte vectors: row v's first element is
+// element `phase(v)` of its first vector.
+struct Phase {
+    uint32_t base, ld;  // elements, modulo the vector's
+    template <typename T>
+    static Phase of(const void *p, long long ld)
+    {
+        return Phase{static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T)),
+                     static_cast<uint32_t>(ld % kPerVec<T>)};
+    }
+    template <typename T>
+    __device__ __forceinline__ int at(uint32_t v) const { return static_cast<int>((base + v * ld) & (kPerVec<T> - 1)); }
+};
+
+// Elements [col, col + E) of a row of `cols`, of which those that exist: whole
+// aligned vectors, or single elements at the row's ends.
+template <typename O, int E>
+__device__ __forceinline__ void store_columns(O *row, int col, int cols, const float (&f)[E])
+{
+    if (col >= 0 && col + E <= cols) {
+        constexpr int V = kPerVec<O>;
+#pragma unroll
+        for (int q = 0; q < E; q += V) {
+            float g[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] = f[q + e];
+            *reinterpret_cast<uint4 *>(row + col + q) = narrow_vec<O>(g);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (col + e >= 0 && col + e < cols) row[col + e] = Elem<O>::put(f[e]);
+    }
+}
+
 // ---------------------------------------------------------------- lookup
 struct EmbedArgs {
     const void *table, *tokens;
     void *out;
     long long ld_table, ld_out, count;
-    int index_bytes, vocab, n;  // n accesses a row
+    int index_bytes, vocab, dim;
+    Phase phase;             // of out
+    const char *lo, *hi;     // the table
     float scale;
 };
 
-// One access of E elements (16 bytes, one 32-bit word, or one element).
-template <typename T, int E>
-struct Access;
-template <typename T>
-struct Access<T, kPerVec<T>> {
-    uint4 v;
-    __device__ __forceinline__ void load(const T *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void get(float *f) const
-    {
-        float g[kPerVec<T>];
-        widen_vec<T>(v, g);
-#pragma unroll
-        for (int i = 0; i < kPerVec<T>; ++i) f[i] = g[i];
-    }
-};
-template <typename T>
-struct Access<T, 1> {
-    T v;
-    __device__ __forceinline__ void load(const T *p) { v = __ldg(p); }
-    __device__ __forceinline__ void get(float *f) const { f[0] = Elem<T>::get(v); }
-};
-
-template <typename T, int E>
-__device__ __forceinline__ void store_elems(T *p, const float *f)
-{
-    if constexpr (E == 1) {
-        p[0] = Elem<T>::put(f[0]);
-    } else {
-        float g[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) g[i] = f[i];
-        *reinterpret_cast<uint4 *>(p) = narrow_vec<T>(g);
-    }
-}
-
-// Thread (x, y): row blockIdx.x * blockDim.y + y, accesses x + k * blockDim.x
-// of the UNROLL * blockDim.x that blockIdx.y takes.
-template <typename T, int E, int UNROLL>
+// Thread (x, y): row blockIdx.x * blockDim.y + y, vectors x + k * blockDim.x of
+// the UNROLL * blockDim.x that blockIdx.y takes.  Vectors are aligned in out;
+// ALIGNED: and in the table, else they are read from two blocks each.
+template <typename T, bool ALIGNED, int UNROLL>
 __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs p)
 {
+    constexpr int E = kPerVec<T>;
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (i >= p.count) return;
     const int t = token_at(p.tokens, p.index_bytes, i, p.vocab);
     const T *src = static_cast<const T *>(p.table) + static_cast<long long>(max(t, 0)) * p.ld_table;
     T *dst = static_cast<T *>(p.out) + i * p.ld_out;
-    const int a0 = blockIdx.y * (blockDim.x * UNROLL) + threadIdx.x;
-    Access<T, E> x[UNROLL];
+    const int col0 = static_cast<int>(blockIdx.y * (blockDim.x * UNROLL) + threadIdx.x) * E -
+                     (ALIGNED ? 0 : p.phase.at<T>(static_cast<uint32_t>(i)));
+    Shifted<T> x[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-        const int a = a0 + u * blockDim.x;
-        if (a < p.n && t >= 0) x[u].load(src + static_cast<long long>(a) * E);
+        const int col = col0 + static_cast<int>(u * blockDim.x) * E;
+        if (col < p.dim && t >= 0) {
+            if (ALIGNED) x[u].a = __ldg(reinterpret_cast<const uint4 *>(src + col));
+            else x[u].load(src + col, p.lo, p.hi, col, p.dim);
+        }
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-        const int a = a0 + u * blockDim.x;
-        if (a >= p.n) break;
+        const int col = col0 + static_cast<int>(u * blockDim.x) * E;
+        if (col >= p.dim) break;
         float f[E];
         if (t >= 0) {
-            x[u].get(f);
+            widen_vec<T>(ALIGNED ? x[u].a : x[u].get(), f);
 #pragma unroll
             for (int e = 0; e < E; ++e) f[e] *= p.scale;
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e) f[e] = 0.0f;
         }
-        store_elems<T, E>(dst + static_cast<long long>(a) * E, f);
+        store_columns<T, E>(dst, col, p.dim, f);
     }
 }
 
-template <typename T, int E, int UNROLL>
+template <typename T, bool ALIGNED, int UNROLL>
 void launch_embed(const EmbedArgs &a, cudaStream_t s)
 {
+    const int n = (a.dim + kPerVec<T> - 1) / kPerVec<T> + (ALIGNED ? 0 : 1);  // vectors a row, at most
     int tx = 8;
-    while (tx < 256 && tx * UNROLL < a.n) tx *= 2;
+    while (tx < 256 && tx * UNROLL < n) tx *= 2;
     const dim3 block(tx, 256 / tx);
-    const dim3 grid(static_cast<unsigned>((a.count + block.y - 1) / block.y), (a.n + tx * UNROLL - 1) / (tx * UNROLL));
-    embed_kernel<T, E, UNROLL><<<grid, block, 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>((a.count + block.y - 1) / block.y), (n + tx * UNROLL - 1) / (tx * UNROLL));
+    embed_kernel<T, ALIGNED, UNROLL><<<grid, block, 0, s>>>(a);
 }
 
 template <typename T>
-void launch_embed(EmbedArgs a, int dim, int sms, cudaStream_t s)
+void launch_embed(EmbedArgs a, int sms, cudaStream_t s)
 {
-    const bool vec = dim % kPerVec<T> == 0 && a.ld_table % kPerVec<T> == 0 && a.ld_out % kPerVec<T> == 0 &&
-                     aligned_to(a.table, 16) && aligned_to(a.out, 16);
-    a.n = vec ? dim / kPerVec<T> : dim;
-    // few accesses: one a thread, spread over the SMs
-    const bool few = a.count * a.n < 1024ll * sms;
-    if (vec && few) launch_embed<T, kPerVec<T>, 1>(a, s);
-    else if (vec) launch_embed<T, kPerVec<T>, 4>(a, s);
-    else if (few) launch_embed<T, 1, 1>(a, s);
-    else launch_embed<T, 1, 8>(a, s);
+    const int E = kPerVec<T>;
+    const bool aligned = a.dim % E == 0 && a.ld_table % E == 0 && a.ld_out % E == 0 && aligned_to(a.table, 16) &&
+                         aligned_to(a.out, 16);
+    a.phase = Phase::of<T>(a.out, a.ld_out);
+    a.lo = static_cast<const char *>(a.table);
+    a.hi = a.lo + matrix_bytes(a.vocab, a.dim, a.ld_table, sizeof(T));
+    // few vectors: one a thread, spread over the SMs
+    const bool few = a.count * (a.dim / E + 1) < 1024ll * sms;
+    if (aligned && few) launch_embed<T, true, 1>(a, s);
+    else if (aligned) launch_embed<T, true, 4>(a, s);
+    else if (few) launch_embed<T, false, 1>(a, s);
+    else launch_embed<T, false, 4>(a, s);
 }
 
 // ---------------------------------------------------------------- sort
 // Up to kRankMax tokens: every token's place is the number of keys before it,
-// counted directly (one launch, N^2 comparisons).  Above: a radix sort of
+// counted directly (one launch, N^2 comparisons; 8192 tokens take 17 us longer
+// that way than by the radix sort).  Above: a radix sort of
 // digits of up to 9 bits, two launches a digit.
-constexpr int kRankMax = 8192;
+constexpr int kRankMax = 4096;
 constexpr int kSortThreads = 256, kMaxBins = 512, kWarps = kSortThreads / 32;
 
 struct SortPass {
@@ -130,6 +143,7 @@ struct SortPass {
     const int *keys, *order;  // later passes: the previous pass's output
     int *keys_out, *order_out;
     int *hist;                // [tiles][bins]
+    int *runs;                // the count of long runs, set to 0
     int index_bytes, count, vocab, shift, bins, tiles;
 };
 
@@ -147,6 +161,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortPass 
     extern __shared__ int4 keys4[];
     int *keys = reinterpret_cast<int *>(keys4);
     const int n4 = (p.count + 3) / 4;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.runs = 0;
     for (int i = threadIdx.x; i < 4 * n4; i += kSortThreads) keys[i] = i < p.count ? sort_key(p, i) : INT_MAX;
     __syncthreads();
     const int i = blockIdx.x * 32 + threadIdx.x / 8, sub = threadIdx.x % 8;
@@ -173,6 +188,7 @@ template <int ROUNDS>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPass p)
 {
     __shared__ int h[kMaxBins];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.runs = 0;
     for (int d = threadIdx.x; d < p.bins; d += kSortThreads) h[d] = 0;
     __syncthreads();
     const int i0 = blockIdx.x * (ROUNDS * kSortThreads) + threadIdx.x;
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPass
     const int d0 = 2 * tid, d1 = d0 + 1;
     int tot0 = 0, tot1 = 0, before0 = 0, before1 = 0;
     if (d0 < p.bins) {
-#pragma unroll 8
+#pragma unroll 16
         for (int t = 0; t < p.tiles; ++t) {
             const int2 h = __ldg(reinterpret_cast<const int2 *>(p.hist + static_cast<long long>(t) * p.bins + d0));
             const bool prior = t < static_cast<int>(blockIdx.x);
@@ -269,44 +285,35 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPass
 }
 
 // ---------------------------------------------------------------- sums
-// The sorted positions are cut into chunks of one size.  A chunk's CTA reads
-// its rows of dout in order, several at once, and writes a token's sum where
-// the token's run lies within the chunk; a run that crosses chunk borders
-// leaves partial sums (fp32): the chunk's first run in slot 0 if it began
-// earlier, its last run in slot 1 if it began here and goes on.  A second
-// launch adds those in chunk order.  So the work is even whatever the tokens'
-// frequencies, and the order of additions is fixed.
-constexpr int kSumThreads = 128, kMaxChunk = 64, kRowsAtOnce = 8;
+// The sorted positions are cut into chunks of one size, a team of threads
+// each.  A token's run of up to a chunk's length belongs to the chunk it begins
+// in, wherever it ends.  A longer run is cut at the chunk borders: each chunk
+// leaves its part's sum (fp32), in slot 0 if the run began earlier, in slot 1 if
+// it begins there, and a second launch adds the parts in a fixed order.  So the
+// work is even whatever the tokens' frequencies, and sums do not depend on
+// scheduling.
+//
+// A thread holds one 16-byte vector of columns (of dout's type), placed so that
+// it is aligned in the row it writes; rows of dout at other alignments are read
+// from two blocks.
+constexpr int kSumThreads = 128, kMaxChunk = 64;
 
 struct EmbedGradArgs {
     const void *dout;
     void *dtable;
     long long ld_dout, ld_dtable;
     const int *keys, *order;  // sorted tokens and their positions
-    float *partial;           // [chunks][2][dim]
+    float *partial;           // [chunks][2][pitch]
+    int *runs;                // long runs: how many, then the chunk each begins in (in any order)
+    const char *lo, *hi;      // dout
+    Phase phase;              // of dtable
     int count, vocab, dim, accumulate;
     int chunk, chunks;        // positions a chunk, chunks
+    int pitch;                // of partial rows: dim and a vector more
     int tx, col_tiles;        // threads across a row; column tiles
     unsigned sum_ctas, zero_ctas;
     float scale;
 };
-
-template <typename O, int E>
-__device__ __forceinline__ void write_sum(const EmbedGradArgs &p, int token, int col, const float (&s)[E])
-{
-    O *dst = static_cast<O *>(p.dtable) + static_cast<long long>(token) * p.ld_dtable + col;
-    constexpr int V = E == 1 ? 1 : kPerVec<O>;
-#pragma unroll
-    for (int q = 0; q < E; q += V) {
-        float f[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            f[e] = s[q + e] * p.scale;
-            if (p.accumulate) f[e] += Elem<O>::get(dst[q + e]);
-        }
-        store_elems<O, V>(dst + q, f);
-    }
-}
 
 // First position with keys[i] >= v, by a warp: 32 probes a step.
 __device__ __forceinline__ int warp_lower_bound(const int *keys, int count, int v, int lane)
@@ -323,12 +330,18 @@ __device__ __forceinline__ int warp_lower_bound(const int *keys, int count, int 
     }
     return lo;
 }
+// How many of key[a .. a + n) are v, by a warp (n <= 64).
+__device__ __forceinline__ int warp_count(const int *key, int a, int n, int v, int lane)
+{
+    return __popc(__ballot_sync(0xFFFFFFFFu, lane < n && key[a + lane] == v)) +
+           __popc(__ballot_sync(0xFFFFFFFFu, lane + 32 < n && key[a + min(lane + 32, n - 1)] == v));
+}
 
-// E elements an access (16 bytes of T, or 1), K accesses a thread.
-template <typename T, typename O, int E, int K>
+template <typename T, typename O, bool ALIGNED, bool ACCUMULATE>
 __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGradArgs p)
 {
-    __shared__ int s_key[kSumThreads / 8][kMaxChunk + 2], s_row[kSumThreads / 8][kMaxChunk];
+    constexpr int E = kPerVec<T>, V = kPerVec<O>, ROWS = ACCUMULATE ? 4 : 8;  // rows read at once
+    __shared__ int s_key[kSumThreads / 32][3 * kMaxChunk + 1], s_row[kSumThreads / 32][2 * kMaxChunk];
     // the CTAs that clear rows without a token lie evenly among the others
     const unsigned all = p.sum_ctas + p.zero_ctas;
     const unsigned z0 = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * p.zero_ctas / all);
@@ -339,12 +352,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
         const int at = warp_lower_bound(p.keys, p.count, row, lane);
         if (at < p.count && __ldg(p.keys + at) == row) return;
         O *dst = static_cast<O *>(p.dtable) + static_cast<long long>(row) * p.ld_dtable;
-        if constexpr (E > 1) {
-            constexpr int V = kPerVec<O>;
-            for (int c = lane; c < p.dim / V; c += 32) reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
-        } else {
-            for (int c = lane; c < p.dim; c += 32) dst[c] = Elem<O>::put(0.0f);
-        }
+        const float zero[V] = {};
+        for (int c = lane * V - p.phase.at<O>(row); c < p.dim; c += 32 * V) store_columns<O, V>(dst, c, p.dim, zero);
         return;
     }
     const unsigned b = blockIdx.x - z0;
@@ -352,97 +361,167 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
     const int tile = static_cast<int>(b % p.col_tiles);
     const long long c = static_cast<long long>(b / p.col_tiles) * ty + y;
     const bool real = c < p.chunks;
-    const int i0 = real ? static_cast<int>(c) * p.chunk : 0, n = real ? min(p.chunk, p.count - i0) : 0;
-    // keys with one neighbour on either side (-1 outside the list)
-    for (int q = x; q < n + 2; q += p.tx) {
-        const int i = i0 + q - 1;
-        s_key[y][q] = real && i >= 0 && i < p.count ? __ldg(p.keys + i) : -1;
+    const int chunk = p.chunk, i0 = real ? static_cast<int>(c) * chunk : 0, n = real ? min(chunk, p.count - i0) : 0;
+    // the keys from one chunk before to one after (-1 before the list, INT_MAX after it)
+    for (int q = x; q < 3 * chunk + 1; q += p.tx) {
+        const int i = i0 + q - chunk;
+        s_key[y][q] = i < 0 ? -1 : i < p.count ? __ldg(p.keys + i) : INT_MAX;
     }
-    for (int q = x; q < n; q += p.tx) s_row[y][q] = __ldg(p.order + i0 + q);
+    for (int q = x; q < 2 * chunk; q += p.tx)
+        if (i0 + q < p.count) s_row[y][q] = __ldg(p.order + i0 + q);
     __syncthreads();
     if (!real) return;
-    const int *key = s_key[y] + 1;
-    const int col0 = tile * p.tx * E * K + x * E;
-    if (col0 >= p.dim) return;
-    const T *src = static_cast<const T *>(p.dout) + col0;
+    const int *key = s_key[y] + chunk;  // key[r]: of position i0 + r
 
-    float acc[K][E];
+    // ---- which positions [p0, p1) are this chunk's
+    const int lane = threadIdx.x % 32, head = key[0], tail = key[n - 1];
+    int p0 = 0, p1 = n;
+    bool began = key[-1] == head;  // a long run's part that began in an earlier chunk
+    if (began) {
+        const int before = warp_count(key, -chunk, chunk, head, lane), here = warp_count(key, 0, chunk, head, lane);
+        if (before + here <= chunk && key[here] != head) {  // a short run of an earlier chunk
+            p0 = here;
+            began = false;
+        }
+    }
+    if (p0 < n && tail < p.vocab && key[n] == tail && !(began && tail == head)) {
+        const int here = warp_count(key, 0, n, tail, lane), after = warp_count(key, n, chunk, tail, lane);
+        if (here + after <= chunk) p1 = n + after;  // a short run: to its end
+        else if (tile == 0 && x == 0) p.runs[1 + atomicAdd(p.runs, 1)] = static_cast<int>(c);
+    }
+
+    const int vec = (tile * p.tx + x) * E;
+    if (vec >= p.pitch) return;
+    float acc[E];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int q0 = p0; q0 < p1; q0 += ROWS) {
+        if (key[q0] >= p.vocab) break;  // no tokens from here on
+        Shifted<T> v[ROWS];
+        uint4 old[ACCUMULATE ? ROWS : 1][ACCUMULATE ? E / V : 1];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[k][e] = 0.0f;
-    bool began = key[-1] == key[0];  // the run began in an earlier chunk
-    for (int q0 = 0; q0 < n; q0 += kRowsAtOnce) {
-        if (key[q0] == p.vocab) break;  // no tokens from here on
-        Access<T, E> v[kRowsAtOnce][K];
-#pragma unroll
-        for (int r = 0; r < kRowsAtOnce; ++r)
-            if (q0 + r < n && key[q0 + r] < p.vocab) {
-                const T *row = src + static_cast<long long>(s_row[y][q0 + r]) * p.ld_dout;
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (k == 0 || col0 + k * p.tx * E < p.dim) v[r][k].load(row + k * p.tx * E);
-            }
-#pragma unroll
-        for (int r = 0; r < kRowsAtOnce; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
             const int q = q0 + r;
-            if (q >= n || key[q] == p.vocab) break;
-            const bool ends = key[q + 1] != key[q], last = q == n - 1;
+            if (q >= p1 || key[q] >= p.vocab) continue;
+            const int col = ALIGNED ? vec : vec - p.phase.at<O>(key[q]);
+            if (col >= p.dim) continue;
+            const T *src = static_cast<const T *>(p.dout) + static_cast<long long>(s_row[y][q]) * p.ld_dout + col;
+            if (ALIGNED) v[r].a = __ldg(reinterpret_cast<const uint4 *>(src));
+            else v[r].load(src, p.lo, p.hi, col, p.dim);
+            if (ACCUMULATE && key[q + 1] != key[q] && col >= 0 && col + E <= p.dim) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const O *>(p.dtable) +
+                                                                  static_cast<long long>(key[q]) * p.ld_dtable + col);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float f[E];
-                v[r][k].get(f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[k][e] += f[e];
+                for (int h = 0; h < E / V; ++h) old[ACCUMULATE ? r : 0][ACCUMULATE ? h : 0] = at[h];
             }
-            if (!ends && !last) continue;
+        }
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int col = col0 + k * p.tx * E;
-                if (k > 0 && col >= p.dim) break;
-                if (ends && !began) {
-                    write_sum<O, E>(p, key[q], col, acc[k]);
-                } else {
-                    float *out = p.partial + (2 * c + (began ? 0 : 1)) * p.dim + col;
+        for (int r = 0; r < ROWS; ++r) {
+            const int q = q0 + r;
+            if (q >= p1 || key[q] >= p.vocab) break;
+            const int col = ALIGNED ? vec : vec - p.phase.at<O>(key[q]);
+            if (col < p.dim) {
+                float f[E];
+                widen_vec<T>(ALIGNED ? v[r].a : v[r].get(), f);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) out[e] = acc[k][e];
+                for (int e = 0; e < E; ++e) acc[e] += f[e];
+            }
+            const bool ends = key[q + 1] != key[q];
+            if (!ends && q != p1 - 1) continue;
+            if (ends && !began) {
+                O *dst = static_cast<O *>(p.dtable) + static_cast<long long>(key[q]) * p.ld_dtable;
+                float f[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[e] = acc[e] * p.scale;
+                if (ACCUMULATE) {
+                    if (col >= 0 && col + E <= p.dim) {
+#pragma unroll
+                        for (int h = 0; h < E / V; ++h) {
+                            float g[V];
+                            widen_vec<O>(old[ACCUMULATE ? r : 0][ACCUMULATE ? h : 0], g);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) f[h * V + e] += g[e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (col + e >= 0 && col + e < p.dim) f[e] += Elem<O>::get(dst[col + e]);
+                    }
                 }
+                store_columns<O, E>(dst, col, p.dim, f);
+            } else {
+                float *out = p.partial + (2 * c + (began ? 0 : 1)) * p.pitch + vec;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[k][e] = 0.0f;
+                for (int e = 0; e < E; e += 4) *reinterpret_cast<float4 *>(out + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
             }
             began = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = 0.0f;
         }
     }
 }
 
-// Runs that cross chunk borders: the chunk where such a run begins adds its
-// slot 1 and the following chunks' slots 0, in order.
+// Long runs: slot 1 of the chunk where one begins and the following chunks'
+// slots 0.  Eight thread rows take every eighth part each, and their sums are
+// added in order; four columns a thread.
 template <typename O>
 __global__ void __launch_bounds__(kSumThreads) embed_grad_join_kernel(const EmbedGradArgs p)
 {
-    const int c = blockIdx.x;
-    const int end = min((c + 1) * p.chunk, p.count);  // first position after the chunk
-    if (end >= p.count) return;
-    const int v = __ldg(p.keys + end - 1);
-    if (v == p.vocab || __ldg(p.keys + end) != v) return;            // its last run ends here
-    const int first = c * p.chunk;
-    if (first > 0 && __ldg(p.keys + first - 1) == v) return;         // and it began here
-    const int run_end = warp_lower_bound(p.keys, p.count, v + 1, threadIdx.x % 32);
-    const int chunks = (run_end - 1) / p.chunk - c;                  // chunks that follow
-    for (int col = blockIdx.y * kSumThreads + threadIdx.x; col < p.dim; col += gridDim.y * kSumThreads) {
-        const float *part = p.partial + 2ll * c * p.dim + col;
-        float s[1] = {part[p.dim]};
+    constexpr int ROWS = 8, COLS = kSumThreads / ROWS;
+    __shared__ float4 part_sum[ROWS][COLS];
+    const int x = threadIdx.x % COLS, y = threadIdx.x / COLS;
+    const int runs = __ldcg(p.runs);
+    for (int r = blockIdx.x; r < runs; r += gridDim.x) {
+        const int c = __ldcg(p.runs + 1 + r);
+        const int v = __ldg(p.keys + (c + 1ll) * p.chunk - 1);
+        const int run_end = warp_lower_bound(p.keys, p.count, v + 1, threadIdx.x % 32);
+        const int parts = (run_end - 1) / p.chunk - c + 1;
+        O *dst = static_cast<O *>(p.dtable) + static_cast<long long>(v) * p.ld_dtable;
+        const int shift = p.phase.at<O>(v);
+        for (int q0 = blockIdx.y * COLS * 4; q0 - shift < p.dim; q0 += gridDim.y * COLS * 4) {
+            const int q = q0 + 4 * x;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (q - shift < p.dim) {
+                const float *part = p.partial + 2ll * c * p.pitch + q;
 #pragma unroll 8
-        for (int k = 1; k <= chunks; ++k) s[0] += part[2ll * k * p.dim];
-        write_sum<O, 1>(p, v, col, s);
+                for (int k = y; k < parts; k += ROWS) {
+                    const float4 w = __ldcg(reinterpret_cast<const float4 *>(part + (k ? 2ll * k : 1ll) * p.pitch));
+                    s.x += w.x;
+                    s.y += w.y;
+                    s.z += w.z;
+                    s.w += w.w;
+                }
+            }
+            part_sum[y][x] = s;
+            __syncthreads();
+            if (y == 0) {
+                float f[4] = {};
+#pragma unroll
+                for (int k = 0; k < ROWS; ++k) {
+                    const float4 w = part_sum[k][x];
+                    f[0] += w.x;
+                    f[1] += w.y;
+                    f[2] += w.z;
+                    f[3] += w.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int col = q - shift + e;
+                    if (col < 0 || col >= p.dim) continue;
+                    const float old = p.accumulate ? Elem<O>::get(dst[col]) : 0.0f;
+                    dst[col] = Elem<O>::put(fmaf(f[e], p.scale, old));
+                }
+            }
+            __syncthreads();
+        }
     }
 }
 
 // Workspace: keys and order twice (the passes alternate), digit counts,
 // partial sums.
 struct GradLayout {
-    size_t keys[2], order[2], hist, partial, bytes;
-    int rounds, tiles, passes, digit, chunk, chunks;
+    size_t keys[2], order[2], hist, runs, partial, bytes;
+    int rounds, tiles, passes, digit, chunk, chunks, pitch;
 };
 GradLayout grad_layout(long long count, int vocab, int dim)
 {
@@ -453,7 +532,9 @@ GradLayout grad_layout(long long count, int vocab, int dim)
     l.digit = std::max(1, (bits + l.passes - 1) / l.passes);
     l.rounds = count <= 262144 ? 4 : 16;
     l.tiles = static_cast<int>((count + l.rounds * kSortThreads - 1) / (l.rounds * kSortThreads));
-    l.chunk = count * dim < (1ll << 24) ? 16 : kMaxChunk;
+    // chunks as long as leave a few hundred thousand threads (of eight columns)
+    l.chunk = kMaxChunk;
+    while (l.chunk > 16 && count * dim / 8 / l.chunk < 400000) l.chunk /= 2;
     l.chunks = static_cast<int>((count + l.chunk - 1) / l.chunk);
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -467,7 +548,9 @@ GradLayout grad_layout(long long count, int vocab, int dim)
         l.order[i] = take(static_cast<size_t>(count) * 4);
     }
     l.hist = take(rank ? 0 : static_cast<size_t>(l.tiles) * (1u << l.digit) * 4);
-    l.partial = take(static_cast<size_t>(l.chunks) * 2 * dim * 4);
+    l.runs = take((1 + static_cast<size_t>(l.chunks)) * 4);
+    l.pitch = dim / 8 * 8 + 16;  // whole vectors, and one more for a row's phase
+    l.partial = take(static_cast<size_t>(l.chunks) * 2 * l.pitch * 4);
     l.bytes = at;
     return l;
 }
@@ -484,31 +567,34 @@ void launch_sort_pass(const SortPass &p, cudaStream_t s)
     sort_place_kernel<ROUNDS><<<p.tiles, kSortThreads, 0, s>>>(p);
 }
 
-template <typename T, typename O, int E, int K>
+template <typename T, typename O>
 cudaError_t launch_sums(EmbedGradArgs a, cudaStream_t s)
 {
-    a.tx = 8;
-    while (a.tx < kSumThreads && a.tx * E * K < a.dim) a.tx *= 2;
-    a.col_tiles = (a.dim + a.tx * E * K - 1) / (a.tx * E * K);
+    constexpr int E = kPerVec<T>;
+    // every row of both matrices starts on 16 bytes
+    const bool aligned = a.dim % E == 0 && a.ld_dout % E == 0 && a.ld_dtable % kPerVec<O> == 0 && aligned_to(a.dout, 16) &&
+                         aligned_to(a.dtable, 16);
+    a.phase = Phase::of<O>(a.dtable, a.ld_dtable);
+    const int n = (a.dim + E - 1) / E + (aligned ? 0 : 1);  // vectors a row, at most
+    a.tx = 32;
+    while (a.tx < kSumThreads && a.tx < n) a.tx *= 2;
+    a.col_tiles = (n + a.tx - 1) / a.tx;
     const int ty = kSumThreads / a.tx;
     const long long sum = (a.chunks + ty - 1ll) / ty * a.col_tiles;
     const long long zero = a.accumulate ? 0 : (a.vocab + kSumThreads / 32 - 1ll) / (kSumThreads / 32);
     if (sum + zero >= (1ll << 31)) return cudaErrorInvalidConfiguration;
     a.sum_ctas = static_cast<unsigned>(sum);
     a.zero_ctas = static_cast<unsigned>(zero);
-    if (sum + zero > 0) embed_grad_kernel<T, O, E, K><<<a.sum_ctas + a.zero_ctas, kSumThreads, 0, s>>>(a);
+    const unsigned grid = a.sum_ctas + a.zero_ctas;
+    if (grid > 0) {
+        if (aligned && a.accumulate) embed_grad_kernel<T, O, true, true><<<grid, kSumThreads, 0, s>>>(a);
+        else if (aligned) embed_grad_kernel<T, O, true, false><<<grid, kSumThreads, 0, s>>>(a);
+        else if (a.accumulate) embed_grad_kernel<T, O, false, true><<<grid, kSumThreads, 0, s>>>(a);
+        else embed_grad_kernel<T, O, false, false><<<grid, kSumThreads, 0, s>>>(a);
+    }
     if (a.chunks > 1)
-        embed_grad_join_kernel<O><<<dim3(a.chunks, std::min(8, (a.dim + kSumThreads - 1) / kSumThreads)), kSumThreads, 0, s>>>(a);
+        embed_grad_join_kernel<O><<<dim3(std::min(a.chunks, 128), std::min(32, (a.pitch + 63) / 64)), kSumThreads, 0, s>>>(a);
     return cudaGetLastError();
-}
-
-template <typename T, typename O>
-cudaError_t launch_sums(const EmbedGradArgs &a, cudaStream_t s)
-{
-    // 16-byte accesses where every row of both matrices starts on 16 bytes
-    const bool vec = a.dim % kPerVec<T> == 0 && a.ld_dout % kPerVec<T> == 0 && a.ld_dtable % kPerVec<O> == 0 &&
-                     aligned_to(a.dout, 16) && aligned_to(a.dtable, 16);
-    return vec ? launch_sums<T, O, kPerVec<T>, 1>(a, s) : launch_sums<T, O, 1, 4>(a, s);
 }
 
 bool is_dtype(int d) { return d == CDG_F16 || d == CDG_BF16 || d == CDG_F32; }
@@ -536,11 +622,21 @@ int cdg_embed(const void *table, long long ld_table, const void *tokens, int ind
         return CDG_ERR_ALIAS;
     const int sms = sm_count();
     if (sms < 1) return CDG_ERR_CUDA;
-    const EmbedArgs a{table, tokens, out, ld_table, ld_out, count, index_bytes, vocab, 0, scale};
+    EmbedArgs a{};
+    a.table = table;
+    a.tokens = tokens;
+    a.out = out;
+    a.ld_table = ld_table;
+    a.ld_out = ld_out;
+    a.count = count;
+    a.index_bytes = index_bytes;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.scale = scale;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == CDG_F32) launch_embed<float>(a, dim, sms, s);
-    else if (dtype == CDG_F16) launch_embed<__half>(a, dim, sms, s);
-    else launch_embed<__nv_bfloat16>(a, dim, sms, s);
+    if (dtype == CDG_F32) launch_embed<float>(a, sms, s);
+    else if (dtype == CDG_F16) launch_embed<__half>(a, sms, s);
+    else launch_embed<__nv_bfloat16>(a, sms, s);
     return cudaGetLastError() == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
 }
 
@@ -571,7 +667,7 @@ int cdg_embed_grad(const void *dout, long long ld_dout, const void *tokens, int 
     char *ws = static_cast<char *>(workspace);
     const int *keys = reinterpret_cast<int *>(ws + l.keys[0]), *order = reinterpret_cast<int *>(ws + l.order[0]);
     SortPass p{tokens, nullptr, nullptr, reinterpret_cast<int *>(ws + l.keys[0]), reinterpret_cast<int *>(ws + l.order[0]),
-               reinterpret_cast<int *>(ws + l.hist), index_bytes, static_cast<int>(count), vocab, 0, 1 << l.digit, l.tiles};
+               reinterpret_cast<int *>(ws + l.hist), reinterpret_cast<int *>(ws + l.runs), index_bytes, static_cast<int>(count), vocab, 0, 1 << l.digit, l.tiles};
     if (count > 0 && count <= kRankMax) {
         sort_rank_kernel<<<static_cast<unsigned>((count + 31) / 32), kSortThreads, (count + 3) / 4 * 16, s>>>(p);
     } else if (count > 0) {
@@ -597,12 +693,16 @@ int cdg_embed_grad(const void *dout, long long ld_dout, const void *tokens, int 
     a.keys = keys;
     a.order = order;
     a.partial = reinterpret_cast<float *>(ws + l.partial);
+    a.runs = reinterpret_cast<int *>(ws + l.runs);
     a.count = static_cast<int>(count);
     a.vocab = vocab;
     a.dim = dim;
     a.accumulate = accumulate;
     a.chunk = l.chunk;
     a.chunks = l.chunks;
+    a.pitch = l.pitch;
+    a.lo = static_cast<const char *>(dout);
+    a.hi = a.lo + matrix_bytes(count, dim, ld_dout, es);
     a.scale = scale;
     const cudaError_t e = dtype == CDG_F32   ? launch_sums<float, float>(a, s)
                           : dtype == CDG_F16 ? (out_f32 ? launch_sums<__half, float>(a, s) : launch_sums<__half, __half>(a, s))

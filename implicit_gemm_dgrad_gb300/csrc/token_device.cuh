@@ -105,6 +105,52 @@ __device__ __forceinline__ int token_at(const void *tokens, int index_bytes, lon
     return t >= 0 && t < vocab ? static_cast<int>(t) : -1;
 }
 
+// One vector of T read from any element address: the two aligned 16-byte
+// blocks that hold it, joined by get().  [lo, hi) is the tensor; blocks that
+// reach past it are read element by element, and of those only columns
+// [0, cols) of the row, `col` being the vector's first (it may begin before the
+// row or end after it; what lies there is any value).
+template <typename T>
+struct Shifted {
+    uint4 a, b;
+    uint32_t sh;  // bytes into a
+    __device__ __forceinline__ void load(const T *p, const char *lo, const char *hi, int col, int cols)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        sh = static_cast<uint32_t>(at) & 15u;
+        const uintptr_t block = at - sh, end = block + (sh ? 32 : 16);
+        if (block >= reinterpret_cast<uintptr_t>(lo) && end <= reinterpret_cast<uintptr_t>(hi)) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(block);
+            a = __ldg(q);
+            b = __ldg(q + (sh ? 1 : 0));
+        } else {
+            float f[kPerVec<T>];
+#pragma unroll
+            for (int e = 0; e < kPerVec<T>; ++e) f[e] = col + e >= 0 && col + e < cols ? Elem<T>::get(p[e]) : 0.0f;
+            a = narrow_vec<T>(f);  // exact: the values are T's
+            sh = 0;
+        }
+    }
+    __device__ __forceinline__ uint4 get() const
+    {
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (sh & 8u) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (sh & 4u) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t bits = (sh & 2u) * 8u;
+            return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                              __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
 // ---------------------------------------------------------------- host side
 static inline int dtype_bytes(int dtype) { return dtype == CDG_F32 ? 4 : 2; }
 
