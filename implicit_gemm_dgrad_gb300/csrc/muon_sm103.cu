@@ -954,7 +954,6 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
     tc_fence_after();
     const uint32_t tmem = *slot;
     const Ctl ctl{abort_flag, p.status};
-    const bool leader = warp == 0 && elect_one_sync();
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // this thread's chunks of 16 columns: from 16 group, and 64 + 16 group
     const bool rows = (warp & 3) * 32 < used;  // warp-uniform
@@ -1011,19 +1010,21 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += y[e];
     };
-    // accumulator d <- X Y: low x high, high x low, high x high
+    // accumulator d <- X Y: low x high, high x low, high x high; by one lane of the first warp
     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(used >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+    const int ksteps = used / 16;
     auto multiply = [&](uint32_t d, uint32_t x, uint32_t y) {
-        uint32_t more = 0;
+        const uint32_t acc = tmem + 128 * d;
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
-            for (int k = 0; k < used; k += 16) {
-                const uint32_t s = k / 64, q = k % 64 / 16;
-                const uint64_t ad = sdesc_k128_sw128(x + (2u * (part == 0) + s) * CMU_HALF_BYTES);
-                const uint64_t bd = sdesc_k128_sw128(y + (2u * (part == 1) + s) * CMU_HALF_BYTES);
-                umma_f16(tmem + 128 * d, ad + 2u * q, bd + 2u * q, idesc, more);
-                more = 1;
+        for (int part = 0; part < 3; ++part) {
+            const uint64_t ad = sdesc_k128_sw128(x + (part == 0 ? 2u * CMU_HALF_BYTES : 0u));
+            const uint64_t bd = sdesc_k128_sw128(y + (part == 1 ? 2u * CMU_HALF_BYTES : 0u));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t step = (k / 4) * (CMU_HALF_BYTES >> 4) + (k % 4) * 2u;  // descriptor units
+                if (k < ksteps) umma_f16(acc, ad + step, bd + step, idesc, (part | k) != 0);
             }
+        }
         umma_commit(bar0 + 8 * d);
     };
     // everything written to shared memory is seen by the products issued next
@@ -1084,8 +1085,10 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
     bool ok = true;
     for (int k = 0; k < p.steps; ++k) {
         // Q = a I + b A + c A A
-        if (leader) multiply(0, mA, mA);
-        __syncwarp();
+        if (warp == 0) {
+            if (elect_one_sync()) multiply(0, mA, mA);
+            __syncwarp();
+        }
         if (!(ok = wait(0))) break;
         store(0, p.c * kInv, mQ, [&](float *v, int s, int q) {
             float x[8];
@@ -1103,17 +1106,21 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
         });
         ready();
         const bool last = k == p.steps - 1;
-        if (leader) {
-            if (!last) multiply(0, mQ, mA);
-            if (k > 0) multiply(1, mQ, mP);
+        if (warp == 0) {
+            if (elect_one_sync()) {
+                if (!last) multiply(0, mQ, mA);
+                if (k > 0) multiply(1, mQ, mP);
+            }
+            __syncwarp();
         }
-        __syncwarp();
         if (!last) {  // T = Q A, in A's place
             if (!(ok = wait(0))) break;
             store(0, kInv, mA, nothing);
             ready();
-            if (leader) multiply(0, mA, mQ);  // A <- T Q
-            __syncwarp();
+            if (warp == 0) {
+                if (elect_one_sync()) multiply(0, mA, mQ);  // A <- T Q
+                __syncwarp();
+            }
         }
         if (k > 0) {  // P <- Q P
             if (!(ok = wait(1))) break;
