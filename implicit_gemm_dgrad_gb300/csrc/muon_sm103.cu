@@ -300,8 +300,11 @@ struct Tile {
 template <int FORM>
 struct Layout {
     static constexpr bool kPair = FORM == CMU_PAIR;
-    static constexpr int kGroups = kPair ? 2 : 1;            // of epilogue warps, 128 columns each (NARROW: 64)
-    static constexpr int kThreads = 128 + 128 * kGroups;
+    // Eight epilogue warps: in two groups that take 64-column chunks of their own halves of the tile (PAIR), or all
+    // eight on one chunk after the other.
+    static constexpr int kGroups = kPair ? 2 : 1;
+    static constexpr int kThreads = 128 + 256, kGroupThreads = 256 / kGroups;
+    static constexpr int kOwn = 64 * 128 / kGroupThreads;    // columns of a chunk a thread holds
     static constexpr int kTileM = kPair ? 256 : 128, kTileN = kPair ? 256 : FORM == CMU_SQUARE ? 128 : 64;
     static constexpr int kCols = kTileN;                     // TMEM columns an accumulator
     static constexpr uint32_t kBBytes = FORM == CMU_NARROW ? CMU_HALF_BYTES / 2 : CMU_HALF_BYTES;
@@ -323,37 +326,40 @@ struct Layout {
     static constexpr int kWords = 8 * (2 * CMU_STAGES + 2 + 2 + 1 + kGroups);  // after the mbarriers
 };
 
-// Epilogue of one group of four warps: thread = row of the CTA's 128, 64
-// columns at a time.
+// Epilogue of one group of warps: a thread holds kOwn columns of one of the
+// CTA's 128 rows, of 64 columns at a time.
 template <int FORM>
 struct Epilogue {
+    using Lay = Layout<FORM>;
+    static constexpr int OWN = Lay::kOwn, PIECES = OWN / 8;
     const CmuGemm &p;
-    const Layout<FORM> &L;
+    const Lay &L;
     Ctl ctl;
-    int group, warp_in_group, lane, row;  // row: of the CTA's 128
+    int group, quad, part, lane, row;  // row: of the CTA's 128; part: which of its columns in a chunk
     bool elected, sym;
     uint32_t buf0, buf1, bar, phase, sw;
 
-    __device__ __forceinline__ Epilogue(const CmuGemm &p_, const Layout<FORM> &L_, Ctl c, bool sym_)
-        : p(p_), L(L_), ctl(c), sym(sym_)
+    __device__ __forceinline__ Epilogue(const CmuGemm &p_, const Lay &L_, Ctl c, bool sym_) : p(p_), L(L_), ctl(c), sym(sym_)
     {
         const int warp = threadIdx.x / 32 - CDG_EPI_WARP0;
         lane = threadIdx.x % 32;
-        group = warp / 4;
-        warp_in_group = warp % 4;
-        row = warp_in_group * 32 + lane;
-        elected = elect_one_sync() && warp_in_group == 0;
+        group = Lay::kGroups == 2 ? warp / 4 : 0;
+        part = Lay::kGroups == 2 ? 0 : warp / 4;
+        quad = warp % 4;
+        row = quad * 32 + lane;
+        elected = elect_one_sync() && quad == 0 && part == 0;
         buf0 = L.staging + group * CMU_STAGING_BYTES;
         buf1 = buf0 + CMU_HALF_BYTES;
         bar = L.epi0 + 8u * group;
         phase = 0;
         sw = row & 7;
     }
-    __device__ __forceinline__ void sync() const { named_bar_sync(1 + group, 128); }
-    // 16-byte piece q (8 columns) of this thread's row in a staging buffer
+    __device__ __forceinline__ void sync() const { named_bar_sync(1 + group, Lay::kGroupThreads); }
+    __device__ __forceinline__ bool any(bool x) const { return named_bar_red_or(1 + group, Lay::kGroupThreads, x); }
+    // this thread's q-th 16-byte piece (8 columns) of its row in a staging buffer
     __device__ __forceinline__ uint32_t piece(uint32_t buf, int q) const
     {
-        return buf + static_cast<uint32_t>(row) * 128u + ((static_cast<uint32_t>(q) ^ sw) << 4);
+        return buf + static_cast<uint32_t>(row) * 128u + ((static_cast<uint32_t>(part * PIECES + q) ^ sw) << 4);
     }
     // The block of the epilogue's input that a later chunk() needs.
     __device__ __forceinline__ void fetch(int b, int i0, int j0) const
@@ -371,7 +377,7 @@ struct Epilogue {
     {
         const bool ok = wait_bar(bar, phase, ctl);
         phase ^= 1u;
-        return !named_bar_red_or(1 + group, 128, !ok);
+        return !any(!ok);
     }
     // Eight values of the input block: high parts, and low parts where there are any.
     __device__ __forceinline__ void input(int q, bool lo, float (&x)[8]) const
@@ -387,54 +393,60 @@ struct Epilogue {
             for (int e = 0; e < 8; ++e) x[e] += y[e];
         }
     }
-    __device__ __forceinline__ void put(uint32_t buf, int q, const float (&x)[8]) const
+    // Eight values rounded to fp16 into a staging buffer; x becomes what the rounding left.
+    __device__ __forceinline__ void put(uint32_t buf, int q, float (&x)[8]) const
     {
-        const uint4 w = narrow_vec<__half>(x);
-        st_shared_v4(piece(buf, q), w.x, w.y, w.z, w.w);
-    }
-    __device__ __forceinline__ static void low_part(float (&x)[8])
-    {
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] -= __half2float(__float2half_rn(x[e]));
+        for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+            const float2 f = __half22float2(h);
+            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+            x[2 * e] -= f.x;
+            x[2 * e + 1] -= f.y;
+        }
+        st_shared_v4(piece(buf, q), w[0], w[1], w[2], w[3]);
     }
 
-    // v: the sums of columns [j0, j0 + 64) of row i0 + row; j0 < N and i0 < M.
-    // False when the launch is giving up.
-    __device__ __forceinline__ bool chunk(int b, int i0, int j0, bool mirror, float xs, float (&v)[64])
+    // v: this thread's sums of the chunk of columns [j0, j0 + 64), row i0 + row;
+    // j0 < N and i0 < M.  False when the launch is giving up.
+    __device__ __forceinline__ bool chunk(int b, int i0, int j0, bool mirror, float xs, float (&v)[OWN])
     {
-        const int i = i0 + row;
+        const int i = i0 + row, mine = j0 + part * OWN;  // this thread's first column
         if (p.mode == CMU_GRAM) {
             const float f = (CMU_SCALE / xs) / xs;
 #pragma unroll
-            for (int q = 0; q < 64; ++q) v[q] *= f;
+            for (int q = 0; q < OWN; ++q) v[q] *= f;
             symmetric(b, i0, j0, mirror, v);
             return true;
         }
         if (!fetched()) return false;
         if (p.mode == CMU_POLY) {
-            float d = 0.0f;
+            const float g = p.c * (1.0f / CMU_SCALE);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < PIECES; ++q) {
                 float a[8];
                 input(q, p.parts == 3, a);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float &x = v[8 * q + e];
-                    x = fmaf(p.b, a[e], p.c * (x * (1.0f / CMU_SCALE)));
-                    if (j0 + 8 * q + e == i) {
-                        d = x;
-                        x = 0.0f;
-                    }
-                }
+                for (int e = 0; e < 8; ++e) v[8 * q + e] = fmaf(p.b, a[e], g * v[8 * q + e]);
             }
-            if (i >= j0 && i < j0 + 64 && i < p.M) p.diag[static_cast<long long>(b) * p.M + i] = d * (1.0f / CMU_SCALE);
+            if (i >= mine && i < mine + OWN && i < p.M) {  // the diagonal, apart
+                float d = 0.0f;
+#pragma unroll
+                for (int q = 0; q < OWN; ++q)
+                    if (mine + q == i) {
+                        d = v[q];
+                        v[q] = 0.0f;
+                    }
+                p.diag[static_cast<long long>(b) * p.M + i] = d * (1.0f / CMU_SCALE);
+            }
             symmetric(b, i0, j0, mirror, v);
             return true;
         }
         const float f = 1.0f / xs, g = f / p.poly_scale;
         const float lin = (p.a + (i < p.M ? p.diag[static_cast<long long>(b) * p.M + i] : 0.0f)) * f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < PIECES; ++q) {
             float x[8];
             input(q, p.has_lo, x);
 #pragma unroll
@@ -443,7 +455,6 @@ struct Epilogue {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = v[8 * q + e] * CMU_SCALE;
                 put(buf0, q, x);
-                low_part(x);
                 put(buf1, q, x);
             }
         }
@@ -455,81 +466,103 @@ struct Epilogue {
                 tma_store_3d(reinterpret_cast<uint64_t>(&p.tmY[1]), buf1, j0, i0, b);
                 bulk_commit_group();
             }
+            __syncwarp();
         } else {
-            result(b, i0, j0, v);
+            if (p.w_in) result<float, true>(b, i0, j0, v);
+            else if (p.out_type == CDG_T_F32) result<float, false>(b, i0, j0, v);
+            else if (p.out_type == CDG_T_BF16) result<__nv_bfloat16, false>(b, i0, j0, v);
+            else result<__half, false>(b, i0, j0, v);
+            __syncwarp();
             fence_proxy_async_smem();  // the block has been read: the next fetch may overwrite it
             sync();
         }
         return true;
     }
     // A block of A or B and, off the diagonal, its transpose; high parts, then low parts.
-    __device__ __forceinline__ void symmetric(int b, int i0, int j0, bool mirror, float (&v)[64]) const
+    __device__ __forceinline__ void symmetric(int b, int i0, int j0, bool mirror, float (&v)[OWN]) const
     {
-        for (int part = 0; part < (p.parts == 3 ? 2 : 1); ++part) {
+        for (int half = 0; half < (p.parts == 3 ? 2 : 1); ++half) {
             if (elected) bulk_wait_group_read<0>();
             sync();
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < PIECES; ++q) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = v[8 * q + e];
-                put(buf0, q, x);
                 if (mirror) {
                     // column j of this row -> row j, column `row` of two 64-column blocks
                     const uint32_t at = buf1 + static_cast<uint32_t>(row / 64) * 8192u + (row & 7) * 2u;
                     const uint32_t c = (row & 63) >> 3;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) st_shared_u16(at + (8 * q + e) * 128u + ((c ^ e) << 4), to_half_bits(x[e]));
+                    for (int e = 0; e < 8; ++e)
+                        st_shared_u16(at + (part * OWN + 8 * q + e) * 128u + ((c ^ e) << 4), to_half_bits(x[e]));
                 }
-                low_part(x);
+                put(buf0, q, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[8 * q + e] = x[e];
             }
             fence_proxy_async_smem();
             sync();
             if (elected) {
-                tma_store_3d(reinterpret_cast<uint64_t>(&p.tmY[part]), buf0, j0, i0, b);
+                tma_store_3d(reinterpret_cast<uint64_t>(&p.tmY[half]), buf0, j0, i0, b);
                 if (mirror) {
-                    tma_store_3d(reinterpret_cast<uint64_t>(&p.tmT[part]), buf1, i0, j0, b);
-                    if (i0 + 64 < p.M) tma_store_3d(reinterpret_cast<uint64_t>(&p.tmT[part]), buf1 + 8192u, i0 + 64, j0, b);
+                    tma_store_3d(reinterpret_cast<uint64_t>(&p.tmT[half]), buf1, i0, j0, b);
+                    if (i0 + 64 < p.M) tma_store_3d(reinterpret_cast<uint64_t>(&p.tmT[half]), buf1 + 8192u, i0 + 64, j0, b);
                 }
                 bulk_commit_group();
             }
+            __syncwarp();
         }
     }
-    __device__ __forceinline__ void write(long long o, float y) const
-    {
-        if (p.w_in) static_cast<float *>(p.out)[o] = fmaf(p.w_keep, p.w_in[o], -p.w_step * y);
-        else if (p.out_type == CDG_T_F32) static_cast<float *>(p.out)[o] = y;
-        else if (p.out_type == CDG_T_BF16) static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(y);
-        else static_cast<__half *>(p.out)[o] = __float2half_rn(y);
-    }
-    // O or W: lanes along the output's rows either way.
-    __device__ __forceinline__ void result(int b, int i0, int j0, const float (&v)[64]) const
+    // O or (STEP) W, lanes along the output's rows either way: eight elements'
+    // loads and stores at a time.
+    template <typename O, bool STEP>
+    __device__ __forceinline__ void result(int b, int i0, int j0, const float (&v)[OWN]) const
     {
         const long long base = static_cast<long long>(b) * p.rows * p.cols;
-        const int n = min(64, p.N - j0);
+        O *const out = static_cast<O *>(p.out) + base;
+        const float *const w_in = STEP ? p.w_in + base : nullptr;
+        const int mine = j0 + part * OWN, n = min(OWN, p.N - mine);
         if (p.transposed) {
             const int i = i0 + row;
-            if (i < p.M) {
-                const long long at = base + static_cast<long long>(j0) * p.cols + i;
+            if (i >= p.M) return;
 #pragma unroll
-                for (int q = 0; q < 64; ++q)
-                    if (q < n) write(at + static_cast<long long>(q) * p.cols, v[q]);
+            for (int q0 = 0; q0 < OWN; q0 += 8) {
+                float w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (STEP && q0 + e < n) w[e] = w_in[static_cast<long long>(mine + q0 + e) * p.cols + i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (q0 + e < n)
+                        out[static_cast<long long>(mine + q0 + e) * p.cols + i] =
+                            Elem<O>::put(STEP ? fmaf(p.w_keep, w[e], -p.w_step * v[q0 + e]) : v[q0 + e]);
             }
             return;
         }
-        // through the staging: a warp's 32 rows x 64 columns of fp32, column c of row r at (c + r) % 64
+        // through the staging: this warp's 32 rows x OWN columns of fp32, column c of row r at (c + r) % OWN
         sync();  // every row's input has been read
-        const uint32_t w0 = buf0 + warp_in_group * 8192u;
+        const uint32_t w0 = buf0 + static_cast<uint32_t>(part * 4 + quad) * (32u * OWN * 4u);
 #pragma unroll
-        for (int q = 0; q < 64; ++q) st_shared_f32(w0 + lane * 256u + ((q + lane) & 63) * 4u, v[q]);
+        for (int q = 0; q < OWN; ++q) st_shared_f32(w0 + lane * (OWN * 4u) + ((q + lane) & (OWN - 1)) * 4u, v[q]);
         __syncwarp();
-        const int r0 = i0 + warp_in_group * 32, rows = min(32, p.M - r0);
-        long long at = base + static_cast<long long>(r0) * p.cols + j0 + lane;
-        for (int r = 0; r < rows; ++r, at += p.cols) {
-            if (lane < n) write(at, ld_shared_f32(w0 + r * 256u + ((lane + r) & 63) * 4u));
-            if (lane + 32 < n) write(at + 32, ld_shared_f32(w0 + r * 256u + ((lane + 32 + r) & 63) * 4u));
+        const int r0 = i0 + quad * 32, rows = min(32, p.M - r0);
+        for (int c0 = 0; c0 < OWN; c0 += 32) {
+            const int c = c0 + lane;
+            const long long at = static_cast<long long>(r0) * p.cols + mine + c;
+            for (int r = 0; r < rows; r += 8) {
+                float y[8], w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = ld_shared_f32(w0 + (r + e) * (OWN * 4u) + ((c + r + e) & (OWN - 1)) * 4u);
+                    if (STEP && r + e < rows && c < n) w[e] = w_in[at + static_cast<long long>(r + e) * p.cols];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (r + e < rows && c < n)
+                        out[at + static_cast<long long>(r + e) * p.cols] =
+                            Elem<O>::put(STEP ? fmaf(p.w_keep, w[e], -p.w_step * y[e]) : y[e]);
+            }
         }
     }
 
@@ -540,11 +573,12 @@ struct Epilogue {
     }
 };
 
-__device__ __forceinline__ void tmem_ld_64(uint32_t at, float (&v)[64])
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[N])
 {
-    uint32_t (&r)[64] = reinterpret_cast<uint32_t(&)[64]>(v);
+    uint32_t (&r)[N] = reinterpret_cast<uint32_t(&)[N]>(v);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x16(at + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * q]));
+    for (int q = 0; q < N / 16; ++q) tmem_ld_32x32b_x16(at + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * q]));
     tmem_ld_wait();
 }
 
@@ -594,7 +628,7 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(L.acc_full0 + 8u * a, 1);
-            mbar_init(L.acc_empty0 + 8u * a, PAIR ? 16 : 4);  // one arrival per epilogue warp (of both CTAs)
+            mbar_init(L.acc_empty0 + 8u * a, PAIR ? 16 : 8);  // one arrival per epilogue warp (of both CTAs)
         }
         mbar_init(L.drain, 1);
         for (int g = 0; g < Lay::kGroups; ++g) mbar_init(L.epi0 + 8u * g, 1);
@@ -721,7 +755,8 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
         wait_bar(L.drain, 0, Ctl{&no_abort, p.status});
     } else if (warp >= CDG_EPI_WARP0) {
         Epilogue<FORM> e(p, L, ctl, sym);
-        const uint32_t lane_base = static_cast<uint32_t>(e.warp_in_group * 32) << 16;
+        constexpr int OWN = Lay::kOwn;
+        const uint32_t lane_base = (static_cast<uint32_t>(e.quad * 32) << 16) + e.part * OWN;
         uint32_t link = 0;
         bool ok = true;
         auto hand_back = [&](uint32_t acc) {
@@ -743,12 +778,12 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
             if constexpr (PAIR) {
                 const uint32_t acc = link & 1u;
                 ok = wait_bar(L.acc_full0 + 8u * acc, (link >> 1) & 1u, ctl);
-                if (named_bar_red_or(1 + e.group, 128, !ok)) break;
+                if (e.any(!ok)) break;
                 ++link;
                 tc_fence_after();
                 for (int c = 0; c < n; ++c) {
-                    float v[64];
-                    tmem_ld_64(tmem + acc * Lay::kCols + e.group * 128 + c * 64 + lane_base, v);
+                    float v[OWN];
+                    tmem_ld(tmem + acc * Lay::kCols + e.group * 128 + c * 64 + lane_base, v);
                     if (c == n - 1) hand_back(acc);
                     if (!(ok = e.chunk(tile.b, i0, j0 + 64 * c, mirror, xs, v))) break;
                     if (c + 1 < n && fetches) e.fetch(tile.b, i0, j0 + 64 * (c + 1));
@@ -756,7 +791,7 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
                 if (n == 0) hand_back(acc);
             } else {
                 constexpr int CHUNKS = Lay::kTileN / 64;
-                float sum[CHUNKS][64];
+                float sum[CHUNKS][OWN];
                 const int links = (p.parts * tile.kn - 1) / chain + 1;
                 for (int k = 0; ok && k < links; ++k, ++link) {
                     const uint32_t acc = link & 1u;
@@ -764,27 +799,26 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < 4 * CHUNKS; ++c) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(tmem + acc * Lay::kCols + c * 16 + lane_base, r);
-                        tmem_ld_wait();
+                    for (int c = 0; c < CHUNKS; ++c) {
+                        float v[OWN];
+                        tmem_ld(tmem + acc * Lay::kCols + c * 64 + lane_base, v);
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            float &x = sum[c / 4][c % 4 * 16 + q];
-                            x = k ? x + __uint_as_float(r[q]) : __uint_as_float(r[q]);
-                        }
+                        for (int q = 0; q < OWN; ++q) sum[c][q] = k ? sum[c][q] + v[q] : v[q];
                     }
                     hand_back(acc);
                 }
-                if (named_bar_red_or(1, 128, !ok)) break;
+                if (e.any(!ok)) {
+                    ok = false;
+                    break;
+                }
                 if (NARROW && p.split > 1) {
-                    // the other CTAs' sums in their ring (all of it read: the range is done), columns 4 c .. + 3 of row r
-                    // in 16-byte piece (c + r) % 16; the first CTA adds them in rank order
-                    const uint32_t own = e.row * 256u;
+                    // the other CTAs' sums in their ring (all of it read: the range is done), four columns in a 16-byte
+                    // piece, piece c of row r at (c + r) % 8 of the thread's eight; the first CTA adds them in rank order
+                    const uint32_t own = (e.part * 128 + e.row) * (OWN * 4u);
                     if (rank) {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            st_shared_v4(L.s0 + own + ((c + e.lane) & 15) * 16u, __float_as_uint(sum[0][4 * c]),
+                        for (int c = 0; c < OWN / 4; ++c)
+                            st_shared_v4(L.s0 + own + ((c + e.lane) % (OWN / 4)) * 16u, __float_as_uint(sum[0][4 * c]),
                                          __float_as_uint(sum[0][4 * c + 1]), __float_as_uint(sum[0][4 * c + 2]),
                                          __float_as_uint(sum[0][4 * c + 3]));
                     }
@@ -795,20 +829,15 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
                     if (rank == 0 && n > 0) {
                         for (int r = 1; r < p.split; ++r) {
                             const uint32_t at = mapa_shared(L.s0, r) + own;
-                            // all loads of a half before its additions: a load takes hundreds of cycles
+                            float4 x[OWN / 4];  // all loads before the additions: a load takes hundreds of cycles
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float4 x[8];
+                            for (int c = 0; c < OWN / 4; ++c) x[c] = ld_cluster_f32x4(at + ((c + e.lane) % (OWN / 4)) * 16u);
 #pragma unroll
-                                for (int c = 0; c < 8; ++c) x[c] = ld_cluster_f32x4(at + ((8 * h + c + e.lane) & 15) * 16u);
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    float *y = sum[0] + 32 * h + 4 * c;
-                                    y[0] += x[c].x;
-                                    y[1] += x[c].y;
-                                    y[2] += x[c].z;
-                                    y[3] += x[c].w;
-                                }
+                            for (int c = 0; c < OWN / 4; ++c) {
+                                sum[0][4 * c] += x[c].x;
+                                sum[0][4 * c + 1] += x[c].y;
+                                sum[0][4 * c + 2] += x[c].z;
+                                sum[0][4 * c + 3] += x[c].w;
                             }
                         }
                     }
@@ -818,11 +847,14 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
                     float *out = p.partial + static_cast<long long>(t) * (CMU_SIDE * CMU_SIDE) + e.row * CMU_SIDE;
                     if (e.row < p.M)
 #pragma unroll
-                        for (int q = 0; q < 128; q += 4)
-                            if (q < p.N)
-                                *reinterpret_cast<float4 *>(out + q) =
-                                    make_float4(sum[q / 64 % CHUNKS][q % 64], sum[q / 64 % CHUNKS][q % 64 + 1],
-                                                sum[q / 64 % CHUNKS][q % 64 + 2], sum[q / 64 % CHUNKS][q % 64 + 3]);
+                        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+                            for (int q = 0; q < OWN; q += 4) {
+                                const int col = 64 * c + e.part * OWN + q;
+                                if (col < p.N)
+                                    *reinterpret_cast<float4 *>(out + col) =
+                                        make_float4(sum[c][q], sum[c][q + 1], sum[c][q + 2], sum[c][q + 3]);
+                            }
                     __syncwarp();
                     continue;
                 }
