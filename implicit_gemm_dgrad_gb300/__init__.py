@@ -752,8 +752,8 @@ def embed_grad(dout, tokens, dtable, workspace, count: int, vocab: int, dim: int
 
 
 class MuonInfo(ctypes.Structure):
-    _fields_ = [("m", ctypes.c_int), ("n", ctypes.c_int), ("transposed", ctypes.c_int), ("tile_m", ctypes.c_int),
-                ("tile_n", ctypes.c_int), ("gram", ctypes.c_int), ("launches", ctypes.c_int)]
+    _fields_ = [("m", ctypes.c_int), ("n", ctypes.c_int), ("transposed", ctypes.c_int),
+                ("gram", ctypes.c_int), ("launches", ctypes.c_int)]
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}

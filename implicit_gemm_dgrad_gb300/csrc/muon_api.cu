@@ -60,8 +60,10 @@ Bounds iteration_bounds(int steps, double a, double b, double c)
     return ok;
 }
 
-// From this smaller side one-part products run in CTA pairs on 256 x 256 tiles.
-constexpr int kPairSide = 1024;
+// Cycles a block of K takes a 256 x 256 tile of a CTA pair and a 128 x 128 tile
+// of one CTA (measured: the one near the tensor cores' rate, the other at the 64
+// bytes a cycle an SM loads).
+constexpr int kPairCycles = 630, kSquareCycles = 512;
 // Ranges of K the Gram form's X X^T is cut into, at most.
 constexpr int kMaxSplits = 8;
 // Blocks of K a split tile's CTA takes at least (512 x 4608: 207 us with 4, 196 us with
@@ -141,7 +143,6 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     h->info.n = n;
     h->info.transposed = h->transposed;
     const bool precise = dtype == CDG_F32;
-    h->info.tile_m = h->info.tile_n = !precise && m >= kPairSide ? 256 : 128;
     h->info.gram = h->gram && !precise;
     h->info.launches = h->info.gram ? 5 : 2 + 3 * steps;
     if (!host_only) {
@@ -192,18 +193,26 @@ int encode_maps(cdg_muon_st *h, void *workspace)
 
 // The products after the norm and the first X; the last one writes `out`.
 // The form of a product of M x N outputs over K (maps of 128-row and of 64-row
-// boxes of the B operand for both): pairs where the matrix is large; else square
-// tiles, or narrow ones where square tiles would occupy at most half of the SMs,
-// and then with K split until all SMs work or a range is down to kMinRange blocks.
-void choose_form(CmuGemm &g, bool pair, int sms, const CUtensorMap *b128, const CUtensorMap *b64)
+// boxes of the B operand for both): of CTA pairs and square tiles the one whose
+// waves take fewer cycles (2048 x 2048 all in pairs: 303 us, in squares: 282;
+// 3000 x 3000: 724 and 876), and narrow tiles where square ones would occupy at
+// most half of the SMs, with K split until all SMs work or a range is down to
+// kMinRange blocks.
+void choose_form(CmuGemm &g, bool precise, int sms, const CUtensorMap *b128, const CUtensorMap *b64)
 {
     const bool sym = g.mode <= CMU_POLY;
-    const long long tm = (g.M + 127) / 128, tn = (g.N + 127) / 128, tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
-    g.form = pair ? CMU_PAIR : 2 * tiles <= sms ? CMU_NARROW : CMU_SQUARE;
+    auto tiles = [&](int side) {
+        const long long tm = (g.M + side - 1) / side, tn = (g.N + side - 1) / side;
+        return (sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
+    };
+    const long long t128 = tiles(128), t256 = tiles(256);
+    const long long waves128 = (t128 + sms - 1) / sms, waves256 = (t256 + sms / 2 - 1) / std::max(1, sms / 2);
+    const bool pair = !precise && sms >= 2 && waves256 * kPairCycles < waves128 * kSquareCycles;
+    g.form = pair ? CMU_PAIR : 2 * t128 <= sms ? CMU_NARROW : CMU_SQUARE;
     g.split = 1;
     const int blocks = (g.K + CMU_BK - 1) / CMU_BK;
     if (g.form == CMU_NARROW)
-        while (g.split < 8 && 2 * tiles * g.split * 2 <= sms && blocks / (2 * g.split) >= kMinRange) g.split *= 2;
+        while (g.split < 8 && 2 * t128 * g.split * 2 <= sms && blocks / (2 * g.split) >= kMinRange) g.split *= 2;
     for (int q = 0; q < 2; ++q) g.tmB[q] = g.form == CMU_NARROW ? b64[q] : b128[q];
 }
 
@@ -238,7 +247,6 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
     g.batch = h->batch;
     g.xs = p.xs;
     g.parts = parts;
-    const bool pair = parts == 1 && h->m >= kPairSide;
     g.poly_scale = CMU_SCALE;
     g.diag = reinterpret_cast<float *>(ws + h->diag);
     g.a = h->a; g.b = h->b; g.c = h->c;
@@ -272,7 +280,7 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
         g.N = h->n;
         g.K = h->m;
         for (int q = 0; q < 2; ++q) g.tmA[q] = h->poly_rows[q];
-        choose_form(g, false, h->sms, h->x_cols[0], h->x_cols[0]);
+        choose_form(g, true, h->sms, h->x_cols[0], h->x_cols[0]);
         return cmu_launch_gemm(g, h->sms, s) == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
     }
     for (int k = 0; k < h->steps; ++k) {
@@ -287,7 +295,7 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
             g.tmY[q] = h->mat_rows[q];
             g.tmT[q] = h->mat_cols[q];
         }
-        choose_form(g, pair, h->sms, h->x_rows[cur], h->x_cols[cur]);
+        choose_form(g, parts != 1, h->sms, h->x_rows[cur], h->x_cols[cur]);
         if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
         g.mode = CMU_POLY;
         g.K = h->m;
@@ -296,7 +304,7 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
             g.tmY[q] = h->poly_rows[q];
             g.tmT[q] = h->poly_cols[q];
         }
-        choose_form(g, pair, h->sms, h->mat_rows, h->mat_cols);
+        choose_form(g, parts != 1, h->sms, h->mat_rows, h->mat_cols);
         if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
         g.mode = k == h->steps - 1 ? CMU_FINAL : CMU_UPDATE;
         g.N = h->n;
@@ -305,7 +313,7 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
             g.tmE[q] = h->x_rows[cur][q];
             g.tmY[q] = h->x_rows[cur ^ 1][q];
         }
-        choose_form(g, pair, h->sms, h->x_cols[cur], h->x_cols[cur]);
+        choose_form(g, parts != 1, h->sms, h->x_cols[cur], h->x_cols[cur]);
         if (cmu_launch_gemm(g, h->sms, s) != cudaSuccess) return CDG_ERR_CUDA;
     }
     return CDG_OK;

@@ -618,7 +618,6 @@ size_t cdg_muon_workspace_bytes(cdg_muon_t h);
 typedef struct {
     int m, n;             /* the smaller and the larger side                      */
     int transposed;       /* 1: rows > cols, the kernels hold U^T                 */
-    int tile_m, tile_n;   /* output tile of the products                          */
     int gram;             /* 1: the steps run on X X^T alone, on one SM a matrix    */
     int launches;         /* kernel launches of one cdg_muon_orthogonalize        */
 } cdg_muon_info_t;
