@@ -300,10 +300,9 @@ struct Tile {
 template <int FORM>
 struct Layout {
     static constexpr bool kPair = FORM == CMU_PAIR;
-    // Eight epilogue warps: in two groups that take 64-column chunks of their own halves of the tile (PAIR), or all
-    // eight on one chunk after the other.
+    // Groups of eight epilogue warps, a 64-column chunk at a time, for every 128 columns of the tile.
     static constexpr int kGroups = kPair ? 2 : 1;
-    static constexpr int kThreads = 128 + 256, kGroupThreads = 256 / kGroups;
+    static constexpr int kGroupThreads = 256, kThreads = 128 + kGroups * kGroupThreads;
     static constexpr int kOwn = 64 * 128 / kGroupThreads;    // columns of a chunk a thread holds
     static constexpr int kTileM = kPair ? 256 : 128, kTileN = kPair ? 256 : FORM == CMU_SQUARE ? 128 : 64;
     static constexpr int kCols = kTileN;                     // TMEM columns an accumulator
@@ -343,8 +342,8 @@ struct Epilogue {
     {
         const int warp = threadIdx.x / 32 - CDG_EPI_WARP0;
         lane = threadIdx.x % 32;
-        group = Lay::kGroups == 2 ? warp / 4 : 0;
-        part = Lay::kGroups == 2 ? 0 : warp / 4;
+        group = warp / 8;
+        part = warp % 8 / 4;
         quad = warp % 4;
         row = quad * 32 + lane;
         elected = elect_one_sync() && quad == 0 && part == 0;
@@ -628,7 +627,7 @@ __global__ void __launch_bounds__(Layout<FORM>::kThreads, 1) gemm_kernel(const _
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(L.acc_full0 + 8u * a, 1);
-            mbar_init(L.acc_empty0 + 8u * a, PAIR ? 16 : 8);  // one arrival per epilogue warp (of both CTAs)
+            mbar_init(L.acc_empty0 + 8u * a, PAIR ? 32 : 8);  // one arrival per epilogue warp (of both CTAs)
         }
         mbar_init(L.drain, 1);
         for (int g = 0; g < Lay::kGroups; ++g) mbar_init(L.epi0 + 8u * g, 1);
