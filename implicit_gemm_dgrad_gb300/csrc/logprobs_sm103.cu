@@ -47,7 +47,7 @@ constexpr int kMaxTop = 32;
 constexpr int kMaxVocab = 1 << 30;  // element numbers stay in 32 bits
 constexpr int kThreads = 256;
 constexpr int kCand = 1024;         // candidate keys a CTA ranks
-constexpr int kMaxCluster = 8;      // CTAs that share a row
+constexpr int kMaxCluster = kThreads / 32;  // CTAs that share a row (a warp for each one's keys at the end)
 constexpr int kUnroll = 4;          // 16-byte loads in flight per thread
 constexpr int kCtasPerSm = 6;
 constexpr float kLn2 = 0.693147180559945309f;
@@ -285,8 +285,9 @@ __device__ __forceinline__ void add_all(Run &a, const uint4 (&v)[N], float c)
         for (int j = 0; j < kPerVec<T>; j += 2) add<CLAMP>(a, f[j], f[j + 1], cc, minus);
     }
 }
+// Returns the largest of the group.
 template <typename T, int N>
-__device__ __forceinline__ void add_group(Run &a, const uint4 (&v)[N], float c)
+__device__ __forceinline__ float add_group(Run &a, const uint4 (&v)[N], float c)
 {
     using W = Words<T>;
     uint32_t hi = W::max(W::max(v[0].x, v[0].y), W::max(v[0].z, v[0].w));
@@ -302,10 +303,11 @@ __device__ __forceinline__ void add_group(Run &a, const uint4 (&v)[N], float c)
         for (int i = 1; i < N; ++i) lo = W::min(lo, W::min(W::min(v[i].x, v[i].y), W::min(v[i].z, v[i].w)));
         if (fmaf(min_word<T>(lo), c, -a.ref) > kFloor) {
             add_all<T, false>(a, v, c);
-            return;
+            return g;
         }
     }
     add_all<T, true>(a, v, c);
+    return g;
 }
 
 // Insert warp-uniform key x into the warp's descending list (lane l holds its
@@ -344,10 +346,20 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// How many of the descending keys[0..n) are larger than x (n <= 32).
+__device__ __forceinline__ int count_larger(const unsigned long long *keys, int n, unsigned long long x)
+{
+    int at = 0;
+#pragma unroll
+    for (int step = 32; step; step >>= 1)
+        if (at + step <= n && keys[at + step - 1] > x) at += step;
+    return at;
+}
+
 // TEAM threads a row: a warp each of eight rows, or the CTA, which a cluster of
-// CTAs may share the row with.
-template <typename T, int TEAM>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const LogprobArgs p)
+// CTAs may share the row with.  TOP: alternatives are wanted.
+template <typename T, int TEAM, bool TOP>
+__global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprobs_kernel(const LogprobArgs p)
 {
     constexpr bool WARP = TEAM == 32;
     constexpr int W = TEAM / 32, TEAMS = kThreads / TEAM, CAND = kCand / TEAMS;
@@ -380,11 +392,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     // ---- one pass: sums and the thread's maximum
     Run run{-INFINITY, -INFINITY, 0ull, 0ull};
     uint4 x[kUnroll];
+    // TOP: the group of vectors that holds the thread's largest logit, and the largest of its other groups
+    float top_group = -INFINITY, other_groups = -INFINITY;
+    int top_at = 0;
+    auto note = [&](float g, int at) {
+        if (!TOP) return;
+        if (g > top_group) {
+            other_groups = top_group;
+            top_group = g;
+            top_at = at;
+        } else {
+            other_groups = fmaxf(other_groups, g);
+        }
+    };
     int v = 0;
     for (; v + kUnroll * TEAM <= sl.nv; v += kUnroll * TEAM) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) x[u] = vec_at(v + u * TEAM);
-        add_group<T, kUnroll>(run, x, p.c);
+        note(add_group<T, kUnroll>(run, x, p.c), v);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
@@ -396,12 +421,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
         const float ref = run.ref == -INFINITY ? 0.0f : run.ref;
         add<true>(run, z, -INFINITY, pack2(p.c, p.c), pack2(-ref, -ref));
     }
+    float last = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
         if (v + u * TEAM + tid < sl.nv) {
             const uint4 y[1] = {x[u]};
-            add_group<T, 1>(run, y, p.c);
+            last = fmaxf(last, add_group<T, 1>(run, y, p.c));
         }
+    note(last, v);
+    // the target's logit, on its way while the sums are joined
+    int target = -1;
+    float z_target = 0.0f;
+    if (tid == 0 && rank == 0 && p.logp) {
+        target = token_at(p.targets, p.index_bytes, i, p.vocab);
+        if (target >= 0) z_target = Elem<T>::get(sl.row[target]);
+    }
     // no element at all in this thread: below every element
     const uint32_t omax = single >= 0 || tid < sl.nv ? ordered(run.zmax) : 0u;
 
@@ -411,29 +445,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     unpack2(run.e, e0, e1);
     Sums all = join_lanes(Sums{run.zmax, s0 + s1, e0 + e1}, p.c);
     uint32_t mo = omax;  // lane l: one of 32 thread maxima
-    if (p.top && tid == 0) *ncand = 0;
+    if (TOP && tid == 0) *ncand = 0;
     if (!WARP) {
         if (lane == 0) part[warp] = all;
-        if (p.top) {
+        if (TOP) {
+            // a round more than gives `top` offers: the bound is closer, and fewer candidates reach it
+            const int rounds = min(PER_WARP, (p.top + W - 1) / W + 1);
             uint32_t m = omax;
-#pragma unroll
             for (int r = 0; r < PER_WARP; ++r) {
-                const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, m);
-                const unsigned holders = __ballot_sync(0xFFFFFFFFu, m == g);
+                uint32_t g = 0u;
+                if (r < rounds) {
+                    g = __reduce_max_sync(0xFFFFFFFFu, m);
+                    const unsigned holders = __ballot_sync(0xFFFFFFFFu, m == g);
+                    if (lane == __ffs(holders) - 1) m = 0u;
+                }
                 if (lane == 0) offer[warp * PER_WARP + r] = g;
-                if (lane == __ffs(holders) - 1) m = 0u;
             }
         }
         __syncthreads();
         if (warp == 0) all = join_lanes(lane < W ? part[lane] : Sums{-INFINITY, 0.0f, 0.0f}, p.c);
-        if (p.top) mo = offer[lane];
-    } else if (p.top) {
+        if (TOP) mo = offer[lane];
+    } else if (TOP) {
         __syncwarp();
     }
 
     // ---- the team's largest logits
     int nbest = 0;
-    if (p.top) {
+    if constexpr (TOP) {
         int larger = 0;
 #pragma unroll
         for (int l = 0; l < 32; ++l) {
@@ -451,8 +489,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
             };
             if (single >= 0) offer_one(Elem<T>::get(sl.row[single]), single);
             const volatile int *listed = ncand;
-            // (a row of less than a full group is still in x)
-            for (int w = 0; w < sl.nv && *listed <= CAND; w += kUnroll * TEAM) {
+            // mostly one group of the thread reaches the bound; (a row of less than a full group is still in x)
+            const bool one = ordered(other_groups) < bound;
+            for (int w = one ? top_at : 0; w < sl.nv && *listed <= CAND; w += kUnroll * TEAM) {
                 if (sl.nv >= kUnroll * TEAM) {
 #pragma unroll
                     for (int u = 0; u < kUnroll; ++u)
@@ -469,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
 #pragma unroll
                     for (int e = 0; e < kPerVec<T>; ++e) offer_one(f[e], sl.v0 + q * kPerVec<T> + e);
                 }
+                if (one) break;
             }
         }
         sync();
@@ -525,16 +565,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
         cluster_arrive();
         cluster_wait();
         if (warp == 0) all = join_lanes(lane < p.cluster ? from_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, p.c);
-        if (p.top) {
-            int n = nbest;
-            if (tid < nbest) cand[tid] = best[tid];
-            for (int r = 1; r < p.cluster; ++r) {
-                const int k = from_count[r];
-                if (tid < k) cand[n + tid] = from_keys[r][tid];
-                n += k;
-            }
+        if (TOP) {
+            // a list a warp, a key a lane: its rank is its own place and what the other lists hold above it (counting
+            // over all keys instead took 1.3 thousand cycles longer)
+            if (tid < nbest) from_keys[0][tid] = best[tid];
+            if (tid == 0) from_count[0] = nbest;
             __syncthreads();
-            rank_keys<TEAM>(cand, n, p.top, best, tid);
+            if (warp < p.cluster && lane < from_count[warp]) {
+                const unsigned long long key = from_keys[warp][lane];
+                int place = lane;
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q)  // independent searches, side by side
+                    place += count_larger(from_keys[q], q < p.cluster && q != warp ? from_count[q] : 0, key);
+                if (place < p.top) best[place] = key;
+            }
             __syncthreads();
         }
     }
@@ -570,12 +614,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     if (tid == 0) {
         if (p.lse) p.lse[i] = none ? -INFINITY : extreme ? fmaf(all.zmax, p.scale, kLn2 * logs) : kLn2 * (ref + logs);
         if (p.entropy) p.entropy[i] = none ? 0.0f : kLn2 * (logs - all.e / all.s);
-        if (p.logp) {
-            const int t = token_at(p.targets, p.index_bytes, i, p.vocab);
-            p.logp[i] = t >= 0 ? logp_of(Elem<T>::get(sl.row[t])) : 0.0f;
-        }
+        if (p.logp) p.logp[i] = target >= 0 ? logp_of(z_target) : 0.0f;
     }
-    if (tid < p.top) {
+    if (TOP && tid < p.top) {
         const unsigned long long key = best[tid];
         const float z = unordered(static_cast<uint32_t>(key >> 32));
         p.top_ids[i * p.top + tid] = bad ? -1 : key_index(key);
@@ -682,7 +723,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
 // alternatives: 4.2 us against 8.9; 65536 rows: 242 us against 154).
 constexpr int kWarpVocab = 4096;
 
-template <typename T>
+template <typename T, bool TOP>
 cudaError_t launch_logprobs(const LogprobArgs &a, int sms, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
@@ -690,7 +731,7 @@ cudaError_t launch_logprobs(const LogprobArgs &a, int sms, cudaStream_t s)
     cfg.stream = s;
     if (a.vocab <= kWarpVocab && a.rows > static_cast<long long>(kCtasPerSm) * sms) {
         cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kThreads / 32 - 1) / (kThreads / 32)));
-        return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 32>, a);
+        return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 32, TOP>, a);
     }
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * a.cluster));
     cudaLaunchAttribute attr[1];
@@ -699,7 +740,13 @@ cudaError_t launch_logprobs(const LogprobArgs &a, int sms, cudaStream_t s)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads>, a);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads, TOP>, a);
+}
+
+template <typename T>
+cudaError_t launch_logprobs(const LogprobArgs &a, int sms, cudaStream_t s)
+{
+    return a.top ? launch_logprobs<T, true>(a, sms, s) : launch_logprobs<T, false>(a, sms, s);
 }
 
 template <typename T>
