@@ -89,6 +89,7 @@ struct cdg_muon_st {
 
 namespace {
 
+// num_sms = 0: this device's.  Arguments are checked before the device is asked.
 int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a, float b, float c, float eps,
                    int num_sms, bool host_only, cdg_muon_t *out)
 {
@@ -96,12 +97,13 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     *out = nullptr;
     if (batch < 1 || rows < 1 || cols < 1 || (dtype != CDG_F16 && dtype != CDG_BF16 && dtype != CDG_F32) || steps < 1 ||
         steps > 32 || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !std::isfinite(eps) ||
-        eps < 0.0f || num_sms < 1)
+        eps < 0.0f || num_sms < (host_only ? 1 : 0))
         return CDG_ERR_INVALID_ARG;
     const Bounds bounds = iteration_bounds(steps, a, b, c);
     if (!bounds.iteration) return CDG_ERR_INVALID_ARG;
     const int m = std::min(rows, cols), n = std::max(rows, cols);
     if (batch > 65535 || m > 32768 || n > (1 << 21)) return CDG_ERR_UNSUPPORTED;
+    if (!host_only && (num_sms = cdg::sm_count()) < 1) return CDG_ERR_CUDA;
     cdg_muon_st *h = new (std::nothrow) cdg_muon_st();
     if (!h) return CDG_ERR_CUDA;
     h->batch = batch; h->rows = rows; h->cols = cols; h->dtype = dtype; h->steps = steps;
@@ -326,14 +328,7 @@ extern "C" {
 int cdg_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a, float b, float c, float eps,
                   cdg_muon_t *out)
 {
-    if (out) *out = nullptr;
-    cdg_muon_t probe = nullptr;
-    const int rc = make_muon_plan(batch, rows, cols, dtype, steps, a, b, c, eps, 148, true, &probe);
-    if (rc != CDG_OK) return rc;
-    cdg_muon_destroy(probe);
-    const int sms = cdg::sm_count();
-    if (sms < 1) return CDG_ERR_CUDA;
-    return make_muon_plan(batch, rows, cols, dtype, steps, a, b, c, eps, sms, false, out);
+    return make_muon_plan(batch, rows, cols, dtype, steps, a, b, c, eps, 0, false, out);
 }
 
 int cdg_muon_plan_host(int batch, int rows, int cols, int dtype, int steps, float a, float b, float c, float eps,
