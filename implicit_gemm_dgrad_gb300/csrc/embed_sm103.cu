@@ -15,6 +15,7 @@
 #include <climits>
 #include <cmath>
 
+#include "ptx.cuh"
 #include "token_device.cuh"
 
 namespace cdg {
@@ -161,28 +162,31 @@ __device__ __forceinline__ int sort_key(const SortPass &p, int i)
     return t < 0 ? p.vocab : t;
 }
 
-// Eight lanes a token, 32 tokens a CTA; the keys in shared memory.
+// LANES lanes a token; the keys in shared memory.
+template <int LANES>
 __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortPass p)
 {
     extern __shared__ int4 keys4[];
     int *keys = reinterpret_cast<int *>(keys4);
     const int n4 = (p.count + 3) / 4;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.runs = 0;
+#pragma unroll 8
     for (int i = threadIdx.x; i < 4 * n4; i += kSortThreads) keys[i] = i < p.count ? sort_key(p, i) : INT_MAX;
     __syncthreads();
-    const int i = blockIdx.x * 32 + threadIdx.x / 8, sub = threadIdx.x % 8;
+    const int i = blockIdx.x * (kSortThreads / LANES) + threadIdx.x / LANES, sub = threadIdx.x % LANES;
     const int key = i < p.count ? keys[i] : 0;
     int before = 0;
     // keys before i count when equal, keys after it do not
 #pragma unroll 4
-    for (int q = sub; q < n4; q += 8) {
+    for (int q = sub; q < n4; q += LANES) {
         const int4 k = keys4[q];
         const int d = i - 4 * q;
         before += (k.x < key + (d > 0)) + (k.y < key + (d > 1)) + (k.z < key + (d > 2)) + (k.w < key + (d > 3));
     }
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, 4);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     if (sub == 0 && i < p.count) {
         p.keys_out[before] = key;
         p.order_out[before] = i;
@@ -194,6 +198,8 @@ template <int ROUNDS>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPass p)
 {
     __shared__ int h[kMaxBins];
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.runs = 0;
     for (int d = threadIdx.x; d < p.bins; d += kSortThreads) h[d] = 0;
     __syncthreads();
@@ -222,6 +228,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPass
     __shared__ int wsum[kWarps];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int i0 = (blockIdx.x * kWarps + warp) * (32 * ROUNDS);
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     int key[ROUNDS], rank[ROUNDS];
 #pragma unroll
     for (int k = 0; k < ROUNDS; ++k) {
@@ -348,6 +356,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
 {
     constexpr int E = kPerVec<T>, V = kPerVec<O>, ROWS = ACCUMULATE ? 4 : 8;  // rows read at once
     __shared__ int s_key[kSumThreads / 32][3 * kMaxChunk + 1], s_row[kSumThreads / 32][2 * kMaxChunk];
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     // the CTAs that clear rows without a token lie evenly among the others
     const unsigned all = p.sum_ctas + p.zero_ctas;
     const unsigned z0 = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * p.zero_ctas / all);
@@ -476,6 +486,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_join_kernel(const Embe
     constexpr int ROWS = 8, COLS = kSumThreads / ROWS;
     __shared__ float4 part_sum[ROWS][COLS];
     const int x = threadIdx.x % COLS, y = threadIdx.x / COLS;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     const int runs = __ldcg(p.runs);
     for (int r = blockIdx.x; r < runs; r += gridDim.x) {
         const int c = __ldcg(p.runs + 1 + r);
@@ -567,10 +579,19 @@ bool grad_sizes_ok(long long count, int vocab, int dim)
 }
 
 template <int ROUNDS>
-void launch_sort_pass(const SortPass &p, cudaStream_t s)
+cudaError_t launch_sort_pass(const SortPass &p, cudaStream_t s)
 {
-    sort_count_kernel<ROUNDS><<<p.tiles, kSortThreads, 0, s>>>(p);
-    sort_place_kernel<ROUNDS><<<p.tiles, kSortThreads, 0, s>>>(p);
+    const cudaError_t e = launch_early(sort_count_kernel<ROUNDS>, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
+    return e != cudaSuccess ? e : launch_early(sort_place_kernel<ROUNDS>, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
+}
+
+cudaError_t launch_rank(const SortPass &p, cudaStream_t s)
+{
+    const int smem = (p.count + 3) / 4 * 16;
+    // the more lanes a token the more CTAs, which all read the whole list
+    return p.count <= kRankMax / 2
+               ? launch_early(sort_rank_kernel<32>, dim3((p.count + 7) / 8), dim3(kSortThreads), smem, s, p)
+               : launch_early(sort_rank_kernel<8>, dim3((p.count + 31) / 32), dim3(kSortThreads), smem, s, p);
 }
 
 template <typename T, typename O>
@@ -591,16 +612,17 @@ cudaError_t launch_sums(EmbedGradArgs a, cudaStream_t s)
     if (sum + zero >= (1ll << 31)) return cudaErrorInvalidConfiguration;
     a.sum_ctas = static_cast<unsigned>(sum);
     a.zero_ctas = static_cast<unsigned>(zero);
-    const unsigned grid = a.sum_ctas + a.zero_ctas;
-    if (grid > 0) {
-        if (aligned && a.accumulate) embed_grad_kernel<T, O, true, true><<<grid, kSumThreads, 0, s>>>(a);
-        else if (aligned) embed_grad_kernel<T, O, true, false><<<grid, kSumThreads, 0, s>>>(a);
-        else if (a.accumulate) embed_grad_kernel<T, O, false, true><<<grid, kSumThreads, 0, s>>>(a);
-        else embed_grad_kernel<T, O, false, false><<<grid, kSumThreads, 0, s>>>(a);
-    }
-    if (a.chunks > 1)
-        embed_grad_join_kernel<O><<<dim3(std::min(a.chunks, 128), std::min(32, (a.pitch + 63) / 64)), kSumThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const dim3 grid(a.sum_ctas + a.zero_ctas), block(kSumThreads);
+    cudaError_t e = cudaSuccess;
+    if (grid.x > 0)
+        e = aligned ? (a.accumulate ? launch_early(embed_grad_kernel<T, O, true, true>, grid, block, 0, s, a)
+                                    : launch_early(embed_grad_kernel<T, O, true, false>, grid, block, 0, s, a))
+                    : (a.accumulate ? launch_early(embed_grad_kernel<T, O, false, true>, grid, block, 0, s, a)
+                                    : launch_early(embed_grad_kernel<T, O, false, false>, grid, block, 0, s, a));
+    if (e == cudaSuccess && a.chunks > 1)
+        e = launch_early(embed_grad_join_kernel<O>, dim3(std::min(a.chunks, 128), std::min(32, (a.pitch + 63) / 64)), block, 0,
+                         s, a);
+    return e;
 }
 
 bool is_dtype(int d) { return d == CDG_F16 || d == CDG_BF16 || d == CDG_F32; }
@@ -675,7 +697,7 @@ int cdg_embed_grad(const void *dout, long long ld_dout, const void *tokens, int 
     SortPass p{tokens, nullptr, nullptr, reinterpret_cast<int *>(ws + l.keys[0]), reinterpret_cast<int *>(ws + l.order[0]),
                reinterpret_cast<int *>(ws + l.hist), reinterpret_cast<int *>(ws + l.runs), index_bytes, static_cast<int>(count), vocab, 0, 1 << l.digit, l.tiles};
     if (count > 0 && count <= kRankMax) {
-        sort_rank_kernel<<<static_cast<unsigned>((count + 31) / 32), kSortThreads, (count + 3) / 4 * 16, s>>>(p);
+        if (launch_rank(p, s) != cudaSuccess) return CDG_ERR_CUDA;
     } else if (count > 0) {
         for (int q = 0; q < l.passes; ++q) {
             p.tokens = q == 0 ? tokens : nullptr;
@@ -684,13 +706,11 @@ int cdg_embed_grad(const void *dout, long long ld_dout, const void *tokens, int 
             p.keys_out = reinterpret_cast<int *>(ws + l.keys[q & 1]);
             p.order_out = reinterpret_cast<int *>(ws + l.order[q & 1]);
             p.shift = q * l.digit;
-            if (l.rounds == 4) launch_sort_pass<4>(p, s);
-            else launch_sort_pass<16>(p, s);
+            if ((l.rounds == 4 ? launch_sort_pass<4>(p, s) : launch_sort_pass<16>(p, s)) != cudaSuccess) return CDG_ERR_CUDA;
             keys = p.keys_out;
             order = p.order_out;
         }
     }
-    if (cudaGetLastError() != cudaSuccess) return CDG_ERR_CUDA;
     EmbedGradArgs a{};
     a.dout = dout;
     a.dtable = dtable;

@@ -1207,23 +1207,6 @@ __global__ void __launch_bounds__(kItThreads, 1) iterate_kernel(const CmuIterate
     }
 }
 
-// A launch that may begin while the one before it ends (its kernel waits).
-template <typename... A>
-cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t s, const A &...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename T>
 cudaError_t launch_norm(const CmuPrepare &p, cudaStream_t s)
 {

@@ -152,6 +152,24 @@ struct Shifted {
 };
 
 // ---------------------------------------------------------------- host side
+// A launch that may begin while the one before it ends: its kernel waits
+// (grid_dep_wait) before it touches memory.
+template <typename... A>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, dim3 block, int smem, cudaStream_t s, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 static inline int dtype_bytes(int dtype) { return dtype == CDG_F32 ? 4 : 2; }
 
 static inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
