@@ -138,6 +138,11 @@ void launch_embed(EmbedArgs a, int sms, cudaStream_t s)
 }
 
 // ---------------------------------------------------------------- sort
+// The first launch of a call begins when all work before it is done; the others
+// may begin while the one before them ends, and wait.  What the call's own
+// launches write (the workspace) is therefore read past L1 (__ldcg), never as
+// read-only data.
+//
 // Up to kRankMax tokens: every token's place is the number of keys before it,
 // counted directly (one launch, N^2 comparisons; 8192 tokens take 17 us longer
 // that way than by the radix sort).  Above: a radix sort of
@@ -157,7 +162,7 @@ struct SortPass {
 // Key i: the token number, or vocab (sorted last) where there is no token.
 __device__ __forceinline__ int sort_key(const SortPass &p, int i)
 {
-    if (!p.tokens) return p.keys[i];
+    if (!p.tokens) return __ldcg(p.keys + i);
     const int t = token_at(p.tokens, p.index_bytes, i, p.vocab);
     return t < 0 ? p.vocab : t;
 }
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPass
     if (d0 < p.bins) {
 #pragma unroll 16
         for (int t = 0; t < p.tiles; ++t) {
-            const int2 h = __ldg(reinterpret_cast<const int2 *>(p.hist + static_cast<long long>(t) * p.bins + d0));
+            const int2 h = __ldcg(reinterpret_cast<const int2 *>(p.hist + static_cast<long long>(t) * p.bins + d0));
             const bool prior = t < static_cast<int>(blockIdx.x);
             before0 += prior ? h.x : 0;
             before1 += prior ? h.y : 0;
@@ -293,8 +298,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPass
         const int i = i0 + k * 32 + lane;
         if (i >= p.count) break;
         const int at = cnt[warp][(key[k] >> p.shift) & (p.bins - 1)] + rank[k];
+        if (static_cast<unsigned>(at) >= static_cast<unsigned>(p.count)) continue;  // tokens changed since they were counted
         p.keys_out[at] = key[k];
-        p.order_out[at] = p.tokens ? i : p.order[i];
+        p.order_out[at] = p.tokens ? i : __ldcg(p.order + i);
     }
 }
 
@@ -310,7 +316,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPass
 // A thread holds one 16-byte vector of columns (of dout's type), placed so that
 // it is aligned in the row it writes; rows of dout at other alignments are read
 // from two blocks.
+//
+// Whatever the sorted lists hold, nothing outside the tensors is touched: keys
+// and positions are checked as they are read.  (A caller that changes the tokens
+// while the call runs leaves lists that no sort made.)
 constexpr int kSumThreads = 128, kMaxChunk = 64;
+
+// A key of the list; one that is none counts as "no token".
+__device__ __forceinline__ int checked_key(const int *keys, int i, int vocab)
+{
+    return static_cast<int>(min(static_cast<unsigned>(__ldcg(keys + i)), static_cast<unsigned>(vocab)));
+}
 
 struct EmbedGradArgs {
     const void *dout;
@@ -335,7 +351,7 @@ __device__ __forceinline__ int warp_lower_bound(const int *keys, int count, int 
     int lo = 0, n = count;  // the answer lies in [lo, lo + n]
     while (n > 0) {
         const int step = (n + 31) / 32, at = min(lo + (lane + 1) * step - 1, lo + n - 1);
-        const unsigned less = __ballot_sync(0xFFFFFFFFu, __ldg(keys + at) < v);
+        const unsigned less = __ballot_sync(0xFFFFFFFFu, __ldcg(keys + at) < v);
         const int full = __popc(less);  // probes below v
         const int to = min(full * step, n);
         lo += to;
@@ -352,7 +368,7 @@ __device__ __forceinline__ int warp_count(const int *key, int a, int n, int v, i
 }
 
 template <typename T, typename O, bool ALIGNED, bool ACCUMULATE>
-__global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGradArgs p)
+__global__ void __launch_bounds__(kSumThreads, ALIGNED && !ACCUMULATE ? 7 : 1) embed_grad_kernel(const EmbedGradArgs p)
 {
     constexpr int E = kPerVec<T>, V = kPerVec<O>, ROWS = ACCUMULATE ? 4 : 8;  // rows read at once
     __shared__ int s_key[kSumThreads / 32][3 * kMaxChunk + 1], s_row[kSumThreads / 32][2 * kMaxChunk];
@@ -366,7 +382,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
         const int lane = threadIdx.x % 32, row = static_cast<int>(z0) * (kSumThreads / 32) + threadIdx.x / 32;
         if (row >= p.vocab) return;
         const int at = warp_lower_bound(p.keys, p.count, row, lane);
-        if (at < p.count && __ldg(p.keys + at) == row) return;
+        if (at < p.count && __ldcg(p.keys + at) == row) return;
         O *dst = static_cast<O *>(p.dtable) + static_cast<long long>(row) * p.ld_dtable;
         const float zero[V] = {};
         for (int c = lane * V - p.phase.at<O>(row); c < p.dim; c += 32 * V) store_columns<O, V>(dst, c, p.dim, zero);
@@ -381,10 +397,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_kernel(const EmbedGrad
     // the keys from one chunk before to one after (-1 before the list, INT_MAX after it)
     for (int q = x; q < 3 * chunk + 1; q += p.tx) {
         const int i = i0 + q - chunk;
-        s_key[y][q] = i < 0 ? -1 : i < p.count ? __ldg(p.keys + i) : INT_MAX;
+        s_key[y][q] = i < 0 ? -1 : i < p.count ? checked_key(p.keys, i, p.vocab) : INT_MAX;
     }
     for (int q = x; q < 2 * chunk; q += p.tx)
-        if (i0 + q < p.count) s_row[y][q] = __ldg(p.order + i0 + q);
+        if (i0 + q < p.count) {
+            const int row = __ldcg(p.order + i0 + q);
+            s_row[y][q] = static_cast<unsigned>(row) < static_cast<unsigned>(p.count) ? row : 0;
+        }
     __syncthreads();
     if (!real) return;
     const int *key = s_key[y] + chunk;  // key[r]: of position i0 + r
@@ -491,7 +510,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_grad_join_kernel(const Embe
     const int runs = __ldcg(p.runs);
     for (int r = blockIdx.x; r < runs; r += gridDim.x) {
         const int c = __ldcg(p.runs + 1 + r);
-        const int v = __ldg(p.keys + (c + 1ll) * p.chunk - 1);
+        const int v = checked_key(p.keys, (c + 1) * p.chunk - 1, p.vocab);
+        if (v >= p.vocab) continue;
         const int run_end = warp_lower_bound(p.keys, p.count, v + 1, threadIdx.x % 32);
         const int parts = (run_end - 1) / p.chunk - c + 1;
         O *dst = static_cast<O *>(p.dtable) + static_cast<long long>(v) * p.ld_dtable;
@@ -581,7 +601,13 @@ bool grad_sizes_ok(long long count, int vocab, int dim)
 template <int ROUNDS>
 cudaError_t launch_sort_pass(const SortPass &p, cudaStream_t s)
 {
-    const cudaError_t e = launch_early(sort_count_kernel<ROUNDS>, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
+    cudaError_t e;
+    if (p.tokens) {  // the call's first launch
+        sort_count_kernel<ROUNDS><<<p.tiles, kSortThreads, 0, s>>>(p);
+        e = cudaGetLastError();
+    } else {
+        e = launch_early(sort_count_kernel<ROUNDS>, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
+    }
     return e != cudaSuccess ? e : launch_early(sort_place_kernel<ROUNDS>, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
 }
 
@@ -589,9 +615,9 @@ cudaError_t launch_rank(const SortPass &p, cudaStream_t s)
 {
     const int smem = (p.count + 3) / 4 * 16;
     // the more lanes a token the more CTAs, which all read the whole list
-    return p.count <= kRankMax / 2
-               ? launch_early(sort_rank_kernel<32>, dim3((p.count + 7) / 8), dim3(kSortThreads), smem, s, p)
-               : launch_early(sort_rank_kernel<8>, dim3((p.count + 31) / 32), dim3(kSortThreads), smem, s, p);
+    if (p.count <= kRankMax / 2) sort_rank_kernel<32><<<(p.count + 7) / 8, kSortThreads, smem, s>>>(p);
+    else sort_rank_kernel<8><<<(p.count + 31) / 32, kSortThreads, smem, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, typename O>
