@@ -345,3 +345,33 @@ def test_gradient_matches_differences():
         diff = (value(z + eps * v) - value(z - eps * v)) / (2 * eps)
         # differences: O(eps^2) third derivatives; the gradient: fp32 throughout
         assert abs(diff - float((d * v).sum())) <= 1e-5 * (1 + abs(diff)) + 1e-5 * np.abs(d * v).sum()
+
+
+# many rows of a small vocabulary: a warp takes a row
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("vocab,top,pad,offset", [(1, 1, 0, 0), (7, 7, 1, 3), (33, 32, 0, 1), (256, 20, 0, 0),
+                                                  (1001, 5, 2, 5), (4096, 32, 0, 0)])
+def test_many_rows_of_a_small_vocabulary(vocab, top, pad, offset, dtype):
+    rng = np.random.default_rng(vocab)
+    rows = 1003
+    z, t = draw(rng, rows, vocab, banned=0.05 if vocab > 7 else 0.0)
+    z[5] = -np.inf                                              # nothing left
+    z[6] = 0.0                                                  # all equal
+    z[7] = np.round(z[7] * 2) / 2                               # many equal
+    z[8] = np.where(np.arange(vocab) < vocab // 2, -np.inf, 1.0)
+    t[5:9] = [0, vocab - 1, 0, vocab - 1]
+    check(z, t, dtype, top=top, pad=pad, offset=offset)
+    check(z, t, dtype, pad=pad, offset=offset)
+
+
+def test_many_rows_with_the_types_lowest_value_and_nan():
+    rng = np.random.default_rng(21)
+    z, t = draw(rng, 1000, 300)
+    t[:] = 3
+    z[11] = np.finfo(np.float32).min
+    check(z, t, "f32", top=4)
+    z[12, 7], z[13, 9] = np.nan, np.inf
+    got = forward(z, t, "f32", top=4)
+    bad = np.isnan(got["lse"])
+    assert list(np.flatnonzero(bad)) == [12, 13] and (got["top_ids"][[12, 13]] == -1).all()
+    assert np.isnan(got["logp"][[12, 13]]).all() and np.isfinite(got["logp"][~bad]).all()

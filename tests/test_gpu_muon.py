@@ -228,3 +228,40 @@ def test_small_matrices_on_both_paths(rows, cols, coefficients, steps, gram):
         torch.cuda.synchronize()
         assert p.device_status() == 0
         assert_near(O, iterate(U, steps, coefficients=coefficients), "bf16", kind)
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 2100, 2300), (1, 2300, 2101), (6, 700, 801), (1, 200, 4608), (1, 4608, 333)])
+def test_large_and_long_matrices(batch, rows, cols):
+    """Products in CTA pairs, alone and mixed with single CTAs, with partial tiles on both sides; K split over clusters."""
+    import torch
+    for kind in ("gauss", "lowrank"):
+        U = make(batch, rows, cols, kind, 14).bfloat16()
+        p = cdg.muon_plan(rows, cols, batch=batch)
+        ws = workspace(p)
+        buf, O = guarded(U.shape, U.dtype)
+        p.orthogonalize(U, O, ws)
+        torch.cuda.synchronize()
+        assert p.device_status() == 0 and intact(buf)
+        assert_near(O, iterate(U), "bf16", kind)
+        again = torch.empty_like(U)
+        p.orthogonalize(U, again, ws)
+        assert torch.equal(again, O), "not the same bits again"
+
+
+def test_large_step_in_place():
+    import torch
+    rows, cols = 2100, 2200
+    G, M, W = make(1, rows, cols, "gauss", 15).bfloat16(), make(1, rows, cols, "lowrank", 16), make(1, rows, cols, "gauss", 17)
+    lr, mu = 0.02, 0.9
+    m = mu * M.double() + G.double()
+    o = iterate(G.double() + mu * m)
+    p = cdg.muon_plan(rows, cols)
+    Wi, Mi = W.clone(), M.clone()
+    p.step(Wi, G, Mi, Wi, Mi, workspace(p), lr=lr, momentum=mu)
+    torch.cuda.synchronize()
+    assert p.device_status() == 0
+    update = (W.double() - Wi.double()) / lr
+    err = float(torch.linalg.vector_norm(update - o) / torch.linalg.vector_norm(o))
+    seen = float(torch.linalg.vector_norm(W.double()) * 2.0 ** -22 / lr / torch.linalg.vector_norm(o))
+    assert err <= BAR + seen, (err, seen)
+    assert bool(((Mi.double() - m).abs() <= 2.0 ** -23 * (mu * M.double().abs() + G.double().abs()) + 1e-30).all())
