@@ -638,15 +638,37 @@ def _dense(t, n: int, esize: int, what: str) -> int | None:
     return _bytes_of(t, n, esize, what)
 
 
+def _row_stride(t, rows: int, cols: int, what: str) -> int:
+    """Row stride of a contiguous tensor as rows of cols elements: dense where
+    trailing dimensions hold just a row, or where the tensor has one dimension
+    or just rows * cols elements; the last dimension where that is wider than a
+    row (a padded vocabulary), which then holds at least rows of them."""
+    shape = getattr(t, "shape", None)
+    if shape is None or len(shape) < 2 or shape[-1] == cols or t.numel() == rows * cols:
+        return cols
+    last = row = shape[-1]
+    for s in reversed(shape[:-1]):
+        if row >= cols:
+            break
+        row *= s
+    if row == cols:
+        return cols
+    if last < cols or t.numel() < rows * last:
+        raise ValueError(f"{what} is {tuple(shape)}; the call needs {(rows, cols)}")
+    return last
+
+
 def _matrix(t, rows: int, cols: int, esize: int, ld: int | None, what: str) -> tuple[int | None, int]:
-    """Address and row stride of a rows x cols argument.  A 2-D tensor may have
-    any row stride with unit column stride (a slice of a wider one); any other
-    tensor is taken as dense; a raw address has row stride ld, or cols."""
+    """Address and row stride of a rows x cols argument.  A contiguous tensor's
+    rows may be wider than cols, and more than rows; another 2-D tensor of shape
+    (rows, cols) may have any row stride with unit column stride (a slice of a
+    wider one); a raw address has row stride ld, or cols."""
     if t is None or isinstance(t, int):
         return t, int(ld if ld is not None else cols)
     own = cols
     if t.is_contiguous() or t.dim() != 2:
-        at = _bytes_of(t, rows * cols, esize, what)
+        own = _row_stride(t, rows, cols, what)
+        at = _bytes_of(t, (rows - 1) * own + cols if rows > 0 else 0, esize, what)
     else:
         if tuple(t.shape) != (rows, cols):
             raise ValueError(f"{what} is {tuple(t.shape)}; the call needs {(rows, cols)}")
@@ -657,7 +679,7 @@ def _matrix(t, rows: int, cols: int, esize: int, ld: int | None, what: str) -> t
         if rows > 1:
             own = t.stride(0)
         at = _bytes_of(t[0, :], cols, esize, what) if rows else t.data_ptr()
-    if ld is not None and int(ld) != own:
+    if ld is not None and int(ld) != own and rows > 1:
         raise ValueError(f"{what} has row stride {own}, not {ld}")
     return at, int(own)
 

@@ -1,0 +1,100 @@
+"""What the binding makes of a tensor argument's shape, without a device: the
+row stride of matrices whose rows are wider than the call's, and refusals of
+tensors that the call would read or write at the wrong place."""
+import pytest
+
+import implicit_gemm_dgrad_gb300 as cdg
+
+P = [1 << 24 << i for i in range(1, 14)]  # far-apart 16-byte aligned addresses
+
+
+class FakeCuda:
+    """Stands in for a contiguous CUDA tensor of a given shape."""
+    is_cuda = True
+
+    def __init__(self, *shape, esize=2, floating=True, at=1 << 24):
+        self.shape, self.esize, self.floating, self.at = shape, esize, floating, at
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def element_size(self):
+        return self.esize
+
+    def is_contiguous(self):
+        return True
+
+    def is_floating_point(self):
+        return self.floating
+
+    def data_ptr(self):
+        return self.at
+
+
+class Recorder:
+    """Stands in for the library: keeps the arguments of every call."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, {}
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_bytes"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            self.calls[name] = args
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    r = Recorder(cdg.load_library())
+    monkeypatch.setattr(cdg, "load_library", lambda path=None: r)
+    return r
+
+
+def logprobs_ld(lib, logits, rows=4, vocab=100, **kw):
+    cdg.token_logprobs(logits, P[1], P[2], None, rows, vocab, stream=0, **kw)
+    return lib.calls["cdg_token_logprobs"][1]
+
+
+def test_a_wider_contiguous_matrix_keeps_its_row_stride(lib):
+    assert logprobs_ld(lib, FakeCuda(4, 128)) == 128
+    assert logprobs_ld(lib, FakeCuda(4, 128), ld=128) == 128
+    assert logprobs_ld(lib, FakeCuda(2, 2, 128)) == 128       # batch x positions x padded vocabulary
+    assert logprobs_ld(lib, FakeCuda(6, 128)) == 128          # and more rows than the call takes
+    assert logprobs_ld(lib, FakeCuda(1, 128), rows=1) == 128
+    assert logprobs_ld(lib, FakeCuda(1, 128), rows=1, ld=100) >= 100  # one row: no stride to check
+    cdg.token_logprobs_grad(FakeCuda(4, 128), P[1], P[2], None, P[3], None, FakeCuda(4, 104, at=P[4]), 4, 100, stream=0)
+    args = lib.calls["cdg_token_logprobs_grad"]
+    assert (args[1], args[13]) == (128, 104)
+    cdg.embed(FakeCuda(10, 24), P[1], FakeCuda(4, 32, at=P[2]), 4, 10, 16, stream=0)
+    args = lib.calls["cdg_embed"]
+    assert (args[1], args[10]) == (24, 32)
+    cdg.embed_grad(FakeCuda(4, 24), P[1], FakeCuda(10, 20, at=P[2]), P[3], 4, 10, 16, stream=0)
+    args = lib.calls["cdg_embed_grad"]
+    assert (args[1], args[10]) == (24, 20)
+
+
+def test_dense_matrices_stay_dense(lib):
+    assert logprobs_ld(lib, FakeCuda(4, 100)) == 100
+    assert logprobs_ld(lib, FakeCuda(9, 100)) == 100          # a buffer for more rows
+    assert logprobs_ld(lib, FakeCuda(2, 2, 100)) == 100
+    assert logprobs_ld(lib, FakeCuda(400)) == 100
+    assert logprobs_ld(lib, FakeCuda(1000)) == 100
+    assert logprobs_ld(lib, FakeCuda(4, 10, 10)) == 100       # a row in two dimensions
+    assert logprobs_ld(lib, FakeCuda(2, 200)) == 100          # as many elements as the call takes, in another shape
+
+
+@pytest.mark.parametrize("shape,ld", [((3, 128), None), ((4, 128), 100), ((4, 128), 130), ((3, 3, 50), None),
+                                      ((8, 60), None), ((5, 10, 11), None)])
+def test_matrices_that_cannot_be_rows_of_the_call_are_refused(lib, shape, ld):
+    with pytest.raises(ValueError, match="logits"):
+        logprobs_ld(lib, FakeCuda(*shape), ld=ld)
