@@ -684,6 +684,14 @@ def _matrix(t, rows: int, cols: int, esize: int, ld: int | None, what: str) -> t
     return at, int(own)
 
 
+def _dense_matrix(t, rows: int, cols: int, esize: int, what: str) -> int | None:
+    """Address of a rows x cols argument whose rows lie one after the other."""
+    at, own = _matrix(t, rows, cols, esize, None, what)
+    if own != cols and rows > 1 and cols > 0:
+        raise ValueError(f"{what} must have dense rows of {cols}; it has row stride {own}")
+    return at
+
+
 def _tokens(t, n: int, what: str) -> tuple[int | None, int]:
     """Address and bytes per number of a token list (int32 or int64; a raw address is int64)."""
     if t is None or isinstance(t, int):
@@ -707,8 +715,8 @@ def token_logprobs(logits, targets, logp, lse, rows: int, vocab: int, dtype="bf1
     tg, ib = _tokens(targets, rows, "targets")
     rc = load_library().cdg_token_logprobs(
         lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), top, _dense(logp, rows, 4, "logp"),
-        _dense(lse, rows, 4, "lse"), _dense(entropy, rows, 4, "entropy"), _dense(top_ids, rows * top, 4, "top_ids"),
-        _dense(top_logp, rows * top, 4, "top_logp"), _stream(stream))
+        _dense(lse, rows, 4, "lse"), _dense(entropy, rows, 4, "entropy"), _dense_matrix(top_ids, rows, top, 4, "top_ids"),
+        _dense_matrix(top_logp, rows, top, 4, "top_logp"), _stream(stream))
     if rc != OK:
         raise CdgError(rc, "cdg_token_logprobs")
 

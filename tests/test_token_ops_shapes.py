@@ -98,3 +98,30 @@ def test_dense_matrices_stay_dense(lib):
 def test_matrices_that_cannot_be_rows_of_the_call_are_refused(lib, shape, ld):
     with pytest.raises(ValueError, match="logits"):
         logprobs_ld(lib, FakeCuda(*shape), ld=ld)
+
+
+def top_call(ids, logp, rows=4, top=20):
+    cdg.token_logprobs(FakeCuda(rows, 100), None, None, P[1], rows, 100, top=top, top_ids=ids, top_logp=logp, stream=0)
+
+
+@pytest.mark.parametrize("shape", [(4, 20), (6, 20), (2, 2, 20), (80,), (100,)])
+def test_alternatives_are_written_dense(lib, shape):
+    top_call(FakeCuda(*shape, esize=4, floating=False), FakeCuda(*shape, esize=4))
+    assert "cdg_token_logprobs" in lib.calls
+
+
+@pytest.mark.parametrize("shape", [(4, 32), (2, 2, 32), (4, 21)])
+def test_alternatives_of_another_width_are_refused(lib, shape):
+    """The alternatives' rows are dense: into a wider tensor they would be written side by side, not at its rows."""
+    good = (4, 20)
+    with pytest.raises(ValueError, match="top_ids"):
+        top_call(FakeCuda(*shape, esize=4, floating=False), FakeCuda(*good, esize=4))
+    with pytest.raises(ValueError, match="top_logp"):
+        top_call(FakeCuda(*good, esize=4, floating=False), FakeCuda(*shape, esize=4))
+    top_call(FakeCuda(1, 32, esize=4, floating=False), FakeCuda(1, 32, esize=4), rows=1)  # a single row has no stride
+
+
+def test_alternatives_without_top_are_the_librarys_refusal():
+    with pytest.raises(cdg.CdgError) as e:
+        top_call(FakeCuda(4, 20, esize=4, floating=False), FakeCuda(4, 20, esize=4), top=0)
+    assert e.value.status == 1
