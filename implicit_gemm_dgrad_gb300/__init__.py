@@ -610,20 +610,44 @@ def _dtype(dtype) -> int:
     return ANY_DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
 
 
-def _esize(dtype) -> int:
-    return 4 if _dtype(dtype) == F32 else 2
+# Element types of the tensor arguments, by torch's names (numpy's are the same), and their bytes
+_TYPES = {F16: "float16", BF16: "bfloat16", F32: "float32"}
+_SIZES = {"float16": 2, "bfloat16": 2, "float32": 4, "int32": 4, "int64": 8, None: 2}
+
+
+def _type(dtype) -> str | None:
+    """The element type of a dtype argument (None for one that the library refuses)."""
+    return _TYPES.get(_dtype(dtype))
+
+
+_type_names: dict = {}  # by dtype object, as they are met
+
+
+def _type_name(t) -> str | None:
+    """The name of a tensor's element type; None for an object that does not say."""
+    dt = getattr(t, "dtype", None)
+    if dt is None:
+        return None
+    name = _type_names.get(dt)
+    if name is None:
+        name = _type_names[dt] = str(dt).rpartition(".")[2]
+    return name
 
 
 _tensor = _cuda_device = None  # torch.Tensor and the current device's number, once a torch tensor has been seen
 
 
-def _bytes_of(t, n: int, esize: int, what: str) -> int:
-    """Address of a dense CUDA tensor of at least n elements of esize bytes."""
-    if type(t) is _tensor and t.itemsize == esize and t.nbytes >= n * esize and t.is_contiguous() and \
+def _bytes_of(t, n: int, kind: str | None, what: str) -> int:
+    """Address of a dense CUDA tensor of at least n elements of type kind."""
+    esize = _SIZES[kind]
+    if type(t) is _tensor and _type_names.get(t.dtype) == kind and t.nbytes >= n * esize and t.is_contiguous() and \
             t.get_device() == _cuda_device():
         return t.data_ptr()  # what the checks below find, without their cost
     if t.element_size() != esize:
         raise ValueError(f"{what} has elements of {t.element_size()} bytes; {esize} are needed")
+    name = _type_name(t)
+    if name is not None and kind is not None and name != kind:
+        raise ValueError(f"{what} has elements of type {name}; {kind} is needed")
     _check_buffer(t, n * esize, what)
     if _tensor is None and type(t).__module__ == "torch":
         import torch
@@ -631,11 +655,11 @@ def _bytes_of(t, n: int, esize: int, what: str) -> int:
     return t.data_ptr()
 
 
-def _dense(t, n: int, esize: int, what: str) -> int | None:
-    """Address of a dense argument of n elements of esize bytes (None stays None)."""
+def _dense(t, n: int, kind: str | None, what: str) -> int | None:
+    """Address of a dense argument of n elements of type kind (None stays None)."""
     if t is None or isinstance(t, int):
         return t
-    return _bytes_of(t, n, esize, what)
+    return _bytes_of(t, n, kind, what)
 
 
 def _row_stride(t, rows: int, cols: int, what: str) -> int:
@@ -658,7 +682,7 @@ def _row_stride(t, rows: int, cols: int, what: str) -> int:
     return last
 
 
-def _matrix(t, rows: int, cols: int, esize: int, ld: int | None, what: str) -> tuple[int | None, int]:
+def _matrix(t, rows: int, cols: int, kind: str | None, ld: int | None, what: str) -> tuple[int | None, int]:
     """Address and row stride of a rows x cols argument.  A contiguous tensor's
     rows may be wider than cols, and more than rows; another 2-D tensor of shape
     (rows, cols) may have any row stride with unit column stride (a slice of a
@@ -668,7 +692,7 @@ def _matrix(t, rows: int, cols: int, esize: int, ld: int | None, what: str) -> t
     own = cols
     if t.is_contiguous() or t.dim() != 2:
         own = _row_stride(t, rows, cols, what)
-        at = _bytes_of(t, (rows - 1) * own + cols if rows > 0 else 0, esize, what)
+        at = _bytes_of(t, (rows - 1) * own + cols if rows > 0 else 0, kind, what)
     else:
         if tuple(t.shape) != (rows, cols):
             raise ValueError(f"{what} is {tuple(t.shape)}; the call needs {(rows, cols)}")
@@ -678,15 +702,15 @@ def _matrix(t, rows: int, cols: int, esize: int, ld: int | None, what: str) -> t
             raise ValueError(f"{what} has overlapping rows (row stride {t.stride(0)} for {cols} columns)")
         if rows > 1:
             own = t.stride(0)
-        at = _bytes_of(t[0, :], cols, esize, what) if rows else t.data_ptr()
+        at = _bytes_of(t[0, :], cols, kind, what) if rows else t.data_ptr()
     if ld is not None and int(ld) != own and rows > 1:
         raise ValueError(f"{what} has row stride {own}, not {ld}")
     return at, int(own)
 
 
-def _dense_matrix(t, rows: int, cols: int, esize: int, what: str) -> int | None:
+def _dense_matrix(t, rows: int, cols: int, kind: str, what: str) -> int | None:
     """Address of a rows x cols argument whose rows lie one after the other."""
-    at, own = _matrix(t, rows, cols, esize, None, what)
+    at, own = _matrix(t, rows, cols, kind, None, what)
     if own != cols and rows > 1 and cols > 0:
         raise ValueError(f"{what} must have dense rows of {cols}; it has row stride {own}")
     return at
@@ -697,9 +721,9 @@ def _tokens(t, n: int, what: str) -> tuple[int | None, int]:
     if t is None or isinstance(t, int):
         return t, 8
     size = t.element_size()
-    if size not in (4, 8) or t.is_floating_point():
+    if size not in (4, 8) or t.is_floating_point() or _type_name(t) not in ("int32", "int64", None):
         raise ValueError(f"{what} must hold int32 or int64 token numbers")
-    return _bytes_of(t, n, size, what), size
+    return _bytes_of(t, n, "int64" if size == 8 else "int32", what), size
 
 
 def token_logprobs(logits, targets, logp, lse, rows: int, vocab: int, dtype="bf16", scale: float = 1.0,
@@ -711,12 +735,12 @@ def token_logprobs(logits, targets, logp, lse, rows: int, vocab: int, dtype="bf1
     entries with their log probabilities.  Outputs fp32 (top_ids int32); a
     target list or output that is not wanted is None."""
     rows, vocab, top = int(rows), int(vocab), int(top)
-    lg, ld = _matrix(logits, rows, vocab, _esize(dtype), ld, "logits")
+    lg, ld = _matrix(logits, rows, vocab, _type(dtype), ld, "logits")
     tg, ib = _tokens(targets, rows, "targets")
     rc = load_library().cdg_token_logprobs(
-        lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), top, _dense(logp, rows, 4, "logp"),
-        _dense(lse, rows, 4, "lse"), _dense(entropy, rows, 4, "entropy"), _dense_matrix(top_ids, rows, top, 4, "top_ids"),
-        _dense_matrix(top_logp, rows, top, 4, "top_logp"), _stream(stream))
+        lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), top, _dense(logp, rows, "float32", "logp"),
+        _dense(lse, rows, "float32", "lse"), _dense(entropy, rows, "float32", "entropy"),
+        _dense_matrix(top_ids, rows, top, "int32", "top_ids"), _dense_matrix(top_logp, rows, top, "float32", "top_logp"), _stream(stream))
     if rc != OK:
         raise CdgError(rc, "cdg_token_logprobs")
 
@@ -728,13 +752,13 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logp, g_entropy, dlogit
     gradients g_logp and g_entropy (None: no entropy term) into dlogits, which
     may be the logits themselves."""
     rows, vocab = int(rows), int(vocab)
-    lg, ld = _matrix(logits, rows, vocab, _esize(dtype), ld, "logits")
-    dl, ld_d = _matrix(dlogits, rows, vocab, _esize(dtype), ld_d, "dlogits")
+    lg, ld = _matrix(logits, rows, vocab, _type(dtype), ld, "logits")
+    dl, ld_d = _matrix(dlogits, rows, vocab, _type(dtype), ld_d, "dlogits")
     tg, ib = _tokens(targets, rows, "targets")
     rc = load_library().cdg_token_logprobs_grad(
-        lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), _dense(lse, rows, 4, "lse"),
-        _dense(entropy, rows, 4, "entropy"), _dense(g_logp, rows, 4, "g_logp"),
-        _dense(g_entropy, rows, 4, "g_entropy"), dl, ld_d, _stream(stream))
+        lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), _dense(lse, rows, "float32", "lse"),
+        _dense(entropy, rows, "float32", "entropy"), _dense(g_logp, rows, "float32", "g_logp"),
+        _dense(g_entropy, rows, "float32", "g_entropy"), dl, ld_d, _stream(stream))
     if rc != OK:
         raise CdgError(rc, "cdg_token_logprobs_grad")
 
@@ -743,8 +767,8 @@ def embed(table, tokens, out, count: int, vocab: int, dim: int, dtype="bf16", sc
           ld_table: int | None = None, ld_out: int | None = None, stream=None) -> None:
     """out[i] = scale * table[tokens[i]], zeros where there is no token (cdg_embed)."""
     count, vocab, dim = int(count), int(vocab), int(dim)
-    tb, ld_table = _matrix(table, vocab, dim, _esize(dtype), ld_table, "table")
-    ou, ld_out = _matrix(out, count, dim, _esize(dtype), ld_out, "out")
+    tb, ld_table = _matrix(table, vocab, dim, _type(dtype), ld_table, "table")
+    ou, ld_out = _matrix(out, count, dim, _type(dtype), ld_out, "out")
     tk, ib = _tokens(tokens, count, "tokens")
     rc = load_library().cdg_embed(tb, ld_table, tk, ib, count, vocab, dim, _dtype(dtype), float(scale), ou, ld_out,
                                   _stream(stream))
@@ -766,8 +790,8 @@ def embed_grad(dout, tokens, dtable, workspace, count: int, vocab: int, dim: int
     """dtable[v] = scale * the sum of dout[i] over the i with tokens[i] = v
     (cdg_embed_grad); accumulate=True adds to the rows that tokens point to."""
     count, vocab, dim = int(count), int(vocab), int(dim)
-    do, ld_dout = _matrix(dout, count, dim, _esize(dtype), ld_dout, "dout")
-    dt, ld_dtable = _matrix(dtable, vocab, dim, 4 if out_f32 else _esize(dtype), ld_dtable, "dtable")
+    do, ld_dout = _matrix(dout, count, dim, _type(dtype), ld_dout, "dout")
+    dt, ld_dtable = _matrix(dtable, vocab, dim, "float32" if out_f32 else _type(dtype), ld_dtable, "dtable")
     tk, ib = _tokens(tokens, count, "tokens")
     if workspace is not None and not isinstance(workspace, int):
         _check_buffer(workspace, embed_grad_workspace_bytes(count, vocab, dim), "workspace")
@@ -834,9 +858,9 @@ class MuonPlan:
 
     def orthogonalize(self, U, O, workspace, stream=None) -> None:
         """O = the Newton-Schulz orthogonalisation of every matrix of U (cdg_muon_orthogonalize)."""
-        n, es = self._elements(), _esize(self.dtype)
+        n, kind = self._elements(), _type(self.dtype)
         _check_buffer(workspace, self.workspace_bytes, "workspace")
-        rc = self.lib.cdg_muon_orthogonalize(self.handle, _dense(U, n, es, "U"), _dense(O, n, es, "O"),
+        rc = self.lib.cdg_muon_orthogonalize(self.handle, _dense(U, n, kind, "U"), _dense(O, n, kind, "O"),
                                              _addr(workspace), _stream(stream))
         if rc != OK:
             raise CdgError(rc, "cdg_muon_orthogonalize")
@@ -849,8 +873,8 @@ class MuonPlan:
         n = self._elements()
         _check_buffer(workspace, self.workspace_bytes, "workspace")
         rc = self.lib.cdg_muon_step(
-            self.handle, _dense(W, n, 4, "W"), _dense(G, n, _esize(self.dtype), "G"), _dense(M, n, 4, "M"),
-            _dense(W_out, n, 4, "W_out"), _dense(M_out, n, 4, "M_out"), float(lr), float(momentum),
+            self.handle, _dense(W, n, "float32", "W"), _dense(G, n, _type(self.dtype), "G"), _dense(M, n, "float32", "M"),
+            _dense(W_out, n, "float32", "W_out"), _dense(M_out, n, "float32", "M_out"), float(lr), float(momentum),
             float(weight_decay), float(update_scale), int(bool(nesterov)), _addr(workspace), _stream(stream))
         if rc != OK:
             raise CdgError(rc, "cdg_muon_step")

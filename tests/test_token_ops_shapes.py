@@ -125,3 +125,66 @@ def test_alternatives_without_top_are_the_librarys_refusal():
     with pytest.raises(cdg.CdgError) as e:
         top_call(FakeCuda(4, 20, esize=4, floating=False), FakeCuda(4, 20, esize=4), top=0)
     assert e.value.status == 1
+
+
+def typed(name, *shape, at=1 << 24):
+    """A contiguous stand-in that says its type, as torch's tensors do."""
+    torch = pytest.importorskip("torch")
+    dt = getattr(torch, name)
+    t = FakeCuda(*shape, esize=dt.itemsize, floating=dt.is_floating_point, at=at)
+    t.dtype = dt
+    return t
+
+
+@pytest.mark.parametrize("dtype,wrong", [("bf16", "float16"), ("f16", "bfloat16"), ("bf16", "int16"), ("f32", "int32")])
+def test_matrices_of_another_type_are_refused(lib, dtype, wrong):
+    """Elements of the right size and the wrong type would be read as other numbers."""
+    right = {"f16": "float16", "bf16": "bfloat16", "f32": "float32"}[dtype]
+    with pytest.raises(ValueError, match="logits.*type"):
+        cdg.token_logprobs(typed(wrong, 4, 100), P[1], P[2], None, 4, 100, dtype, stream=0)
+    with pytest.raises(ValueError, match="dlogits.*type"):
+        cdg.token_logprobs_grad(typed(right, 4, 100), P[1], P[2], None, P[3], None, typed(wrong, 4, 100), 4, 100, dtype, stream=0)
+    with pytest.raises(ValueError, match="table.*type"):
+        cdg.embed(typed(wrong, 10, 16), P[1], P[2], 4, 10, 16, dtype, stream=0)
+    with pytest.raises(ValueError, match="out.*type"):
+        cdg.embed(P[0], P[1], typed(wrong, 4, 16), 4, 10, 16, dtype, stream=0)
+    with pytest.raises(ValueError, match="dout.*type"):
+        cdg.embed_grad(typed(wrong, 4, 16), P[1], P[2], P[3], 4, 10, 16, dtype, stream=0)
+    with pytest.raises(ValueError, match="dtable.*type"):
+        cdg.embed_grad(P[0], P[1], typed(wrong, 10, 16), P[3], 4, 10, 16, dtype, stream=0)
+    p = cdg.muon_plan_host(8, 16, dtype=dtype)
+    ws = typed("uint8", p.workspace_bytes)
+    for a, b in ((typed(wrong, 8, 16), P[1]), (P[0], typed(wrong, 8, 16))):
+        with pytest.raises(ValueError, match="[UO] .*type"):
+            p.orthogonalize(a, b, ws)
+    with pytest.raises(ValueError, match="G.*type"):
+        p.step(P[0], typed(wrong, 8, 16), P[1], P[2], P[3], ws, lr=0.1)
+
+
+def test_fp32_arguments_and_token_numbers_have_their_types(lib):
+    logits = typed("bfloat16", 4, 100)
+    for bad in ("int32",):
+        with pytest.raises(ValueError, match="logp.*type"):
+            cdg.token_logprobs(logits, P[1], typed(bad, 4), None, 4, 100, stream=0)
+        with pytest.raises(ValueError, match="entropy.*type"):
+            cdg.token_logprobs(logits, None, None, P[2], 4, 100, entropy=typed(bad, 4), stream=0)
+        with pytest.raises(ValueError, match="g_logp.*type"):
+            cdg.token_logprobs_grad(logits, P[1], P[2], None, typed(bad, 4), None, P[4], 4, 100, stream=0)
+    with pytest.raises(ValueError, match="top_ids.*type"):
+        top_call(typed("float32", 4, 20), typed("float32", 4, 20))
+    with pytest.raises(ValueError, match="token numbers"):
+        cdg.embed(P[0], typed("complex64", 4), P[2], 4, 10, 16, stream=0)
+    with pytest.raises(ValueError, match="dtable.*type"):
+        cdg.embed_grad(P[0], P[1], typed("int32", 10, 16), P[3], 4, 10, 16, out_f32=True, stream=0)
+    p = cdg.muon_plan_host(8, 16)
+    with pytest.raises(ValueError, match="M_out.*type"):
+        p.step(P[0], P[1], P[2], P[3], typed("int32", 8, 16), typed("uint8", p.workspace_bytes), lr=0.1)
+
+
+def test_the_right_types_pass(lib):
+    for dtype, name in (("f16", "float16"), ("bf16", "bfloat16"), ("f32", "float32"), (cdg.BF16, "bfloat16")):
+        for index in ("int32", "int64"):
+            cdg.token_logprobs(typed(name, 4, 100), typed(index, 4), typed("float32", 4), None, 4, 100, dtype, top=2,
+                               top_ids=typed("int32", 4, 2), top_logp=typed("float32", 4, 2), stream=0)
+            cdg.embed_grad(typed(name, 4, 16), typed(index, 4), typed("float32", 10, 16), P[3], 4, 10, 16, dtype, out_f32=True,
+                           stream=0)
