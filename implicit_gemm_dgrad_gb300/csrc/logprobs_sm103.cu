@@ -8,8 +8,9 @@
 //
 // and when a thread's group of vectors holds a larger value, s and e move to
 // the new reference: with r = 2^(ref - ref'), s' = s r and
-// e' = r (e + (ref - ref') s).  The reference is the rounded product itself,
-// so it drops out exactly: lse = ln2 (ref + log2 s), and the entropy is
+// e' = r (e + (ref - ref') s).  The reference is the rounded product itself, so
+// its rounding is known: lse = scale zmax + ln2 (log2 s - (zmax c - ref)), one
+// rounding of lse's size (ln2 (ref + log2 s) takes three), and the entropy is
 // ln2 (log2 s - e / s).  Threads, warps and the CTAs of a cluster are joined by
 // the same rule, in a fixed order.
 //
@@ -605,6 +606,8 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprob
     const float ref = reference(all.zmax, p.c);
 
     const float logs = log2f(all.s);
+    // log of the sum of exp(scale (z - zmax)): the reference's own rounding, zmax c - ref, comes off
+    const float spread = kLn2 * (extreme ? logs : logs - fmaf(all.zmax, p.c, -ref));
     const bool none = all.zmax == -INFINITY && all.s == 0.0f;  // nothing but -inf
     const bool bad = isnan(all.s);
     auto logp_of = [&](float z) {
@@ -612,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprob
         return kLn2 * ((extreme ? (z - all.zmax) * p.c : fmaf(z, p.c, -ref)) - logs);
     };
     if (tid == 0) {
-        if (p.lse) p.lse[i] = none ? -INFINITY : extreme ? fmaf(all.zmax, p.scale, kLn2 * logs) : kLn2 * (ref + logs);
+        if (p.lse) p.lse[i] = none ? -INFINITY : fmaf(all.zmax, p.scale, spread);
         if (p.entropy) p.entropy[i] = none ? 0.0f : kLn2 * (logs - all.e / all.s);
         if (p.logp) p.logp[i] = target >= 0 ? logp_of(z_target) : 0.0f;
     }

@@ -1,0 +1,100 @@
+"""GPU tests of the token log probabilities over the whole range of their
+logits: rows far from zero, and finite values at the type's limits beside
+ordinary ones.  Against the definition in 64 bits.
+
+Tolerances (u = 2^-24, L = lse - max y, D = the mean of max y - y under p): the
+sums hold exponentials within 2^-22 of exponents within 2 u D, added in trees of
+vocab/512 + 16 terms; one rounding of the result, half a unit of its last
+place, and for logp one of z - max z, u |logp - L|.  The entropy is a difference
+of two such sums, of size up to 1 + log vocab."""
+import numpy as np
+import pytest
+
+import implicit_gemm_dgrad_gb300 as cdg
+
+pytestmark = pytest.mark.gpu
+
+# rows, vocab: a warp a row, a CTA a row, a row over a cluster of CTAs
+FORMS = [(1000, 300), (5, 3000), (2, 20011)]
+
+
+def _dt(dtype):
+    import torch
+    return {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+
+
+def lowest(dtype):
+    import torch
+    return torch.finfo(_dt(dtype)).min
+
+
+def run(z, targets, dtype, scale=1.0, top=0):
+    """Answers as float64, and the logits as the type holds them."""
+    import torch
+    rows, vocab = z.shape
+    lg = torch.from_numpy(z).to(_dt(dtype)).cuda()
+    f32 = dict(device="cuda", dtype=torch.float32)
+    out = {k: torch.empty(rows, **f32) for k in ("logp", "lse", "entropy")}
+    ids, tl = torch.empty(rows, top, device="cuda", dtype=torch.int32), torch.empty(rows, top, **f32)
+    cdg.token_logprobs(lg, torch.from_numpy(targets).cuda(), out["logp"], out["lse"], rows, vocab, dtype, scale=scale,
+                       entropy=out["entropy"], top=top, top_ids=ids if top else None, top_logp=tl if top else None)
+    res = {k: v.cpu().numpy().astype(np.float64) for k, v in out.items()}
+    return dict(res, top_ids=ids.cpu().numpy(), top=tl.cpu().numpy().astype(np.float64), z=lg.double().cpu().numpy())
+
+
+def definition(z, targets, scale, top):
+    y = z * float(np.float32(scale))
+    m = y.max(1, keepdims=True)
+    with np.errstate(under="ignore"):
+        w = np.exp(y - m)
+        L = np.log(w.sum(1))
+        p = w / w.sum(1, keepdims=True)
+        D = (p * (m - y)).sum(1)
+    lp = (y - m) - L[:, None]
+    ids = np.argsort(-z, axis=1, kind="stable")[:, :top]
+    has = (targets >= 0) & (targets < z.shape[1])
+    return dict(lse=m[:, 0] + L, L=L, D=D, logp=np.where(has, lp[np.arange(len(z)), np.where(has, targets, 0)], 0.0), ids=ids,
+                top=np.take_along_axis(lp, ids, 1), entropy=L + D)
+
+
+def half_unit(x):
+    """Half a unit of the last place of fp32 numbers of x's size."""
+    return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -126))) - 24)
+
+
+def within(got, ref, tol, what):
+    with np.errstate(over="ignore"):
+        held = ref.astype(np.float32).astype(np.float64)
+    far = np.isinf(held)  # past fp32
+    assert np.array_equal(got[far], held[far]), what
+    worst = np.max(np.abs(got - ref)[~far] / np.broadcast_to(tol, ref.shape)[~far], initial=0.0)
+    assert worst <= 1.0, f"{what}: {worst:.3g} times the tolerance"
+
+
+def check(z, targets, dtype, scale=1.0, top=0, what=("lse", "entropy", "logp", "top")):
+    got = run(z, targets, dtype, scale, top)
+    ref = definition(got["z"], targets, scale, top)
+    u, vocab = 2.0 ** -24, z.shape[1]
+    sums = u * (vocab / 512 + 16) + 2.0 ** -22 + 2 * u * ref["D"] + half_unit(ref["L"]) + 2.0 ** -24
+    if "lse" in what:
+        within(got["lse"], ref["lse"], sums + half_unit(ref["lse"]), "lse")
+    if "entropy" in what:
+        within(got["entropy"], ref["entropy"], sums * (3 + np.log(vocab)), "entropy")
+    if "logp" in what:
+        within(got["logp"], ref["logp"], sums + half_unit(ref["logp"]) + 2 * u * (np.abs(ref["logp"]) + ref["L"]), "logp")
+    if "top" in what:
+        assert np.array_equal(got["top_ids"], ref["ids"])
+        within(got["top"], ref["top"], sums[:, None] + half_unit(ref["top"]) + 2 * u * (np.abs(ref["top"]) + ref["L"][:, None]),
+               "top_logp")
+    return got
+
+
+@pytest.mark.parametrize("offset", [20.0, 90.0, -500.0, 3000.0])
+@pytest.mark.parametrize("rows,vocab", [(2000, 1000), (600, 2000), (8, 30000)])
+def test_lse_of_rows_far_from_zero(rows, vocab, offset):
+    """lse takes one rounding, whatever the size of the logits."""
+    rng = np.random.default_rng(int(abs(offset)))
+    z = rng.standard_normal((rows, vocab)) * 1.5 + offset
+    t = rng.integers(0, vocab, rows)
+    check(z, t, "f32", what=("lse", "entropy"))
+    check(z, t, "f32", scale=0.7, what=("lse", "entropy"))
