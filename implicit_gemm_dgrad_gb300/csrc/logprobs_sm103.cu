@@ -53,6 +53,13 @@ constexpr int kUnroll = 4;          // 16-byte loads in flight per thread
 constexpr int kCtasPerSm = 6;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1000.0f;  // 2^-1000 is 0 in fp32: exponents are clamped here so that 0 * -inf does not arise
+// The lowest reference.  Beyond 2^24 the rounding of z c alone is more than a
+// half, beyond 2^31 more than an fp32 exponent holds: the sums of a thread that
+// has met nothing but masked entries (-1e10, the type's lowest value) would be
+// inf, and NaN once joined.  About this reference they are 0 instead, as they
+// are beside any logit that is not as far out.  Rows whose largest logit comes
+// within a factor of two of it, on either side of zero, take a second pass.
+constexpr float kLowest = -16777216.0f;
 
 struct LogprobArgs {
     const void *logits, *targets;
@@ -240,7 +247,7 @@ struct Slice {
 };
 
 // A thread's running sums while it reads: s and e as two numbers each (even
-// and odd elements).
+// and odd elements), about ref, the larger of kLowest and zmax c.
 struct Run {
     float ref, zmax;
     f32x2 s, e;
@@ -249,7 +256,7 @@ struct Run {
 // The reference moves up to y.
 __device__ __forceinline__ void raise(Run &a, float y)
 {
-    if (y > a.ref) {
+    if (y > a.ref) {  // (false for NaN)
         const float d = fmaxf(a.ref - y, kFloor), r = exp2_fast(d);
         const f32x2 rr = pack2(r, r);
         a.e = mul2(rr, fma2(pack2(d, d), a.s, a.e));
@@ -276,8 +283,7 @@ __device__ __forceinline__ void add(Run &a, float z0, float z1, f32x2 c, f32x2 m
 template <typename T, bool CLAMP, int N>
 __device__ __forceinline__ void add_all(Run &a, const uint4 (&v)[N], float c)
 {
-    const float ref = a.ref == -INFINITY ? 0.0f : a.ref;
-    const f32x2 cc = pack2(c, c), minus = pack2(-ref, -ref);
+    const f32x2 cc = pack2(c, c), minus = pack2(-a.ref, -a.ref);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float f[kPerVec<T>];
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprob
     const auto vec_at = [&](int v) { return sl.vec(v + tid); };
 
     // ---- one pass: sums and the thread's maximum
-    Run run{-INFINITY, -INFINITY, 0ull, 0ull};
+    Run run{kLowest, -INFINITY, 0ull, 0ull};
     uint4 x[kUnroll];
     // TOP: the group of vectors that holds the thread's largest logit, and the largest of its other groups
     float top_group = -INFINITY, other_groups = -INFINITY;
@@ -419,8 +425,7 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprob
         const float z = Elem<T>::get(sl.row[single]);
         run.zmax = fmaxf(run.zmax, z);
         raise(run, __fmul_rn(z, p.c));
-        const float ref = run.ref == -INFINITY ? 0.0f : run.ref;
-        add<true>(run, z, -INFINITY, pack2(p.c, p.c), pack2(-ref, -ref));
+        add<true>(run, z, -INFINITY, pack2(p.c, p.c), pack2(-run.ref, -run.ref));
     }
     float last = -INFINITY;
 #pragma unroll
@@ -586,10 +591,10 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprob
 
     if (warp != 0) return;  // the first warp of the team has the sums and writes the row's answers
 
-    // The largest logit is finite, its product with c is not (logits near the
-    // type's limits, e.g. a row masked with its lowest value): sums about the
-    // logit itself, in a second pass by this warp alone.
-    const bool extreme = fabsf(all.zmax) < INFINITY && !(fabsf(all.zmax * p.c) < INFINITY);
+    // The largest logit is finite, its product with c far from zero or infinite
+    // (e.g. a row masked with -1e9 or the type's lowest value): sums about the logit
+    // itself, in a second pass by this warp alone.
+    const bool extreme = fabsf(all.zmax) < INFINITY && !(fabsf(all.zmax * p.c) < -kLowest / 2);
     if (extreme) {
         all.s = all.e = 0.0f;
         for (int j = lane; j < p.vocab; j += 32) {

@@ -98,3 +98,40 @@ def test_lse_of_rows_far_from_zero(rows, vocab, offset):
     t = rng.integers(0, vocab, rows)
     check(z, t, "f32", what=("lse", "entropy"))
     check(z, t, "f32", scale=0.7, what=("lse", "entropy"))
+
+
+def masked(rng, rows, vocab, value):
+    """Ordinary logits with entries at a mask's value: some of each row, and in
+    every fifth row all but three; targets masked or not."""
+    z = rng.standard_normal((rows, vocab)) * 2.5
+    z[rng.random((rows, vocab)) < 0.3] = value
+    z[::5, 3:] = value
+    z[:, 1] = 0.5
+    targets = rng.integers(0, vocab, rows)
+    targets[::5] = vocab - 1
+    return z, targets
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.7, 0.3, 1.3])
+@pytest.mark.parametrize("dtype,value", [("f32", v) for v in (None, -1e30, -1e20, -1e10, -1e9, -2e7, -1e4)] +
+                         [("bf16", v) for v in (None, -1e30, -1e10, -1e9, -1e4)] + [("f16", None), ("f16", -1e4)])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_masks_of_any_value_and_scale(rows, vocab, dtype, value, scale):
+    """Masked entries, however large, leave ordinary rows as they are; a row of
+    nothing but masks shares its probability among them."""
+    z, t = masked(np.random.default_rng(vocab), rows, vocab, lowest(dtype) if value is None else value)
+    z[1] = z[0, 4]  # a mask alone
+    t[1] = 2
+    got = check(z, t, dtype, scale, what=("lse", "entropy"))
+    assert abs(got["entropy"][1] - np.log(vocab)) < 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("exponent", [20, 23, 24, 26, 30, 31, 40])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_rows_of_large_logits(rows, vocab, dtype, exponent):
+    """Every logit about 2^exponent / log2(e), on either side of zero."""
+    rng = np.random.default_rng(exponent)
+    size = 2.0 ** exponent / 1.4426950408889634
+    z = np.sign(rng.standard_normal((rows, 1))) * size * (1 + 2.0 ** -20 * rng.integers(-8, 9, (rows, vocab)))
+    check(z, rng.integers(0, vocab, rows), dtype, what=("lse", "entropy"))
