@@ -615,12 +615,16 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprob
     const float spread = kLn2 * (extreme ? logs : logs - fmaf(all.zmax, p.c, -ref));
     const bool none = all.zmax == -INFINITY && all.s == 0.0f;  // nothing but -inf
     const bool bad = isnan(all.s);
+    const float lse = fmaf(all.zmax, p.scale, spread);
+    // scale (z - zmax) rather than z c - ref: a product with c can pass fp32 where the answer does not
     auto logp_of = [&](float z) {
         if (none) return -INFINITY;
-        return kLn2 * ((extreme ? (z - all.zmax) * p.c : fmaf(z, p.c, -ref)) - logs);
+        const float d = z - all.zmax;
+        return d == -INFINITY && z > -INFINITY ? fmaf(z, p.scale, -lse)  // further apart than fp32 reaches
+                                               : fmaf(d, p.scale, -spread);
     };
     if (tid == 0) {
-        if (p.lse) p.lse[i] = none ? -INFINITY : fmaf(all.zmax, p.scale, spread);
+        if (p.lse) p.lse[i] = none ? -INFINITY : lse;
         if (p.entropy) p.entropy[i] = none ? 0.0f : kLn2 * (logs - all.e / all.s);
         if (p.logp) p.logp[i] = target >= 0 ? logp_of(z_target) : 0.0f;
     }

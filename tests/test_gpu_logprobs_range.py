@@ -135,3 +135,44 @@ def test_rows_of_large_logits(rows, vocab, dtype, exponent):
     size = 2.0 ** exponent / 1.4426950408889634
     z = np.sign(rng.standard_normal((rows, 1))) * size * (1 + 2.0 ** -20 * rng.integers(-8, 9, (rows, vocab)))
     check(z, rng.integers(0, vocab, rows), dtype, what=("lse", "entropy"))
+
+
+@pytest.mark.parametrize("offset", [20.0, 90.0, -500.0, 3000.0])
+@pytest.mark.parametrize("rows,vocab", [(2000, 1000), (600, 2000), (8, 30000)])
+def test_logp_of_rows_far_from_zero(rows, vocab, offset):
+    rng = np.random.default_rng(int(abs(offset)))
+    z = rng.standard_normal((rows, vocab)) * 1.5 + offset
+    check(z, rng.integers(0, vocab, rows), "f32", scale=0.7, top=3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_the_types_lowest_value_beside_ordinary_logits(rows, vocab, dtype):
+    """A masked entry is as improbable as its logit says, not impossible."""
+    z, t = masked(np.random.default_rng(vocab), rows, vocab, lowest(dtype))
+    got = check(z, t, dtype, top=8)
+    assert np.isfinite(got["logp"]).all() and np.isfinite(got["top"]).all()
+
+
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_logits_further_apart_than_the_type_reaches(rows, vocab):
+    """z - max z passes fp32; scale times it need not."""
+    rng = np.random.default_rng(3)
+    z = np.where(rng.random((rows, vocab)) < 0.5, 3e38, -3e38)
+    z[:, :2] = [3e38, -3e38]
+    t = rng.integers(0, vocab, rows)
+    t[0] = 1
+    for scale in (0.3, 1.0):
+        check(z, t, "f32", scale, top=5)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.7, 0.3, 1.3])
+@pytest.mark.parametrize("dtype,value", [("f32", None), ("f32", -1e30), ("f32", -1e9), ("bf16", None), ("bf16", -1e10), ("f16", None)])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_logp_of_masked_tokens(rows, vocab, dtype, value, scale):
+    """The answers are -inf only where scale times the logit passes fp32."""
+    z, t = masked(np.random.default_rng(vocab), rows, vocab, lowest(dtype) if value is None else value)
+    z[1] = z[0, 4]  # a mask alone
+    t[1] = 2
+    got = check(z, t, dtype, scale, top=8)
+    assert abs(got["logp"][1] + np.log(vocab)) < 1e-5
