@@ -51,7 +51,7 @@ constexpr int kCand = 1024;         // candidate keys a CTA ranks
 constexpr int kMaxCluster = kThreads / 32;  // CTAs that share a row (a warp for each one's keys at the end)
 constexpr int kUnroll = 4;          // 16-byte loads in flight per thread
 constexpr int kCtasPerSm = 6;
-constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 constexpr float kFloor = -1000.0f;  // 2^-1000 is 0 in fp32: exponents are clamped here so that 0 * -inf does not arise
 // The lowest reference.  Beyond 2^24 the rounding of z c alone is more than a
 // half, beyond 2^31 more than an fp32 exponent holds: the sums of a thread that
@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 4 : kCtasPerSm) logprob
     if (extreme) {
         all.s = all.e = 0.0f;
         for (int j = lane; j < p.vocab; j += 32) {
-            const float u = max_nan((Elem<T>::get(sl.row[j]) - all.zmax) * p.c, kFloor), w = exp2_fast(u);
+            // (not times c, which passes fp32 for the largest scales)
+            const float u = max_nan((Elem<T>::get(sl.row[j]) - all.zmax) * p.scale * kLog2e, kFloor), w = exp2_fast(u);
             all.s += w;
             all.e = fmaf(w, u, all.e);
         }
@@ -656,7 +657,7 @@ struct GradRow {
     {
         const float t = max_nan(fmaf(z, scale, -lse), kFloor);  // p = 0 there, and its weight stays finite
         const float q = fmaxf(fmaf(z, scale, -lse_h) - lse_h_lo, kFloor);
-        const float p = exp2_fast(t * 1.44269504088896341f);
+        const float p = exp2_fast(t * kLog2e);
         return -scale * fmaf(h, q, g) * p;
     }
 };

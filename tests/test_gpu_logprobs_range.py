@@ -176,3 +176,16 @@ def test_logp_of_masked_tokens(rows, vocab, dtype, value, scale):
     t[1] = 2
     got = check(z, t, dtype, scale, top=8)
     assert abs(got["logp"][1] + np.log(vocab)) < 1e-5
+
+
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_largest_scales(rows, vocab):
+    """scale up to the largest fp32 number: the row's largest logits share the probability."""
+    rng = np.random.default_rng(5)
+    z = rng.integers(-3, 1, (rows, vocab)).astype(float) * 0.25
+    z[:, 0] = 0.0
+    t = rng.integers(0, vocab, rows)
+    t[0] = 0
+    for scale in (1e30, 3e38):
+        got = check(z, t, "f32", scale, top=4)
+        assert np.abs(got["entropy"] - np.log((z == 0.0).sum(1))).max() < 1e-5
