@@ -525,6 +525,8 @@ int cdg_token_logprobs(const void *logits, long long ld, const void *targets, in
  *
  * with log p_j = z_j - lse[i]; lse and entropy as cdg_token_logprobs wrote
  * them.  A row without a token has g = 0; a row of -inf alone gets zeros.
+ * p_j is as exact as an fp32 lse holds it (|lse| 2^-24, relative) and at most
+ * 1: a row of nothing but finite masks gets a bounded gradient, not 1 / vocab.
  * g_entropy may be NULL (h = 0; entropy may then be NULL too).  dlogits has
  * the logits' dtype and may be the logits themselves (same pointer, same
  * stride); any other overlap is CDG_ERR_ALIAS.

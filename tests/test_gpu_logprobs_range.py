@@ -189,3 +189,41 @@ def test_largest_scales(rows, vocab):
     for scale in (1e30, 3e38):
         got = check(z, t, "f32", scale, top=4)
         assert np.abs(got["entropy"] - np.log((z == 0.0).sum(1))).max() < 1e-5
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.7, 1.25, 1.3])
+@pytest.mark.parametrize("dtype,value", [("f32", v) for v in (None, -1e30, -1e20, -1e10, -1e9)] + [("bf16", None), ("bf16", -1e10)])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradient_of_rows_that_are_all_mask(dtype, value, scale, entropy):
+    """lse does not hold such a row's probabilities (one unit of its last place
+    is a large number), but the gradient stays that of probabilities in [0, 1]:
+    zero where the row's gradients are zero, and else no larger than they are."""
+    import torch
+    rows, vocab = 6, 1003
+    z = np.random.default_rng(1).standard_normal((rows, vocab))
+    z[:4] = lowest(dtype) if value is None else value
+    lg = torch.from_numpy(z).to(_dt(dtype)).cuda()
+    t = torch.tensor([-100, 5, -100, 5, 5, -100], device="cuda")
+    g = torch.tensor([0.0, 0.0, 0.5, 0.5, 0.5, 0.5], device="cuda")
+    h = torch.tensor([0.0, 0.0, 0.0, 0.25, 0.25, 0.25], device="cuda") if entropy else None
+    f32 = dict(device="cuda", dtype=torch.float32)
+    logp, lse, H = (torch.empty(rows, **f32) for _ in range(3))
+    cdg.token_logprobs(lg, t, logp, lse, rows, vocab, dtype, scale=scale, entropy=H)
+    d = torch.empty_like(lg)
+    cdg.token_logprobs_grad(lg, t, lse, H if entropy else None, g, h, d, rows, vocab, dtype, scale=scale)
+    got = d.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (got[:3] == 0).all()  # no gradient, or no token
+    assert np.abs(got[3]).max() <= 1.01 * scale * (0.5 + (0.25 * np.log(vocab) if entropy else 0.0))
+    # the ordinary rows beside them
+    zz = lg.double().cpu().numpy()[4:] * float(np.float32(scale))
+    p = np.exp(zz - lse.double().cpu().numpy()[4:, None])
+    ref = -p * np.array([[0.5], [0.0]])
+    if entropy:
+        ref -= 0.25 * p * (np.log(p) + H.double().cpu().numpy()[4:, None])
+    ref[0, 5] += 0.5
+    ref *= float(np.float32(scale))
+    # p within 2^-20 (4 + max|y|), the result rounded to the type
+    unit = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}[dtype]
+    tol = 2.0 ** -20 * (4 + np.abs(zz).max()) * scale * p * (0.5 + 0.25 * (np.abs(np.log(p)) + np.log(vocab)))
+    assert (np.abs(got[4:] - ref) <= tol + unit * 1.001 * np.abs(ref) + 1e-30).all()
