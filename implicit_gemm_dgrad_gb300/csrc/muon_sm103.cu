@@ -163,7 +163,8 @@ __device__ __forceinline__ float first_scale(const CmuPrepare &p, int b, bool wr
             const int k = norm > 0.0f && finite ? max(-100, min(100, 10 - ilogbf(norm))) : 0;
             const float f = ldexpf(1.0f, k);
             pw2 = finite ? f : NAN;  // an infinity or NaN in U: X is NaN
-            if (write) p.xs[b] = f * (norm + p.eps);
+            // (a zero X: any divisor that has a finite square, which a small eps has not)
+            if (write) p.xs[b] = norm == 0.0f ? 1.0f : f * (norm + p.eps);
         }
     }
     __syncthreads();

@@ -584,7 +584,8 @@ size_t cdg_embed_grad_workspace_bytes(long long count, int vocab, int dim);
  * in fp32, so that O is within about 1e-3 of the iteration in exact arithmetic
  * (relative, Frobenius).  With CDG_F32 every operand is two fp16 parts, at
  * three products for one, and O is within about 1e-5.  |U|_F must be representable: its square is summed in
- * fp32.  A zero U gives a zero O; a U with a NaN or an infinity gives NaN.
+ * fp32.  A zero U gives a zero O, whatever eps is; a U with a NaN or an infinity
+ * gives NaN.
  *
  * cdg_muon_step: the whole update of fp32 weights W from a gradient G (dtype)
  * and its momentum M (fp32), all batch x rows x cols, dense:
