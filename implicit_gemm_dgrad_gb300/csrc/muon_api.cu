@@ -125,7 +125,8 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     };
     const size_t nb = static_cast<size_t>(batch);
     const size_t xb = nb * m * h->pitch_x * 2, ab = nb * m * h->pitch_a * 2;
-    h->gram = m <= CMU_SIDE && bounds.gram;
+    // an fp32 plan keeps fp32 accuracy, in both calls; the Gram form does not have it
+    h->gram = m <= CMU_SIDE && bounds.gram && dtype != CDG_F32;
     h->splits = std::min((n + CMU_BK - 1) / CMU_BK, kMaxSplits);
     h->sms = num_sms;
     // low parts of A and B: three products for one (fp32 updates, and small matrices without the Gram form), or P's
@@ -144,9 +145,8 @@ int make_muon_plan(int batch, int rows, int cols, int dtype, int steps, float a,
     h->info.m = m;
     h->info.n = n;
     h->info.transposed = h->transposed;
-    const bool precise = dtype == CDG_F32;
-    h->info.gram = h->gram && !precise;
-    h->info.launches = h->info.gram ? 5 : 2 + 3 * steps;
+    h->info.gram = h->gram;
+    h->info.launches = h->gram ? 5 : 2 + 3 * steps;
     if (!host_only) {
         if (cmu_prepare_kernels() != cudaSuccess || cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess ||
             cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) {
@@ -239,8 +239,7 @@ int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStrea
     p.x_hi = at16(h->x[0][0]);
     p.x_lo = at16(h->x[0][1]);
     p.pitch_x = h->pitch_x;
-    // an fp32 update keeps fp32 accuracy; a step's is scaled by the learning rate
-    const bool precise = p.nesterov < 0 && h->dtype == CDG_F32, gram = h->gram && !precise;
+    const bool precise = h->dtype == CDG_F32, gram = h->gram;
     const int parts = precise || h->m <= CMU_SIDE ? 3 : 1;
     p.has_lo = p.nesterov >= 0 || precise || (parts == 3 && !gram);
     if (cmu_launch_norm(p, s) != cudaSuccess || cmu_launch_split(p, s) != cudaSuccess) return CDG_ERR_CUDA;

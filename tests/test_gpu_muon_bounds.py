@@ -51,3 +51,34 @@ def test_zero_update_of_any_eps(rows, cols, dtype, eps):
     keep = float(np.float32(1.0 - np.float64(np.float32(0.1)) * 0.25))
     assert torch.equal(W_out[1], W[1] * keep) and not M_out[1].any()
     assert torch.isfinite(W_out).all() and torch.isfinite(M_out).all()
+
+
+F32_SHAPES = [(3, 64, 576), (1, 128, 128), (2, 130, 257), (1, 511, 513), (1, 300, 1000), (1, 1000, 300), (1, 1100, 1300),
+              (1, 200, 4608), (1, 200, 9000), (1, 9000, 200)]
+
+
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("kind", ["gauss", "lowrank"])
+@pytest.mark.parametrize("batch,rows,cols", F32_SHAPES)
+def test_fp32_step_keeps_fp32_accuracy(batch, rows, cols, kind, nesterov):
+    """The update of an fp32 plan's step is as exact as its orthogonalize."""
+    import torch
+    G, M = make(batch, rows, cols, kind, 20), make(batch, rows, cols, "gauss", 21)
+    W = torch.zeros_like(G)
+    mu = float(np.float32(0.9))
+    m = mu * M.double() + G.double()
+    o = iterate(G.double() + mu * m if nesterov else m)
+    p = cdg.muon_plan(rows, cols, batch=batch, dtype="f32")
+    bw, W_out = guarded(W.shape, torch.float32)
+    M_out = torch.empty_like(M)
+    p.step(W, G, M, W_out, M_out, workspace(p), lr=1.0, momentum=0.9, nesterov=nesterov)
+    torch.cuda.synchronize()
+    assert p.device_status() == 0 and intact(bw)
+    assert off(-W_out, o) <= BAR["f32"] + 6e-5 / min(rows, cols) ** 0.5 + 2.0 ** -24
+
+
+def test_fp32_plans_say_how_they_run():
+    """No fp32 plan takes the Gram form, whose error exceeds its bound."""
+    small, wide = cdg.muon_plan_host(64, 576, dtype="f32").info(), cdg.muon_plan_host(300, 576, dtype="f32").info()
+    assert small["gram"] == 0 and small["launches"] == wide["launches"] == 17
+    assert cdg.muon_plan_host(64, 576, dtype="bf16").info()["gram"] == 1
