@@ -82,3 +82,50 @@ def test_fp32_plans_say_how_they_run():
     small, wide = cdg.muon_plan_host(64, 576, dtype="f32").info(), cdg.muon_plan_host(300, 576, dtype="f32").info()
     assert small["gram"] == 0 and small["launches"] == wide["launches"] == 17
     assert cdg.muon_plan_host(64, 576, dtype="bf16").info()["gram"] == 1
+
+
+def spectrum(kind, rows, cols, seed):
+    """U with the singular values of `kind` between random orthonormal bases."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    m, n = min(rows, cols), max(rows, cols)
+    q = torch.linalg.qr(torch.randn(n, m, generator=g, device="cuda", dtype=torch.float64))[0]
+    p = torch.linalg.qr(torch.randn(m, m, generator=g, device="cuda", dtype=torch.float64))[0]
+    i = torch.arange(m, device="cuda", dtype=torch.float64)
+    s = {"flat": torch.ones_like(i), "few": torch.where(i < max(1, m // 8), 1.0, 0.02), "decay": 1.0 / (i + 1) ** 2,
+         "wide": 10.0 ** (-4.0 * i / max(1, m - 1))}[kind]
+    u = (p * s) @ q.mT
+    return (u if rows <= cols else u.mT).float()[None].contiguous()
+
+
+@pytest.mark.parametrize("kind", ["flat", "few", "decay", "wide"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(64, 576), (128, 128), (256, 256), (512, 512), (511, 513), (512, 2048), (1100, 1300),
+                                       (200, 4608), (200, 9000), (9000, 200)])
+def test_orthogonalize_is_within_its_stated_bound(rows, cols, dtype, kind):
+    """Spectra other than random matrices'; rows of up to 512 with long K split it
+    over two, four and eight CTAs of a cluster, in one-part and in three-part products."""
+    import torch
+    U = spectrum(kind, rows, cols, rows).to(_dt(dtype))
+    p = cdg.muon_plan(rows, cols, dtype=dtype)
+    ws = workspace(p)
+    buf, O = guarded(U.shape, U.dtype)
+    p.orthogonalize(U, O, ws)
+    torch.cuda.synchronize()
+    assert p.device_status() == 0 and intact(buf)
+    assert off(O, iterate(U)) <= BAR[dtype] + ROUND[dtype]
+    again = torch.empty_like(U)
+    ws.fill_(255)
+    p.orthogonalize(U, again, ws)
+    assert torch.equal(again, O), "not the same bits again"
+
+
+@pytest.mark.parametrize("kind", ["gauss", "lowrank"])
+@pytest.mark.parametrize("batch,rows,cols", F32_SHAPES)
+def test_fp32_orthogonalize_on_all_paths(batch, rows, cols, kind):
+    import torch
+    U = make(batch, rows, cols, kind, 22)
+    p = cdg.muon_plan(rows, cols, batch=batch, dtype="f32")
+    O = torch.empty_like(U)
+    p.orthogonalize(U, O, workspace(p))
+    assert off(O, iterate(U)) <= BAR["f32"]
