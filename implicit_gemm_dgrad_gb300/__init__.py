@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcdg.so")
@@ -611,14 +612,9 @@ def _dtype(dtype) -> int:
 
 
 # Element types of the tensor arguments, by torch's names (numpy's are the same), and their bytes
-_TYPES = {F16: "float16", BF16: "bfloat16", F32: "float32"}
+# (the element type is None for a dtype that the library refuses).
+_TYPES = {F16: "float16", BF16: "bfloat16", F32: "float32", "f16": "float16", "bf16": "bfloat16", "f32": "float32"}
 _SIZES = {"float16": 2, "bfloat16": 2, "float32": 4, "int32": 4, "int64": 8, None: 2}
-
-
-def _type(dtype) -> str | None:
-    """The element type of a dtype argument (None for one that the library refuses)."""
-    return _TYPES.get(_dtype(dtype))
-
 
 _type_names: dict = {}  # by dtype object, as they are met
 
@@ -630,7 +626,7 @@ def _type_name(t) -> str | None:
         return None
     name = _type_names.get(dt)
     if name is None:
-        name = _type_names[dt] = str(dt).rpartition(".")[2]
+        name = _type_names[dt] = sys.intern(str(dt).rpartition(".")[2])
     return name
 
 
@@ -689,6 +685,9 @@ def _matrix(t, rows: int, cols: int, kind: str | None, ld: int | None, what: str
     wider one); a raw address has row stride ld, or cols."""
     if t is None or isinstance(t, int):
         return t, int(ld if ld is not None else cols)
+    if type(t) is _tensor and _type_names.get(t.dtype) == kind and t.nbytes == rows * cols * _SIZES[kind] and ld is None and \
+            t.is_contiguous() and t.get_device() == _cuda_device():
+        return t.data_ptr(), cols  # as in _bytes_of
     own = cols
     if t.is_contiguous() or t.dim() != 2:
         own = _row_stride(t, rows, cols, what)
@@ -720,6 +719,8 @@ def _tokens(t, n: int, what: str) -> tuple[int | None, int]:
     """Address and bytes per number of a token list (int32 or int64; a raw address is int64)."""
     if t is None or isinstance(t, int):
         return t, 8
+    if type(t) is _tensor and _type_names.get(t.dtype) == "int64":
+        return _bytes_of(t, n, "int64", what), 8
     size = t.element_size()
     if size not in (4, 8) or t.is_floating_point() or _type_name(t) not in ("int32", "int64", None):
         raise ValueError(f"{what} must hold int32 or int64 token numbers")
@@ -735,12 +736,13 @@ def token_logprobs(logits, targets, logp, lse, rows: int, vocab: int, dtype="bf1
     entries with their log probabilities.  Outputs fp32 (top_ids int32); a
     target list or output that is not wanted is None."""
     rows, vocab, top = int(rows), int(vocab), int(top)
-    lg, ld = _matrix(logits, rows, vocab, _type(dtype), ld, "logits")
+    lg, ld = _matrix(logits, rows, vocab, _TYPES.get(dtype), ld, "logits")
     tg, ib = _tokens(targets, rows, "targets")
     rc = load_library().cdg_token_logprobs(
         lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), top, _dense(logp, rows, "float32", "logp"),
         _dense(lse, rows, "float32", "lse"), _dense(entropy, rows, "float32", "entropy"),
-        _dense_matrix(top_ids, rows, top, "int32", "top_ids"), _dense_matrix(top_logp, rows, top, "float32", "top_logp"), _stream(stream))
+        _dense_matrix(top_ids, rows, top, "int32", "top_ids"),
+        _dense_matrix(top_logp, rows, top, "float32", "top_logp"), _stream(stream))
     if rc != OK:
         raise CdgError(rc, "cdg_token_logprobs")
 
@@ -752,8 +754,8 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logp, g_entropy, dlogit
     gradients g_logp and g_entropy (None: no entropy term) into dlogits, which
     may be the logits themselves."""
     rows, vocab = int(rows), int(vocab)
-    lg, ld = _matrix(logits, rows, vocab, _type(dtype), ld, "logits")
-    dl, ld_d = _matrix(dlogits, rows, vocab, _type(dtype), ld_d, "dlogits")
+    lg, ld = _matrix(logits, rows, vocab, _TYPES.get(dtype), ld, "logits")
+    dl, ld_d = _matrix(dlogits, rows, vocab, _TYPES.get(dtype), ld_d, "dlogits")
     tg, ib = _tokens(targets, rows, "targets")
     rc = load_library().cdg_token_logprobs_grad(
         lg, ld, tg, ib, rows, vocab, _dtype(dtype), float(scale), _dense(lse, rows, "float32", "lse"),
@@ -767,8 +769,8 @@ def embed(table, tokens, out, count: int, vocab: int, dim: int, dtype="bf16", sc
           ld_table: int | None = None, ld_out: int | None = None, stream=None) -> None:
     """out[i] = scale * table[tokens[i]], zeros where there is no token (cdg_embed)."""
     count, vocab, dim = int(count), int(vocab), int(dim)
-    tb, ld_table = _matrix(table, vocab, dim, _type(dtype), ld_table, "table")
-    ou, ld_out = _matrix(out, count, dim, _type(dtype), ld_out, "out")
+    tb, ld_table = _matrix(table, vocab, dim, _TYPES.get(dtype), ld_table, "table")
+    ou, ld_out = _matrix(out, count, dim, _TYPES.get(dtype), ld_out, "out")
     tk, ib = _tokens(tokens, count, "tokens")
     rc = load_library().cdg_embed(tb, ld_table, tk, ib, count, vocab, dim, _dtype(dtype), float(scale), ou, ld_out,
                                   _stream(stream))
@@ -790,8 +792,8 @@ def embed_grad(dout, tokens, dtable, workspace, count: int, vocab: int, dim: int
     """dtable[v] = scale * the sum of dout[i] over the i with tokens[i] = v
     (cdg_embed_grad); accumulate=True adds to the rows that tokens point to."""
     count, vocab, dim = int(count), int(vocab), int(dim)
-    do, ld_dout = _matrix(dout, count, dim, _type(dtype), ld_dout, "dout")
-    dt, ld_dtable = _matrix(dtable, vocab, dim, "float32" if out_f32 else _type(dtype), ld_dtable, "dtable")
+    do, ld_dout = _matrix(dout, count, dim, _TYPES.get(dtype), ld_dout, "dout")
+    dt, ld_dtable = _matrix(dtable, vocab, dim, "float32" if out_f32 else _TYPES.get(dtype), ld_dtable, "dtable")
     tk, ib = _tokens(tokens, count, "tokens")
     if workspace is not None and not isinstance(workspace, int):
         _check_buffer(workspace, embed_grad_workspace_bytes(count, vocab, dim), "workspace")
@@ -858,7 +860,7 @@ class MuonPlan:
 
     def orthogonalize(self, U, O, workspace, stream=None) -> None:
         """O = the Newton-Schulz orthogonalisation of every matrix of U (cdg_muon_orthogonalize)."""
-        n, kind = self._elements(), _type(self.dtype)
+        n, kind = self._elements(), _TYPES.get(self.dtype)
         _check_buffer(workspace, self.workspace_bytes, "workspace")
         rc = self.lib.cdg_muon_orthogonalize(self.handle, _dense(U, n, kind, "U"), _dense(O, n, kind, "O"),
                                              _addr(workspace), _stream(stream))
@@ -873,7 +875,7 @@ class MuonPlan:
         n = self._elements()
         _check_buffer(workspace, self.workspace_bytes, "workspace")
         rc = self.lib.cdg_muon_step(
-            self.handle, _dense(W, n, "float32", "W"), _dense(G, n, _type(self.dtype), "G"), _dense(M, n, "float32", "M"),
+            self.handle, _dense(W, n, "float32", "W"), _dense(G, n, _TYPES.get(self.dtype), "G"), _dense(M, n, "float32", "M"),
             _dense(W_out, n, "float32", "W_out"), _dense(M_out, n, "float32", "M_out"), float(lr), float(momentum),
             float(weight_decay), float(update_scale), int(bool(nesterov)), _addr(workspace), _stream(stream))
         if rc != OK:
