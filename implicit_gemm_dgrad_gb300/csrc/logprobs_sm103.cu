@@ -20,10 +20,11 @@
 // and smallest of a group on packed 16-bit pairs, and only the first warp of a
 // CTA joins the others' sums (all of them doing so cost 20 us of 105 at 8192 x
 // 32000).  256 threads and 40 registers leave six rows in flight an SM, whose
-// joins overlap the others' reads.  Measured: 8192 x 32000 bf16 84 us (6.2 TB/s),
-// fp32 149 us (7.0 TB/s), 65536 x 1000 bf16 37 us; one row of 131072 4.3 us, by
+// joins overlap the others' reads.  Measured: 8192 x 32000 bf16 85 us (6.2 TB/s),
+// fp32 153 us (6.8 TB/s), 65536 x 1000 bf16 39 us; one row of 131072 3.8 us, by
 // a cluster of eight CTAs that push their sums to the first one (a second
-// exchange would cost another microsecond).
+// exchange would cost another microsecond).  A row that takes the second pass
+// (nothing but finite masks): one of 131072 73 us, 8192 x 32000 of them 206 us.
 //
 // The largest logits: each thread keeps the maximum of its elements (the
 // running maximum above, needed anyway).  The k-th largest of some thread
@@ -32,10 +33,12 @@
 // reach it: a few dozen, ranked by counting larger 64-bit keys (ordered value,
 // then lowest number).  If more than kCand reach it (many equal values) each
 // warp instead keeps an exact sorted list of its k largest keys in one scan.
-// That adds 3.5 us to a single row and 68 us to 8192 x 32000 (20 of them).
+// That adds 3.3 us to a single row (8 of them) and 61 us to 8192 x 32000 (20).
 //
 // Gradient.  One read and one write of every element, nothing joined: 8192 x
-// 32000 bf16 155 us (6.75 TB/s), 6145 x 50021 (rows at every alignment) 187 us.
+// 32000 bf16 152 us (6.9 TB/s), 6145 x 50021 (rows at every alignment) 190 us with
+// the entropy's term, 182 without; 504 us where a row of the logits and its row of
+// the gradient lie differently in 16 bytes, and go element by element.
 #include <cmath>
 
 #include "ptx.cuh"
@@ -753,8 +756,10 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
 }
 
 // Up to this vocabulary a warp takes a row, if there are more rows than run at
-// once with a CTA each; fewer rows end sooner that way (256 x 1000 with 5
-// alternatives: 4.2 us against 8.9; 65536 rows: 242 us against 154).
+// once with a CTA each (65536 x 1000: 39 us against 172, with 5 alternatives 82
+// against 369).  Fewer rows get a CTA each, which ends the longer of them sooner
+// (256 x 4096 with 5 alternatives: 5.1 us against 7.2; 256 x 1000: 4.6 against
+// 4.3).
 constexpr int kWarpVocab = 4096;
 
 template <typename T, bool TOP>

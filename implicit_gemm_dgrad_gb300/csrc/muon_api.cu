@@ -193,7 +193,6 @@ int encode_maps(cdg_muon_st *h, void *workspace)
     return CDG_OK;
 }
 
-// The products after the norm and the first X; the last one writes `out`.
 // The form of a product of M x N outputs over K (maps of 128-row and of 64-row
 // boxes of the B operand for both): of CTA pairs and square tiles the one whose
 // waves take fewer cycles (2048 x 2048 all in pairs: 303 us, in squares: 282;
@@ -225,6 +224,7 @@ struct Final {
     float w_keep, w_step;
 };
 
+// The norm, the first X and the products; the last one writes `out`.
 int run(cdg_muon_st *h, CmuPrepare p, const Final &f, void *workspace, cudaStream_t s)
 {
     const int rc = encode_maps(h, workspace);

@@ -17,7 +17,7 @@
 #define CMU_BK 64
 #define CMU_STAGES 5
 #define CMU_HALF_BYTES (128 * CMU_BK * 2)
-#define CMU_STAGING_BYTES (2 * CMU_HALF_BYTES)  // per group of four epilogue warps: 128 x 64 fp16, twice
+#define CMU_STAGING_BYTES (2 * CMU_HALF_BYTES)  // per group of eight epilogue warps: 128 x 64 fp16, twice
 #define CMU_BAR_BYTES 512
 // Two-part products move their sums from tensor memory to registers after this
 // many K blocks (see gemm_kernel); one-part products once.

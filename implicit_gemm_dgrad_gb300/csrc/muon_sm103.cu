@@ -14,20 +14,26 @@
 //   - B is dominated by its diagonal: kept in fp32 apart and applied row-wise
 //     (1.5e-3 -> 8e-4 on a Gaussian U);
 //   - A and the rest of B are rounded once to fp16, times 1024.
-// Where that is not enough -- fp32 gradients, and small matrices, whose few
-// directions do not average the rounding -- every operand is two fp16 parts
-// (22 bits) and a product three: high x high, high x low, low x high.  The
-// result then has fp32 accuracy.
+// That is 1e-4 to 1e-3 off, and up to 1.8e-3 where all singular values are equal
+// (512 x 512).  Where it is not enough -- fp32 gradients, and small matrices,
+// whose few directions do not average the rounding -- every operand is two fp16
+// parts (22 bits) and a product three: high x high, high x low, low x high.  The
+// result then has fp32 accuracy (3e-7 to 8e-6), at two to four times the time
+// from 512 x 512 on (512 x 4608: 280 us against 171; 4096 x 4096: 4.7 ms against
+// 1.06).
 // X starts as U times a power of two, exact for fp16 and bf16 gradients; the
 // rest of the division by |U|_F goes into the first step's factors.
 //
-// What bounds it.  Large matrices: the tensor cores; 4096 x 4096 takes 1.0 ms of
+// What bounds it.  Large matrices: the tensor cores; 4096 x 4096 takes 1.06 ms of
 // which the products without their mirrored halves need 0.71 at cuBLAS's rate
 // (136 of 152 tiles' worth of pairs busy in a symmetric product's two waves, 630
 // cycles a block of K against 512 of tensor work).  Middle ones: what a launch
 // costs beyond its products, about 4 us (start, first load, epilogue, end), and
 // the 64 bytes a cycle an SM loads (512 cycles a block of a 128 x 128 tile):
-// 512 x 4608 170 us.  Small ones: the chain of 14 dependent products.
+// 512 x 4608 171 us.  Small ones: five launches, each of which reads from L2 what
+// the one before it wrote (three 64 x 576: 37.5 us; the chain of 14 dependent
+// products in one of them is about 13, and that launch 23.5 of the five's 55
+// when each starts cold).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -304,7 +310,7 @@ struct Tile {
 };
 
 // Shared memory: the operand ring, the epilogue's staging (a 128 x 64 fp16
-// block in 128-byte-swizzled rows, twice, for each group of four warps),
+// block in 128-byte-swizzled rows, twice, for each group of eight warps),
 // mbarriers.
 template <int FORM>
 struct Layout {

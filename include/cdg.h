@@ -557,7 +557,8 @@ int cdg_embed(const void *table, long long ld_table, const void *tokens, int ind
  *   workspace   device, cdg_embed_grad_workspace_bytes(count, vocab, dim)
  *               bytes, 16-byte aligned, overwritten
  * dtable and workspace overlap each other and the inputs nowhere
- * (CDG_ERR_ALIAS).  count below 2^30, dim at most 2^24.
+ * (CDG_ERR_ALIAS).  count below 2^30, dim at most 2^24; above some millions of
+ * tokens the sort's time grows with the square of count (2^24: about 4 ms).
  */
 int cdg_embed_grad(const void *dout, long long ld_dout, const void *tokens, int index_bytes, long long count,
                    int vocab, int dim, int dtype, float scale, void *dtable, long long ld_dtable, int out_f32,
@@ -581,11 +582,12 @@ size_t cdg_embed_grad_workspace_bytes(long long count, int vocab, int dim);
  * (CDG_F16, CDG_BF16 or CDG_F32), dense, batch x rows x cols; O may not
  * overlap U.  Products run on the tensor cores on fp16 operands with fp32
  * sums; X is held as a high and a low fp16 part and the diagonal of b A + c A^2
- * in fp32, so that O is within about 1e-3 of the iteration in exact arithmetic
- * (relative, Frobenius).  With CDG_F32 every operand is two fp16 parts, at
- * three products for one, and O is within about 1e-5.  |U|_F must be representable: its square is summed in
- * fp32.  A zero U gives a zero O, whatever eps is; a U with a NaN or an infinity
- * gives NaN.
+ * in fp32, so that O is within 2e-3 of the iteration in exact arithmetic
+ * (relative, Frobenius, five steps; up to 1.8e-3 where all singular values are
+ * equal, else mostly below 1e-3), beside its own rounding.  With CDG_F32 every
+ * operand is two fp16 parts, at three products for one, and O is within 1e-5.
+ * |U|_F must be representable: its square is summed in fp32.  A zero U gives a
+ * zero O, whatever eps is; a U with a NaN or an infinity gives NaN.
  *
  * cdg_muon_step: the whole update of fp32 weights W from a gradient G (dtype)
  * and its momentum M (fp32), all batch x rows x cols, dense:
