@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
     const float H = p.g_entropy && !none ? __ldg(p.entropy + i) : 0.0f;
     // two-sum of lse and -H (Knuth): the rounding error of lse - H, exactly
     const float lh = lse - H, back = lh - lse, lo = (lse - (lh - back)) + (-H - back);
-    const bool far = !none && !(fabsf(lse) < 1048576.0f);
+    const bool far = !none && !(fabsf(lse) < 1048576.0f);  // from 2^20 on lse is off by up to 1/16; NaN too
     const GradRow f{p.scale, none ? 0.0f : lse, none ? 0.0f : lh, none ? 0.0f : lo, H, h, g};
     auto put = [&](int j, float r) {
         if (j == t) r = fmaf(p.scale, g, r);

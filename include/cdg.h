@@ -505,7 +505,8 @@ int cdg_wgrad_device_status(cdg_wgrad_t h, cdg_stream_t stream);
  *
  * Sums are fp32.  Logits of -inf (masked tokens) have probability 0.  A row of
  * -inf alone has lse = logp = top_logp = -inf, entropy 0 and top_ids 0, 1, ...
- * A row that holds NaN or +inf answers NaN everywhere, and top_ids -1.
+ * A row that holds NaN or +inf answers NaN everywhere (logp: where there is a
+ * token), and top_ids -1.
  *   scale       > 0, finite (1 / temperature)
  *   vocab       at most 2^30
  *   top         0 .. 32, at most vocab
