@@ -18,8 +18,8 @@
 // (512 x 512).  Where it is not enough -- fp32 gradients, and small matrices,
 // whose few directions do not average the rounding -- every operand is two fp16
 // parts (22 bits) and a product three: high x high, high x low, low x high.  The
-// result then has fp32 accuracy (3e-7 to 8e-6), at two to four times the time
-// from 512 x 512 on (512 x 4608: 280 us against 171; 4096 x 4096: 4.7 ms against
+// result then has fp32 accuracy (2e-7 to 8e-6), at 1.6 to 4.5 times the time of
+// 16-bit updates (512 x 4608: 280 us against 171; 4096 x 4096: 4.7 ms against
 // 1.06).
 // X starts as U times a power of two, exact for fp16 and bf16 gradients; the
 // rest of the division by |U|_F goes into the first step's factors.
