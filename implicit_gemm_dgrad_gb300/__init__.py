@@ -50,7 +50,10 @@ EXPORTS = ("cdg_plan", "cdg_plan_host", "cdg_destroy", "cdg_get_output_dims", "c
            "cdg_token_logprobs", "cdg_token_logprobs_grad", "cdg_embed", "cdg_embed_grad",
            "cdg_embed_grad_workspace_bytes", "cdg_muon_plan", "cdg_muon_plan_host", "cdg_muon_destroy",
            "cdg_muon_workspace_bytes", "cdg_muon_get_info", "cdg_muon_orthogonalize", "cdg_muon_step",
-           "cdg_muon_device_status")
+           "cdg_muon_device_status", "cdg_attention_plan", "cdg_attention_plan_host", "cdg_attention_destroy",
+           "cdg_attention_workspace_bytes", "cdg_attention_grad_workspace_bytes", "cdg_attention", "cdg_attention_grad",
+           "cdg_attention_device_status", "cdg_qk_rope", "cdg_qk_rope_grad", "cdg_qk_rope_grad_workspace_bytes",
+           "cdg_rope_frequencies")
 
 
 class CdgError(RuntimeError):
@@ -186,6 +189,32 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.cdg_muon_step.restype = i
     lib.cdg_muon_device_status.argtypes = [hp, vp]
     lib.cdg_muon_device_status.restype = i
+    lib.cdg_attention_plan.argtypes = [i] * 6 + [f, ctypes.POINTER(hp)]
+    lib.cdg_attention_plan.restype = i
+    lib.cdg_attention_plan_host.argtypes = [i] * 6 + [f, ctypes.POINTER(hp)]
+    lib.cdg_attention_plan_host.restype = i
+    lib.cdg_attention_destroy.argtypes = [hp]
+    lib.cdg_attention_destroy.restype = None
+    lib.cdg_attention_workspace_bytes.argtypes = [hp, ll, ll, i]
+    lib.cdg_attention_workspace_bytes.restype = sz
+    lib.cdg_attention_grad_workspace_bytes.argtypes = [hp, ll, ll, i]
+    lib.cdg_attention_grad_workspace_bytes.restype = sz
+    lib.cdg_attention.argtypes = [hp] + [vp, ll] * 3 + [ll, ll, vp, vp, i, i, vp, ll, vp, vp, vp]
+    lib.cdg_attention.restype = i
+    lib.cdg_attention_grad.argtypes = [hp] + [vp, ll] * 4 + [vp, vp, ll, ll, ll, vp, vp, i, i] + [vp, ll] * 3 + [vp, vp]
+    lib.cdg_attention_grad.restype = i
+    lib.cdg_attention_device_status.argtypes = [hp, vp]
+    lib.cdg_attention_device_status.restype = i
+    rope = [vp, ll, vp, ll, vp, i, ll, i, i, i, i, vp, i, i, f, i, f, vp, vp]
+    lib.cdg_qk_rope.argtypes = rope + [vp, ll, vp, ll, vp]
+    lib.cdg_qk_rope.restype = i
+    lib.cdg_qk_rope_grad.argtypes = rope + [vp, ll] * 4 + [vp, vp, vp, vp]
+    lib.cdg_qk_rope_grad.restype = i
+    lib.cdg_qk_rope_grad_workspace_bytes.argtypes = [ll, i, i, i]
+    lib.cdg_qk_rope_grad_workspace_bytes.restype = sz
+    d = ctypes.c_double
+    lib.cdg_rope_frequencies.argtypes = [i, d, d, ll, d, d, ctypes.POINTER(f)]
+    lib.cdg_rope_frequencies.restype = i
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -892,3 +921,209 @@ def muon_plan(rows, cols, batch=1, dtype="bf16", steps=5, coefficients=MUON_COEF
 def muon_plan_host(rows, cols, batch=1, dtype="bf16", steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7,
                    num_sms=148) -> MuonPlan:
     return MuonPlan(rows, cols, batch, dtype, steps, coefficients, eps, host_sms=num_sms)
+
+
+# ---- attention over packed sequences, and its gradient
+
+
+class AttentionPlan:
+    """Heads and mask of an attention (a ``cdg_attention_t``)."""
+
+    def __init__(self, heads, kv_heads, dim, dtype="bf16", causal=True, window=0, scale: float | None = None,
+                 host_only: bool = False):
+        self.lib = load_library()
+        self.heads, self.kv_heads, self.dim, self.dtype = int(heads), int(kv_heads), int(dim), dtype
+        if scale is None:
+            scale = max(self.dim, 1) ** -0.5
+        make = self.lib.cdg_attention_plan_host if host_only else self.lib.cdg_attention_plan
+        h = ctypes.c_void_p()
+        rc = make(self.heads, self.kv_heads, self.dim, _dtype(dtype), int(bool(causal)), int(window), float(scale),
+                  ctypes.byref(h))
+        if rc != OK:
+            raise CdgError(rc, "cdg_attention_plan")
+        self.handle = h
+        self._need: dict = {}  # bytes of workspace, by the sizes that calls have had
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            self.lib.cdg_attention_destroy(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        self.close()
+
+    def workspace_bytes(self, q_tokens: int, k_tokens: int, sequences: int = 1) -> int:
+        """Bytes of attend's workspace (cdg_attention_workspace_bytes)."""
+        return self._bytes(self.lib.cdg_attention_workspace_bytes, q_tokens, k_tokens, sequences)
+
+    def grad_workspace_bytes(self, q_tokens: int, k_tokens: int, sequences: int = 1) -> int:
+        """Bytes of attend_grad's workspace (cdg_attention_grad_workspace_bytes)."""
+        return self._bytes(self.lib.cdg_attention_grad_workspace_bytes, q_tokens, k_tokens, sequences)
+
+    def _bytes(self, fn, *sizes) -> int:
+        n = int(fn(self.handle, *(int(v) for v in sizes)))
+        if n == 0:
+            raise CdgError(ERR_INVALID_ARG, fn.__name__)
+        return n
+
+    def _q(self, t, tokens: int, ld, what: str):
+        return _matrix(t, tokens, self.heads * self.dim, _TYPES.get(self.dtype), ld, what)
+
+    def _k(self, t, tokens: int, ld, what: str):
+        return _matrix(t, tokens, self.kv_heads * self.dim, _TYPES.get(self.dtype), ld, what)
+
+    def attend(self, q, k, v, o, lse, workspace, q_tokens: int, k_tokens: int, q_offsets=None, k_offsets=None,
+               sequences: int | None = None, ld_q=None, ld_k=None, ld_v=None, ld_o=None, stream=None) -> None:
+        """o and lse (heads x q_tokens, fp32) of the queries over the keys and
+        values (cdg_attention).  Offsets are int32 or int64 tensors of
+        sequences + 1 numbers; without them all rows are one sequence."""
+        nq, nk = int(q_tokens), int(k_tokens)
+        qo, ko, ib, n = _offsets(q_offsets, k_offsets, sequences)
+        _check_workspace(workspace, self, self.workspace_bytes, nq, nk, n)
+        rc = self.lib.cdg_attention(
+            self.handle, *self._q(q, nq, ld_q, "q"), *self._k(k, nk, ld_k, "k"), *self._k(v, nk, ld_v, "v"), nq, nk, qo, ko, ib,
+            n, *self._q(o, nq, ld_o, "o"), _dense(lse, self.heads * nq, "float32", "lse"), _addr(workspace), _stream(stream))
+        if rc != OK:
+            raise CdgError(rc, "cdg_attention")
+
+    def attend_grad(self, q, k, v, o, lse, do, dq, dk, dv, workspace, q_tokens: int, k_tokens: int, q_offsets=None,
+                    k_offsets=None, sequences: int | None = None, ld_q=None, ld_k=None, ld_v=None, ld_o=None, ld_do=None,
+                    ld_dq=None, ld_dk=None, ld_dv=None, stream=None) -> None:
+        """dq, dk and dv for the gradient do of o (cdg_attention_grad); o and
+        lse as attend wrote them."""
+        nq, nk = int(q_tokens), int(k_tokens)
+        qo, ko, ib, n = _offsets(q_offsets, k_offsets, sequences)
+        _check_workspace(workspace, self, self.grad_workspace_bytes, nq, nk, n)
+        rc = self.lib.cdg_attention_grad(
+            self.handle, *self._q(q, nq, ld_q, "q"), *self._k(k, nk, ld_k, "k"), *self._k(v, nk, ld_v, "v"),
+            *self._q(o, nq, ld_o, "o"), _dense(lse, self.heads * nq, "float32", "lse"), *self._q(do, nq, ld_do, "do"), nq, nk, qo,
+            ko, ib, n, *self._q(dq, nq, ld_dq, "dq"), *self._k(dk, nk, ld_dk, "dk"), *self._k(dv, nk, ld_dv, "dv"),
+            _addr(workspace), _stream(stream))
+        if rc != OK:
+            raise CdgError(rc, "cdg_attention_grad")
+
+    def device_status(self, stream=None) -> int:
+        return int(self.lib.cdg_attention_device_status(self.handle, _stream(stream)))
+
+
+def _check_workspace(t, plan, need, *sizes) -> None:
+    if t is None or isinstance(t, int):
+        return
+    key = (need.__name__, *sizes)
+    n = plan._need.get(key)
+    if n is None:
+        if len(plan._need) > 64:
+            plan._need.clear()
+        n = plan._need[key] = need(*sizes)
+    if type(t) is _tensor and t.nbytes >= n and t.is_contiguous() and t.get_device() == _cuda_device():
+        return  # what the check below finds, without its cost
+    _check_buffer(t, n, "workspace")
+
+
+def _offsets(q_offsets, k_offsets, sequences) -> tuple:
+    """Addresses of two offset lists, bytes per number, and the number of
+    sequences (of raw addresses, which hold int64 numbers: as given, or one)."""
+    n = sequences
+    for t in (q_offsets, k_offsets):
+        if n is None and t is not None and not isinstance(t, int):
+            n = t.numel() - 1
+    n = 1 if n is None else int(n)
+    qo, qb = _tokens(q_offsets, n + 1, "q_offsets")
+    ko, kb = _tokens(k_offsets, n + 1, "k_offsets")
+    if q_offsets is None:
+        qb = kb
+    elif k_offsets is not None and qb != kb:
+        raise ValueError("q_offsets and k_offsets must hold numbers of one type")
+    return qo, ko, qb, n
+
+
+def attention_plan(heads, kv_heads, dim, dtype="bf16", causal=True, window=0, scale: float | None = None) -> AttentionPlan:
+    """Attention of `heads` query heads over `kv_heads` key and value heads of
+    width dim; scale defaults to dim ** -0.5."""
+    return AttentionPlan(heads, kv_heads, dim, dtype, causal, window, scale)
+
+
+def attention_plan_host(heads, kv_heads, dim, dtype="bf16", causal=True, window=0, scale: float | None = None) -> AttentionPlan:
+    return AttentionPlan(heads, kv_heads, dim, dtype, causal, window, scale, host_only=True)
+
+
+# ---- norms of queries and keys with the position rotation, and their gradient
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, stretch: float = 1.0, trained: int = 0, low: float = 1.0,
+                     high: float = 32.0) -> list:
+    """inv_freq for qk_rope (cdg_rope_frequencies): rot / 2 numbers, stretched
+    for contexts longer than the `trained` tokens a model has seen."""
+    out = (ctypes.c_float * max(1, int(rot) // 2))()
+    rc = load_library().cdg_rope_frequencies(int(rot), float(base), float(stretch), int(trained), float(low), float(high), out)
+    if rc != OK:
+        raise CdgError(rc, "cdg_rope_frequencies")
+    return list(out)[: int(rot) // 2]
+
+
+def _rope_args(q, k, positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved, factor, norm, eps, w_q, w_k,
+               ld_q, ld_k, read: bool):
+    """The arguments that qk_rope and qk_rope_grad share; read: whether q and k are."""
+    kind = _TYPES.get(dtype)
+    if read and heads:
+        q, ld_q = _matrix(q, tokens, heads * dim, kind, ld_q, "q")
+    else:
+        q, ld_q = None, 0
+    if read and kv_heads:
+        k, ld_k = _matrix(k, tokens, kv_heads * dim, kind, ld_k, "k")
+    else:
+        k, ld_k = None, 0
+    at, ib = _tokens(positions, tokens, "positions")
+    return (q, ld_q, k, ld_k, at, ib, tokens, heads, kv_heads, dim, _dtype(dtype),
+            _dense(inv_freq, rot // 2, "float32", "inv_freq"), rot, int(bool(interleaved)), float(factor), int(bool(norm)),
+            float(eps), _dense(w_q, dim, "float32", "w_q"), _dense(w_k, dim, "float32", "w_k"))
+
+
+def qk_rope(q, k, positions, inv_freq, q_out, k_out, tokens: int, heads: int, kv_heads: int, dim: int, dtype="bf16",
+            rot: int | None = None, interleaved: bool = False, factor: float = 1.0, norm: bool = False, eps: float = 1e-6,
+            w_q=None, w_k=None, ld_q=None, ld_k=None, ld_qo=None, ld_ko=None, stream=None) -> None:
+    """Norms of queries and keys for each head (norm=True: weights w_q, w_k, or
+    ones) and the position rotation of a head's first `rot` values (all of them
+    by default) in one pass (cdg_qk_rope).  positions: int32 or int64, None for
+    the token's number.  q_out may be q, and k_out k."""
+    tokens, heads, kv_heads, dim = int(tokens), int(heads), int(kv_heads), int(dim)
+    rot, kind = dim if rot is None else int(rot), _TYPES.get(dtype)
+    args = _rope_args(q, k, positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved, factor, norm, eps, w_q,
+                      w_k, ld_q, ld_k, True)
+    outs = (*(_matrix(q_out, tokens, heads * dim, kind, ld_qo, "q_out") if heads else (None, 0)),
+            *(_matrix(k_out, tokens, kv_heads * dim, kind, ld_ko, "k_out") if kv_heads else (None, 0)))
+    rc = load_library().cdg_qk_rope(*args, *outs, _stream(stream))
+    if rc != OK:
+        raise CdgError(rc, "cdg_qk_rope")
+
+
+def qk_rope_grad_workspace_bytes(tokens: int, heads: int, kv_heads: int, dim: int) -> int:
+    """Bytes of qk_rope_grad's workspace (cdg_qk_rope_grad_workspace_bytes)."""
+    n = int(load_library().cdg_qk_rope_grad_workspace_bytes(int(tokens), int(heads), int(kv_heads), int(dim)))
+    if n == 0:
+        raise CdgError(ERR_INVALID_ARG, "cdg_qk_rope_grad_workspace_bytes")
+    return n
+
+
+def qk_rope_grad(q, k, positions, inv_freq, dq_out, dk_out, dq, dk, workspace, tokens: int, heads: int, kv_heads: int, dim: int,
+                 dtype="bf16", rot: int | None = None, interleaved: bool = False, factor: float = 1.0, norm: bool = False,
+                 eps: float = 1e-6, w_q=None, w_k=None, dw_q=None, dw_k=None, ld_q=None, ld_k=None, ld_dqo=None, ld_dko=None,
+                 ld_dq=None, ld_dk=None, stream=None) -> None:
+    """The gradient of qk_rope (cdg_qk_rope_grad): dq and dk for the gradients
+    dq_out and dk_out of its outputs, and with norm=True the weights' gradients
+    dw_q and dw_k (fp32; None: not wanted).  q and k are qk_rope's inputs, not
+    read without the norm.  dq may be dq_out, and dk dk_out."""
+    tokens, heads, kv_heads, dim = int(tokens), int(heads), int(kv_heads), int(dim)
+    rot, kind = dim if rot is None else int(rot), _TYPES.get(dtype)
+    args = _rope_args(q, k, positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved, factor, norm, eps, w_q,
+                      w_k, ld_q, ld_k, bool(norm))
+    mats = []
+    for t, ld, n, what in ((dq_out, ld_dqo, heads, "dq_out"), (dk_out, ld_dko, kv_heads, "dk_out"), (dq, ld_dq, heads, "dq"),
+                           (dk, ld_dk, kv_heads, "dk")):
+        mats += _matrix(t, tokens, n * dim, kind, ld, what) if n else (None, 0)
+    if workspace is not None and not isinstance(workspace, int):
+        _check_buffer(workspace, qk_rope_grad_workspace_bytes(tokens, heads, kv_heads, dim), "workspace")
+    rc = load_library().cdg_qk_rope_grad(*args, *mats, _dense(dw_q, dim, "float32", "dw_q"), _dense(dw_k, dim, "float32", "dw_k"),
+                                         _addr(workspace), _stream(stream))
+    if rc != OK:
+        raise CdgError(rc, "cdg_qk_rope_grad")

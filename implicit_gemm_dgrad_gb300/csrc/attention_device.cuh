@@ -1,0 +1,251 @@
+// Shared by the attention's kernels (attention_sm103.cu, attention_grad_sm103.cu):
+// which sequence and tile a CTA works on, what a query sees, and the small
+// pieces of the tensor-memory pipelines.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attention_params.h"
+#include "ptx.cuh"
+#include "wait.cuh"
+
+namespace cdg {
+
+constexpr uint32_t kSliceBytes = CAT_TILE * 128;  // 64 columns x 128 rows of 16-bit values: 16 KB
+
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^x to about two units in the last place, 0 below 2^-126.
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 values rounded to the 16-bit type, the first in the low half.
+template <bool BF16>
+__device__ __forceinline__ uint32_t round2(float a, float b)
+{
+    if (BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 32 TMEM lanes x 32 columns into registers; the values are there after tmem_wait.
+__device__ __forceinline__ void tmem_ld_32(uint32_t taddr, float (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's loads; tied to the registers, so that no use of them moves above it.
+__device__ __forceinline__ void tmem_wait(float (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                   "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
+                   "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                   "+f"(r[30]), "+f"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared-memory matrix descriptor of an MN-major operand in 128-byte-swizzled
+// atoms (64 columns x 8 rows, 1 KB), slices of 64 columns kSliceBytes apart:
+// the same tile that sdesc_k128_sw128 reads K-major.
+__device__ __forceinline__ uint64_t sdesc_mn_slices(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((kSliceBytes >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// D (128 x 128) = A B^T over the head's width, both K-major tiles of 64-column slices.
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int ksteps)
+{
+    const uint64_t ad = sdesc_k128_sw128(a), bd = sdesc_k128_sw128(b);
+    for (int k = 0; k < ksteps; ++k) {
+        const uint32_t at = (k >> 2) * (kSliceBytes >> 4) + 2u * (k & 3);
+        umma_f16(d, ad + at, bd + at, idesc, k != 0);
+    }
+}
+
+// D (128 x dim) (+)= A B over 128 rows of the MN-major tile B, A in tensor
+// memory: 16-bit values, columns [0, 64) at a, [64, 128) at a_high.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t idesc, bool add)
+{
+    const uint64_t bd = sdesc_mn_slices(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        umma_f16_ts(d, (k < 4 ? a : a_high) + 8u * (k & 3), bd + 128u * k, idesc, add || k != 0);
+}
+
+// ---------------------------------------------------------------- sequences
+
+__device__ __forceinline__ int offset_at(const void *offsets, int index_bytes, int i, int tokens)
+{
+    if (!offsets) return i == 0 ? 0 : tokens;
+    const long long t = index_bytes == 8 ? __ldg(static_cast<const long long *>(offsets) + i)
+                                         : static_cast<long long>(__ldg(static_cast<const int *>(offsets) + i));
+    return static_cast<int>(t < 0 ? 0 : t > tokens ? tokens : t);
+}
+
+// A CTA's sequence and tile of `rows` queries (or keys): sequences' tiles are
+// counted in order.  Any offsets stay inside the tensors: they are cut to
+// [0, tokens], and a sequence that ends before it begins is empty.
+struct Place {
+    int q0, ql, k0, kl;  // first row and length of the queries and of the keys
+    int tile;            // of this sequence; -1: no such tile
+};
+__device__ __forceinline__ Place find_tile(const CatParams &p, long long item, int rows, bool of_keys)
+{
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int s0 = 0; s0 < p.sequences; s0 += 32) {
+        const int s = s0 + lane;
+        int q0 = 0, ql = 0, k0 = 0, kl = 0;
+        if (s < p.sequences) {
+            q0 = offset_at(p.q_offsets, p.index_bytes, s, p.q_tokens);
+            ql = max(0, offset_at(p.q_offsets, p.index_bytes, s + 1, p.q_tokens) - q0);
+            k0 = offset_at(p.k_offsets, p.index_bytes, s, p.k_tokens);
+            kl = max(0, offset_at(p.k_offsets, p.index_bytes, s + 1, p.k_tokens) - k0);
+        }
+        const int n = ((of_keys ? kl : ql) + rows - 1) / rows;
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += v;
+        }
+        const unsigned here = __ballot_sync(0xFFFFFFFFu, before + upto > item);
+        if (here) {
+            const int w = __ffs(here) - 1;
+            Place r;
+            r.q0 = __shfl_sync(0xFFFFFFFFu, q0, w);
+            r.ql = __shfl_sync(0xFFFFFFFFu, ql, w);
+            r.k0 = __shfl_sync(0xFFFFFFFFu, k0, w);
+            r.kl = __shfl_sync(0xFFFFFFFFu, kl, w);
+            r.tile = static_cast<int>(item - before) - (__shfl_sync(0xFFFFFFFFu, upto, w) - __shfl_sync(0xFFFFFFFFu, n, w));
+            return r;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    return Place{0, 0, 0, 0, -1};
+}
+
+// Key steps [lo, hi) that some query of [i0, i1) sees.
+__device__ __forceinline__ void key_steps(const CatParams &p, const Place &at, int i0, int i1, int &lo, int &hi)
+{
+    const int off = at.kl - at.ql;
+    const int end = p.causal ? min(at.kl, i1 + off) : at.kl;
+    const int first = p.window ? max(0, i0 + off - p.window + 1) : 0;
+    lo = first / CAT_TILE;
+    hi = end > first ? (end + CAT_TILE - 1) / CAT_TILE : lo;
+}
+
+// ---------------------------------------------------------------- pieces
+
+// Zeroes rows [valid, 128) of a tile (this warp alone), for the async proxy to see.
+// What lies behind a sequence's end is another's, and may be NaN: as an operand that
+// is summed over its rows it has to be zero.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int slices, int valid)
+{
+    const int lane = threadIdx.x & 31;
+    for (int s = 0; s < slices; ++s)
+        for (uint32_t at = static_cast<uint32_t>(valid) * 128u + lane * 16u; at < kSliceBytes; at += 512u)
+            st_shared_v4(tile + s * kSliceBytes + at, 0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap &map, uint32_t bar, int slices, int head, int token)
+{
+    for (int s = 0; s < slices; ++s)
+        tma_load_3d(dst + s * kSliceBytes, reinterpret_cast<uint64_t>(&map), bar, 64 * s, head, token);
+}
+
+// One lane of a converged warp arrives for it, after all lanes' work on tensor memory.
+__device__ __forceinline__ void warp_arrive(uint32_t bar)
+{
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// A row of `dim` fp32 sums from tensor memory, times f, to 16-bit values at `out`.
+template <bool BF16>
+__device__ __forceinline__ void store_row(uint32_t taddr, int dim, float f, void *out, bool valid)
+{
+    for (int c0 = 0; c0 < dim; c0 += 32) {
+        float v[32];
+        tmem_ld_32(taddr + c0, v);
+        tmem_wait(v);
+        if (valid) {
+            uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c0 + 8 * i < dim)
+                    q[i] = make_uint4(round2<BF16>(v[8 * i] * f, v[8 * i + 1] * f), round2<BF16>(v[8 * i + 2] * f, v[8 * i + 3] * f),
+                                      round2<BF16>(v[8 * i + 4] * f, v[8 * i + 5] * f),
+                                      round2<BF16>(v[8 * i + 6] * f, v[8 * i + 7] * f));
+        }
+    }
+}
+__device__ __forceinline__ void zero_row(void *out, int dim)
+{
+    for (int c = 0; c < dim; c += 8) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + c) = make_uint4(0, 0, 0, 0);
+}
+
+}  // namespace cdg

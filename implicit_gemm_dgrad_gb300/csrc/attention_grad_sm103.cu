@@ -1,0 +1,627 @@
+// The attention's gradient for sm_103a.  With p = exp(s - lse) recomputed from
+// the forward's lse, D_i = do_i . o_i, dp = do v^T and ds = p (dp - D):
+//
+//   dv = p^T do,   dk = scale ds^T q,   dq = scale ds k
+//
+// Three kernels: the rows' statistics (- lse log2 e and D), then dk and dv by
+// CTAs of 128 keys, then dq by CTAs of 128 queries.  The second and the third
+// both compute s and dp, so the gradient takes seven products of a pair of
+// tiles rather than five; but each of its sums belongs to one CTA, stays in
+// tensor memory from the first step to the last and is added in a fixed order
+// (no atomics, no fp32 copy of dq in memory), and p and ds go back to tensor
+// memory as the 16-bit A operand of the next product, never to shared memory.
+// For dk and dv the scores are computed transposed (a thread a key, columns
+// queries), so that P^T and dS^T lie as those products need them.
+//
+// p and ds are rounded to 16 bits as operands of the products that sum them.
+//
+// Each kernel's warps (384 threads): 0-7 compute (128 rows x 64 columns a
+// warpgroup), 8 loads by TMA, 9 issues MMAs, 10 fetches the queries'
+// statistics of a step (dk and dv).  The two phases of a step, p and ds, each
+// overlap two products of the tensor cores: dk and dv run
+//   p(i) | dS^T(i-1) Q, dP^T(i)      then      ds(i) | P^T(i) dO, S^T(i+1)
+#include "attention_device.cuh"
+#include "token_device.cuh"
+
+namespace cdg {
+namespace {
+
+constexpr int kSlots = 2;  // steps of each streamed operand in shared memory
+
+// (- lse log2 e, D) of every row and head; a row that saw nothing (lse = -inf)
+// gets -inf there, so that every p of it is 0.  16 lanes a row.
+template <bool BF16>
+__global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_constant__ CatParams p)
+{
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const long long g = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 16;
+    const int lane = threadIdx.x & 15;
+    const long long token = g / p.heads;
+    const int head = static_cast<int>(g - token * p.heads);
+    float sum = 0.0f;
+    if (token < p.q_tokens) {
+        const uint4 *a = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.d_o) + token * p.ld_do + static_cast<long long>(head) * p.dim);
+        const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o_in) + token * p.ld_oi + static_cast<long long>(head) * p.dim);
+        if (8 * lane < p.dim) {
+            using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+            float x[8], y[8];
+            widen_vec<T>(__ldg(a + lane), x);
+            widen_vec<T>(__ldg(b + lane), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+        }
+    }
+#pragma unroll
+    for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == 0 && token < p.q_tokens) {
+        const long long at = static_cast<long long>(head) * p.q_tokens + token;
+        const float lse = p.lse_in[at];
+        p.stats[at] = make_float2(lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f, sum);
+    }
+}
+
+struct GradBars {
+    uint32_t fixed_full;           // the CTA's own two tiles
+    uint32_t full_a0, empty_a0;    // [kSlots]: the streamed operand of the scores (Q, or K)
+    uint32_t full_b0, empty_b0;    // [kSlots]: the streamed operand of dP (dO, or V)
+    uint32_t st_full0, st_empty0;  // [kSlots]: statistics
+    uint32_t s_full, s_read, dp_full, ds_ready, out_full, drain;
+};
+
+struct GradSmem {
+    uint32_t fixed_a, fixed_b, ring_a, ring_b, stats, tile_bytes;
+    GradBars B;
+    uint32_t *tmem_slot;
+    volatile uint32_t *abort_flag, *slot_parity;  // parity of each slot's last load: a, b, then the fixed tiles'
+};
+
+__device__ __forceinline__ GradSmem grad_layout(const CatParams &p, uint8_t *smem_raw)
+{
+    GradSmem S;
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    S.tile_bytes = kSliceBytes * p.slices;
+    S.fixed_a = base;
+    S.fixed_b = base + S.tile_bytes;
+    S.ring_a = base + 2 * S.tile_bytes;
+    S.ring_b = S.ring_a + kSlots * S.tile_bytes;
+    S.stats = S.ring_b + kSlots * S.tile_bytes;  // kSlots x 128 float2
+    const uint32_t bars = S.stats + kSlots * CAT_TILE * 8;
+    uint32_t at = bars;
+    auto take = [&](int n) {
+        const uint32_t was = at;
+        at += 8 * n;
+        return was;
+    };
+    S.B.fixed_full = take(1);
+    S.B.full_a0 = take(kSlots);
+    S.B.empty_a0 = take(kSlots);
+    S.B.full_b0 = take(kSlots);
+    S.B.empty_b0 = take(kSlots);
+    S.B.st_full0 = take(kSlots);
+    S.B.st_empty0 = take(kSlots);
+    S.B.s_full = take(1);
+    S.B.s_read = take(1);
+    S.B.dp_full = take(1);
+    S.B.ds_ready = take(1);
+    S.B.out_full = take(1);
+    S.B.drain = take(1);
+    S.tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (at - raw));
+    S.abort_flag = S.tmem_slot + 1;
+    S.slot_parity = S.tmem_slot + 2;
+    if (threadIdx.x == 0) {
+        mbar_init(S.B.fixed_full, 1);
+        for (int s = 0; s < kSlots; ++s) {
+            for (uint32_t b : {S.B.full_a0, S.B.empty_a0, S.B.full_b0, S.B.empty_b0}) mbar_init(b + 8u * s, 1);
+            mbar_init(S.B.st_full0 + 8u * s, 32);
+            mbar_init(S.B.st_empty0 + 8u * s, 8);
+        }
+        for (uint32_t b : {S.B.s_full, S.B.dp_full, S.B.out_full, S.B.drain}) mbar_init(b, 1);
+        for (uint32_t b : {S.B.s_read, S.B.ds_ready}) mbar_init(b, 8);
+        for (int s = 0; s <= 2 * kSlots; ++s) S.slot_parity[s] = 0u;
+        *S.abort_flag = 0u;
+        fence_mbar_init();
+    }
+    return S;
+}
+
+// After all roles: on an abort the latest load of every used slot lands before the CTA exits.
+__device__ __forceinline__ void grad_end(const CatParams &p, const GradSmem &S, uint32_t tmem)
+{
+    __syncthreads();
+    if (*S.abort_flag && threadIdx.x == 0) {
+        volatile uint32_t no_abort = 0;
+        const Ctl drain_ctl{&no_abort, p.status};
+        for (int s = 0; s <= 2 * kSlots; ++s) {
+            const uint32_t v = S.slot_parity[s];
+            const uint32_t bar = s == 2 * kSlots ? S.B.fixed_full : s < kSlots ? S.B.full_a0 + 8u * s : S.B.full_b0 + 8u * (s - kSlots);
+            if (v & 2u) wait_bar(bar, v & 1u, drain_ctl);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x / 32 == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+__device__ __forceinline__ void drain_mmas(const CatParams &p, const GradSmem &S, bool leader)
+{
+    if (leader) umma_commit(S.B.drain);
+    __syncwarp();
+    volatile uint32_t no_abort = 0;
+    wait_bar(S.B.drain, 0, Ctl{&no_abort, p.status});
+}
+
+// The loads of one CTA: its own two tiles, then pairs of streamed tiles.
+// row(n) and head(n): token and head of the n-th.
+template <typename At>
+__device__ __forceinline__ void run_grad_loads(const CatParams &p, const GradSmem &S, Ctl ctl, int steps,
+                                               const CUtensorMap &fixed_a, const CUtensorMap &fixed_b, int fixed_head,
+                                               int fixed_token, const CUtensorMap &map_a, const CUtensorMap &map_b, At where)
+{
+    const bool leader = elect_one_sync();
+    if (leader) {
+        S.slot_parity[2 * kSlots] = 2u;
+        mbar_arrive_expect_tx(S.B.fixed_full, 2 * S.tile_bytes);
+        load_tile(S.fixed_a, fixed_a, S.B.fixed_full, p.slices, fixed_head, fixed_token);
+        load_tile(S.fixed_b, fixed_b, S.B.fixed_full, p.slices, fixed_head, fixed_token);
+    }
+    for (int n = 0; n < steps; ++n) {
+        const int slot = n % kSlots;
+        const uint32_t parity = (n / kSlots) & 1;
+        int head, token;
+        where(n, head, token);
+        for (int b = 0; b < 2; ++b) {
+            if (!wait_bar((b ? S.B.empty_b0 : S.B.empty_a0) + 8u * slot, parity ^ 1u, ctl)) return;
+            if (leader) {
+                const uint32_t bar = (b ? S.B.full_b0 : S.B.full_a0) + 8u * slot;
+                S.slot_parity[b * kSlots + slot] = parity | 2u;
+                mbar_arrive_expect_tx(bar, S.tile_bytes);
+                load_tile((b ? S.ring_b : S.ring_a) + slot * S.tile_bytes, b ? map_b : map_a, bar, p.slices, head, token);
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// Columns of tensor memory: scores, dP, and the sums (dV and dK, or dQ).
+constexpr uint32_t kS = 0, kDP = 128, kSum = 256;
+
+// ------------------------------------------------------------------ dk, dv
+
+// A CTA's steps: for every query head of its group the query tiles that see some of its keys.
+struct KeyTile {
+    int j0;          // first key of the tile, in its sequence
+    int lo, count;   // first query tile and their number, for each head
+};
+
+template <bool BF16>
+__device__ __forceinline__ void compute_dkv(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
+                                            const KeyTile &kt, int steps, int kv_head)
+{
+    const int warp = threadIdx.x / 32, half = warp / 4, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t s_col = tmem + lanes + kS + 64u * half, dp_col = tmem + lanes + kDP + 64u * half;
+    const f32x2 c2 = pack2(p.scale_log2, p.scale_log2);
+    const int off = at.kl - at.ql, j = kt.j0 + row;
+    bool ok = true;
+    int tile = kt.lo;
+    for (int n = 0; n < steps; ++n) {
+        const int slot = n % kSlots;
+        const uint32_t stats = S.stats + slot * CAT_TILE * 8 + half * 64 * 8;
+        const int i0 = tile * CAT_TILE;
+        if (++tile == kt.lo + kt.count) tile = kt.lo;
+        // columns [lo, hi) of this half see the key
+        const bool whole = (!p.causal || kt.j0 + CAT_TILE - 1 <= i0 + off) && (!p.window || kt.j0 > i0 + CAT_TILE - 1 + off - p.window);
+        const int lo = p.causal ? j - off - i0 - 64 * half : 0, hi = p.window ? j - off + p.window - i0 - 64 * half : 64;
+        if (!wait_bar(S.B.st_full0 + 8u * slot, (n / kSlots) & 1, ctl) || !wait_bar(S.B.s_full, n & 1, ctl)) {
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        float s[2][32];
+        tmem_ld_32(s_col, s[0]);
+        tmem_ld_32(s_col + 32u, s[1]);
+        tmem_wait(s[0]);
+        tmem_wait(s[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float n0, d0, n1, d1;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(n0), "=f"(d0), "=f"(n1), "=f"(d1) : "r"(stats + (32 * q + e) * 8u));
+                float a, b;
+                unpack2(fma2(pack2(s[q][e], s[q][e + 1]), c2, pack2(n0, n1)), a, b);
+                a = exp2_approx(a);
+                b = exp2_approx(b);
+                if (!whole) {
+                    if (32 * q + e < lo || 32 * q + e >= hi) a = 0.0f;
+                    if (32 * q + e + 1 < lo || 32 * q + e + 1 >= hi) b = 0.0f;
+                }
+                s[q][e] = a;
+                s[q][e + 1] = b;
+                w[e / 2] = round2<BF16>(a, b);
+            }
+            tmem_st_16(s_col + 16u * q, w);
+        }
+        tmem_st_wait();
+        warp_arrive(S.B.s_read);
+        if (!wait_bar(S.B.dp_full, n & 1, ctl)) {
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        float dp[2][32];
+        tmem_ld_32(dp_col, dp[0]);
+        tmem_ld_32(dp_col + 32u, dp[1]);
+        tmem_wait(dp[0]);
+        tmem_wait(dp[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float n0, d0, n1, d1;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(n0), "=f"(d0), "=f"(n1), "=f"(d1) : "r"(stats + (32 * q + e) * 8u));
+                float a = s[q][e] * (dp[q][e] - d0), b = s[q][e + 1] * (dp[q][e + 1] - d1);
+                if (!whole) {  // (dP of an unseen pair may be anything)
+                    if (32 * q + e < lo || 32 * q + e >= hi) a = 0.0f;
+                    if (32 * q + e + 1 < lo || 32 * q + e + 1 >= hi) b = 0.0f;
+                }
+                w[e / 2] = round2<BF16>(a, b);
+            }
+            tmem_st_16(dp_col + 16u * q, w);
+        }
+        tmem_st_wait();
+        warp_arrive(S.B.ds_ready);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(S.B.st_empty0 + 8u * slot);
+    }
+    if (ok && steps > 0) ok = wait_bar(S.B.out_full, 0, ctl);
+    if (!ok) return;
+    tc_fence_after();
+    // the first warpgroup stores dv, the second dk
+    const long long token = at.k0 + j;
+    uint16_t *out = half ? static_cast<uint16_t *>(p.dk) + token * p.ld_dk : static_cast<uint16_t *>(p.dv) + token * p.ld_dv;
+    out += static_cast<long long>(kv_head) * p.dim;
+    if (steps > 0) store_row<BF16>(tmem + lanes + kSum + 64u * p.slices * half, p.dim, half ? p.scale : 1.0f, out, j < at.kl);
+    else if (j < at.kl) zero_row(out, p.dim);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(CAT_THREADS, 1) attention_dkv_kernel(const __grid_constant__ CatParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const GradSmem S = grad_layout(p, smem_raw);
+    const int warp = threadIdx.x / 32;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    if (warp == 9) {
+        tmem_alloc(smem_u32(S.tmem_slot), 512);
+        tmem_relinquish();
+    }
+    const int kv_head = static_cast<int>(blockIdx.x % p.kv_heads);
+    const Place at = find_tile(p, blockIdx.x / p.kv_heads, CAT_TILE, true);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *S.tmem_slot;
+    const Ctl ctl{S.abort_flag, p.status};
+    if (at.tile >= 0) {
+        // (a sequence's first keys, which under a causal mask most queries see, come first)
+        KeyTile kt;
+        kt.j0 = at.tile * CAT_TILE;
+        const int off = at.kl - at.ql, j1 = min(kt.j0 + CAT_TILE, at.kl);
+        const int first = p.causal ? max(0, kt.j0 - off) : 0, end = p.window ? min(at.ql, j1 - 1 - off + p.window) : at.ql;
+        kt.lo = first / CAT_TILE;
+        kt.count = end > first ? (end + CAT_TILE - 1) / CAT_TILE - kt.lo : 0;
+        const int steps = kt.count * p.group;
+        auto where = [&](int n, int &head, int &tile) {
+            const int h = n / kt.count;
+            head = kv_head * p.group + h;
+            tile = kt.lo + n - h * kt.count;
+        };
+        if (steps == 0) {
+            if (warp < 8) compute_dkv<BF16>(p, S, ctl, tmem, at, kt, 0, kv_head);
+        } else if (warp == 8) {
+            run_grad_loads(p, S, ctl, steps, p.tmK, p.tmV, kv_head, at.k0 + kt.j0, p.tmQ, p.tmDO,
+                           [&](int n, int &head, int &token) {
+                               int tile;
+                               where(n, head, tile);
+                               token = at.q0 + tile * CAT_TILE;
+                           });
+        } else if (warp == 10) {
+            const int lane = threadIdx.x & 31;
+            for (int n = 0; n < steps; ++n) {
+                const int slot = n % kSlots;
+                int head, tile;
+                where(n, head, tile);
+                if (!wait_bar(S.B.st_empty0 + 8u * slot, ((n / kSlots) & 1) ^ 1u, ctl)) break;
+                const float2 *src = p.stats + static_cast<long long>(head) * p.q_tokens + at.q0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 32 * e + lane, i = tile * CAT_TILE + c;
+                    const float2 v = i < at.ql ? __ldg(src + i) : make_float2(-INFINITY, 0.0f);
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(S.stats + (slot * CAT_TILE + c) * 8u), "f"(v.x), "f"(v.y) : "memory");
+                }
+                mbar_arrive(S.B.st_full0 + 8u * slot);
+            }
+        } else if (warp == 9) {
+            const bool leader = elect_one_sync();
+            const uint32_t s = tmem + kS, dp = tmem + kDP, dv = tmem + kSum, dk = dv + 64u * p.slices;
+            auto a_tile = [&](int n) { return S.ring_a + (n % kSlots) * S.tile_bytes; };
+            auto b_tile = [&](int n) { return S.ring_b + (n % kSlots) * S.tile_bytes; };
+            // waits for the n-th streamed tile; rows behind the sequence's end become zeros
+            auto filled = [&](uint32_t full0, uint32_t tile, int n) {
+                if (!wait_bar(full0 + 8u * (n % kSlots), (n / kSlots) & 1, ctl)) return false;
+                int head, q;
+                where(n, head, q);
+                tc_fence_after();
+                if (at.ql - q * CAT_TILE < CAT_TILE) zero_rows(tile, p.slices, at.ql - q * CAT_TILE);
+                return true;
+            };
+            bool ok = wait_bar(S.B.fixed_full, 0, ctl) && filled(S.B.full_a0, a_tile(0), 0);
+            if (ok && leader) {
+                issue_qk(s, S.fixed_a, a_tile(0), p.idesc_qk, p.ksteps);
+                umma_commit(S.B.s_full);
+            }
+            __syncwarp();
+            ok = ok && filled(S.B.full_b0, b_tile(0), 0);
+            if (ok && leader) {
+                issue_qk(dp, S.fixed_b, b_tile(0), p.idesc_qk, p.ksteps);
+                umma_commit(S.B.dp_full);
+            }
+            __syncwarp();
+            for (int n = 0; ok && n < steps; ++n) {
+                const bool next = n + 1 < steps;
+                if (!wait_bar(S.B.s_read, n & 1, ctl)) break;
+                tc_fence_after();
+                if (leader) {
+                    issue_pv(dv, s, s + 64u, b_tile(n), p.idesc_pv, n != 0);
+                    umma_commit(S.B.empty_b0 + 8u * (n % kSlots));
+                }
+                __syncwarp();
+                if (next) {
+                    if (!filled(S.B.full_a0, a_tile(n + 1), n + 1)) break;
+                    if (leader) {
+                        issue_qk(s, S.fixed_a, a_tile(n + 1), p.idesc_qk, p.ksteps);
+                        umma_commit(S.B.s_full);
+                    }
+                    __syncwarp();
+                }
+                if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
+                tc_fence_after();
+                if (leader) {
+                    issue_pv(dk, dp, dp + 64u, a_tile(n), p.idesc_pv, n != 0);
+                    umma_commit(S.B.empty_a0 + 8u * (n % kSlots));
+                }
+                __syncwarp();
+                if (next) {
+                    if (!filled(S.B.full_b0, b_tile(n + 1), n + 1)) break;
+                    if (leader) {
+                        issue_qk(dp, S.fixed_b, b_tile(n + 1), p.idesc_qk, p.ksteps);
+                        umma_commit(S.B.dp_full);
+                    }
+                    __syncwarp();
+                } else if (leader) {
+                    umma_commit(S.B.out_full);
+                }
+            }
+            __syncwarp();
+            drain_mmas(p, S, leader);
+        } else if (warp < 8) {
+            compute_dkv<BF16>(p, S, ctl, tmem, at, kt, steps, kv_head);
+        }
+    }
+    grad_end(p, S, tmem);
+}
+
+// ------------------------------------------------------------------ dq
+
+template <bool BF16>
+__device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
+                                           int i0, int head, int lo, int hi)
+{
+    const int warp = threadIdx.x / 32, half = warp / 4, row = threadIdx.x & 127, i = i0 + row;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t s_col = tmem + lanes + kS + 64u * half, dp_col = tmem + lanes + kDP + 64u * half;
+    const f32x2 c2 = pack2(p.scale_log2, p.scale_log2);
+    const int r_first = i0 + at.kl - at.ql, r = r_first + row;
+    const long long token = at.q0 + i;
+    const bool valid = i < at.ql;
+    const float2 st = valid ? __ldg(p.stats + static_cast<long long>(head) * p.q_tokens + token) : make_float2(-INFINITY, 0.0f);
+    const f32x2 shift = pack2(st.x, st.x), minus_d = pack2(-st.y, -st.y);
+    bool ok = true;
+    for (int j = lo; j < hi; ++j) {
+        const int n = j - lo, k0 = j * CAT_TILE;
+        const bool whole = k0 + CAT_TILE <= at.kl && (!p.causal || k0 + CAT_TILE - 1 <= r_first) &&
+                           (!p.window || k0 > r_first + CAT_TILE - 1 - p.window);
+        const int c_hi = min(at.kl, p.causal ? r + 1 : at.kl) - k0 - 64 * half, c_lo = p.window ? r - p.window + 1 - k0 - 64 * half : 0;
+        if (!wait_bar(S.B.s_full, n & 1, ctl)) {
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        float s[2][32];
+        tmem_ld_32(s_col, s[0]);
+        tmem_ld_32(s_col + 32u, s[1]);
+        tmem_wait(s[0]);
+        tmem_wait(s[1]);
+        warp_arrive(S.B.s_read);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float a, b;
+                unpack2(fma2(pack2(s[q][e], s[q][e + 1]), c2, shift), a, b);
+                s[q][e] = exp2_approx(a);
+                s[q][e + 1] = exp2_approx(b);
+            }
+        if (!wait_bar(S.B.dp_full, n & 1, ctl)) {
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        float dp[2][32];
+        tmem_ld_32(dp_col, dp[0]);
+        tmem_ld_32(dp_col + 32u, dp[1]);
+        tmem_wait(dp[0]);
+        tmem_wait(dp[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float a, b;
+                unpack2(mul2(pack2(s[q][e], s[q][e + 1]), add2(pack2(dp[q][e], dp[q][e + 1]), minus_d)), a, b);
+                if (!whole) {  // (scores and dP of an unseen pair may be anything)
+                    if (32 * q + e < c_lo || 32 * q + e >= c_hi) a = 0.0f;
+                    if (32 * q + e + 1 < c_lo || 32 * q + e + 1 >= c_hi) b = 0.0f;
+                }
+                w[e / 2] = round2<BF16>(a, b);
+            }
+            tmem_st_16(dp_col + 16u * q, w);
+        }
+        tmem_st_wait();
+        warp_arrive(S.B.ds_ready);
+    }
+    if (ok && hi > lo) ok = wait_bar(S.B.out_full, 0, ctl);
+    if (!ok) return;
+    tc_fence_after();
+    uint16_t *out = static_cast<uint16_t *>(p.dq) + token * p.ld_dq + static_cast<long long>(head) * p.dim;
+    if (half == 0) {
+        if (hi > lo) store_row<BF16>(tmem + lanes + kSum, p.dim, p.scale, out, valid);
+        else if (valid) zero_row(out, p.dim);
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(CAT_THREADS, 1) attention_dq_kernel(const __grid_constant__ CatParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const GradSmem S = grad_layout(p, smem_raw);
+    const int warp = threadIdx.x / 32;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    if (warp == 9) {
+        tmem_alloc(smem_u32(S.tmem_slot), 512);
+        tmem_relinquish();
+    }
+    const int head = static_cast<int>(blockIdx.x % p.heads);
+    const Place at = find_tile(p, blockIdx.x / p.heads, CAT_TILE, false);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *S.tmem_slot;
+    const Ctl ctl{S.abort_flag, p.status};
+    if (at.tile >= 0) {
+        // a sequence's last queries first: under a causal mask they see most keys
+        const int i0 = ((at.ql + CAT_TILE - 1) / CAT_TILE - 1 - at.tile) * CAT_TILE;
+        int lo, hi;
+        key_steps(p, at, i0, min(i0 + CAT_TILE, at.ql), lo, hi);
+        const int steps = hi - lo, kv_head = head / p.group;
+        if (steps == 0) {
+            if (warp < 8) compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
+        } else if (warp == 8) {
+            // (one tensor map a loop: the CTA's own tiles come from the query side)
+            run_grad_loads(p, S, ctl, steps, p.tmQ, p.tmDO, head, at.q0 + i0, p.tmK, p.tmV, [&](int n, int &h, int &token) {
+                h = kv_head;
+                token = at.k0 + (lo + n) * CAT_TILE;
+            });
+        } else if (warp == 9) {
+            const bool leader = elect_one_sync();
+            const uint32_t s = tmem + kS, dp = tmem + kDP, dq = tmem + kSum;
+            auto a_tile = [&](int n) { return S.ring_a + (n % kSlots) * S.tile_bytes; };
+            auto b_tile = [&](int n) { return S.ring_b + (n % kSlots) * S.tile_bytes; };
+            auto scores = [&](int n) {
+                if (!wait_bar(S.B.full_a0 + 8u * (n % kSlots), (n / kSlots) & 1, ctl)) return false;
+                tc_fence_after();
+                // keys behind the sequence's end become zeros: dS K sums over them
+                const int valid = at.kl - (lo + n) * CAT_TILE;
+                if (valid < CAT_TILE) zero_rows(a_tile(n), p.slices, valid);
+                if (leader) {
+                    issue_qk(s, S.fixed_a, a_tile(n), p.idesc_qk, p.ksteps);
+                    umma_commit(S.B.s_full);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto dps = [&](int n) {
+                if (!wait_bar(S.B.full_b0 + 8u * (n % kSlots), (n / kSlots) & 1, ctl)) return false;
+                tc_fence_after();
+                if (leader) {
+                    issue_qk(dp, S.fixed_b, b_tile(n), p.idesc_qk, p.ksteps);
+                    umma_commit(S.B.dp_full);
+                    umma_commit(S.B.empty_b0 + 8u * (n % kSlots));
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = wait_bar(S.B.fixed_full, 0, ctl) && scores(0) && dps(0);
+            for (int n = 0; ok && n < steps; ++n) {
+                const bool next = n + 1 < steps;
+                if (!wait_bar(S.B.s_read, n & 1, ctl)) break;
+                tc_fence_after();
+                if (next && !scores(n + 1)) break;
+                if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
+                tc_fence_after();
+                if (leader) {
+                    issue_pv(dq, dp, dp + 64u, a_tile(n), p.idesc_pv, n != 0);
+                    umma_commit(S.B.empty_a0 + 8u * (n % kSlots));
+                    if (!next) umma_commit(S.B.out_full);
+                }
+                __syncwarp();
+                if (next && !dps(n + 1)) break;
+            }
+            __syncwarp();
+            drain_mmas(p, S, leader);
+        } else if (warp < 8) {
+            compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
+        }
+    }
+    grad_end(p, S, tmem);
+}
+
+}  // namespace
+}  // namespace cdg
+
+size_t cat_smem_grad(int slices) { return 1024 + (2 + 2 * cdg::kSlots) * cdg::kSliceBytes * slices + cdg::kSlots * CAT_TILE * 8 + 256; }
+
+cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
+{
+    using namespace cdg;
+    const long long rows = static_cast<long long>(p.q_tokens) * p.heads;
+    const dim3 grid(static_cast<unsigned>((rows + 15) / 16)), block(256);
+    return bf16 ? launch_early(attention_stats_kernel<true>, grid, block, 0, s, p)
+                : launch_early(attention_stats_kernel<false>, grid, block, 0, s, p);
+}
+
+cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaStream_t s)
+{
+    using namespace cdg;
+    const dim3 grid(static_cast<unsigned>(items)), block(CAT_THREADS);
+    const int smem = static_cast<int>(cat_smem_grad(p.slices));
+    return bf16 ? launch_early(attention_dkv_kernel<true>, grid, block, smem, s, p)
+                : launch_early(attention_dkv_kernel<false>, grid, block, smem, s, p);
+}
+
+cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStream_t s)
+{
+    using namespace cdg;
+    const dim3 grid(static_cast<unsigned>(items)), block(CAT_THREADS);
+    const int smem = static_cast<int>(cat_smem_grad(p.slices));
+    return bf16 ? launch_early(attention_dq_kernel<true>, grid, block, smem, s, p)
+                : launch_early(attention_dq_kernel<false>, grid, block, smem, s, p);
+}
+
+cudaError_t cat_prepare_grad()
+{
+    for (auto *k : {cdg::attention_dkv_kernel<true>, cdg::attention_dkv_kernel<false>, cdg::attention_dq_kernel<true>,
+                    cdg::attention_dq_kernel<false>}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CDG_MAX_DYN_SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}

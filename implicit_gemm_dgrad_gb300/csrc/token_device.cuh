@@ -190,6 +190,24 @@ static inline size_t matrix_bytes(long long rows, long long cols, long long ld, 
     return rows > 0 ? static_cast<size_t>((rows - 1) * ld + cols) * static_cast<size_t>(esize) : 0;
 }
 
+// Rows of a tensor argument.  Two of one row stride that lie side by side in the
+// rows of one buffer (the parts of a projection's output) share no element.
+struct Rows {
+    const void *p;
+    long long rows, width, ld;  // width and ld in elements
+    int esize;
+    Extent extent() const { return Extent{static_cast<const char *>(p), p ? matrix_bytes(rows, width, ld, esize) : 0}; }
+};
+static inline bool overlap(const Rows &a, const Rows &b)
+{
+    if (!overlap(a.extent(), b.extent())) return false;
+    const long long ld = a.ld * a.esize, wa = a.width * a.esize, wb = b.width * b.esize;
+    if (ld != b.ld * b.esize || wa > ld || wb > ld) return true;
+    long long d = (static_cast<const char *>(b.p) - static_cast<const char *>(a.p)) % ld;
+    if (d < 0) d += ld;
+    return d < wa || d + wb > ld;
+}
+
 // SM count of the current device (0 on an error); the runtime's own query takes
 // a fifth of a launch, so the answer is kept per device.
 static inline int sm_count()

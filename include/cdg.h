@@ -637,6 +637,133 @@ int cdg_muon_step(cdg_muon_t h, const float *W, const void *G, const float *M, f
 /* Synchronise stream, then read and clear the plan's device status word. */
 int cdg_muon_device_status(cdg_muon_t h, cdg_stream_t stream);
 
+/*
+ * Attention over packed sequences and its gradient: the block between the two
+ * ends of a token model's training step.
+ *
+ * q is q_tokens x (heads * dim), k and v are k_tokens x (kv_heads * dim), rows
+ * of all heads one after the other; query head h reads key and value head
+ * h / (heads / kv_heads).  Sequence s has the rows q_offsets[s] ..
+ * q_offsets[s + 1] of q and k_offsets[s] .. k_offsets[s + 1] of k and v.  For
+ * its query i of ql and key j of kl, r = i + kl - ql (the last query sees the
+ * last key), i sees j where
+ *
+ *     causal = 0: always;   causal = 1: j <= r;   window = w > 0: also j > r - w
+ *
+ * cdg_attention:       s_ij = scale q_i . k_j over the keys that i sees,
+ *     lse_i = log sum_j exp(s_ij),   o_i = sum_j exp(s_ij - lse_i) v_j
+ * A query that sees no key has o = 0 and lse = -inf.
+ *
+ * cdg_attention_grad:  with p_ij = exp(s_ij - lse_i) from the given lse, and
+ *     ds_ij = p_ij (do_i . v_j - do_i . o_i),
+ *     dv_j = sum_i p_ij do_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+ * dk and dv are sums over the query heads of their group too.  Rows that no
+ * sequence holds are neither read into a result nor written.
+ *
+ * All matrices are dtype (CDG_F16 or CDG_BF16); products have fp32 sums, p and
+ * ds are rounded to dtype as their operands; row sums, lse (heads x q_tokens,
+ * natural log) and do . o are fp32.  Repeated calls give the same bits.
+ * A NaN or an infinity in a row of a sequence may reach other results of that
+ * sequence and head, masked or not, and none of another sequence or head
+ * (group of heads, for k and v).
+ *   dim        a multiple of 8, at most 128; heads a multiple of kv_heads, at most 1024
+ *   ld_*       row strides in elements, multiples of 8; matrices 16-byte aligned.
+ *              Matrices of one stride may lie side by side in the rows of one
+ *              buffer, inputs and outputs alike; no other overlap of an output (CDG_ERR_ALIAS)
+ *   q_offsets, k_offsets   device, sequences + 1 int32 (index_bytes = 4) or
+ *              int64 (8) numbers, ascending; both may be NULL for one sequence of
+ *              all rows.  Numbers outside [0, tokens] are cut to it, and a
+ *              sequence that ends before it begins is empty; sequences that
+ *              overlap leave their rows' results undefined
+ *   tokens     below 2^30, sequences at most 2^20
+ *   workspace  device, 256-byte aligned, cdg_attention_workspace_bytes or
+ *              cdg_attention_grad_workspace_bytes bytes, overwritten
+ *
+ * A plan holds the heads and the mask, and belongs to the device that was
+ * current when it was made (CDG_ERR_INVALID_ARG on another).  Calls on one plan
+ * may overlap on the GPU unless they share a workspace or an output.  No call
+ * allocates or synchronises.  A device-side pipeline timeout (which a correct
+ * launch never hits) is reported by cdg_attention_device_status.
+ */
+typedef struct cdg_attention_st *cdg_attention_t;
+
+/* window 0 (none), or > 0 with causal = 1; scale > 0, finite. */
+int cdg_attention_plan(int heads, int kv_heads, int dim, int dtype, int causal, int window, float scale,
+                       cdg_attention_t *out);
+/* The same without a device: for the checks and sizes. */
+int cdg_attention_plan_host(int heads, int kv_heads, int dim, int dtype, int causal, int window, float scale,
+                            cdg_attention_t *out);
+void cdg_attention_destroy(cdg_attention_t h);
+/* Bytes of workspace; 0 for sizes that are refused. */
+size_t cdg_attention_workspace_bytes(cdg_attention_t h, long long q_tokens, long long k_tokens, int sequences);
+size_t cdg_attention_grad_workspace_bytes(cdg_attention_t h, long long q_tokens, long long k_tokens, int sequences);
+
+int cdg_attention(cdg_attention_t h, const void *q, long long ld_q, const void *k, long long ld_k, const void *v,
+                  long long ld_v, long long q_tokens, long long k_tokens, const void *q_offsets, const void *k_offsets,
+                  int index_bytes, int sequences, void *o, long long ld_o, float *lse, void *workspace,
+                  cdg_stream_t stream);
+int cdg_attention_grad(cdg_attention_t h, const void *q, long long ld_q, const void *k, long long ld_k, const void *v,
+                       long long ld_v, const void *o, long long ld_o, const float *lse, const void *d_o,
+                       long long ld_do, long long q_tokens, long long k_tokens, const void *q_offsets,
+                       const void *k_offsets, int index_bytes, int sequences, void *dq, long long ld_dq, void *dk,
+                       long long ld_dk, void *dv, long long ld_dv, void *workspace, cdg_stream_t stream);
+/* Synchronise stream, then read and clear the plan's device status word. */
+int cdg_attention_device_status(cdg_attention_t h, cdg_stream_t stream);
+
+/*
+ * Norms of queries and keys for each head with the position rotation in the
+ * same pass, and their gradient.  For every token t and head of q (tokens x
+ * heads * dim) and of k (tokens x kv_heads * dim), x the head's dim values:
+ *
+ *     norm = 1:  z = x / sqrt(mean(x^2) + eps) * w;     norm = 0:  z = x
+ *     angle_i = positions[t] * inv_freq[i], i < rot / 2
+ *     (y_a, y_b) = factor * (z_a cos - z_b sin, z_b cos + z_a sin)
+ *         interleaved = 0:  a = i, b = i + rot / 2;     1:  a = 2 i, b = 2 i + 1
+ *     y = z behind the first rot values
+ *
+ * and the gradient, for dy, with n = x / sqrt(mean(x^2) + eps) and dz = dy
+ * turned back: dw = sum over tokens and heads of dz n, dn = dz w,
+ * dx = (dn - n mean(dn n)) / sqrt(mean(x^2) + eps); dx = dz without the norm.
+ *
+ * Matrices are dtype (CDG_F16, CDG_BF16, CDG_F32) with row strides ld_*, aligned
+ * to the element; inv_freq, w_q, w_k, dw_q and dw_k are fp32.  Computed in
+ * fp32, rounded once; angles are reduced exactly at any position.  Repeated
+ * calls give the same bits.
+ *   heads, kv_heads   either may be 0 (that side's pointers are not used)
+ *   dim        at most 256;  rot even, 0 .. dim (0: no rotation, inv_freq may be NULL)
+ *   positions  int32 or int64 (index_bytes 4, 8), any value; NULL: the token's number
+ *   w_q, w_k   NULL: ones; NULL without the norm
+ *   outputs    may be the input of the same side (same pointer, same stride): q_out
+ *              q, dq dq_out; matrices of one stride may lie side by side in the
+ *              rows of one buffer; no other overlap (CDG_ERR_ALIAS)
+ *   q, k       of the gradient: not read without the norm (may be NULL)
+ *   dw_q, dw_k NULL: not wanted
+ *   workspace  of the gradient: device, cdg_qk_rope_grad_workspace_bytes bytes,
+ *              16-byte aligned, overwritten
+ */
+int cdg_qk_rope(const void *q, long long ld_q, const void *k, long long ld_k, const void *positions, int index_bytes,
+                long long tokens, int heads, int kv_heads, int dim, int dtype, const float *inv_freq, int rot,
+                int interleaved, float factor, int norm, float eps, const float *w_q, const float *w_k, void *q_out,
+                long long ld_qo, void *k_out, long long ld_ko, cdg_stream_t stream);
+int cdg_qk_rope_grad(const void *q, long long ld_q, const void *k, long long ld_k, const void *positions,
+                     int index_bytes, long long tokens, int heads, int kv_heads, int dim, int dtype,
+                     const float *inv_freq, int rot, int interleaved, float factor, int norm, float eps,
+                     const float *w_q, const float *w_k, const void *dq_out, long long ld_dqo, const void *dk_out,
+                     long long ld_dko, void *dq, long long ld_dq, void *dk, long long ld_dk, float *dw_q, float *dw_k,
+                     void *workspace, cdg_stream_t stream);
+/* Bytes of cdg_qk_rope_grad's workspace; 0 for sizes it refuses.  Host only. */
+size_t cdg_qk_rope_grad_workspace_bytes(long long tokens, int heads, int kv_heads, int dim);
+
+/*
+ * inv_freq (host, rot / 2 numbers) for cdg_qk_rope: f_i = base^(-2 i / rot),
+ * stretched for contexts longer than the `trained` tokens a model has seen: a
+ * frequency that makes `low` turns or fewer over them is divided by `stretch`,
+ * one that makes `high` turns or more is kept, and those between are blended
+ * linearly in their turns.  trained = 0: all are divided.  stretch = 1: none.
+ */
+int cdg_rope_frequencies(int rot, double base, double stretch, long long trained, double low, double high,
+                         float *inv_freq);
+
 #ifdef __cplusplus
 }
 #endif
