@@ -717,6 +717,12 @@ def _matrix(t, rows: int, cols: int, kind: str | None, ld: int | None, what: str
     if type(t) is _tensor and _type_names.get(t.dtype) == kind and t.nbytes == rows * cols * _SIZES[kind] and ld is None and \
             t.is_contiguous() and t.get_device() == _cuda_device():
         return t.data_ptr(), cols  # as in _bytes_of
+    if type(t) is _tensor and _type_names.get(t.dtype) == kind and rows > 1 and ld is None and t.get_device() == _cuda_device():
+        shape = t.shape
+        if len(shape) == 2 and shape[0] == rows and shape[1] == cols:
+            own, step = t.stride()
+            if step == 1 and own >= cols:
+                return t.data_ptr(), own  # as below
     own = cols
     if t.is_contiguous() or t.dim() != 2:
         own = _row_stride(t, rows, cols, what)

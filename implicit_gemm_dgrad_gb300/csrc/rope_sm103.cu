@@ -22,7 +22,7 @@
 namespace cdg {
 namespace {
 
-constexpr int kMaxHead = 256;
+constexpr int kMaxHead = 256, kMaxHeads = 65536;
 constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
 constexpr int kCtas = 1216;    // of a launch, at most: 8 an SM
 constexpr int kGradCtas = 608;
@@ -64,36 +64,55 @@ struct Pair {
     }
 };
 
+// V values as they lie in memory, and as fp32 pairs (one instruction for both;
+// a single value is a pair with 0).
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T *src, float (&f)[V])
-{
-    constexpr int bytes = V * sizeof(T);
-    if constexpr (bytes >= 4) {
-        uint32_t w[bytes / 4];
-        if constexpr (bytes == 16) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(src);
-        else if constexpr (bytes == 8) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(src);
-        else w[0] = *reinterpret_cast<const uint32_t *>(src);
+struct Raw {
+    static constexpr int kBytes = V * static_cast<int>(sizeof(T)), kWords = kBytes < 4 ? 1 : kBytes / 4;
+    static constexpr int kPacks = (V + 1) / 2;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-        for (int i = 0; i < bytes / 4; ++i) widen<T>(w[i], f + i * kPerWord<T>);
-    } else {
-        f[0] = Elem<T>::get(*src);
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T *dst, const float (&f)[V])
-{
-    constexpr int bytes = V * sizeof(T);
-    if constexpr (bytes >= 4) {
-        uint32_t w[bytes / 4];
+    __device__ __forceinline__ void load(const T *src)
+    {
+        if constexpr (kBytes == 16) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(src);
+        else if constexpr (kBytes == 8) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(src);
+        else if constexpr (kBytes == 4) w[0] = *reinterpret_cast<const uint32_t *>(src);
+        else w[0] = *reinterpret_cast<const uint16_t *>(src);
+    }
+    __device__ __forceinline__ void get(f32x2 (&f)[kPacks]) const
+    {
+        float g[2 * kPacks];
+        g[2 * kPacks - 1] = 0.0f;
+        if constexpr (kBytes >= 4) {
 #pragma unroll
-        for (int i = 0; i < bytes / 4; ++i) w[i] = narrow<T>(f + i * kPerWord<T>);
-        if constexpr (bytes == 16) *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(w);
-        else if constexpr (bytes == 8) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(w);
-        else *reinterpret_cast<uint32_t *>(dst) = w[0];
-    } else {
-        *dst = Elem<T>::put(f[0]);
+            for (int i = 0; i < kWords; ++i) widen<T>(w[i], g + i * kPerWord<T>);
+        } else {
+            widen<T>(w[0], g);
+        }
+#pragma unroll
+        for (int i = 0; i < kPacks; ++i) f[i] = pack2(g[2 * i], g[2 * i + 1]);
     }
-}
+    __device__ __forceinline__ static void store(T *dst, const f32x2 (&f)[kPacks])
+    {
+        float g[2 * kPacks];
+#pragma unroll
+        for (int i = 0; i < kPacks; ++i) unpack2(f[i], g[2 * i], g[2 * i + 1]);
+        if constexpr (kBytes < 4) {
+            *dst = Elem<T>::put(g[0]);
+        } else {
+            uint32_t v[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) v[i] = narrow<T>(g + i * kPerWord<T>);
+            if constexpr (kBytes == 16) *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(v);
+            else if constexpr (kBytes == 8) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(v);
+            else *reinterpret_cast<uint32_t *>(dst) = v[0];
+        }
+    }
+};
 
 // f / (2 pi) turns, times 2^64, modulo 2^64: f's mantissa times 2^66 / (2 pi), shifted.
 __device__ __forceinline__ uint64_t turns_of(float f)
@@ -135,35 +154,37 @@ __device__ __forceinline__ int64_t position_of(const RopeArgs &p, long long toke
                               : __ldg(static_cast<const int *>(p.positions) + token);
 }
 
-// (a, b) turned by the angles of (c, s); back: by the opposite angles.  In the
-// interleaved layout the pairs lie within a, then within b.
-template <int V, bool BACK>
-__device__ __forceinline__ void turn(bool interleaved, const float (&c)[V], const float (&s)[V], float (&a)[V], float (&b)[V])
+// (a, b) turned by the angles of (c, s).  In the interleaved layout the pairs
+// lie within a, then within b.
+template <int V, bool INTERLEAVED>
+__device__ __forceinline__ void turn(const float (&c)[V], const float (&s)[V], f32x2 (&a)[(V + 1) / 2], f32x2 (&b)[(V + 1) / 2])
 {
-    auto one = [](float c, float s, float &x, float &y) {
-        if (BACK) s = -s;
-        const float u = x * c - y * s;
-        y = y * c + x * s;
-        x = u;
-    };
-    if (V > 1 && interleaved) {
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-            one(c[e], s[e], a[(2 * e) % V], a[(2 * e + 1) % V]);
-            one(c[(V / 2 + e) % V], s[(V / 2 + e) % V], b[(2 * e) % V], b[(2 * e + 1) % V]);
+    for (int i = 0; i < (V + 1) / 2; ++i) {
+        if constexpr (V > 1 && INTERLEAVED) {
+            const int j = V / 2 + i;  // b's angles follow a's
+            float x, y;
+            unpack2(a[i], x, y);
+            a[i] = fma2(pack2(y, x), pack2(-s[i], s[i]), mul2(a[i], pack2(c[i], c[i])));
+            unpack2(b[i], x, y);
+            b[i] = fma2(pack2(y, x), pack2(-s[j], s[j]), mul2(b[i], pack2(c[j], c[j])));
+        } else {
+            const int j = V > 1 ? 2 * i + 1 : 0;
+            const f32x2 cc = pack2(c[2 * i], c[j]), u = a[i];
+            a[i] = fma2(b[i], pack2(-s[2 * i], -s[j]), mul2(u, cc));
+            b[i] = fma2(u, pack2(s[2 * i], s[j]), mul2(b[i], cc));
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) one(c[e], s[e], a[e], b[e]);
     }
 }
 
-// GRAD: dx from dy and (with the norm) x, and the sums for dw.  A lane has R vector pairs.
-template <typename T, int V, int UNROLL, bool GRAD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p)
+// GRAD: dx from dy and (with the norm) x, and the sums for dw.  A lane has R
+// vector pairs; FULL: every lane has its one, whole.
+template <typename T, int V, int UNROLL, bool GRAD, bool NORM, bool INTERLEAVED, bool FULL>
+__global__ void __launch_bounds__(kRopeThreads, !GRAD ? 4 : NORM ? 2 : 3) rope_kernel(const __grid_constant__ RopeArgs p)
 {
-    constexpr int R = V >= 4 ? 1 : 4 / V;
-    __shared__ float red[GRAD ? kRopeWarps : 1][GRAD ? kMaxHead : 1];
+    constexpr int R = V >= 4 ? 1 : 4 / V, N = (V + 1) / 2;
+    constexpr bool X = !GRAD || NORM;  // whether x is read
+    __shared__ float red[GRAD && NORM ? kRopeWarps : 1][GRAD && NORM ? kMaxHead : 1];
     grid_dep_launch_dependents();
     grid_dep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -179,132 +200,163 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     int at_a[R], at_b[R];
     bool has_a[R], has_b[R], turned[R];
     uint64_t freq[R][V];
-    float wa[R][V], wb[R][V], dwa[R][V], dwb[R][V];
+    f32x2 wa[R][N], wb[R][N], dwa[R][N], dwb[R][N];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const Pair<V> v(p, l + i * 32);
         at_a[i] = v.a;
         at_b[i] = v.b;
         turned[i] = v.turned;
-        has_a[i] = l + i * 32 < p.pairs && v.a < p.dim;
-        has_b[i] = has_a[i] && v.b < p.dim;
+        has_a[i] = FULL || (l + i * 32 < p.pairs && v.a < p.dim);
+        has_b[i] = FULL || (has_a[i] && v.b < p.dim);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             // rotated pairs' numbers: those of the vector pair; past the rotated part the angle is 0
-            const int k = p.interleaved ? v.a / 2 + e : v.a + e;
+            const int k = INTERLEAVED ? v.a / 2 + e : v.a + e;
             freq[i][e] = turned[i] && 2 * k < p.rot ? turns_of(__ldg(p.inv_freq + k)) : 0;
-            wa[i][e] = sd.w && has_a[i] ? __ldg(sd.w + v.a + e) : 1.0f;
-            wb[i][e] = sd.w && has_b[i] ? __ldg(sd.w + v.b + e) : 1.0f;
-            dwa[i][e] = dwb[i][e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            auto weight = [&](bool has, int at, bool second) {
+                return second && V == 1 ? 0.0f : sd.w && has ? __ldg(sd.w + at + 2 * e + second) : 1.0f;
+            };
+            wa[i][e] = pack2(weight(has_a[i], v.a, false), weight(has_a[i], v.a, true));
+            wb[i][e] = pack2(weight(has_b[i], v.b, false), weight(has_b[i], v.b, true));
+            dwa[i][e] = dwb[i][e] = pack2(0.0f, 0.0f);
         }
     }
+    const bool all_turned = p.rot == p.dim;
     const float inv_dim = 1.0f / static_cast<float>(p.dim);
     for (long long token = static_cast<long long>(part) * kRopeWarps + warp; token < p.tokens;
          token += static_cast<long long>(sd.ctas) * kRopeWarps) {
         const T *x = static_cast<const T *>(sd.x) + token * sd.ld_x, *dy = static_cast<const T *>(sd.dy) + token * sd.ld_dy;
         T *out = static_cast<T *>(sd.out) + token * sd.ld_out;
-        float xa[UNROLL][R][V], xb[UNROLL][R][V];
-        float ya[GRAD ? UNROLL : 1][R][V], yb[GRAD ? UNROLL : 1][R][V];
+        float c[R][V], s[R][V];
+        bool first = true;
+        for (int hb = h0; hb - group < h_end; hb += UNROLL * groups) {
+            Raw<T, V> xa[X ? UNROLL : 1][R], xb[X ? UNROLL : 1][R], ya[GRAD ? UNROLL : 1][R], yb[GRAD ? UNROLL : 1][R];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int h = h0 + u * groups;
+            for (int u = 0; u < UNROLL; ++u) {
+                const int h = hb + u * groups, row = h * p.dim;  // (heads * dim is below 2^24)
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    xa[u][i][e] = xb[u][i][e] = 0.0f;
-                    if (GRAD) ya[u][i][e] = yb[u][i][e] = 0.0f;
-                }
-                if (h < h_end) {
-                    const long long row = static_cast<long long>(h) * p.dim;
-                    if (!GRAD || p.norm) {
-                        if (has_a[i]) load_vec<T, V>(x + row + at_a[i], xa[u][i]);
-                        if (has_b[i]) load_vec<T, V>(x + row + at_b[i], xb[u][i]);
+                for (int i = 0; i < R; ++i) {
+                    if (X) {
+                        xa[u][i].clear();
+                        xb[u][i].clear();
+                        if (h < h_end && has_a[i]) xa[u][i].load(x + row + at_a[i]);
+                        if (h < h_end && has_b[i]) xb[u][i].load(x + row + at_b[i]);
                     }
                     if (GRAD) {
-                        if (has_a[i]) load_vec<T, V>(dy + row + at_a[i], ya[u][i]);
-                        if (has_b[i]) load_vec<T, V>(dy + row + at_b[i], yb[u][i]);
+                        ya[u][i].clear();
+                        yb[u][i].clear();
+                        if (h < h_end && has_a[i]) ya[u][i].load(dy + row + at_a[i]);
+                        if (h < h_end && has_b[i]) yb[u][i].load(dy + row + at_b[i]);
                     }
                 }
             }
-        }
-        const uint64_t pos = static_cast<uint64_t>(position_of(p, token));
-        float c[R][V], s[R][V];
+            if (first) {  // (beneath the first loads)
+                first = false;
+                const uint64_t pos = static_cast<uint64_t>(position_of(p, token));
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int k = p.interleaved ? at_a[i] / 2 + e : at_a[i] + e;
-                if (turned[i] && 2 * k < p.rot) cos_sin<T>(pos * freq[i][e], p.factor, c[i][e], s[i][e]);
-                else c[i][e] = 1.0f, s[i][e] = 0.0f;
-            }
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int h = h0 + u * groups;
-            if (h0 - group + u * groups >= h_end) break;  // (the same for the whole warp)
-            float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                if (GRAD && turned[i]) turn<V, true>(p.interleaved, c[i], s[i], ya[u][i], yb[u][i]);
-                if (p.norm) {
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        sum = fmaf(xa[u][i][e], xa[u][i][e], sum);
-                        sum = fmaf(xb[u][i][e], xb[u][i][e], sum);
-                        if (GRAD) {
-                            dot = fmaf(ya[u][i][e] * wa[i][e], xa[u][i][e], dot);
-                            dot = fmaf(yb[u][i][e] * wb[i][e], xb[u][i][e], dot);
+                        const int k = INTERLEAVED ? at_a[i] / 2 + e : at_a[i] + e;
+                        if (all_turned || (turned[i] && 2 * k < p.rot)) cos_sin<T>(pos * freq[i][e], p.factor, c[i][e], s[i][e]);
+                        else c[i][e] = 1.0f, s[i][e] = 0.0f;
+                        if (GRAD) s[i][e] = -s[i][e];  // back
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int h = hb + u * groups;
+                if (hb - group + u * groups >= h_end) break;  // (the same for the whole warp)
+                f32x2 fa[R][N], fb[R][N], ga[R][N], gb[R][N];  // x, and the gradient dz
+                f32x2 sum = pack2(0.0f, 0.0f), dot = sum;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    if (X) {
+                        xa[u][i].get(fa[i]);
+                        xb[u][i].get(fb[i]);
+                    }
+                    if (GRAD) {
+                        ya[u][i].get(ga[i]);
+                        yb[u][i].get(gb[i]);
+                        if (all_turned || turned[i]) turn<V, INTERLEAVED>(c[i], s[i], ga[i], gb[i]);
+                    }
+                    if (NORM) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            sum = fma2(fa[i][e], fa[i][e], sum);
+                            sum = fma2(fb[i][e], fb[i][e], sum);
+                            if (GRAD) {
+                                dot = fma2(mul2(ga[i][e], wa[i][e]), fa[i][e], dot);
+                                dot = fma2(mul2(gb[i][e], wb[i][e]), fb[i][e], dot);
+                            }
                         }
                     }
                 }
-            }
-            float scale = 1.0f, back = 0.0f;
-            if (p.norm) {
-                for (int d = p.lanes / 2; d; d /= 2) {
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-                    if (GRAD) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-                }
-                scale = 1.0f / sqrtf(fmaf(sum, inv_dim, p.eps));
-                if (GRAD) back = scale * scale * (dot * inv_dim);
-            }
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float a[V], b[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    if (!GRAD) {
-                        a[e] = xa[u][i][e] * scale * wa[i][e];
-                        b[e] = xb[u][i][e] * scale * wb[i][e];
-                    } else {
-                        a[e] = scale * (ya[u][i][e] * wa[i][e] - xa[u][i][e] * back);
-                        b[e] = scale * (yb[u][i][e] * wb[i][e] - xb[u][i][e] * back);
-                        if (h < h_end) {
-                            dwa[i][e] = fmaf(ya[u][i][e], xa[u][i][e] * scale, dwa[i][e]);
-                            dwb[i][e] = fmaf(yb[u][i][e], xb[u][i][e] * scale, dwb[i][e]);
-                        }
+                f32x2 scale, back;  // 1 / sqrt(mean(x^2) + eps), and - mean(dn n) times it
+                if (NORM) {
+                    float v, v1, g, g1;
+                    unpack2(sum, v, v1);
+                    unpack2(dot, g, g1);
+                    v += v1;
+                    g += g1;
+                    for (int d = p.lanes / 2; d; d /= 2) {
+                        v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+                        if (GRAD) g += __shfl_xor_sync(0xFFFFFFFFu, g, d);
+                    }
+                    v = rsqrtf(fmaf(v, inv_dim, p.eps));
+                    scale = pack2(v, v);
+                    if (GRAD) {
+                        g = -(v * v * (g * inv_dim));
+                        back = pack2(g, g);
                     }
                 }
-                if (!GRAD && turned[i]) turn<V, false>(p.interleaved, c[i], s[i], a, b);
-                if (h < h_end) {
-                    const long long row = static_cast<long long>(h) * p.dim;
-                    if (has_a[i]) store_vec<T, V>(out + row + at_a[i], a);
-                    if (has_b[i]) store_vec<T, V>(out + row + at_b[i], b);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    if (NORM) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            if (!GRAD) {
+                                fa[i][e] = mul2(fa[i][e], mul2(scale, wa[i][e]));
+                                fb[i][e] = mul2(fb[i][e], mul2(scale, wb[i][e]));
+                            } else {
+                                // (a head past the last has dz = x = 0)
+                                dwa[i][e] = fma2(ga[i][e], mul2(fa[i][e], scale), dwa[i][e]);
+                                dwb[i][e] = fma2(gb[i][e], mul2(fb[i][e], scale), dwb[i][e]);
+                                ga[i][e] = mul2(scale, fma2(fa[i][e], back, mul2(ga[i][e], wa[i][e])));
+                                gb[i][e] = mul2(scale, fma2(fb[i][e], back, mul2(gb[i][e], wb[i][e])));
+                            }
+                        }
+                    }
+                    if (!GRAD && (all_turned || turned[i])) turn<V, INTERLEAVED>(c[i], s[i], fa[i], fb[i]);
+                    if (h < h_end) {
+                        const int row = h * p.dim;
+                        if (has_a[i]) Raw<T, V>::store(out + row + at_a[i], GRAD ? ga[i] : fa[i]);
+                        if (has_b[i]) Raw<T, V>::store(out + row + at_b[i], GRAD ? gb[i] : fb[i]);
+                    }
                 }
             }
         }
     }
-    if (GRAD && sd.dw) {
+    if (GRAD && NORM && sd.dw) {
         // a warp's groups of lanes, then the CTA's warps, in order
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
+                float a[2], b[2];
+                unpack2(dwa[i][e / 2], a[0], a[1]);
+                unpack2(dwb[i][e / 2], b[0], b[1]);
+                float va = a[e & 1], vb = b[e & 1];
                 for (int d = p.lanes; d < 32; d *= 2) {
-                    dwa[i][e] += __shfl_xor_sync(0xFFFFFFFFu, dwa[i][e], d);
-                    dwb[i][e] += __shfl_xor_sync(0xFFFFFFFFu, dwb[i][e], d);
+                    va += __shfl_xor_sync(0xFFFFFFFFu, va, d);
+                    vb += __shfl_xor_sync(0xFFFFFFFFu, vb, d);
                 }
-                if (group == 0 && has_a[i]) red[warp][at_a[i] + e] = dwa[i][e];
-                if (group == 0 && has_b[i]) red[warp][at_b[i] + e] = dwb[i][e];
+                if (group == 0 && has_a[i]) red[warp][at_a[i] + e] = va;
+                if (group == 0 && has_b[i]) red[warp][at_b[i] + e] = vb;
             }
         __syncthreads();
         for (int d = threadIdx.x; d < p.dim; d += kRopeThreads) {
@@ -341,7 +393,7 @@ __global__ void __launch_bounds__(1024) rope_sum_kernel(const __grid_constant__ 
 template <typename T>
 int vector_width(const RopeArgs &a, bool grad)
 {
-    for (int v = kPerVec<T>; v > 1; v /= 2) {
+    for (int v = 4; v > 1; v /= 2) {
         bool fits = a.dim % v == 0 && a.rot % (a.interleaved ? 2 : 2 * v) == 0;
         for (const RopeSide &s : a.side) {
             if (s.heads == 0) continue;
@@ -355,17 +407,19 @@ int vector_width(const RopeArgs &a, bool grad)
     return 1;
 }
 
-template <typename T, int V, bool GRAD>
+template <typename T, int V, bool GRAD, bool NORM>
 cudaError_t launch_width(RopeArgs &a, cudaStream_t s)
 {
-    constexpr int UNROLL = GRAD ? 2 : 4;
+    constexpr int UNROLL = V == 4 ? 4 : 2;
     const int n = a.interleaved ? (a.dim + 2 * V - 1) / (2 * V) : a.rot / (2 * V) + (a.dim - a.rot + 2 * V - 1) / (2 * V);
     a.pairs = n;
     a.lanes = 1;
     while (a.lanes < 32 && a.lanes < n) a.lanes *= 2;
-    a.block_heads = 32 / a.lanes * UNROLL;
-    // a block's CTAs in proportion to its side's heads
     const int heads = a.side[0].heads + a.side[1].heads;
+    // a side's heads in one block where the tokens alone give every warp work: the angles are computed once a block
+    a.block_heads = 32 / a.lanes * UNROLL;
+    if (a.tokens >= kCtas * kRopeWarps / 2) a.block_heads = std::max({a.block_heads, a.side[0].heads, a.side[1].heads});
+    // a block's CTAs in proportion to its side's heads
     const long long most = (a.tokens + kRopeWarps - 1) / kRopeWarps;
     long long ctas = 0;
     for (RopeSide &sd : a.side) {
@@ -375,18 +429,23 @@ cudaError_t launch_width(RopeArgs &a, cudaStream_t s)
         sd.ctas = static_cast<int>(std::max(1ll, std::min(most, share)));
         ctas += static_cast<long long>(sd.blocks) * sd.ctas;
     }
-    return launch_early(rope_kernel<T, V, UNROLL, GRAD>, dim3(static_cast<unsigned>(ctas)), dim3(kRopeThreads), 0, s, a);
+    const dim3 grid(static_cast<unsigned>(ctas)), block(kRopeThreads);
+    if constexpr (V == 4) {
+        if (a.pairs == a.lanes && a.dim == 2 * V * a.pairs)
+            return a.interleaved ? launch_early(rope_kernel<T, V, UNROLL, GRAD, NORM, true, true>, grid, block, 0, s, a)
+                                 : launch_early(rope_kernel<T, V, UNROLL, GRAD, NORM, false, true>, grid, block, 0, s, a);
+    }
+    return a.interleaved ? launch_early(rope_kernel<T, V, UNROLL, GRAD, NORM, true, false>, grid, block, 0, s, a)
+                         : launch_early(rope_kernel<T, V, UNROLL, GRAD, NORM, false, false>, grid, block, 0, s, a);
 }
 
 template <typename T, bool GRAD>
 cudaError_t launch_rope(RopeArgs &a, cudaStream_t s)
 {
     switch (vector_width<T>(a, GRAD)) {
-    case 8:
-        if constexpr (sizeof(T) == 2) return launch_width<T, 8, GRAD>(a, s);
-    case 4: return launch_width<T, 4, GRAD>(a, s);
-    case 2: return launch_width<T, 2, GRAD>(a, s);
-    default: return launch_width<T, 1, GRAD>(a, s);
+    case 4: return a.norm ? launch_width<T, 4, GRAD, true>(a, s) : launch_width<T, 4, GRAD, false>(a, s);
+    case 2: return a.norm ? launch_width<T, 2, GRAD, true>(a, s) : launch_width<T, 2, GRAD, false>(a, s);
+    default: return a.norm ? launch_width<T, 1, GRAD, true>(a, s) : launch_width<T, 1, GRAD, false>(a, s);
     }
 }
 
@@ -410,7 +469,7 @@ int check_call(const RopeCall &c)
         !std::isfinite(c.factor) || !std::isfinite(c.eps) || c.eps < 0.0f || (c.rot > 0 && !c.inv_freq) ||
         (!c.norm && (c.w_q || c.w_k)))
         return CDG_ERR_INVALID_ARG;
-    if (c.dim > kMaxHead || c.heads > 65536 || c.kv_heads > 65536 || c.tokens >= (1ll << 31)) return CDG_ERR_UNSUPPORTED;
+    if (c.dim > kMaxHead || c.heads > kMaxHeads || c.kv_heads > kMaxHeads || c.tokens >= (1ll << 31)) return CDG_ERR_UNSUPPORTED;
     if (!aligned_to(c.inv_freq, 4) || !aligned_to(c.w_q, 4) || !aligned_to(c.w_k, 4) || !aligned_to(c.positions, c.index_bytes))
         return CDG_ERR_ALIGNMENT;
     return CDG_OK;
@@ -518,7 +577,7 @@ int cdg_qk_rope(const void *q, long long ld_q, const void *k, long long ld_k, co
 
 size_t cdg_qk_rope_grad_workspace_bytes(long long tokens, int heads, int kv_heads, int dim)
 {
-    if (tokens < 0 || tokens >= (1ll << 31) || heads < 0 || kv_heads < 0 || heads > 65536 || kv_heads > 65536 || heads + kv_heads < 1 ||
+    if (tokens < 0 || tokens >= (1ll << 31) || heads < 0 || kv_heads < 0 || heads > cdg::kMaxHeads || kv_heads > cdg::kMaxHeads || heads + kv_heads < 1 ||
         dim < 1 || dim > cdg::kMaxHead)
         return 0;
     return static_cast<size_t>(cdg::partial_rows(heads, kv_heads)) * dim * 4;
