@@ -62,6 +62,24 @@ __device__ __forceinline__ void tmem_wait(float (&r)[32])
                  :
                  : "memory");
 }
+// Eight columns of tensor memory times f.
+__device__ __forceinline__ void tmem_scale_8(uint32_t taddr, float f)
+{
+    float r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])
+                 :
+                 : "memory");
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] *= f;
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(r[0]),
+                 "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t *r)
 {
     asm volatile(
@@ -97,13 +115,15 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uin
 }
 
 // D (128 x dim) (+)= A B over 128 rows of the MN-major tile B, A in tensor
-// memory: 16-bit values, columns [0, 64) at a, [64, 128) at a_high.
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t idesc, bool add)
+// memory: 16-bit values, CHUNK of them (CHUNK / 2 columns) from every CHUNK-th
+// column of fp32 scores that they were made from.
+template <int CHUNK>
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
     const uint64_t bd = sdesc_mn_slices(b);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        umma_f16_ts(d, (k < 4 ? a : a_high) + 8u * (k & 3), bd + 128u * k, idesc, add || k != 0);
+        umma_f16_ts(d, a + (16 * k / CHUNK) * CHUNK + 8u * (k % (CHUNK / 16)), bd + 128u * k, idesc, add || k != 0);
 }
 
 // ---------------------------------------------------------------- sequences
@@ -198,11 +218,12 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// A row of `dim` fp32 sums from tensor memory, times f, to 16-bit values at `out`.
+// Columns [c0, c1) of a row of fp32 sums in tensor memory (both multiples of 8;
+// taddr the row's first column), times f, to 16-bit values of the row at `out`.
 template <bool BF16>
-__device__ __forceinline__ void store_row(uint32_t taddr, int dim, float f, void *out, bool valid)
+__device__ __forceinline__ void store_row(uint32_t taddr, int c0, int c1, float f, void *out, bool valid)
 {
-    for (int c0 = 0; c0 < dim; c0 += 32) {
+    for (; c0 < c1; c0 += 32) {
         float v[32];
         tmem_ld_32(taddr + c0, v);
         tmem_wait(v);
@@ -210,16 +231,16 @@ __device__ __forceinline__ void store_row(uint32_t taddr, int dim, float f, void
             uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + c0);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (c0 + 8 * i < dim)
+                if (c0 + 8 * i < c1)
                     q[i] = make_uint4(round2<BF16>(v[8 * i] * f, v[8 * i + 1] * f), round2<BF16>(v[8 * i + 2] * f, v[8 * i + 3] * f),
                                       round2<BF16>(v[8 * i + 4] * f, v[8 * i + 5] * f),
                                       round2<BF16>(v[8 * i + 6] * f, v[8 * i + 7] * f));
         }
     }
 }
-__device__ __forceinline__ void zero_row(void *out, int dim)
+__device__ __forceinline__ void zero_row(void *out, int c0, int c1)
 {
-    for (int c = 0; c < dim; c += 8) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + c) = make_uint4(0, 0, 0, 0);
+    for (; c0 < c1; c0 += 8) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + c0) = make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace cdg

@@ -15,17 +15,17 @@
 //
 // p and ds are rounded to 16 bits as operands of the products that sum them.
 //
-// Each kernel's warps (384 threads): 0-7 compute (128 rows x 64 columns a
-// warpgroup), 8 loads by TMA, 9 issues MMAs, 10 fetches the queries'
+// Each kernel's warps (640 threads): 0-15 compute (128 rows x 32 columns a
+// warpgroup), 16 loads by TMA, 17 issues MMAs, 18 fetches the queries'
 // statistics of a step (dk and dv).  The two phases of a step, p and ds, each
 // overlap two products of the tensor cores: dk and dv run
 //   p(i) | dS^T(i-1) Q, dP^T(i)      then      ds(i) | P^T(i) dO, S^T(i+1)
 #include "attention_device.cuh"
-#include "token_device.cuh"
 
 namespace cdg {
 namespace {
 
+constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpStats = 18;
 constexpr int kSlots = 2;  // steps of each streamed operand in shared memory
 
 // (- lse log2 e, D) of every row and head; a row that saw nothing (lse = -inf)
@@ -85,7 +85,7 @@ __device__ __forceinline__ GradSmem grad_layout(const CatParams &p, uint8_t *sme
     S.fixed_b = base + S.tile_bytes;
     S.ring_a = base + 2 * S.tile_bytes;
     S.ring_b = S.ring_a + kSlots * S.tile_bytes;
-    S.stats = S.ring_b + kSlots * S.tile_bytes;  // kSlots x 128 float2
+    S.stats = S.ring_b + kSlots * S.tile_bytes;  // kSlots x 128 shifts, then 128 sums
     const uint32_t bars = S.stats + kSlots * CAT_TILE * 8;
     uint32_t at = bars;
     auto take = [&](int n) {
@@ -114,10 +114,10 @@ __device__ __forceinline__ GradSmem grad_layout(const CatParams &p, uint8_t *sme
         for (int s = 0; s < kSlots; ++s) {
             for (uint32_t b : {S.B.full_a0, S.B.empty_a0, S.B.full_b0, S.B.empty_b0}) mbar_init(b + 8u * s, 1);
             mbar_init(S.B.st_full0 + 8u * s, 32);
-            mbar_init(S.B.st_empty0 + 8u * s, 8);
+            mbar_init(S.B.st_empty0 + 8u * s, 16);
         }
         for (uint32_t b : {S.B.s_full, S.B.dp_full, S.B.out_full, S.B.drain}) mbar_init(b, 1);
-        for (uint32_t b : {S.B.s_read, S.B.ds_ready}) mbar_init(b, 8);
+        for (uint32_t b : {S.B.s_read, S.B.ds_ready}) mbar_init(b, 16);
         for (int s = 0; s <= 2 * kSlots; ++s) S.slot_parity[s] = 0u;
         *S.abort_flag = 0u;
         fence_mbar_init();
@@ -140,7 +140,7 @@ __device__ __forceinline__ void grad_end(const CatParams &p, const GradSmem &S, 
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x / 32 == 9) {
+    if (threadIdx.x / 32 == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -197,108 +197,116 @@ struct KeyTile {
     int lo, count;   // first query tile and their number, for each head
 };
 
+// Four numbers of shared memory that the whole warp reads.
+__device__ __forceinline__ void ld_shared_4(uint32_t at, float (&v)[4])
+{
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(at));
+}
+
+// Zeroes the columns past [lo, hi).
+__device__ __forceinline__ void hide(float (&s)[32], int lo, int hi)
+{
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (e < lo || e >= hi) s[e] = 0.0f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void put_rounded(uint32_t taddr, const float (&s)[32])
+{
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = round2<BF16>(s[2 * e], s[2 * e + 1]);
+    tmem_st_16(taddr, w);
+    tmem_st_wait();
+}
+
 template <bool BF16>
 __device__ __forceinline__ void compute_dkv(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
                                             const KeyTile &kt, int steps, int kv_head)
 {
-    const int warp = threadIdx.x / 32, half = warp / 4, row = threadIdx.x & 127;
+    const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t s_col = tmem + lanes + kS + 64u * half, dp_col = tmem + lanes + kDP + 64u * half;
-    const f32x2 c2 = pack2(p.scale_log2, p.scale_log2);
+    const uint32_t s_col = tmem + lanes + kS + 32u * part, dp_col = tmem + lanes + kDP + 32u * part;
+    const f32x2 c2 = pack2(p.scale_log2, p.scale_log2), minus = pack2(-1.0f, -1.0f);
     const int off = at.kl - at.ql, j = kt.j0 + row;
     bool ok = true;
     int tile = kt.lo;
     for (int n = 0; n < steps; ++n) {
         const int slot = n % kSlots;
-        const uint32_t stats = S.stats + slot * CAT_TILE * 8 + half * 64 * 8;
+        const uint32_t stats = S.stats + slot * 2 * CAT_TILE * 4 + part * 32 * 4;
         const int i0 = tile * CAT_TILE;
         if (++tile == kt.lo + kt.count) tile = kt.lo;
-        // columns [lo, hi) of this half see the key
+        // columns [lo, hi) of this part see the key
         const bool whole = (!p.causal || kt.j0 + CAT_TILE - 1 <= i0 + off) && (!p.window || kt.j0 > i0 + CAT_TILE - 1 + off - p.window);
-        const int lo = p.causal ? j - off - i0 - 64 * half : 0, hi = p.window ? j - off + p.window - i0 - 64 * half : 64;
+        const int lo = p.causal ? j - off - i0 - 32 * part : 0, hi = p.window ? j - off + p.window - i0 - 32 * part : 32;
         if (!wait_bar(S.B.st_full0 + 8u * slot, (n / kSlots) & 1, ctl) || !wait_bar(S.B.s_full, n & 1, ctl)) {
             ok = false;
             break;
         }
         tc_fence_after();
-        float s[2][32];
-        tmem_ld_32(s_col, s[0]);
-        tmem_ld_32(s_col + 32u, s[1]);
-        tmem_wait(s[0]);
-        tmem_wait(s[1]);
+        float s[32];
+        tmem_ld_32(s_col, s);
+        tmem_wait(s);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t w[16];
+        for (int e = 0; e < 32; e += 4) {
+            float shift[4];
+            ld_shared_4(stats + e * 4u, shift);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float n0, d0, n1, d1;
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(n0), "=f"(d0), "=f"(n1), "=f"(d1) : "r"(stats + (32 * q + e) * 8u));
+            for (int f = 0; f < 4; f += 2) {
                 float a, b;
-                unpack2(fma2(pack2(s[q][e], s[q][e + 1]), c2, pack2(n0, n1)), a, b);
-                a = exp2_approx(a);
-                b = exp2_approx(b);
-                if (!whole) {
-                    if (32 * q + e < lo || 32 * q + e >= hi) a = 0.0f;
-                    if (32 * q + e + 1 < lo || 32 * q + e + 1 >= hi) b = 0.0f;
-                }
-                s[q][e] = a;
-                s[q][e + 1] = b;
-                w[e / 2] = round2<BF16>(a, b);
+                unpack2(fma2(pack2(s[e + f], s[e + f + 1]), c2, pack2(shift[f], shift[f + 1])), a, b);
+                s[e + f] = exp2_approx(a);
+                s[e + f + 1] = exp2_approx(b);
             }
-            tmem_st_16(s_col + 16u * q, w);
         }
-        tmem_st_wait();
+        if (!whole) hide(s, lo, hi);
+        put_rounded<BF16>(s_col, s);
         warp_arrive(S.B.s_read);
         if (!wait_bar(S.B.dp_full, n & 1, ctl)) {
             ok = false;
             break;
         }
         tc_fence_after();
-        float dp[2][32];
-        tmem_ld_32(dp_col, dp[0]);
-        tmem_ld_32(dp_col + 32u, dp[1]);
-        tmem_wait(dp[0]);
-        tmem_wait(dp[1]);
+        float dp[32];
+        tmem_ld_32(dp_col, dp);
+        tmem_wait(dp);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t w[16];
+        for (int e = 0; e < 32; e += 4) {
+            float d[4];
+            ld_shared_4(stats + (CAT_TILE + e) * 4u, d);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float n0, d0, n1, d1;
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(n0), "=f"(d0), "=f"(n1), "=f"(d1) : "r"(stats + (32 * q + e) * 8u));
-                float a = s[q][e] * (dp[q][e] - d0), b = s[q][e + 1] * (dp[q][e + 1] - d1);
-                if (!whole) {  // (dP of an unseen pair may be anything)
-                    if (32 * q + e < lo || 32 * q + e >= hi) a = 0.0f;
-                    if (32 * q + e + 1 < lo || 32 * q + e + 1 >= hi) b = 0.0f;
-                }
-                w[e / 2] = round2<BF16>(a, b);
-            }
-            tmem_st_16(dp_col + 16u * q, w);
+            for (int f = 0; f < 4; f += 2)
+                unpack2(mul2(pack2(s[e + f], s[e + f + 1]), fma2(pack2(d[f], d[f + 1]), minus, pack2(dp[e + f], dp[e + f + 1]))),
+                        dp[e + f], dp[e + f + 1]);
         }
-        tmem_st_wait();
+        if (!whole) hide(dp, lo, hi);  // (dP of an unseen pair may be anything)
+        put_rounded<BF16>(dp_col, dp);
         warp_arrive(S.B.ds_ready);
         if ((threadIdx.x & 31) == 0) mbar_arrive(S.B.st_empty0 + 8u * slot);
     }
     if (ok && steps > 0) ok = wait_bar(S.B.out_full, 0, ctl);
     if (!ok) return;
     tc_fence_after();
-    // the first warpgroup stores dv, the second dk
+    // the first two warpgroups store dv, the others dk, half of the columns each
     const long long token = at.k0 + j;
-    uint16_t *out = half ? static_cast<uint16_t *>(p.dk) + token * p.ld_dk : static_cast<uint16_t *>(p.dv) + token * p.ld_dv;
+    const bool is_dk = part >= 2;
+    uint16_t *out = is_dk ? static_cast<uint16_t *>(p.dk) + token * p.ld_dk : static_cast<uint16_t *>(p.dv) + token * p.ld_dv;
     out += static_cast<long long>(kv_head) * p.dim;
-    if (steps > 0) store_row<BF16>(tmem + lanes + kSum + 64u * p.slices * half, p.dim, half ? p.scale : 1.0f, out, j < at.kl);
-    else if (j < at.kl) zero_row(out, p.dim);
+    const int c0 = 32 * p.slices * (part & 1), c1 = min(p.dim, c0 + 32 * p.slices);
+    if (steps > 0) store_row<BF16>(tmem + lanes + kSum + 64u * p.slices * is_dk, c0, c1, is_dk ? p.scale : 1.0f, out, j < at.kl);
+    else if (j < at.kl) zero_row(out, c0, c1);
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(CAT_THREADS, 1) attention_dkv_kernel(const __grid_constant__ CatParams p)
+__global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(const __grid_constant__ CatParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const GradSmem S = grad_layout(p, smem_raw);
     const int warp = threadIdx.x / 32;
     grid_dep_launch_dependents();
     grid_dep_wait();
-    if (warp == 9) {
+    if (warp == kWarpMma) {
         tmem_alloc(smem_u32(S.tmem_slot), 512);
         tmem_relinquish();
     }
@@ -324,15 +332,15 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dkv_kernel(const __g
             tile = kt.lo + n - h * kt.count;
         };
         if (steps == 0) {
-            if (warp < 8) compute_dkv<BF16>(p, S, ctl, tmem, at, kt, 0, kv_head);
-        } else if (warp == 8) {
+            if (warp < 16) compute_dkv<BF16>(p, S, ctl, tmem, at, kt, 0, kv_head);
+        } else if (warp == kWarpLoad) {
             run_grad_loads(p, S, ctl, steps, p.tmK, p.tmV, kv_head, at.k0 + kt.j0, p.tmQ, p.tmDO,
                            [&](int n, int &head, int &token) {
                                int tile;
                                where(n, head, tile);
                                token = at.q0 + tile * CAT_TILE;
                            });
-        } else if (warp == 10) {
+        } else if (warp == kWarpStats) {
             const int lane = threadIdx.x & 31;
             for (int n = 0; n < steps; ++n) {
                 const int slot = n % kSlots;
@@ -344,11 +352,12 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dkv_kernel(const __g
                 for (int e = 0; e < 4; ++e) {
                     const int c = 32 * e + lane, i = tile * CAT_TILE + c;
                     const float2 v = i < at.ql ? __ldg(src + i) : make_float2(-INFINITY, 0.0f);
-                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(S.stats + (slot * CAT_TILE + c) * 8u), "f"(v.x), "f"(v.y) : "memory");
+                    st_shared_f32(S.stats + (slot * 2 * CAT_TILE + c) * 4u, v.x);
+                    st_shared_f32(S.stats + ((slot * 2 + 1) * CAT_TILE + c) * 4u, v.y);
                 }
                 mbar_arrive(S.B.st_full0 + 8u * slot);
             }
-        } else if (warp == 9) {
+        } else if (warp == kWarpMma) {
             const bool leader = elect_one_sync();
             const uint32_t s = tmem + kS, dp = tmem + kDP, dv = tmem + kSum, dk = dv + 64u * p.slices;
             auto a_tile = [&](int n) { return S.ring_a + (n % kSlots) * S.tile_bytes; };
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dkv_kernel(const __g
                 if (!wait_bar(S.B.s_read, n & 1, ctl)) break;
                 tc_fence_after();
                 if (leader) {
-                    issue_pv(dv, s, s + 64u, b_tile(n), p.idesc_pv, n != 0);
+                    issue_pv<32>(dv, s, b_tile(n), p.idesc_pv, n != 0);
                     umma_commit(S.B.empty_b0 + 8u * (n % kSlots));
                 }
                 __syncwarp();
@@ -394,7 +403,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dkv_kernel(const __g
                 if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
                 tc_fence_after();
                 if (leader) {
-                    issue_pv(dk, dp, dp + 64u, a_tile(n), p.idesc_pv, n != 0);
+                    issue_pv<32>(dk, dp, a_tile(n), p.idesc_pv, n != 0);
                     umma_commit(S.B.empty_a0 + 8u * (n % kSlots));
                 }
                 __syncwarp();
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dkv_kernel(const __g
             }
             __syncwarp();
             drain_mmas(p, S, leader);
-        } else if (warp < 8) {
+        } else if (warp < 16) {
             compute_dkv<BF16>(p, S, ctl, tmem, at, kt, steps, kv_head);
         }
     }
@@ -424,9 +433,9 @@ template <bool BF16>
 __device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
                                            int i0, int head, int lo, int hi)
 {
-    const int warp = threadIdx.x / 32, half = warp / 4, row = threadIdx.x & 127, i = i0 + row;
+    const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127, i = i0 + row;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t s_col = tmem + lanes + kS + 64u * half, dp_col = tmem + lanes + kDP + 64u * half;
+    const uint32_t s_col = tmem + lanes + kS + 32u * part, dp_col = tmem + lanes + kDP + 32u * part;
     const f32x2 c2 = pack2(p.scale_log2, p.scale_log2);
     const int r_first = i0 + at.kl - at.ql, r = r_first + row;
     const long long token = at.q0 + i;
@@ -438,74 +447,56 @@ __device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S
         const int n = j - lo, k0 = j * CAT_TILE;
         const bool whole = k0 + CAT_TILE <= at.kl && (!p.causal || k0 + CAT_TILE - 1 <= r_first) &&
                            (!p.window || k0 > r_first + CAT_TILE - 1 - p.window);
-        const int c_hi = min(at.kl, p.causal ? r + 1 : at.kl) - k0 - 64 * half, c_lo = p.window ? r - p.window + 1 - k0 - 64 * half : 0;
         if (!wait_bar(S.B.s_full, n & 1, ctl)) {
             ok = false;
             break;
         }
         tc_fence_after();
-        float s[2][32];
-        tmem_ld_32(s_col, s[0]);
-        tmem_ld_32(s_col + 32u, s[1]);
-        tmem_wait(s[0]);
-        tmem_wait(s[1]);
+        float s[32];
+        tmem_ld_32(s_col, s);
+        tmem_wait(s);
         warp_arrive(S.B.s_read);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float a, b;
-                unpack2(fma2(pack2(s[q][e], s[q][e + 1]), c2, shift), a, b);
-                s[q][e] = exp2_approx(a);
-                s[q][e + 1] = exp2_approx(b);
-            }
+        for (int e = 0; e < 32; e += 2) {
+            float a, b;
+            unpack2(fma2(pack2(s[e], s[e + 1]), c2, shift), a, b);
+            s[e] = exp2_approx(a);
+            s[e + 1] = exp2_approx(b);
+        }
         if (!wait_bar(S.B.dp_full, n & 1, ctl)) {
             ok = false;
             break;
         }
         tc_fence_after();
-        float dp[2][32];
-        tmem_ld_32(dp_col, dp[0]);
-        tmem_ld_32(dp_col + 32u, dp[1]);
-        tmem_wait(dp[0]);
-        tmem_wait(dp[1]);
+        float dp[32];
+        tmem_ld_32(dp_col, dp);
+        tmem_wait(dp);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float a, b;
-                unpack2(mul2(pack2(s[q][e], s[q][e + 1]), add2(pack2(dp[q][e], dp[q][e + 1]), minus_d)), a, b);
-                if (!whole) {  // (scores and dP of an unseen pair may be anything)
-                    if (32 * q + e < c_lo || 32 * q + e >= c_hi) a = 0.0f;
-                    if (32 * q + e + 1 < c_lo || 32 * q + e + 1 >= c_hi) b = 0.0f;
-                }
-                w[e / 2] = round2<BF16>(a, b);
-            }
-            tmem_st_16(dp_col + 16u * q, w);
-        }
-        tmem_st_wait();
+        for (int e = 0; e < 32; e += 2)
+            unpack2(mul2(pack2(s[e], s[e + 1]), add2(pack2(dp[e], dp[e + 1]), minus_d)), dp[e], dp[e + 1]);
+        if (!whole)  // (scores and dP of an unseen pair may be anything)
+            hide(dp, p.window ? r - p.window + 1 - k0 - 32 * part : 0, min(at.kl, p.causal ? r + 1 : at.kl) - k0 - 32 * part);
+        put_rounded<BF16>(dp_col, dp);
         warp_arrive(S.B.ds_ready);
     }
     if (ok && hi > lo) ok = wait_bar(S.B.out_full, 0, ctl);
     if (!ok) return;
     tc_fence_after();
     uint16_t *out = static_cast<uint16_t *>(p.dq) + token * p.ld_dq + static_cast<long long>(head) * p.dim;
-    if (half == 0) {
-        if (hi > lo) store_row<BF16>(tmem + lanes + kSum, p.dim, p.scale, out, valid);
-        else if (valid) zero_row(out, p.dim);
-    }
+    const int c0 = 32 * part, c1 = min(p.dim, c0 + 32);
+    if (hi > lo) store_row<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out, valid);
+    else if (valid) zero_row(out, c0, c1);
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(CAT_THREADS, 1) attention_dq_kernel(const __grid_constant__ CatParams p)
+__global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const __grid_constant__ CatParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const GradSmem S = grad_layout(p, smem_raw);
     const int warp = threadIdx.x / 32;
     grid_dep_launch_dependents();
     grid_dep_wait();
-    if (warp == 9) {
+    if (warp == kWarpMma) {
         tmem_alloc(smem_u32(S.tmem_slot), 512);
         tmem_relinquish();
     }
@@ -523,14 +514,14 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dq_kernel(const __gr
         key_steps(p, at, i0, min(i0 + CAT_TILE, at.ql), lo, hi);
         const int steps = hi - lo, kv_head = head / p.group;
         if (steps == 0) {
-            if (warp < 8) compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
-        } else if (warp == 8) {
+            if (warp < 16) compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
+        } else if (warp == kWarpLoad) {
             // (one tensor map a loop: the CTA's own tiles come from the query side)
             run_grad_loads(p, S, ctl, steps, p.tmQ, p.tmDO, head, at.q0 + i0, p.tmK, p.tmV, [&](int n, int &h, int &token) {
                 h = kv_head;
                 token = at.k0 + (lo + n) * CAT_TILE;
             });
-        } else if (warp == 9) {
+        } else if (warp == kWarpMma) {
             const bool leader = elect_one_sync();
             const uint32_t s = tmem + kS, dp = tmem + kDP, dq = tmem + kSum;
             auto a_tile = [&](int n) { return S.ring_a + (n % kSlots) * S.tile_bytes; };
@@ -568,7 +559,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dq_kernel(const __gr
                 if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
                 tc_fence_after();
                 if (leader) {
-                    issue_pv(dq, dp, dp + 64u, a_tile(n), p.idesc_pv, n != 0);
+                    issue_pv<32>(dq, dp, a_tile(n), p.idesc_pv, n != 0);
                     umma_commit(S.B.empty_a0 + 8u * (n % kSlots));
                     if (!next) umma_commit(S.B.out_full);
                 }
@@ -577,7 +568,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_dq_kernel(const __gr
             }
             __syncwarp();
             drain_mmas(p, S, leader);
-        } else if (warp < 8) {
+        } else if (warp < 16) {
             compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
         }
     }
@@ -601,7 +592,7 @@ cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
 cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaStream_t s)
 {
     using namespace cdg;
-    const dim3 grid(static_cast<unsigned>(items)), block(CAT_THREADS);
+    const dim3 grid(static_cast<unsigned>(items)), block(CAT_GRAD_THREADS);
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
     return bf16 ? launch_early(attention_dkv_kernel<true>, grid, block, smem, s, p)
                 : launch_early(attention_dkv_kernel<false>, grid, block, smem, s, p);
@@ -610,7 +601,7 @@ cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaSt
 cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStream_t s)
 {
     using namespace cdg;
-    const dim3 grid(static_cast<unsigned>(items)), block(CAT_THREADS);
+    const dim3 grid(static_cast<unsigned>(items)), block(CAT_GRAD_THREADS);
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
     return bf16 ? launch_early(attention_dq_kernel<true>, grid, block, smem, s, p)
                 : launch_early(attention_dq_kernel<false>, grid, block, smem, s, p);

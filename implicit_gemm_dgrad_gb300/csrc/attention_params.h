@@ -9,7 +9,8 @@
 #include "cdg_params.h"
 
 #define CAT_TILE 128      // queries of an MMA tile, keys of a step
-#define CAT_THREADS 384   // 8 warps that compute, 1 that loads, 1 that issues MMAs, 2 more
+#define CAT_THREADS 384   // forward: 8 warps that compute, 1 that loads, 1 that issues MMAs, 2 more
+#define CAT_GRAD_THREADS 640  // gradient: 16 warps that compute, 1 that loads, 1 that issues MMAs, 2 more
 
 struct CatParams {
     CUtensorMap tmQ, tmK, tmV, tmDO;  // {dim, heads, tokens}, boxes of 64 columns x 1 head x 128 tokens, 128-byte swizzle

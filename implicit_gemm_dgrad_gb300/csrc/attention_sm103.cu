@@ -17,7 +17,6 @@
 // Roles (384 threads): warps 0-3 and 4-7 the tiles' softmax, warp 8 TMA loads
 // (Q once, K and V steps through a ring), warp 9 MMA issue.
 #include "attention_device.cuh"
-#include "token_device.cuh"
 
 namespace cdg {
 namespace {
@@ -85,15 +84,8 @@ __device__ __forceinline__ void run_softmax(const CatParams &p, const FwdBars &B
                 const float f = grow ? exp2_approx((m - top) * c) : 1.0f;
                 l *= f;
                 if (grow) m = top;
-                for (int c0 = 0; c0 < 64 * p.slices; c0 += 32) {
-                    float v[32];
-                    tmem_ld_32(o_col + c0, v);
-                    tmem_wait(v);
-                    uint32_t w[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e] * f);
-                    tmem_st_32x32b_x32(o_col + c0, w);
-                }
+#pragma unroll 1
+                for (int c0 = 0; c0 < 64 * p.slices; c0 += 8) tmem_scale_8(o_col + c0, f);
             }
         }
         const float mc = m == -INFINITY ? 0.0f : __fmul_rn(m, c);
@@ -128,9 +120,9 @@ __device__ __forceinline__ void run_softmax(const CatParams &p, const FwdBars &B
     // a row that sees nothing (l = 0, m = -inf) answers 0 and -inf
     const bool none = m == -INFINITY && l == 0.0f;
     if (range.hi > range.lo) {
-        store_row<BF16>(o_col, p.dim, none ? 0.0f : 1.0f / l, out, valid);
+        store_row<BF16>(o_col, 0, p.dim, none ? 0.0f : 1.0f / l, out, valid);
     } else if (valid) {
-        zero_row(out, p.dim);
+        zero_row(out, 0, p.dim);
     }
     if (valid)
         p.lse[static_cast<long long>(head) * p.q_tokens + token] =
@@ -261,7 +253,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_
                         tc_fence_after();
                         if (leader) {
                             const uint32_t a = tmem + 128u * t;
-                            issue_pv(tmem + 256u + o_cols * t, a, a + 32u, slot(nv), p.idesc_pv, n != 0);
+                            issue_pv<128>(tmem + 256u + o_cols * t, a, slot(nv), p.idesc_pv, n != 0);
                             if (j + 1 == range[t].hi) umma_commit(B.o_full0 + 8u * t);
                         }
                         __syncwarp();
