@@ -24,6 +24,13 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // Two fp32 values rounded to the 16-bit type, the first in the low half.
 template <bool BF16>
 __device__ __forceinline__ uint32_t round2(float a, float b)
@@ -104,13 +111,52 @@ __device__ __forceinline__ uint64_t sdesc_mn_slices(uint32_t saddr)
     return d;
 }
 
+// A value that is the same in all lanes of the (converged) warp, in a form that
+// the compiler knows to be: what is computed from it, the descriptors of MMAs
+// above all, then lives in uniform registers, where the instruction wants it.
+__device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce_or_sync(0xFFFFFFFFu, static_cast<unsigned>(v))); }
+
+// MMAs and commits under a predicate instead of a branch: the whole warp runs
+// the code around them, one lane issues.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+
 // D (128 x 128) = A B^T over the head's width, both K-major tiles of 64-column slices.
-__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int ksteps)
+template <int SLICES>
+__device__ __forceinline__ void issue_qk(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int ksteps)
 {
     const uint64_t ad = sdesc_k128_sw128(a), bd = sdesc_k128_sw128(b);
-    for (int k = 0; k < ksteps; ++k) {
+#pragma unroll
+    for (int k = 0; k < 4 * SLICES; ++k) {
         const uint32_t at = (k >> 2) * (kSliceBytes >> 4) + 2u * (k & 3);
-        umma_f16(d, ad + at, bd + at, idesc, k != 0);
+        if (k < ksteps) mma_ss(leader, d, ad + at, bd + at, idesc, k != 0);
     }
 }
 
@@ -118,12 +164,12 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uin
 // memory: 16-bit values, CHUNK of them (CHUNK / 2 columns) from every CHUNK-th
 // column of fp32 scores that they were made from.
 template <int CHUNK>
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void issue_pv(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
     const uint64_t bd = sdesc_mn_slices(b);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        umma_f16_ts(d, a + (16 * k / CHUNK) * CHUNK + 8u * (k % (CHUNK / 16)), bd + 128u * k, idesc, add || k != 0);
+        mma_ts(leader, d, a + (16 * k / CHUNK) * CHUNK + 8u * (k % (CHUNK / 16)), bd + 128u * k, idesc, add || k != 0);
 }
 
 // ---------------------------------------------------------------- sequences
@@ -179,6 +225,102 @@ __device__ __forceinline__ Place find_tile(const CatParams &p, long long item, i
     return Place{0, 0, 0, 0, -1};
 }
 
+// ---------------------------------------------------------------- work items
+// A launch has a CTA for every item it could have; those that run take over,
+// one by one, the items of CTAs that have not started yet (the hardware hands
+// out their numbers in order), so that barriers, tensor memory and the loads of
+// the next item are set up while the last one ends.  One warp fetches items and
+// finds their tiles ahead of the others, into two slots of shared memory; it asks
+// for an item once the loads of the one before have all been issued (sooner, and
+// CTAs in long items would keep others' work to themselves).
+struct Item {
+    int head;
+    Place at;
+};
+struct ItemBars {
+    uint32_t full0, empty0, reply_full, go, reply;  // reply: 16 bytes, 16-byte aligned
+    volatile int *slots;                        // [2][8]: 1 if there is an item, head, q0, ql, k0, kl, tile
+};
+constexpr int kItemBytes = 8 * 6 + 16 + 64;  // barriers, reply, slots
+
+__device__ __forceinline__ void run_items(const CatParams &p, const ItemBars &I, Ctl ctl, int rows, bool of_keys, int heads)
+{
+    const int lane = threadIdx.x & 31;
+    long long item = blockIdx.x;
+    int n = 0;
+    for (uint32_t asked = 0;; ++asked) {
+        const Place at = find_tile(p, item / heads, rows, of_keys);
+        if (at.tile >= 0) {
+            if (!wait_bar(I.empty0 + 8u * (n & 1), ((n >> 1) & 1) ^ 1u, ctl)) return;
+            if (lane == 0) {
+                volatile int *v = I.slots + 8 * (n & 1);
+                v[0] = 1; v[1] = static_cast<int>(item % heads);
+                v[2] = at.q0; v[3] = at.ql; v[4] = at.k0; v[5] = at.kl; v[6] = at.tile;
+                mbar_arrive(I.full0 + 8u * (n & 1));
+            }
+            __syncwarp();
+            if (!wait_bar(I.go, n & 1, ctl)) return;
+            ++n;
+        }
+        if (lane == 0) {
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(I.reply_full, 16);
+            asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(I.reply),
+                         "r"(I.reply_full)
+                         : "memory");
+        }
+        __syncwarp();
+        if (!wait_bar(I.reply_full, asked & 1u, ctl)) return;
+        uint32_t x, more;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z;\n\t"
+            "ld.shared.b128 r, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+            "selp.u32 %1, 1, 0, p;\n\t"
+            "mov.u32 %0, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, _}, r;\n\t}"
+            : "=&r"(x), "=&r"(more)
+            : "r"(I.reply)
+            : "memory");
+        __syncwarp();
+        if (!more) break;
+        item = x;
+    }
+    if (!wait_bar(I.empty0 + 8u * (n & 1), ((n >> 1) & 1) ^ 1u, ctl)) return;
+    if (lane == 0) {
+        I.slots[8 * (n & 1)] = 0;
+        mbar_arrive(I.full0 + 8u * (n & 1));
+    }
+}
+
+// The n-th item, for one of the warps that work on items; false after the last.
+__device__ __forceinline__ bool next_item(const ItemBars &I, Ctl ctl, int n, Item &item)
+{
+    if (!wait_bar(I.full0 + 8u * (n & 1), (n >> 1) & 1, ctl)) return false;
+    volatile int *v = I.slots + 8 * (n & 1);
+    const int some = v[0];
+    item.head = v[1];
+    item.at = Place{v[2], v[3], v[4], v[5], v[6]};
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(I.empty0 + 8u * (n & 1));
+    return some != 0;
+}
+
+// Lays out and initialises the barriers at `at` (16-byte aligned); `warps` work on items.
+__device__ __forceinline__ ItemBars init_items(uint8_t *generic, uint32_t at, int warps)
+{
+    const ItemBars I{at, at + 16, at + 32, at + 40, at + 48, reinterpret_cast<volatile int *>(generic + 64)};
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(I.full0 + 8u * s, 1);
+            mbar_init(I.empty0 + 8u * s, warps);
+        }
+        mbar_init(I.reply_full, 1);
+        mbar_init(I.go, 1);
+    }
+    return I;
+}
+
 // Key steps [lo, hi) that some query of [i0, i1) sees.
 __device__ __forceinline__ void key_steps(const CatParams &p, const Place &at, int i0, int i1, int &lo, int &hi)
 {
@@ -218,23 +360,41 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// Columns [c0, c1) of a row of fp32 sums in tensor memory (both multiples of 8;
-// taddr the row's first column), times f, to 16-bit values of the row at `out`.
+// Columns [c0, c1) of 32 rows of fp32 sums in tensor memory (both multiples of 8;
+// taddr the warp's first column), times the rows' f, to 16-bit values: lane i's
+// row at out + i * ld (elements), rows [0, rows) of the warp.  Four lanes
+// exchange their 16-byte pieces, so that a store writes 64 bytes of a row.
 template <bool BF16>
-__device__ __forceinline__ void store_row(uint32_t taddr, int c0, int c1, float f, void *out, bool valid)
+__device__ __forceinline__ void store_rows(uint32_t taddr, int c0, int c1, float f, uint16_t *out, long long ld, int rows)
 {
+    const int lane = threadIdx.x & 31;
     for (; c0 < c1; c0 += 32) {
         float v[32];
         tmem_ld_32(taddr + c0, v);
         tmem_wait(v);
-        if (valid) {
-            uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + c0);
+        uint32_t w[4][4];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = round2<BF16>(v[2 * e] * f, v[2 * e + 1] * f);
+        // transpose of four lanes' four pieces: piece i of lane j goes to piece j of lane i
+#pragma unroll
+        for (int d = 1; d <= 2; d *= 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (c0 + 8 * i < c1)
-                    q[i] = make_uint4(round2<BF16>(v[8 * i] * f, v[8 * i + 1] * f), round2<BF16>(v[8 * i + 2] * f, v[8 * i + 3] * f),
-                                      round2<BF16>(v[8 * i + 4] * f, v[8 * i + 5] * f),
-                                      round2<BF16>(v[8 * i + 6] * f, v[8 * i + 7] * f));
+                if (!(i & d)) {
+                    const bool high = lane & d;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t give = high ? w[i][e] : w[i + d][e];
+                        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, d);
+                        if (high) w[i][e] = got;
+                        else w[i + d][e] = got;
+                    }
+                }
+        const int col = c0 + 8 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (lane & ~3) + i;
+            if (row < rows && col < c1) *reinterpret_cast<uint4 *>(out + row * ld + col) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
         }
     }
 }

@@ -76,11 +76,12 @@ struct GradSmem {
     volatile uint32_t *abort_flag, *slot_parity;  // parity of each slot's last load: a, b, then the fixed tiles'
 };
 
-__device__ __forceinline__ GradSmem grad_layout(const CatParams &p, uint8_t *smem_raw)
+template <int SLICES>
+__device__ __forceinline__ GradSmem grad_layout(uint8_t *smem_raw)
 {
     GradSmem S;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    S.tile_bytes = kSliceBytes * p.slices;
+    S.tile_bytes = kSliceBytes * SLICES;
     S.fixed_a = base;
     S.fixed_b = base + S.tile_bytes;
     S.ring_a = base + 2 * S.tile_bytes;
@@ -146,10 +147,9 @@ __device__ __forceinline__ void grad_end(const CatParams &p, const GradSmem &S, 
     }
 }
 
-__device__ __forceinline__ void drain_mmas(const CatParams &p, const GradSmem &S, bool leader)
+__device__ __forceinline__ void drain_mmas(const CatParams &p, const GradSmem &S, uint32_t leader)
 {
-    if (leader) umma_commit(S.B.drain);
-    __syncwarp();
+    mma_commit(leader, S.B.drain);
     volatile uint32_t no_abort = 0;
     wait_bar(S.B.drain, 0, Ctl{&no_abort, p.status});
 }
@@ -294,15 +294,19 @@ __device__ __forceinline__ void compute_dkv(const CatParams &p, const GradSmem &
     uint16_t *out = is_dk ? static_cast<uint16_t *>(p.dk) + token * p.ld_dk : static_cast<uint16_t *>(p.dv) + token * p.ld_dv;
     out += static_cast<long long>(kv_head) * p.dim;
     const int c0 = 32 * p.slices * (part & 1), c1 = min(p.dim, c0 + 32 * p.slices);
-    if (steps > 0) store_row<BF16>(tmem + lanes + kSum + 64u * p.slices * is_dk, c0, c1, is_dk ? p.scale : 1.0f, out, j < at.kl);
+    const long long ld = is_dk ? p.ld_dk : p.ld_dv;
+    if (steps > 0)
+        store_rows<BF16>(tmem + lanes + kSum + 64u * p.slices * is_dk, c0, c1, is_dk ? p.scale : 1.0f, out - (threadIdx.x & 31) * ld, ld,
+                         at.kl - (j & ~31));
     else if (j < at.kl) zero_row(out, c0, c1);
 }
 
-template <bool BF16>
+template <bool BF16, int SLICES>
 __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(const __grid_constant__ CatParams p)
 {
+    constexpr uint32_t tile_bytes = kSliceBytes * SLICES;
     extern __shared__ uint8_t smem_raw[];
-    const GradSmem S = grad_layout(p, smem_raw);
+    const GradSmem S = grad_layout<SLICES>(smem_raw);
     const int warp = threadIdx.x / 32;
     grid_dep_launch_dependents();
     grid_dep_wait();
@@ -358,67 +362,45 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
                 mbar_arrive(S.B.st_full0 + 8u * slot);
             }
         } else if (warp == kWarpMma) {
-            const bool leader = elect_one_sync();
-            const uint32_t s = tmem + kS, dp = tmem + kDP, dv = tmem + kSum, dk = dv + 64u * p.slices;
-            auto a_tile = [&](int n) { return S.ring_a + (n % kSlots) * S.tile_bytes; };
-            auto b_tile = [&](int n) { return S.ring_b + (n % kSlots) * S.tile_bytes; };
+            const uint32_t leader = elect_one_sync();
+            const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dv = tm + kSum, dk = dv + 64u * SLICES;
+            const int total = uniform(steps), count = uniform(kt.count), rest = uniform(at.ql - kt.lo * CAT_TILE);
             // waits for the n-th streamed tile; rows behind the sequence's end become zeros
-            auto filled = [&](uint32_t full0, uint32_t tile, int n) {
+            auto filled = [&](uint32_t full0, uint32_t ring, int n) {
                 if (!wait_bar(full0 + 8u * (n % kSlots), (n / kSlots) & 1, ctl)) return false;
-                int head, q;
-                where(n, head, q);
                 tc_fence_after();
-                if (at.ql - q * CAT_TILE < CAT_TILE) zero_rows(tile, p.slices, at.ql - q * CAT_TILE);
+                const int valid = rest - n % count * CAT_TILE;
+                if (valid < CAT_TILE) zero_rows(ring + (n % kSlots) * tile_bytes, SLICES, valid);
                 return true;
             };
-            bool ok = wait_bar(S.B.fixed_full, 0, ctl) && filled(S.B.full_a0, a_tile(0), 0);
-            if (ok && leader) {
-                issue_qk(s, S.fixed_a, a_tile(0), p.idesc_qk, p.ksteps);
-                umma_commit(S.B.s_full);
-            }
-            __syncwarp();
-            ok = ok && filled(S.B.full_b0, b_tile(0), 0);
-            if (ok && leader) {
-                issue_qk(dp, S.fixed_b, b_tile(0), p.idesc_qk, p.ksteps);
-                umma_commit(S.B.dp_full);
-            }
-            __syncwarp();
-            for (int n = 0; ok && n < steps; ++n) {
-                const bool next = n + 1 < steps;
+            auto scores = [&](int n) {
+                if (!filled(S.B.full_a0, S.ring_a, n)) return false;
+                issue_qk<SLICES>(leader, s, S.fixed_a, S.ring_a + (n % kSlots) * tile_bytes, p.idesc_qk, p.ksteps);
+                mma_commit(leader, S.B.s_full);
+                return true;
+            };
+            auto dps = [&](int n) {
+                if (!filled(S.B.full_b0, S.ring_b, n)) return false;
+                issue_qk<SLICES>(leader, dp, S.fixed_b, S.ring_b + (n % kSlots) * tile_bytes, p.idesc_qk, p.ksteps);
+                mma_commit(leader, S.B.dp_full);
+                return true;
+            };
+            bool ok = wait_bar(S.B.fixed_full, 0, ctl) && scores(0) && dps(0);
+            for (int n = 0; ok && n < total; ++n) {
+                const bool next = n + 1 < total;
+                const int slot = n % kSlots;
                 if (!wait_bar(S.B.s_read, n & 1, ctl)) break;
                 tc_fence_after();
-                if (leader) {
-                    issue_pv<32>(dv, s, b_tile(n), p.idesc_pv, n != 0);
-                    umma_commit(S.B.empty_b0 + 8u * (n % kSlots));
-                }
-                __syncwarp();
-                if (next) {
-                    if (!filled(S.B.full_a0, a_tile(n + 1), n + 1)) break;
-                    if (leader) {
-                        issue_qk(s, S.fixed_a, a_tile(n + 1), p.idesc_qk, p.ksteps);
-                        umma_commit(S.B.s_full);
-                    }
-                    __syncwarp();
-                }
+                issue_pv<32>(leader, dv, s, S.ring_b + slot * tile_bytes, p.idesc_pv, n != 0);
+                mma_commit(leader, S.B.empty_b0 + 8u * slot);
+                if (next && !scores(n + 1)) break;
                 if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
                 tc_fence_after();
-                if (leader) {
-                    issue_pv<32>(dk, dp, a_tile(n), p.idesc_pv, n != 0);
-                    umma_commit(S.B.empty_a0 + 8u * (n % kSlots));
-                }
-                __syncwarp();
-                if (next) {
-                    if (!filled(S.B.full_b0, b_tile(n + 1), n + 1)) break;
-                    if (leader) {
-                        issue_qk(dp, S.fixed_b, b_tile(n + 1), p.idesc_qk, p.ksteps);
-                        umma_commit(S.B.dp_full);
-                    }
-                    __syncwarp();
-                } else if (leader) {
-                    umma_commit(S.B.out_full);
-                }
+                issue_pv<32>(leader, dk, dp, S.ring_a + slot * tile_bytes, p.idesc_pv, n != 0);
+                mma_commit(leader, S.B.empty_a0 + 8u * slot);
+                if (!next) mma_commit(leader, S.B.out_full);
+                else if (!dps(n + 1)) break;
             }
-            __syncwarp();
             drain_mmas(p, S, leader);
         } else if (warp < 16) {
             compute_dkv<BF16>(p, S, ctl, tmem, at, kt, steps, kv_head);
@@ -484,15 +466,16 @@ __device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S
     tc_fence_after();
     uint16_t *out = static_cast<uint16_t *>(p.dq) + token * p.ld_dq + static_cast<long long>(head) * p.dim;
     const int c0 = 32 * part, c1 = min(p.dim, c0 + 32);
-    if (hi > lo) store_row<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out, valid);
+    if (hi > lo) store_rows<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out - (threadIdx.x & 31) * p.ld_dq, p.ld_dq, at.ql - (i & ~31));
     else if (valid) zero_row(out, c0, c1);
 }
 
-template <bool BF16>
+template <bool BF16, int SLICES>
 __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const __grid_constant__ CatParams p)
 {
+    constexpr uint32_t tile_bytes = kSliceBytes * SLICES;
     extern __shared__ uint8_t smem_raw[];
-    const GradSmem S = grad_layout(p, smem_raw);
+    const GradSmem S = grad_layout<SLICES>(smem_raw);
     const int warp = threadIdx.x / 32;
     grid_dep_launch_dependents();
     grid_dep_wait();
@@ -522,51 +505,41 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const
                 token = at.k0 + (lo + n) * CAT_TILE;
             });
         } else if (warp == kWarpMma) {
-            const bool leader = elect_one_sync();
-            const uint32_t s = tmem + kS, dp = tmem + kDP, dq = tmem + kSum;
-            auto a_tile = [&](int n) { return S.ring_a + (n % kSlots) * S.tile_bytes; };
-            auto b_tile = [&](int n) { return S.ring_b + (n % kSlots) * S.tile_bytes; };
+            const uint32_t leader = elect_one_sync();
+            const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dq = tm + kSum;
+            const int total = uniform(steps), rest = uniform(at.kl - lo * CAT_TILE);
             auto scores = [&](int n) {
-                if (!wait_bar(S.B.full_a0 + 8u * (n % kSlots), (n / kSlots) & 1, ctl)) return false;
+                const int slot = n % kSlots;
+                if (!wait_bar(S.B.full_a0 + 8u * slot, (n / kSlots) & 1, ctl)) return false;
                 tc_fence_after();
                 // keys behind the sequence's end become zeros: dS K sums over them
-                const int valid = at.kl - (lo + n) * CAT_TILE;
-                if (valid < CAT_TILE) zero_rows(a_tile(n), p.slices, valid);
-                if (leader) {
-                    issue_qk(s, S.fixed_a, a_tile(n), p.idesc_qk, p.ksteps);
-                    umma_commit(S.B.s_full);
-                }
-                __syncwarp();
+                if (rest - n * CAT_TILE < CAT_TILE) zero_rows(S.ring_a + slot * tile_bytes, SLICES, rest - n * CAT_TILE);
+                issue_qk<SLICES>(leader, s, S.fixed_a, S.ring_a + slot * tile_bytes, p.idesc_qk, p.ksteps);
+                mma_commit(leader, S.B.s_full);
                 return true;
             };
             auto dps = [&](int n) {
-                if (!wait_bar(S.B.full_b0 + 8u * (n % kSlots), (n / kSlots) & 1, ctl)) return false;
+                const int slot = n % kSlots;
+                if (!wait_bar(S.B.full_b0 + 8u * slot, (n / kSlots) & 1, ctl)) return false;
                 tc_fence_after();
-                if (leader) {
-                    issue_qk(dp, S.fixed_b, b_tile(n), p.idesc_qk, p.ksteps);
-                    umma_commit(S.B.dp_full);
-                    umma_commit(S.B.empty_b0 + 8u * (n % kSlots));
-                }
-                __syncwarp();
+                issue_qk<SLICES>(leader, dp, S.fixed_b, S.ring_b + slot * tile_bytes, p.idesc_qk, p.ksteps);
+                mma_commit(leader, S.B.dp_full);
+                mma_commit(leader, S.B.empty_b0 + 8u * slot);
                 return true;
             };
             bool ok = wait_bar(S.B.fixed_full, 0, ctl) && scores(0) && dps(0);
-            for (int n = 0; ok && n < steps; ++n) {
-                const bool next = n + 1 < steps;
+            for (int n = 0; ok && n < total; ++n) {
+                const bool next = n + 1 < total;
                 if (!wait_bar(S.B.s_read, n & 1, ctl)) break;
                 tc_fence_after();
                 if (next && !scores(n + 1)) break;
                 if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
                 tc_fence_after();
-                if (leader) {
-                    issue_pv<32>(dq, dp, a_tile(n), p.idesc_pv, n != 0);
-                    umma_commit(S.B.empty_a0 + 8u * (n % kSlots));
-                    if (!next) umma_commit(S.B.out_full);
-                }
-                __syncwarp();
-                if (next && !dps(n + 1)) break;
+                issue_pv<32>(leader, dq, dp, S.ring_a + (n % kSlots) * tile_bytes, p.idesc_pv, n != 0);
+                mma_commit(leader, S.B.empty_a0 + 8u * (n % kSlots));
+                if (!next) mma_commit(leader, S.B.out_full);
+                else if (!dps(n + 1)) break;
             }
-            __syncwarp();
             drain_mmas(p, S, leader);
         } else if (warp < 16) {
             compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
@@ -594,8 +567,9 @@ cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaSt
     using namespace cdg;
     const dim3 grid(static_cast<unsigned>(items)), block(CAT_GRAD_THREADS);
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
-    return bf16 ? launch_early(attention_dkv_kernel<true>, grid, block, smem, s, p)
-                : launch_early(attention_dkv_kernel<false>, grid, block, smem, s, p);
+    void (*k)(CatParams) = p.slices == 2 ? (bf16 ? attention_dkv_kernel<true, 2> : attention_dkv_kernel<false, 2>)
+                                         : (bf16 ? attention_dkv_kernel<true, 1> : attention_dkv_kernel<false, 1>);
+    return launch_early(k, grid, block, smem, s, p);
 }
 
 cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStream_t s)
@@ -603,14 +577,16 @@ cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStr
     using namespace cdg;
     const dim3 grid(static_cast<unsigned>(items)), block(CAT_GRAD_THREADS);
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
-    return bf16 ? launch_early(attention_dq_kernel<true>, grid, block, smem, s, p)
-                : launch_early(attention_dq_kernel<false>, grid, block, smem, s, p);
+    void (*k)(CatParams) = p.slices == 2 ? (bf16 ? attention_dq_kernel<true, 2> : attention_dq_kernel<false, 2>)
+                                         : (bf16 ? attention_dq_kernel<true, 1> : attention_dq_kernel<false, 1>);
+    return launch_early(k, grid, block, smem, s, p);
 }
 
 cudaError_t cat_prepare_grad()
 {
-    for (auto *k : {cdg::attention_dkv_kernel<true>, cdg::attention_dkv_kernel<false>, cdg::attention_dq_kernel<true>,
-                    cdg::attention_dq_kernel<false>}) {
+    for (auto *k : {cdg::attention_dkv_kernel<true, 1>, cdg::attention_dkv_kernel<false, 1>, cdg::attention_dkv_kernel<true, 2>,
+                    cdg::attention_dkv_kernel<false, 2>, cdg::attention_dq_kernel<true, 1>, cdg::attention_dq_kernel<false, 1>,
+                    cdg::attention_dq_kernel<true, 2>, cdg::attention_dq_kernel<false, 2>}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CDG_MAX_DYN_SMEM);
         if (e != cudaSuccess) return e;
     }
