@@ -39,7 +39,7 @@ constexpr int kMaxSequences = 1 << 20;
 }  // namespace
 
 struct cdg_attention_st {
-    int heads, kv_heads, dim, dtype, causal, window, device;
+    int heads, kv_heads, dim, dtype, causal, window, device, sms;
     float scale;
     bool host_only;
     int *d_status;
@@ -61,8 +61,9 @@ int make_attention_plan(int heads, int kv_heads, int dim, int dtype, int causal,
     h->heads = heads; h->kv_heads = kv_heads; h->dim = dim; h->dtype = dtype;
     h->causal = causal; h->window = window; h->scale = scale;
     h->host_only = host_only;
+    h->sms = host_only ? 152 : cdg::sm_count();
     if (!host_only) {
-        if (cudaGetDevice(&h->device) != cudaSuccess || cat_prepare_forward() != cudaSuccess || cat_prepare_grad() != cudaSuccess ||
+        if (h->sms < 1 || cudaGetDevice(&h->device) != cudaSuccess || cat_prepare_forward() != cudaSuccess || cat_prepare_grad() != cudaSuccess ||
             cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess || cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) {
             if (h->d_status) cudaFree(h->d_status);
             delete h;
@@ -161,6 +162,27 @@ long long items(long long tokens, int sequences, int rows, int heads)
     return (tokens + (rows - 1) * std::min<long long>(sequences, tokens)) / rows * heads;
 }
 
+// The gradient's workspace: the rows' statistics, then the splits' sums.  A
+// group's query heads are split over CTAs until there are two for every SM
+// (8192 causal tokens, 16 heads over 4, whose 256 tiles of keys take up to 256
+// steps each: see attention_grad_sm103.cu).
+struct GradWorkspace {
+    int splits;
+    size_t partial, bytes;
+    GradWorkspace(const cdg_attention_st *h, long long q_tokens, long long k_tokens, int sequences)
+    {
+        const int group = h->heads / h->kv_heads;
+        const long long n = items(k_tokens, sequences, CAT_TILE, h->kv_heads);
+        splits = 1;
+        if (q_tokens > 0 && n > 0)
+            for (int s = 2; s <= group && n * splits < 2ll * h->sms; ++s)
+                if (group % s == 0) splits = s;
+        partial = (static_cast<size_t>(q_tokens) * h->heads * sizeof(float2) + 255) / 256 * 256;
+        bytes = partial + (splits > 1 ? 2ull * splits * k_tokens * h->kv_heads * h->dim * sizeof(float) : 0);
+        bytes = std::max<size_t>(256, bytes);
+    }
+};
+
 int usable(const cdg_attention_st *h)
 {
     if (!h) return CDG_ERR_INVALID_ARG;
@@ -198,9 +220,7 @@ size_t cdg_attention_workspace_bytes(cdg_attention_t h, long long q_tokens, long
 
 size_t cdg_attention_grad_workspace_bytes(cdg_attention_t h, long long q_tokens, long long k_tokens, int sequences)
 {
-    return sizes_ok(h, q_tokens, k_tokens, sequences)
-               ? std::max<size_t>(256, static_cast<size_t>(q_tokens) * h->heads * sizeof(float2))
-               : 0;
+    return sizes_ok(h, q_tokens, k_tokens, sequences) ? GradWorkspace(h, q_tokens, k_tokens, sequences).bytes : 0;
 }
 
 int cdg_attention(cdg_attention_t h, const void *q, long long ld_q, const void *k, long long ld_k, const void *v, long long ld_v,
@@ -278,14 +298,18 @@ int cdg_attention_grad(cdg_attention_t h, const void *q, long long ld_q, const v
     p.o_in = o; p.ld_oi = ld_o;
     p.d_o = d_o; p.ld_do = ld_do;
     p.lse_in = lse;
+    const GradWorkspace ws(h, q_tokens, k_tokens, sequences);
     p.stats = static_cast<float2 *>(workspace);
+    p.splits = ws.splits;
+    p.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.partial);
     const int bf16 = h->dtype == CDG_BF16;
     const long long nq = items(q_tokens, sequences, CAT_TILE, h->heads), nk = items(k_tokens, sequences, CAT_TILE, h->kv_heads);
-    if (nq >= (1ll << 31) || nk >= (1ll << 31) || q_tokens * h->heads >= (1ll << 34)) return CDG_ERR_UNSUPPORTED;
+    if (nq >= (1ll << 31) || nk * ws.splits >= (1ll << 31) || q_tokens * h->heads >= (1ll << 34)) return CDG_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (q_tokens > 0 && cat_launch_stats(p, bf16, s) != cudaSuccess) return CDG_ERR_CUDA;
     if (k_tokens > 0 && cat_launch_dkv(p, bf16, nk, s) != cudaSuccess) return CDG_ERR_CUDA;
     if (q_tokens > 0 && cat_launch_dq(p, bf16, nq, s) != cudaSuccess) return CDG_ERR_CUDA;
+    if (p.splits > 1 && cat_launch_join(p, bf16, nk, s) != cudaSuccess) return CDG_ERR_CUDA;
     return CDG_OK;
 }
 

@@ -360,10 +360,30 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// Four lanes' four 16-byte pieces transposed: piece i of lane j goes to piece j of lane i.
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[4][4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d <= 2; d *= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (!(i & d)) {
+                const bool high = lane & d;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t give = high ? w[i][e] : w[i + d][e];
+                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, d);
+                    if (high) w[i][e] = got;
+                    else w[i + d][e] = got;
+                }
+            }
+}
+
 // Columns [c0, c1) of 32 rows of fp32 sums in tensor memory (both multiples of 8;
 // taddr the warp's first column), times the rows' f, to 16-bit values: lane i's
-// row at out + i * ld (elements), rows [0, rows) of the warp.  Four lanes
-// exchange their 16-byte pieces, so that a store writes 64 bytes of a row.
+// row at out + i * ld (elements), rows [0, rows) of the warp.  After the exchange
+// a store writes 64 bytes of a row.
 template <bool BF16>
 __device__ __forceinline__ void store_rows(uint32_t taddr, int c0, int c1, float f, uint16_t *out, long long ld, int rows)
 {
@@ -375,26 +395,35 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, int c0, int c1, float
         uint32_t w[4][4];
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = round2<BF16>(v[2 * e] * f, v[2 * e + 1] * f);
-        // transpose of four lanes' four pieces: piece i of lane j goes to piece j of lane i
-#pragma unroll
-        for (int d = 1; d <= 2; d *= 2)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (!(i & d)) {
-                    const bool high = lane & d;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t give = high ? w[i][e] : w[i + d][e];
-                        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, d);
-                        if (high) w[i][e] = got;
-                        else w[i + d][e] = got;
-                    }
-                }
+        transpose_pieces(w);
         const int col = c0 + 8 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = (lane & ~3) + i;
             if (row < rows && col < c1) *reinterpret_cast<uint4 *>(out + row * ld + col) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        }
+    }
+}
+// The same, as fp32.
+__device__ __forceinline__ void store_rows_f32(uint32_t taddr, int c0, int c1, float *out, long long ld, int rows)
+{
+    const int lane = threadIdx.x & 31;
+    for (; c0 < c1; c0 += 32) {
+        float v[32];
+        tmem_ld_32(taddr + c0, v);
+        tmem_wait(v);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t w[4][4];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = __float_as_uint(v[16 * half + e]);
+            transpose_pieces(w);
+            const int col = c0 + 16 * half + 4 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (lane & ~3) + i;
+                if (row < rows && col < c1) *reinterpret_cast<uint4 *>(out + row * ld + col) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+            }
         }
     }
 }

@@ -17,7 +17,7 @@
 //
 // Each kernel's warps (640 threads): 0-15 compute (128 rows x 32 columns a
 // warpgroup), 16 loads by TMA, 17 issues MMAs, 18 fetches the queries'
-// statistics of a step (dk and dv).  The two phases of a step, p and ds, each
+// statistics of a step (dk and dv), 19 items.  The two phases of a step, p and ds, each
 // overlap two products of the tensor cores: dk and dv run
 //   p(i) | dS^T(i-1) Q, dP^T(i)      then      ds(i) | P^T(i) dO, S^T(i+1)
 #include "attention_device.cuh"
@@ -61,40 +61,45 @@ __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_const
     }
 }
 
+constexpr int kWarpItems = 19;
+
 struct GradBars {
-    uint32_t fixed_full;           // the CTA's own two tiles
-    uint32_t full_a0, empty_a0;    // [kSlots]: the streamed operand of the scores (Q, or K)
-    uint32_t full_b0, empty_b0;    // [kSlots]: the streamed operand of dP (dO, or V)
-    uint32_t st_full0, st_empty0;  // [kSlots]: statistics
-    uint32_t s_full, s_read, dp_full, ds_ready, out_full, drain;
+    uint32_t own_full0, own_empty0;  // [2]: the item's own tiles (K and V, or Q and dO)
+    uint32_t full_a0, empty_a0;      // [kSlots]: the streamed operand of the scores (Q, or K)
+    uint32_t full_b0, empty_b0;      // [kSlots]: the streamed operand of dP (dO, or V)
+    uint32_t st_full0, st_empty0;    // [kSlots]: statistics
+    uint32_t s_full, s_read, dp_full, ds_ready, out_full, out_empty, drain;
 };
 
 struct GradSmem {
-    uint32_t fixed_a, fixed_b, ring_a, ring_b, stats, tile_bytes;
+    uint32_t own, ring_a, ring_b, stats, tile_bytes;
     GradBars B;
+    ItemBars I;
     uint32_t *tmem_slot;
-    volatile uint32_t *abort_flag, *slot_parity;  // parity of each slot's last load: a, b, then the fixed tiles'
+    volatile uint32_t *abort_flag, *slot_parity;  // parity of each slot's last load: a, b, then the own tiles'
 };
+constexpr int kGradTail = kItemBytes + 512;
 
 template <int SLICES>
-__device__ __forceinline__ GradSmem grad_layout(uint8_t *smem_raw)
+__device__ __forceinline__ GradSmem grad_layout(uint8_t *smem_raw, int item_warps)
 {
     GradSmem S;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     S.tile_bytes = kSliceBytes * SLICES;
-    S.fixed_a = base;
-    S.fixed_b = base + S.tile_bytes;
+    S.own = base;
     S.ring_a = base + 2 * S.tile_bytes;
     S.ring_b = S.ring_a + kSlots * S.tile_bytes;
     S.stats = S.ring_b + kSlots * S.tile_bytes;  // kSlots x 128 shifts, then 128 sums
-    const uint32_t bars = S.stats + kSlots * CAT_TILE * 8;
-    uint32_t at = bars;
+    const uint32_t items = S.stats + kSlots * CAT_TILE * 8;
+    S.I = init_items(smem_raw + (items - raw), items, item_warps);
+    uint32_t at = items + kItemBytes;
     auto take = [&](int n) {
         const uint32_t was = at;
         at += 8 * n;
         return was;
     };
-    S.B.fixed_full = take(1);
+    S.B.own_full0 = take(2);
+    S.B.own_empty0 = take(2);
     S.B.full_a0 = take(kSlots);
     S.B.empty_a0 = take(kSlots);
     S.B.full_b0 = take(kSlots);
@@ -106,20 +111,24 @@ __device__ __forceinline__ GradSmem grad_layout(uint8_t *smem_raw)
     S.B.dp_full = take(1);
     S.B.ds_ready = take(1);
     S.B.out_full = take(1);
+    S.B.out_empty = take(1);
     S.B.drain = take(1);
     S.tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (at - raw));
     S.abort_flag = S.tmem_slot + 1;
     S.slot_parity = S.tmem_slot + 2;
     if (threadIdx.x == 0) {
-        mbar_init(S.B.fixed_full, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(S.B.own_full0 + 8u * s, 1);
+            mbar_init(S.B.own_empty0 + 8u * s, 1);
+        }
         for (int s = 0; s < kSlots; ++s) {
             for (uint32_t b : {S.B.full_a0, S.B.empty_a0, S.B.full_b0, S.B.empty_b0}) mbar_init(b + 8u * s, 1);
             mbar_init(S.B.st_full0 + 8u * s, 32);
             mbar_init(S.B.st_empty0 + 8u * s, 16);
         }
         for (uint32_t b : {S.B.s_full, S.B.dp_full, S.B.out_full, S.B.drain}) mbar_init(b, 1);
-        for (uint32_t b : {S.B.s_read, S.B.ds_ready}) mbar_init(b, 16);
-        for (int s = 0; s <= 2 * kSlots; ++s) S.slot_parity[s] = 0u;
+        for (uint32_t b : {S.B.s_read, S.B.ds_ready, S.B.out_empty}) mbar_init(b, 16);
+        for (int s = 0; s < 2 * kSlots + 2; ++s) S.slot_parity[s] = 0u;
         *S.abort_flag = 0u;
         fence_mbar_init();
     }
@@ -133,9 +142,11 @@ __device__ __forceinline__ void grad_end(const CatParams &p, const GradSmem &S, 
     if (*S.abort_flag && threadIdx.x == 0) {
         volatile uint32_t no_abort = 0;
         const Ctl drain_ctl{&no_abort, p.status};
-        for (int s = 0; s <= 2 * kSlots; ++s) {
+        for (int s = 0; s < 2 * kSlots + 2; ++s) {
             const uint32_t v = S.slot_parity[s];
-            const uint32_t bar = s == 2 * kSlots ? S.B.fixed_full : s < kSlots ? S.B.full_a0 + 8u * s : S.B.full_b0 + 8u * (s - kSlots);
+            const uint32_t bar = s >= 2 * kSlots ? S.B.own_full0 + 8u * (s - 2 * kSlots)
+                                 : s < kSlots    ? S.B.full_a0 + 8u * s
+                                                 : S.B.full_b0 + 8u * (s - kSlots);
             if (v & 2u) wait_bar(bar, v & 1u, drain_ctl);
         }
     }
@@ -154,27 +165,29 @@ __device__ __forceinline__ void drain_mmas(const CatParams &p, const GradSmem &S
     wait_bar(S.B.drain, 0, Ctl{&no_abort, p.status});
 }
 
-// The loads of one CTA: its own two tiles, then pairs of streamed tiles.
-// row(n) and head(n): token and head of the n-th.
+// The loads of one item: its own two tiles, and pairs of streamed tiles.
+// where(n, head, token): of the n-th pair.  items, steps: what came before.
 template <typename At>
-__device__ __forceinline__ void run_grad_loads(const CatParams &p, const GradSmem &S, Ctl ctl, int steps,
-                                               const CUtensorMap &fixed_a, const CUtensorMap &fixed_b, int fixed_head,
-                                               int fixed_token, const CUtensorMap &map_a, const CUtensorMap &map_b, At where)
+__device__ __forceinline__ bool run_grad_loads(const CatParams &p, const GradSmem &S, Ctl ctl, bool leader, int count,
+                                               const CUtensorMap &own_a, const CUtensorMap &own_b, int own_head, int own_token,
+                                               const CUtensorMap &map_a, const CUtensorMap &map_b, uint32_t &items, uint32_t &steps,
+                                               At where)
 {
-    const bool leader = elect_one_sync();
-    if (leader) {
-        S.slot_parity[2 * kSlots] = 2u;
-        mbar_arrive_expect_tx(S.B.fixed_full, 2 * S.tile_bytes);
-        load_tile(S.fixed_a, fixed_a, S.B.fixed_full, p.slices, fixed_head, fixed_token);
-        load_tile(S.fixed_b, fixed_b, S.B.fixed_full, p.slices, fixed_head, fixed_token);
-    }
-    for (int n = 0; n < steps; ++n) {
-        const int slot = n % kSlots;
-        const uint32_t parity = (n / kSlots) & 1;
+    for (int n = 0; n < count; ++n, ++steps) {
+        const uint32_t slot = steps % kSlots, parity = (steps / kSlots) & 1u;
         int head, token;
         where(n, head, token);
         for (int b = 0; b < 2; ++b) {
-            if (!wait_bar((b ? S.B.empty_b0 : S.B.empty_a0) + 8u * slot, parity ^ 1u, ctl)) return;
+            if (n == 0) {  // (the scores' operands first)
+                if (!wait_bar(S.B.own_empty0 + 8u * b, (items & 1u) ^ 1u, ctl)) return false;
+                if (leader) {
+                    S.slot_parity[2 * kSlots + b] = (items & 1u) | 2u;
+                    mbar_arrive_expect_tx(S.B.own_full0 + 8u * b, S.tile_bytes);
+                    load_tile(S.own + b * S.tile_bytes, b ? own_b : own_a, S.B.own_full0 + 8u * b, p.slices, own_head, own_token);
+                }
+                __syncwarp();
+            }
+            if (!wait_bar((b ? S.B.empty_b0 : S.B.empty_a0) + 8u * slot, parity ^ 1u, ctl)) return false;
             if (leader) {
                 const uint32_t bar = (b ? S.B.full_b0 : S.B.full_a0) + 8u * slot;
                 S.slot_parity[b * kSlots + slot] = parity | 2u;
@@ -184,6 +197,8 @@ __device__ __forceinline__ void run_grad_loads(const CatParams &p, const GradSme
             __syncwarp();
         }
     }
+    if (count > 0) ++items;
+    return true;
 }
 
 // Columns of tensor memory: scores, dP, and the sums (dV and dK, or dQ).
@@ -191,10 +206,34 @@ constexpr uint32_t kS = 0, kDP = 128, kSum = 256;
 
 // ------------------------------------------------------------------ dk, dv
 
-// A CTA's steps: for every query head of its group the query tiles that see some of its keys.
+// An item of dk and dv: 128 keys, and the steps of its part of their group's
+// query heads over the query tiles that see some of them.
 struct KeyTile {
-    int j0;          // first key of the tile, in its sequence
-    int lo, count;   // first query tile and their number, for each head
+    int j0;              // first key of the tile, in its sequence
+    int lo, count;       // first query tile and their number, for each head
+    int kv_head, split;
+    int head0, heads;    // the part's query heads
+    __device__ __forceinline__ KeyTile(const CatParams &p, const Item &item)
+    {
+        const Place &at = item.at;
+        kv_head = item.head / p.splits;
+        split = item.head - kv_head * p.splits;
+        heads = p.group / p.splits;
+        head0 = kv_head * p.group + split * heads;
+        // (a sequence's first keys, which under a causal mask most queries see, come first)
+        j0 = at.tile * CAT_TILE;
+        const int off = at.kl - at.ql, j1 = min(j0 + CAT_TILE, at.kl);
+        const int first = p.causal ? max(0, j0 - off) : 0, end = p.window ? min(at.ql, j1 - 1 - off + p.window) : at.ql;
+        lo = first / CAT_TILE;
+        count = end > first ? (end + CAT_TILE - 1) / CAT_TILE - lo : 0;
+    }
+    __device__ __forceinline__ int steps() const { return count * heads; }
+    __device__ __forceinline__ void where(int n, int &head, int &tile) const
+    {
+        const int h = n / count;
+        head = head0 + h;
+        tile = lo + n - h * count;
+    }
 };
 
 // Four numbers of shared memory that the whole warp reads.
@@ -222,28 +261,25 @@ __device__ __forceinline__ void put_rounded(uint32_t taddr, const float (&s)[32]
 }
 
 template <bool BF16>
-__device__ __forceinline__ void compute_dkv(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
-                                            const KeyTile &kt, int steps, int kv_head)
+__device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
+                                            const KeyTile &kt, uint32_t &done, uint32_t &items)
 {
     const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t s_col = tmem + lanes + kS + 32u * part, dp_col = tmem + lanes + kDP + 32u * part;
     const f32x2 c2 = pack2(p.scale_log2, p.scale_log2), minus = pack2(-1.0f, -1.0f);
     const int off = at.kl - at.ql, j = kt.j0 + row;
-    bool ok = true;
+    const int steps = kt.steps();
     int tile = kt.lo;
-    for (int n = 0; n < steps; ++n) {
-        const int slot = n % kSlots;
+    for (int n = 0; n < steps; ++n, ++done) {
+        const uint32_t slot = done % kSlots;
         const uint32_t stats = S.stats + slot * 2 * CAT_TILE * 4 + part * 32 * 4;
         const int i0 = tile * CAT_TILE;
         if (++tile == kt.lo + kt.count) tile = kt.lo;
         // columns [lo, hi) of this part see the key
         const bool whole = (!p.causal || kt.j0 + CAT_TILE - 1 <= i0 + off) && (!p.window || kt.j0 > i0 + CAT_TILE - 1 + off - p.window);
         const int lo = p.causal ? j - off - i0 - 32 * part : 0, hi = p.window ? j - off + p.window - i0 - 32 * part : 32;
-        if (!wait_bar(S.B.st_full0 + 8u * slot, (n / kSlots) & 1, ctl) || !wait_bar(S.B.s_full, n & 1, ctl)) {
-            ok = false;
-            break;
-        }
+        if (!wait_bar(S.B.st_full0 + 8u * slot, (done / kSlots) & 1u, ctl) || !wait_bar(S.B.s_full, done & 1u, ctl)) return false;
         tc_fence_after();
         float s[32];
         tmem_ld_32(s_col, s);
@@ -263,10 +299,7 @@ __device__ __forceinline__ void compute_dkv(const CatParams &p, const GradSmem &
         if (!whole) hide(s, lo, hi);
         put_rounded<BF16>(s_col, s);
         warp_arrive(S.B.s_read);
-        if (!wait_bar(S.B.dp_full, n & 1, ctl)) {
-            ok = false;
-            break;
-        }
+        if (!wait_bar(S.B.dp_full, done & 1u, ctl)) return false;
         tc_fence_after();
         float dp[32];
         tmem_ld_32(dp_col, dp);
@@ -285,20 +318,29 @@ __device__ __forceinline__ void compute_dkv(const CatParams &p, const GradSmem &
         warp_arrive(S.B.ds_ready);
         if ((threadIdx.x & 31) == 0) mbar_arrive(S.B.st_empty0 + 8u * slot);
     }
-    if (ok && steps > 0) ok = wait_bar(S.B.out_full, 0, ctl);
-    if (!ok) return;
-    tc_fence_after();
     // the first two warpgroups store dv, the others dk, half of the columns each
-    const long long token = at.k0 + j;
+    const long long token = at.k0 + j, first = token - (threadIdx.x & 31);
     const bool is_dk = part >= 2;
-    uint16_t *out = is_dk ? static_cast<uint16_t *>(p.dk) + token * p.ld_dk : static_cast<uint16_t *>(p.dv) + token * p.ld_dv;
-    out += static_cast<long long>(kv_head) * p.dim;
-    const int c0 = 32 * p.slices * (part & 1), c1 = min(p.dim, c0 + 32 * p.slices);
-    const long long ld = is_dk ? p.ld_dk : p.ld_dv;
-    if (steps > 0)
-        store_rows<BF16>(tmem + lanes + kSum + 64u * p.slices * is_dk, c0, c1, is_dk ? p.scale : 1.0f, out - (threadIdx.x & 31) * ld, ld,
-                         at.kl - (j & ~31));
-    else if (j < at.kl) zero_row(out, c0, c1);
+    const int c0 = 32 * p.slices * (part & 1), c1 = min(p.dim, c0 + 32 * p.slices), rows = at.kl - (j & ~31);
+    const long long ld = p.splits > 1 ? static_cast<long long>(p.kv_heads) * p.dim : is_dk ? p.ld_dk : p.ld_dv;
+    uint16_t *out = static_cast<uint16_t *>(is_dk ? p.dk : p.dv) + first * ld + static_cast<long long>(kt.kv_head) * p.dim;
+    float *sum = p.partial + ((2ll * kt.split + is_dk) * p.k_tokens + first) * ld + static_cast<long long>(kt.kv_head) * p.dim;
+    if (steps > 0) {
+        if (!wait_bar(S.B.out_full, items & 1u, ctl)) return false;
+        ++items;
+        tc_fence_after();
+        const uint32_t taddr = tmem + lanes + kSum + 64u * p.slices * is_dk;
+        if (p.splits > 1) store_rows_f32(taddr, c0, c1, sum, ld, rows);
+        else store_rows<BF16>(taddr, c0, c1, is_dk ? p.scale : 1.0f, out, ld, rows);
+        warp_arrive(S.B.out_empty);
+    } else if (j < at.kl) {
+        const int lane = threadIdx.x & 31;
+        if (p.splits > 1)
+            for (int c = c0; c < c1; c += 4) *reinterpret_cast<float4 *>(sum + lane * ld + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        else
+            zero_row(out + lane * ld, c0, c1);
+    }
+    return true;
 }
 
 template <bool BF16, int SLICES>
@@ -306,114 +348,154 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
 {
     constexpr uint32_t tile_bytes = kSliceBytes * SLICES;
     extern __shared__ uint8_t smem_raw[];
-    const GradSmem S = grad_layout<SLICES>(smem_raw);
+    const GradSmem S = grad_layout<SLICES>(smem_raw, 19);
     const int warp = threadIdx.x / 32;
-    grid_dep_launch_dependents();
     grid_dep_wait();
+    // dq needs the statistics alone: its CTAs may start as soon as all of these have
+    grid_dep_launch_dependents();
     if (warp == kWarpMma) {
         tmem_alloc(smem_u32(S.tmem_slot), 512);
         tmem_relinquish();
     }
-    const int kv_head = static_cast<int>(blockIdx.x % p.kv_heads);
-    const Place at = find_tile(p, blockIdx.x / p.kv_heads, CAT_TILE, true);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *S.tmem_slot;
     const Ctl ctl{S.abort_flag, p.status};
-    if (at.tile >= 0) {
-        // (a sequence's first keys, which under a causal mask most queries see, come first)
-        KeyTile kt;
-        kt.j0 = at.tile * CAT_TILE;
-        const int off = at.kl - at.ql, j1 = min(kt.j0 + CAT_TILE, at.kl);
-        const int first = p.causal ? max(0, kt.j0 - off) : 0, end = p.window ? min(at.ql, j1 - 1 - off + p.window) : at.ql;
-        kt.lo = first / CAT_TILE;
-        kt.count = end > first ? (end + CAT_TILE - 1) / CAT_TILE - kt.lo : 0;
-        const int steps = kt.count * p.group;
-        auto where = [&](int n, int &head, int &tile) {
-            const int h = n / kt.count;
-            head = kv_head * p.group + h;
-            tile = kt.lo + n - h * kt.count;
-        };
-        if (steps == 0) {
-            if (warp < 16) compute_dkv<BF16>(p, S, ctl, tmem, at, kt, 0, kv_head);
-        } else if (warp == kWarpLoad) {
-            run_grad_loads(p, S, ctl, steps, p.tmK, p.tmV, kv_head, at.k0 + kt.j0, p.tmQ, p.tmDO,
-                           [&](int n, int &head, int &token) {
-                               int tile;
-                               where(n, head, tile);
-                               token = at.q0 + tile * CAT_TILE;
-                           });
-        } else if (warp == kWarpStats) {
-            const int lane = threadIdx.x & 31;
-            for (int n = 0; n < steps; ++n) {
-                const int slot = n % kSlots;
+    Item item;
+    uint32_t done = 0, items = 0;  // steps, and items that had some
+    if (warp == kWarpItems) {
+        run_items(p, S.I, ctl, CAT_TILE, true, p.kv_heads * p.splits);
+    } else if (warp == kWarpLoad) {
+        const bool leader = elect_one_sync();
+        for (int n = 0; next_item(S.I, ctl, n, item); ++n) {
+            const KeyTile kt(p, item);
+            if (!run_grad_loads(p, S, ctl, leader, kt.steps(), p.tmK, p.tmV, kt.kv_head, item.at.k0 + kt.j0, p.tmQ, p.tmDO, items, done,
+                                [&](int k, int &head, int &token) {
+                                    int tile;
+                                    kt.where(k, head, tile);
+                                    token = item.at.q0 + tile * CAT_TILE;
+                                }))
+                break;
+            if (leader) mbar_arrive(S.I.go);
+            __syncwarp();
+        }
+    } else if (warp == kWarpStats) {
+        const int lane = threadIdx.x & 31;
+        bool ok = true;
+        for (int n = 0; ok && next_item(S.I, ctl, n, item); ++n) {
+            const KeyTile kt(p, item);
+            for (int k = 0; k < kt.steps(); ++k, ++done) {
+                const uint32_t slot = done % kSlots;
                 int head, tile;
-                where(n, head, tile);
-                if (!wait_bar(S.B.st_empty0 + 8u * slot, ((n / kSlots) & 1) ^ 1u, ctl)) break;
-                const float2 *src = p.stats + static_cast<long long>(head) * p.q_tokens + at.q0;
+                kt.where(k, head, tile);
+                ok = wait_bar(S.B.st_empty0 + 8u * slot, ((done / kSlots) & 1u) ^ 1u, ctl);
+                if (!ok) break;
+                const float2 *src = p.stats + static_cast<long long>(head) * p.q_tokens + item.at.q0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = 32 * e + lane, i = tile * CAT_TILE + c;
-                    const float2 v = i < at.ql ? __ldg(src + i) : make_float2(-INFINITY, 0.0f);
+                    const float2 v = i < item.at.ql ? __ldg(src + i) : make_float2(-INFINITY, 0.0f);
                     st_shared_f32(S.stats + (slot * 2 * CAT_TILE + c) * 4u, v.x);
                     st_shared_f32(S.stats + ((slot * 2 + 1) * CAT_TILE + c) * 4u, v.y);
                 }
                 mbar_arrive(S.B.st_full0 + 8u * slot);
             }
-        } else if (warp == kWarpMma) {
-            const uint32_t leader = elect_one_sync();
-            const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dv = tm + kSum, dk = dv + 64u * SLICES;
-            const int total = uniform(steps), count = uniform(kt.count), rest = uniform(at.ql - kt.lo * CAT_TILE);
-            // waits for the n-th streamed tile; rows behind the sequence's end become zeros
-            auto filled = [&](uint32_t full0, uint32_t ring, int n) {
-                if (!wait_bar(full0 + 8u * (n % kSlots), (n / kSlots) & 1, ctl)) return false;
+        }
+    } else if (warp == kWarpMma) {
+        const uint32_t leader = elect_one_sync();
+        const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dv = tm + kSum, dk = dv + 64u * SLICES;
+        bool ok = true;
+        for (int n = 0; ok && next_item(S.I, ctl, n, item); ++n) {
+            const KeyTile kt(p, item);
+            const int total = uniform(kt.steps()), count = uniform(kt.count), rest = uniform(item.at.ql - kt.lo * CAT_TILE);
+            if (total == 0) continue;
+            // waits for the k-th streamed tile; rows behind the sequence's end become zeros
+            auto filled = [&](uint32_t full0, uint32_t ring, int k, uint32_t step) {
+                if (!wait_bar(full0 + 8u * (step % kSlots), (step / kSlots) & 1u, ctl)) return false;
                 tc_fence_after();
-                const int valid = rest - n % count * CAT_TILE;
-                if (valid < CAT_TILE) zero_rows(ring + (n % kSlots) * tile_bytes, SLICES, valid);
+                const int valid = rest - k % count * CAT_TILE;
+                if (valid < CAT_TILE) zero_rows(ring + (step % kSlots) * tile_bytes, SLICES, valid);
                 return true;
             };
-            auto scores = [&](int n) {
-                if (!filled(S.B.full_a0, S.ring_a, n)) return false;
-                issue_qk<SLICES>(leader, s, S.fixed_a, S.ring_a + (n % kSlots) * tile_bytes, p.idesc_qk, p.ksteps);
+            auto scores = [&](int k) {
+                const uint32_t step = done + k;
+                if (!filled(S.B.full_a0, S.ring_a, k, step)) return false;
+                issue_qk<SLICES>(leader, s, S.own, S.ring_a + (step % kSlots) * tile_bytes, p.idesc_qk, p.ksteps);
                 mma_commit(leader, S.B.s_full);
+                if (k + 1 == total) mma_commit(leader, S.B.own_empty0);
                 return true;
             };
-            auto dps = [&](int n) {
-                if (!filled(S.B.full_b0, S.ring_b, n)) return false;
-                issue_qk<SLICES>(leader, dp, S.fixed_b, S.ring_b + (n % kSlots) * tile_bytes, p.idesc_qk, p.ksteps);
+            auto dps = [&](int k) {
+                const uint32_t step = done + k;
+                if (!filled(S.B.full_b0, S.ring_b, k, step)) return false;
+                issue_qk<SLICES>(leader, dp, S.own + tile_bytes, S.ring_b + (step % kSlots) * tile_bytes, p.idesc_qk, p.ksteps);
                 mma_commit(leader, S.B.dp_full);
+                if (k + 1 == total) mma_commit(leader, S.B.own_empty0 + 8u);
                 return true;
             };
-            bool ok = wait_bar(S.B.fixed_full, 0, ctl) && scores(0) && dps(0);
-            for (int n = 0; ok && n < total; ++n) {
-                const bool next = n + 1 < total;
-                const int slot = n % kSlots;
-                if (!wait_bar(S.B.s_read, n & 1, ctl)) break;
+            ok = wait_bar(S.B.own_full0, items & 1u, ctl) && scores(0) && wait_bar(S.B.own_full0 + 8u, items & 1u, ctl) && dps(0);
+            for (int k = 0; ok && k < total; ++k) {
+                const bool next = k + 1 < total;
+                const uint32_t step = done + k, slot = step % kSlots;
+                ok = wait_bar(S.B.s_read, step & 1u, ctl);
+                // the item before has left the sums
+                if (ok && k == 0) ok = wait_bar(S.B.out_empty, (items & 1u) ^ 1u, ctl);
+                if (!ok) break;
                 tc_fence_after();
-                issue_pv<32>(leader, dv, s, S.ring_b + slot * tile_bytes, p.idesc_pv, n != 0);
+                issue_pv<32>(leader, dv, s, S.ring_b + slot * tile_bytes, p.idesc_pv, k != 0);
                 mma_commit(leader, S.B.empty_b0 + 8u * slot);
-                if (next && !scores(n + 1)) break;
-                if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
+                ok = (!next || scores(k + 1)) && wait_bar(S.B.ds_ready, step & 1u, ctl);
+                if (!ok) break;
                 tc_fence_after();
-                issue_pv<32>(leader, dk, dp, S.ring_a + slot * tile_bytes, p.idesc_pv, n != 0);
+                issue_pv<32>(leader, dk, dp, S.ring_a + slot * tile_bytes, p.idesc_pv, k != 0);
                 mma_commit(leader, S.B.empty_a0 + 8u * slot);
                 if (!next) mma_commit(leader, S.B.out_full);
-                else if (!dps(n + 1)) break;
+                else ok = dps(k + 1);
             }
-            drain_mmas(p, S, leader);
-        } else if (warp < 16) {
-            compute_dkv<BF16>(p, S, ctl, tmem, at, kt, steps, kv_head);
+            done += total;
+            ++items;
         }
+        drain_mmas(p, S, leader);
+    } else if (warp < 16) {
+        for (int n = 0; next_item(S.I, ctl, n, item); ++n)
+            if (!compute_dkv<BF16>(p, S, ctl, tmem, item.at, KeyTile(p, item), done, items)) break;
     }
     grad_end(p, S, tmem);
+}
+
+// dk and dv of a tile of keys and a head: the splits' sums, added in order.
+template <bool BF16>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ CatParams p)
+{
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int kv_head = static_cast<int>(blockIdx.x % p.kv_heads);
+    const Place at = find_tile(p, blockIdx.x / p.kv_heads, CAT_TILE, true);
+    if (at.tile < 0) return;
+    const int rows = min(CAT_TILE, at.kl - at.tile * CAT_TILE), vecs = p.dim / 4;
+    const long long ld = static_cast<long long>(p.kv_heads) * p.dim, token0 = at.k0 + at.tile * CAT_TILE;
+    for (int i = threadIdx.x; i < 2 * rows * vecs; i += 256) {
+        const int kind = i / (rows * vecs), r = (i - kind * rows * vecs) / vecs, c = (i - (kind * rows + r) * vecs) * 4;
+        const long long token = token0 + r;
+        const float *src = p.partial + (static_cast<long long>(kind) * p.k_tokens + token) * ld + static_cast<long long>(kv_head) * p.dim + c;
+        float4 v = __ldg(reinterpret_cast<const float4 *>(src));
+        for (int s = 1; s < p.splits; ++s) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(src + 2ll * s * p.k_tokens * ld));
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        const float f = kind ? p.scale : 1.0f;
+        uint16_t *out = kind ? static_cast<uint16_t *>(p.dk) + token * p.ld_dk : static_cast<uint16_t *>(p.dv) + token * p.ld_dv;
+        *reinterpret_cast<uint2 *>(out + static_cast<long long>(kv_head) * p.dim + c) =
+            make_uint2(round2<BF16>(v.x * f, v.y * f), round2<BF16>(v.z * f, v.w * f));
+    }
 }
 
 // ------------------------------------------------------------------ dq
 
 template <bool BF16>
-__device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
-                                           int i0, int head, int lo, int hi)
+__device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
+                                           int i0, int head, int lo, int hi, uint32_t &done, uint32_t &items)
 {
     const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127, i = i0 + row;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -424,15 +506,11 @@ __device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S
     const bool valid = i < at.ql;
     const float2 st = valid ? __ldg(p.stats + static_cast<long long>(head) * p.q_tokens + token) : make_float2(-INFINITY, 0.0f);
     const f32x2 shift = pack2(st.x, st.x), minus_d = pack2(-st.y, -st.y);
-    bool ok = true;
-    for (int j = lo; j < hi; ++j) {
-        const int n = j - lo, k0 = j * CAT_TILE;
+    for (int j = lo; j < hi; ++j, ++done) {
+        const int k0 = j * CAT_TILE;
         const bool whole = k0 + CAT_TILE <= at.kl && (!p.causal || k0 + CAT_TILE - 1 <= r_first) &&
                            (!p.window || k0 > r_first + CAT_TILE - 1 - p.window);
-        if (!wait_bar(S.B.s_full, n & 1, ctl)) {
-            ok = false;
-            break;
-        }
+        if (!wait_bar(S.B.s_full, done & 1u, ctl)) return false;
         tc_fence_after();
         float s[32];
         tmem_ld_32(s_col, s);
@@ -445,10 +523,7 @@ __device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S
             s[e] = exp2_approx(a);
             s[e + 1] = exp2_approx(b);
         }
-        if (!wait_bar(S.B.dp_full, n & 1, ctl)) {
-            ok = false;
-            break;
-        }
+        if (!wait_bar(S.B.dp_full, done & 1u, ctl)) return false;
         tc_fence_after();
         float dp[32];
         tmem_ld_32(dp_col, dp);
@@ -461,97 +536,130 @@ __device__ __forceinline__ void compute_dq(const CatParams &p, const GradSmem &S
         put_rounded<BF16>(dp_col, dp);
         warp_arrive(S.B.ds_ready);
     }
-    if (ok && hi > lo) ok = wait_bar(S.B.out_full, 0, ctl);
-    if (!ok) return;
-    tc_fence_after();
-    uint16_t *out = static_cast<uint16_t *>(p.dq) + token * p.ld_dq + static_cast<long long>(head) * p.dim;
+    uint16_t *out = static_cast<uint16_t *>(p.dq) + (token - (threadIdx.x & 31)) * p.ld_dq + static_cast<long long>(head) * p.dim;
     const int c0 = 32 * part, c1 = min(p.dim, c0 + 32);
-    if (hi > lo) store_rows<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out - (threadIdx.x & 31) * p.ld_dq, p.ld_dq, at.ql - (i & ~31));
-    else if (valid) zero_row(out, c0, c1);
+    if (hi > lo) {
+        if (!wait_bar(S.B.out_full, items & 1u, ctl)) return false;
+        ++items;
+        tc_fence_after();
+        store_rows<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out, p.ld_dq, at.ql - (i & ~31));
+        warp_arrive(S.B.out_empty);
+    } else if (valid) {
+        zero_row(out + (threadIdx.x & 31) * p.ld_dq, c0, c1);
+    }
+    return true;
 }
+
+// An item of dq: 128 queries from i0 of a head, steps [lo, hi) of keys.
+struct QueryTile {
+    int i0, lo, hi;
+    __device__ __forceinline__ QueryTile(const CatParams &p, const Place &at)
+    {
+        // a sequence's last queries first: under a causal mask they see most keys
+        i0 = ((at.ql + CAT_TILE - 1) / CAT_TILE - 1 - at.tile) * CAT_TILE;
+        key_steps(p, at, i0, min(i0 + CAT_TILE, at.ql), lo, hi);
+    }
+};
 
 template <bool BF16, int SLICES>
 __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const __grid_constant__ CatParams p)
 {
     constexpr uint32_t tile_bytes = kSliceBytes * SLICES;
     extern __shared__ uint8_t smem_raw[];
-    const GradSmem S = grad_layout<SLICES>(smem_raw);
+    const GradSmem S = grad_layout<SLICES>(smem_raw, 18);
     const int warp = threadIdx.x / 32;
-    grid_dep_launch_dependents();
-    grid_dep_wait();
     if (warp == kWarpMma) {
         tmem_alloc(smem_u32(S.tmem_slot), 512);
         tmem_relinquish();
     }
-    const int head = static_cast<int>(blockIdx.x % p.heads);
-    const Place at = find_tile(p, blockIdx.x / p.heads, CAT_TILE, false);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *S.tmem_slot;
     const Ctl ctl{S.abort_flag, p.status};
-    if (at.tile >= 0) {
-        // a sequence's last queries first: under a causal mask they see most keys
-        const int i0 = ((at.ql + CAT_TILE - 1) / CAT_TILE - 1 - at.tile) * CAT_TILE;
-        int lo, hi;
-        key_steps(p, at, i0, min(i0 + CAT_TILE, at.ql), lo, hi);
-        const int steps = hi - lo, kv_head = head / p.group;
-        if (steps == 0) {
-            if (warp < 16) compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
-        } else if (warp == kWarpLoad) {
-            // (one tensor map a loop: the CTA's own tiles come from the query side)
-            run_grad_loads(p, S, ctl, steps, p.tmQ, p.tmDO, head, at.q0 + i0, p.tmK, p.tmV, [&](int n, int &h, int &token) {
-                h = kv_head;
-                token = at.k0 + (lo + n) * CAT_TILE;
-            });
-        } else if (warp == kWarpMma) {
-            const uint32_t leader = elect_one_sync();
-            const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dq = tm + kSum;
-            const int total = uniform(steps), rest = uniform(at.kl - lo * CAT_TILE);
-            auto scores = [&](int n) {
-                const int slot = n % kSlots;
-                if (!wait_bar(S.B.full_a0 + 8u * slot, (n / kSlots) & 1, ctl)) return false;
+    Item item;
+    uint32_t done = 0, items = 0;  // steps, and items that had some
+    if (warp == kWarpItems) {
+        run_items(p, S.I, ctl, CAT_TILE, false, p.heads);
+    } else if (warp == kWarpLoad) {
+        const bool leader = elect_one_sync();
+        for (int n = 0; next_item(S.I, ctl, n, item); ++n) {
+            const QueryTile qt(p, item.at);
+            if (!run_grad_loads(p, S, ctl, leader, qt.hi - qt.lo, p.tmQ, p.tmDO, item.head, item.at.q0 + qt.i0, p.tmK, p.tmV, items, done,
+                                [&](int k, int &head, int &token) {
+                                    head = item.head / p.group;
+                                    token = item.at.k0 + (qt.lo + k) * CAT_TILE;
+                                }))
+                break;
+            if (leader) mbar_arrive(S.I.go);
+            __syncwarp();
+        }
+    } else if (warp == kWarpMma) {
+        const uint32_t leader = elect_one_sync();
+        const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dq = tm + kSum;
+        bool ok = true;
+        for (int n = 0; ok && next_item(S.I, ctl, n, item); ++n) {
+            const QueryTile qt(p, item.at);
+            const int total = uniform(qt.hi - qt.lo), rest = uniform(item.at.kl - qt.lo * CAT_TILE);
+            if (total <= 0) continue;
+            auto scores = [&](int k) {
+                const uint32_t step = done + k, slot = step % kSlots;
+                if (!wait_bar(S.B.full_a0 + 8u * slot, (step / kSlots) & 1u, ctl)) return false;
                 tc_fence_after();
                 // keys behind the sequence's end become zeros: dS K sums over them
-                if (rest - n * CAT_TILE < CAT_TILE) zero_rows(S.ring_a + slot * tile_bytes, SLICES, rest - n * CAT_TILE);
-                issue_qk<SLICES>(leader, s, S.fixed_a, S.ring_a + slot * tile_bytes, p.idesc_qk, p.ksteps);
+                if (rest - k * CAT_TILE < CAT_TILE) zero_rows(S.ring_a + slot * tile_bytes, SLICES, rest - k * CAT_TILE);
+                issue_qk<SLICES>(leader, s, S.own, S.ring_a + slot * tile_bytes, p.idesc_qk, p.ksteps);
                 mma_commit(leader, S.B.s_full);
+                if (k + 1 == total) mma_commit(leader, S.B.own_empty0);
                 return true;
             };
-            auto dps = [&](int n) {
-                const int slot = n % kSlots;
-                if (!wait_bar(S.B.full_b0 + 8u * slot, (n / kSlots) & 1, ctl)) return false;
+            auto dps = [&](int k) {
+                const uint32_t step = done + k, slot = step % kSlots;
+                if (!wait_bar(S.B.full_b0 + 8u * slot, (step / kSlots) & 1u, ctl)) return false;
                 tc_fence_after();
-                issue_qk<SLICES>(leader, dp, S.fixed_b, S.ring_b + slot * tile_bytes, p.idesc_qk, p.ksteps);
+                issue_qk<SLICES>(leader, dp, S.own + tile_bytes, S.ring_b + slot * tile_bytes, p.idesc_qk, p.ksteps);
                 mma_commit(leader, S.B.dp_full);
                 mma_commit(leader, S.B.empty_b0 + 8u * slot);
+                if (k + 1 == total) mma_commit(leader, S.B.own_empty0 + 8u);
                 return true;
             };
-            bool ok = wait_bar(S.B.fixed_full, 0, ctl) && scores(0) && dps(0);
-            for (int n = 0; ok && n < total; ++n) {
-                const bool next = n + 1 < total;
-                if (!wait_bar(S.B.s_read, n & 1, ctl)) break;
+            ok = wait_bar(S.B.own_full0, items & 1u, ctl) && scores(0) && wait_bar(S.B.own_full0 + 8u, items & 1u, ctl) && dps(0);
+            for (int k = 0; ok && k < total; ++k) {
+                const bool next = k + 1 < total;
+                const uint32_t step = done + k, slot = step % kSlots;
+                ok = wait_bar(S.B.s_read, step & 1u, ctl);
+                if (!ok) break;
                 tc_fence_after();
-                if (next && !scores(n + 1)) break;
-                if (!wait_bar(S.B.ds_ready, n & 1, ctl)) break;
+                ok = (!next || scores(k + 1)) && wait_bar(S.B.ds_ready, step & 1u, ctl);
+                // the item before has left the sums
+                if (ok && k == 0) ok = wait_bar(S.B.out_empty, (items & 1u) ^ 1u, ctl);
+                if (!ok) break;
                 tc_fence_after();
-                issue_pv<32>(leader, dq, dp, S.ring_a + (n % kSlots) * tile_bytes, p.idesc_pv, n != 0);
-                mma_commit(leader, S.B.empty_a0 + 8u * (n % kSlots));
+                issue_pv<32>(leader, dq, dp, S.ring_a + slot * tile_bytes, p.idesc_pv, k != 0);
+                mma_commit(leader, S.B.empty_a0 + 8u * slot);
                 if (!next) mma_commit(leader, S.B.out_full);
-                else if (!dps(n + 1)) break;
+                else ok = dps(k + 1);
             }
-            drain_mmas(p, S, leader);
-        } else if (warp < 16) {
-            compute_dq<BF16>(p, S, ctl, tmem, at, i0, head, lo, hi);
+            done += total;
+            ++items;
+        }
+        drain_mmas(p, S, leader);
+    } else if (warp < 16) {
+        for (int n = 0; next_item(S.I, ctl, n, item); ++n) {
+            const QueryTile qt(p, item.at);
+            if (!compute_dq<BF16>(p, S, ctl, tmem, item.at, qt.i0, item.head, qt.lo, qt.hi, done, items)) break;
         }
     }
     grad_end(p, S, tmem);
+    // This kernel began without waiting for the one before it (the statistics that
+    // both need were complete before either began); what follows waits for this one alone.
+    grid_dep_wait();
 }
 
 }  // namespace
 }  // namespace cdg
 
-size_t cat_smem_grad(int slices) { return 1024 + (2 + 2 * cdg::kSlots) * cdg::kSliceBytes * slices + cdg::kSlots * CAT_TILE * 8 + 256; }
+size_t cat_smem_grad(int slices) { return 1024 + (2 + 2 * cdg::kSlots) * cdg::kSliceBytes * slices + cdg::kSlots * CAT_TILE * 8 + cdg::kGradTail; }
 
 cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
 {
@@ -565,13 +673,22 @@ cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
 cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaStream_t s)
 {
     using namespace cdg;
-    const dim3 grid(static_cast<unsigned>(items)), block(CAT_GRAD_THREADS);
+    const dim3 grid(static_cast<unsigned>(items * p.splits)), block(CAT_GRAD_THREADS);
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
     void (*k)(CatParams) = p.slices == 2 ? (bf16 ? attention_dkv_kernel<true, 2> : attention_dkv_kernel<false, 2>)
                                          : (bf16 ? attention_dkv_kernel<true, 1> : attention_dkv_kernel<false, 1>);
     return launch_early(k, grid, block, smem, s, p);
 }
 
+cudaError_t cat_launch_join(const CatParams &p, int bf16, long long items, cudaStream_t s)
+{
+    using namespace cdg;
+    const dim3 grid(static_cast<unsigned>(items)), block(256);
+    return bf16 ? launch_early(attention_join_kernel<true>, grid, block, 0, s, p) : launch_early(attention_join_kernel<false>, grid, block, 0, s, p);
+}
+
+// After cat_launch_dkv on the same stream, beside whose end it begins; without
+// keys there is no such launch, and this one waits for all before it.
 cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStream_t s)
 {
     using namespace cdg;
@@ -579,7 +696,9 @@ cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStr
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
     void (*k)(CatParams) = p.slices == 2 ? (bf16 ? attention_dq_kernel<true, 2> : attention_dq_kernel<false, 2>)
                                          : (bf16 ? attention_dq_kernel<true, 1> : attention_dq_kernel<false, 1>);
-    return launch_early(k, grid, block, smem, s, p);
+    if (p.k_tokens > 0) return launch_early(k, grid, block, smem, s, p);
+    k<<<grid, block, smem, s>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t cat_prepare_grad()

@@ -34,6 +34,8 @@ struct CatParams {
     long long ld_oi, ld_do;
     const float *lse_in;
     float2 *stats;
+    int splits;                  // dk and dv: parts of a group's query heads, a CTA each; above 1 their fp32 sums go to
+    float *partial;              // [splits][dk, dv][k_tokens][kv_heads * dim], and are added in order by a kernel of their own
     int *status;
 };
 
@@ -41,8 +43,9 @@ size_t cat_smem_forward(int slices);
 size_t cat_smem_grad(int slices);
 cudaError_t cat_prepare_forward();
 cudaError_t cat_prepare_grad();
-// bf16: 1 for bfloat16, 0 for float16; items: CTAs of a launch
+// bf16: 1 for bfloat16, 0 for float16; items: CTAs of a launch (of dk and dv: without the splits)
 cudaError_t cat_launch_forward(const CatParams &p, int bf16, long long items, cudaStream_t s);
 cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s);
 cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaStream_t s);
 cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStream_t s);
+cudaError_t cat_launch_join(const CatParams &p, int bf16, long long items, cudaStream_t s);
