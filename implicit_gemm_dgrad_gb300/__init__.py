@@ -677,6 +677,7 @@ def _bytes_of(t, n: int, kind: str | None, what: str) -> int:
     if _tensor is None and type(t).__module__ == "torch":
         import torch
         globals().update(_tensor=torch.Tensor, _cuda_device=getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
+        _torch_types.update({n: getattr(torch, n) for n in ("float16", "bfloat16", "float32")})
     return t.data_ptr()
 
 
@@ -740,6 +741,40 @@ def _matrix(t, rows: int, cols: int, kind: str | None, ld: int | None, what: str
     if ld is not None and int(ld) != own and rows > 1:
         raise ValueError(f"{what} has row stride {own}, not {ld}")
     return at, int(own)
+
+
+_torch_types: dict = {}  # torch's element types by name, once a torch tensor has been seen
+
+
+def _matrices(kind: str | None, *specs) -> list:
+    """Addresses and row strides of several _matrix arguments of one element
+    type, one after the other: the same answers, with the checks of a dense
+    tensor in line (a third of a call's time on the host where it has ten)."""
+    out: list = []
+    want = _torch_types.get(kind)
+    here = _cuda_device() if want is not None else -1
+    for t, rows, cols, ld, what in specs:
+        if type(t) is _tensor and t.dtype is want and ld is None and t.get_device() == here and \
+                t.nbytes == rows * cols * _SIZES[kind] and t.is_contiguous():
+            out += (t.data_ptr(), cols)
+        else:
+            out += _matrix(t, rows, cols, kind, ld, what)
+    return out
+
+
+def _vectors(n: int, *specs) -> list:
+    """Addresses of several dense fp32 arguments of n elements (None stays None)."""
+    out: list = []
+    want = _torch_types.get("float32")
+    here = _cuda_device() if want is not None else -1
+    for t, what in specs:
+        if t is None:
+            out.append(None)
+        elif type(t) is _tensor and t.dtype is want and t.get_device() == here and t.nbytes >= 4 * n and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            out.append(_dense(t, n, "float32", what))
+    return out
 
 
 def _dense_matrix(t, rows: int, cols: int, kind: str, what: str) -> int | None:
@@ -972,12 +1007,6 @@ class AttentionPlan:
             raise CdgError(ERR_INVALID_ARG, fn.__name__)
         return n
 
-    def _q(self, t, tokens: int, ld, what: str):
-        return _matrix(t, tokens, self.heads * self.dim, _TYPES.get(self.dtype), ld, what)
-
-    def _k(self, t, tokens: int, ld, what: str):
-        return _matrix(t, tokens, self.kv_heads * self.dim, _TYPES.get(self.dtype), ld, what)
-
     def attend(self, q, k, v, o, lse, workspace, q_tokens: int, k_tokens: int, q_offsets=None, k_offsets=None,
                sequences: int | None = None, ld_q=None, ld_k=None, ld_v=None, ld_o=None, stream=None) -> None:
         """o and lse (heads x q_tokens, fp32) of the queries over the keys and
@@ -985,10 +1014,12 @@ class AttentionPlan:
         sequences + 1 numbers; without them all rows are one sequence."""
         nq, nk = int(q_tokens), int(k_tokens)
         qo, ko, ib, n = _offsets(q_offsets, k_offsets, sequences)
-        _check_workspace(workspace, self, self.workspace_bytes, nq, nk, n)
-        rc = self.lib.cdg_attention(
-            self.handle, *self._q(q, nq, ld_q, "q"), *self._k(k, nk, ld_k, "k"), *self._k(v, nk, ld_v, "v"), nq, nk, qo, ko, ib,
-            n, *self._q(o, nq, ld_o, "o"), _dense(lse, self.heads * nq, "float32", "lse"), _addr(workspace), _stream(stream))
+        _check_workspace(workspace, self._need, self.workspace_bytes, nq, nk, n)
+        wq, wk = self.heads * self.dim, self.kv_heads * self.dim
+        m = _matrices(_TYPES.get(self.dtype), (q, nq, wq, ld_q, "q"), (k, nk, wk, ld_k, "k"), (v, nk, wk, ld_v, "v"),
+                      (o, nq, wq, ld_o, "o"))
+        rc = self.lib.cdg_attention(self.handle, *m[:6], nq, nk, qo, ko, ib, n, m[6], m[7],
+                                    *_vectors(self.heads * nq, (lse, "lse")), _addr(workspace), _stream(stream))
         if rc != OK:
             raise CdgError(rc, "cdg_attention")
 
@@ -999,12 +1030,13 @@ class AttentionPlan:
         lse as attend wrote them."""
         nq, nk = int(q_tokens), int(k_tokens)
         qo, ko, ib, n = _offsets(q_offsets, k_offsets, sequences)
-        _check_workspace(workspace, self, self.grad_workspace_bytes, nq, nk, n)
-        rc = self.lib.cdg_attention_grad(
-            self.handle, *self._q(q, nq, ld_q, "q"), *self._k(k, nk, ld_k, "k"), *self._k(v, nk, ld_v, "v"),
-            *self._q(o, nq, ld_o, "o"), _dense(lse, self.heads * nq, "float32", "lse"), *self._q(do, nq, ld_do, "do"), nq, nk, qo,
-            ko, ib, n, *self._q(dq, nq, ld_dq, "dq"), *self._k(dk, nk, ld_dk, "dk"), *self._k(dv, nk, ld_dv, "dv"),
-            _addr(workspace), _stream(stream))
+        _check_workspace(workspace, self._need, self.grad_workspace_bytes, nq, nk, n)
+        wq, wk = self.heads * self.dim, self.kv_heads * self.dim
+        m = _matrices(_TYPES.get(self.dtype), (q, nq, wq, ld_q, "q"), (k, nk, wk, ld_k, "k"), (v, nk, wk, ld_v, "v"),
+                      (o, nq, wq, ld_o, "o"), (do, nq, wq, ld_do, "do"), (dq, nq, wq, ld_dq, "dq"), (dk, nk, wk, ld_dk, "dk"),
+                      (dv, nk, wk, ld_dv, "dv"))
+        rc = self.lib.cdg_attention_grad(self.handle, *m[:8], *_vectors(self.heads * nq, (lse, "lse")), m[8], m[9], nq, nk, qo, ko,
+                                         ib, n, *m[10:], _addr(workspace), _stream(stream))
         if rc != OK:
             raise CdgError(rc, "cdg_attention_grad")
 
@@ -1012,15 +1044,17 @@ class AttentionPlan:
         return int(self.lib.cdg_attention_device_status(self.handle, _stream(stream)))
 
 
-def _check_workspace(t, plan, need, *sizes) -> None:
+def _check_workspace(t, known: dict, need, *sizes) -> None:
+    """Checks a workspace of need(*sizes) bytes; known holds what need has
+    answered (its own call takes as long as all of the tensor's checks)."""
     if t is None or isinstance(t, int):
         return
-    key = (need.__name__, *sizes)
-    n = plan._need.get(key)
+    key = (need.__name__, sizes)
+    n = known.get(key)
     if n is None:
-        if len(plan._need) > 64:
-            plan._need.clear()
-        n = plan._need[key] = need(*sizes)
+        if len(known) > 64:
+            known.clear()
+        n = known[key] = need(*sizes)
     if type(t) is _tensor and t.nbytes >= n and t.is_contiguous() and t.get_device() == _cuda_device():
         return  # what the check below finds, without its cost
     _check_buffer(t, n, "workspace")
@@ -1067,22 +1101,14 @@ def rope_frequencies(rot: int, base: float = 10000.0, stretch: float = 1.0, trai
     return list(out)[: int(rot) // 2]
 
 
-def _rope_args(q, k, positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved, factor, norm, eps, w_q, w_k,
-               ld_q, ld_k, read: bool):
-    """The arguments that qk_rope and qk_rope_grad share; read: whether q and k are."""
-    kind = _TYPES.get(dtype)
-    if read and heads:
-        q, ld_q = _matrix(q, tokens, heads * dim, kind, ld_q, "q")
-    else:
-        q, ld_q = None, 0
-    if read and kv_heads:
-        k, ld_k = _matrix(k, tokens, kv_heads * dim, kind, ld_k, "k")
-    else:
-        k, ld_k = None, 0
+def _rope_args(m, positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved, factor, norm, eps, w_q, w_k):
+    """The arguments that qk_rope and qk_rope_grad share; m: q's and k's addresses and row strides."""
     at, ib = _tokens(positions, tokens, "positions")
-    return (q, ld_q, k, ld_k, at, ib, tokens, heads, kv_heads, dim, _dtype(dtype),
-            _dense(inv_freq, rot // 2, "float32", "inv_freq"), rot, int(bool(interleaved)), float(factor), int(bool(norm)),
-            float(eps), _dense(w_q, dim, "float32", "w_q"), _dense(w_k, dim, "float32", "w_k"))
+    return (*m, at, ib, tokens, heads, kv_heads, dim, _dtype(dtype), *_vectors(rot // 2, (inv_freq, "inv_freq")), rot,
+            int(bool(interleaved)), float(factor), int(bool(norm)), float(eps), *_vectors(dim, (w_q, "w_q"), (w_k, "w_k")))
+
+
+_rope_need: dict = {}  # bytes of qk_rope_grad's workspace, by the sizes that calls have had
 
 
 def qk_rope(q, k, positions, inv_freq, q_out, k_out, tokens: int, heads: int, kv_heads: int, dim: int, dtype="bf16",
@@ -1093,12 +1119,12 @@ def qk_rope(q, k, positions, inv_freq, q_out, k_out, tokens: int, heads: int, kv
     by default) in one pass (cdg_qk_rope).  positions: int32 or int64, None for
     the token's number.  q_out may be q, and k_out k."""
     tokens, heads, kv_heads, dim = int(tokens), int(heads), int(kv_heads), int(dim)
-    rot, kind = dim if rot is None else int(rot), _TYPES.get(dtype)
-    args = _rope_args(q, k, positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved, factor, norm, eps, w_q,
-                      w_k, ld_q, ld_k, True)
-    outs = (*(_matrix(q_out, tokens, heads * dim, kind, ld_qo, "q_out") if heads else (None, 0)),
-            *(_matrix(k_out, tokens, kv_heads * dim, kind, ld_ko, "k_out") if kv_heads else (None, 0)))
-    rc = load_library().cdg_qk_rope(*args, *outs, _stream(stream))
+    rot = dim if rot is None else int(rot)
+    wq, wk = heads * dim, kv_heads * dim
+    m = _matrices(_TYPES.get(dtype), (q if heads else None, tokens, wq, ld_q, "q"), (k if kv_heads else None, tokens, wk, ld_k, "k"),
+                  (q_out if heads else None, tokens, wq, ld_qo, "q_out"), (k_out if kv_heads else None, tokens, wk, ld_ko, "k_out"))
+    rc = load_library().cdg_qk_rope(*_rope_args(m[:4], positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved,
+                                                factor, norm, eps, w_q, w_k), *m[4:], _stream(stream))
     if rc != OK:
         raise CdgError(rc, "cdg_qk_rope")
 
@@ -1120,16 +1146,15 @@ def qk_rope_grad(q, k, positions, inv_freq, dq_out, dk_out, dq, dk, workspace, t
     dw_q and dw_k (fp32; None: not wanted).  q and k are qk_rope's inputs, not
     read without the norm.  dq may be dq_out, and dk dk_out."""
     tokens, heads, kv_heads, dim = int(tokens), int(heads), int(kv_heads), int(dim)
-    rot, kind = dim if rot is None else int(rot), _TYPES.get(dtype)
-    args = _rope_args(q, k, positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot, interleaved, factor, norm, eps, w_q,
-                      w_k, ld_q, ld_k, bool(norm))
-    mats = []
-    for t, ld, n, what in ((dq_out, ld_dqo, heads, "dq_out"), (dk_out, ld_dko, kv_heads, "dk_out"), (dq, ld_dq, heads, "dq"),
-                           (dk, ld_dk, kv_heads, "dk")):
-        mats += _matrix(t, tokens, n * dim, kind, ld, what) if n else (None, 0)
-    if workspace is not None and not isinstance(workspace, int):
-        _check_buffer(workspace, qk_rope_grad_workspace_bytes(tokens, heads, kv_heads, dim), "workspace")
-    rc = load_library().cdg_qk_rope_grad(*args, *mats, _dense(dw_q, dim, "float32", "dw_q"), _dense(dw_k, dim, "float32", "dw_k"),
-                                         _addr(workspace), _stream(stream))
+    rot = dim if rot is None else int(rot)
+    wq, wk, qs, ks = heads * dim, kv_heads * dim, heads > 0, kv_heads > 0
+    m = _matrices(_TYPES.get(dtype), (q if norm and qs else None, tokens, wq, ld_q, "q"),
+                  (k if norm and ks else None, tokens, wk, ld_k, "k"),
+                  (dq_out if qs else None, tokens, wq, ld_dqo, "dq_out"), (dk_out if ks else None, tokens, wk, ld_dko, "dk_out"),
+                  (dq if qs else None, tokens, wq, ld_dq, "dq"), (dk if ks else None, tokens, wk, ld_dk, "dk"))
+    _check_workspace(workspace, _rope_need, qk_rope_grad_workspace_bytes, tokens, heads, kv_heads, dim)
+    rc = load_library().cdg_qk_rope_grad(*_rope_args(m[:4], positions, inv_freq, tokens, heads, kv_heads, dim, dtype, rot,
+                                                     interleaved, factor, norm, eps, w_q, w_k), *m[4:],
+                                         *_vectors(dim, (dw_q, "dw_q"), (dw_k, "dw_k")), _addr(workspace), _stream(stream))
     if rc != OK:
         raise CdgError(rc, "cdg_qk_rope_grad")
