@@ -2,7 +2,7 @@
 
     python -m implicit_gemm_dgrad_gb300.build [--force]
 
-Fifteen translation units compiled in parallel (the dgrad and wgrad host APIs,
+Sixteen translation units compiled in parallel (the dgrad and wgrad host APIs,
 the plain, per-channel-sum and activation variants of the dgrad kernels, the
 other dgrad kernels, the wgrad kernels, the token log probabilities, the
 embedding, the host API and kernels of the weight update and of the attention,
@@ -25,9 +25,10 @@ LIB = os.path.join(HERE, "libcdg.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["cdg_api.cu", "cwg_api.cu", "dgrad_sm103.cu", "dgrad_plain_sm103.cu", "dgrad_ext_sm103.cu",
            "dgrad_act_sm103.cu", "wgrad_sm103.cu", "logprobs_sm103.cu", "embed_sm103.cu", "muon_api.cu",
-           "muon_sm103.cu", "attention_api.cu", "attention_sm103.cu", "attention_grad_sm103.cu", "rope_sm103.cu"]
+           "muon_sm103.cu", "attention_api.cu", "attention_sm103.cu", "attention_grad_sm103.cu", "rope_sm103.cu",
+           "rope_grad_sm103.cu"]
 HEADERS = ["cdg_params.h", "cwg_params.h", "ptx.cuh", "wait.cuh", "dgrad_device.cuh", "dgrad_variant.cuh",
-           "token_device.cuh", "muon_params.h", "attention_params.h", "attention_device.cuh"]
+           "token_device.cuh", "muon_params.h", "attention_params.h", "attention_device.cuh", "rope_device.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
