@@ -162,23 +162,50 @@ long long items(long long tokens, int sequences, int rows, int heads)
     return (tokens + (rows - 1) * std::min<long long>(sequences, tokens)) / rows * heads;
 }
 
-// The gradient's workspace: the rows' statistics, then the splits' sums.  A
-// group's query heads are split over CTAs until there are two for every SM
-// (8192 causal tokens, 16 heads over 4, whose 256 tiles of keys take up to 256
-// steps each: see attention_grad_sm103.cu).
+// Parts that the steps of `n` items are split into: until there is an item for
+// every SM, but no part of fewer than four of an average item's `steps`.
+int parts_of(long long n, long long steps, int sms)
+{
+    int parts = 1;
+    while (n > 0 && n * parts < sms && steps >= 8ll * parts && parts < 32) parts *= 2;
+    return parts;
+}
+// Tiles of the other side that a tile sees, on average: of sequences of `tokens`
+// rows in all, within the window, half of them under a causal mask.
+long long steps_of(const cdg_attention_st *h, long long tokens, int sequences)
+{
+    long long rows = tokens / sequences;
+    if (h->causal) rows = (rows + 1) / 2;
+    if (h->window) rows = std::min<long long>(rows, h->window);
+    return (rows + CAT_TILE - 1) / CAT_TILE;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The forward's workspace: o and lse of each part.
+struct Workspace {
+    int parts;
+    size_t lse, bytes;
+    Workspace(const cdg_attention_st *h, long long q_tokens, long long k_tokens, int sequences)
+    {
+        parts = parts_of(items(q_tokens, sequences, 2 * CAT_TILE, h->heads), steps_of(h, k_tokens, sequences), h->sms);
+        const size_t rows = static_cast<size_t>(parts) * q_tokens * h->heads * 4;
+        lse = up256(rows * h->dim);
+        bytes = parts > 1 ? lse + up256(rows) : 256;
+    }
+};
+
+// The gradient's: the rows' statistics, then the sums of the parts of dq, and of dk and dv.
 struct GradWorkspace {
-    int splits;
-    size_t partial, bytes;
+    int q_parts, k_parts;
+    size_t dq, dkv, bytes;
     GradWorkspace(const cdg_attention_st *h, long long q_tokens, long long k_tokens, int sequences)
     {
-        const int group = h->heads / h->kv_heads;
-        const long long n = items(k_tokens, sequences, CAT_TILE, h->kv_heads);
-        splits = 1;
-        if (q_tokens > 0 && n > 0)
-            for (int s = 2; s <= group && n * splits < 2ll * h->sms; ++s)
-                if (group % s == 0) splits = s;
-        partial = (static_cast<size_t>(q_tokens) * h->heads * sizeof(float2) + 255) / 256 * 256;
-        bytes = partial + (splits > 1 ? 2ull * splits * k_tokens * h->kv_heads * h->dim * sizeof(float) : 0);
+        q_parts = parts_of(items(q_tokens, sequences, CAT_TILE, h->heads), steps_of(h, k_tokens, sequences), h->sms);
+        k_parts = parts_of(items(k_tokens, sequences, CAT_TILE, h->kv_heads), h->heads / h->kv_heads * steps_of(h, q_tokens, sequences), h->sms);
+        dq = up256(static_cast<size_t>(q_tokens) * h->heads * sizeof(float2));
+        dkv = dq + (q_parts > 1 ? up256(static_cast<size_t>(q_parts) * q_tokens * h->heads * h->dim * 4) : 0);
+        bytes = dkv + (k_parts > 1 ? up256(2ull * k_parts * k_tokens * h->kv_heads * h->dim * 4) : 0);
         bytes = std::max<size_t>(256, bytes);
     }
 };
@@ -215,7 +242,7 @@ void cdg_attention_destroy(cdg_attention_t h)
 
 size_t cdg_attention_workspace_bytes(cdg_attention_t h, long long q_tokens, long long k_tokens, int sequences)
 {
-    return sizes_ok(h, q_tokens, k_tokens, sequences) ? 256 : 0;
+    return sizes_ok(h, q_tokens, k_tokens, sequences) ? Workspace(h, q_tokens, k_tokens, sequences).bytes : 0;
 }
 
 size_t cdg_attention_grad_workspace_bytes(cdg_attention_t h, long long q_tokens, long long k_tokens, int sequences)
@@ -253,9 +280,15 @@ int cdg_attention(cdg_attention_t h, const void *q, long long ld_q, const void *
     p.o = o;
     p.ld_o = ld_o;
     p.lse = lse;
+    const Workspace ws(h, q_tokens, k_tokens, sequences);
+    p.q_splits = ws.parts;
+    p.q_partial = static_cast<float *>(workspace);
+    p.lse_partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.lse);
     const long long n = items(q_tokens, sequences, 2 * CAT_TILE, h->heads);
-    if (n >= (1ll << 31)) return CDG_ERR_UNSUPPORTED;
-    return cat_launch_forward(p, h->dtype == CDG_BF16, n, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
+    if (n * p.q_splits >= (1ll << 31)) return CDG_ERR_UNSUPPORTED;
+    // (few items are split, so that a join has few CTAs too)
+    const long long joins = items(q_tokens, sequences, CAT_JOIN_ROWS, h->heads);
+    return cat_launch_forward(p, h->dtype == CDG_BF16, n, joins, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CDG_OK : CDG_ERR_CUDA;
 }
 
 int cdg_attention_grad(cdg_attention_t h, const void *q, long long ld_q, const void *k, long long ld_k, const void *v,
@@ -300,16 +333,20 @@ int cdg_attention_grad(cdg_attention_t h, const void *q, long long ld_q, const v
     p.lse_in = lse;
     const GradWorkspace ws(h, q_tokens, k_tokens, sequences);
     p.stats = static_cast<float2 *>(workspace);
-    p.splits = ws.splits;
-    p.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.partial);
+    p.q_splits = ws.q_parts;
+    p.k_splits = ws.k_parts;
+    p.q_partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.dq);
+    p.k_partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.dkv);
     const int bf16 = h->dtype == CDG_BF16;
     const long long nq = items(q_tokens, sequences, CAT_TILE, h->heads), nk = items(k_tokens, sequences, CAT_TILE, h->kv_heads);
-    if (nq >= (1ll << 31) || nk * ws.splits >= (1ll << 31) || q_tokens * h->heads >= (1ll << 34)) return CDG_ERR_UNSUPPORTED;
+    if (nq * p.q_splits >= (1ll << 31) || nk * p.k_splits >= (1ll << 31) || q_tokens * h->heads >= (1ll << 34)) return CDG_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (q_tokens > 0 && cat_launch_stats(p, bf16, s) != cudaSuccess) return CDG_ERR_CUDA;
     if (k_tokens > 0 && cat_launch_dkv(p, bf16, nk, s) != cudaSuccess) return CDG_ERR_CUDA;
     if (q_tokens > 0 && cat_launch_dq(p, bf16, nq, s) != cudaSuccess) return CDG_ERR_CUDA;
-    if (p.splits > 1 && cat_launch_join(p, bf16, nk, s) != cudaSuccess) return CDG_ERR_CUDA;
+    if (cat_launch_grad_join(p, bf16, items(k_tokens, sequences, CAT_JOIN_ROWS, h->kv_heads), items(q_tokens, sequences, CAT_JOIN_ROWS, h->heads),
+                             s) != cudaSuccess)
+        return CDG_ERR_CUDA;
     return CDG_OK;
 }
 

@@ -331,6 +331,14 @@ __device__ __forceinline__ void key_steps(const CatParams &p, const Place &at, i
     hi = end > first ? (end + CAT_TILE - 1) / CAT_TILE : lo;
 }
 
+// Part `part` of `parts` of the steps [lo, hi).
+__device__ __forceinline__ void take_part(int &lo, int &hi, int part, int parts)
+{
+    const int first = lo, n = hi - lo;
+    lo = first + static_cast<int>(static_cast<long long>(n) * part / parts);
+    hi = first + static_cast<int>(static_cast<long long>(n) * (part + 1) / parts);
+}
+
 // ---------------------------------------------------------------- pieces
 
 // Zeroes rows [valid, 128) of a tile (this warp alone), for the async proxy to see.
@@ -405,7 +413,7 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, int c0, int c1, float
     }
 }
 // The same, as fp32.
-__device__ __forceinline__ void store_rows_f32(uint32_t taddr, int c0, int c1, float *out, long long ld, int rows)
+__device__ __forceinline__ void store_rows_f32(uint32_t taddr, int c0, int c1, float f, float *out, long long ld, int rows)
 {
     const int lane = threadIdx.x & 31;
     for (; c0 < c1; c0 += 32) {
@@ -416,7 +424,7 @@ __device__ __forceinline__ void store_rows_f32(uint32_t taddr, int c0, int c1, f
         for (int half = 0; half < 2; ++half) {
             uint32_t w[4][4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = __float_as_uint(v[16 * half + e]);
+            for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = __float_as_uint(v[16 * half + e] * f);
             transpose_pieces(w);
             const int col = c0 + 16 * half + 4 * (lane & 3);
 #pragma unroll

@@ -206,32 +206,35 @@ constexpr uint32_t kS = 0, kDP = 128, kSum = 256;
 
 // ------------------------------------------------------------------ dk, dv
 
-// An item of dk and dv: 128 keys, and the steps of its part of their group's
-// query heads over the query tiles that see some of them.
+// An item of dk and dv: 128 keys, and its part of the steps of their group's query
+// heads over the query tiles that see some of them.
+template <bool SPLIT>
 struct KeyTile {
     int j0;              // first key of the tile, in its sequence
     int lo, count;       // first query tile and their number, for each head
-    int kv_head, split;
-    int head0, heads;    // the part's query heads
+    int kv_head, part;
+    int begin, end;      // the part's steps: of head n / count, query tile lo + n % count
     __device__ __forceinline__ KeyTile(const CatParams &p, const Item &item)
     {
         const Place &at = item.at;
-        kv_head = item.head / p.splits;
-        split = item.head - kv_head * p.splits;
-        heads = p.group / p.splits;
-        head0 = kv_head * p.group + split * heads;
+        kv_head = SPLIT ? item.head / p.k_splits : item.head;
+        part = SPLIT ? item.head - kv_head * p.k_splits : 0;
         // (a sequence's first keys, which under a causal mask most queries see, come first)
         j0 = at.tile * CAT_TILE;
         const int off = at.kl - at.ql, j1 = min(j0 + CAT_TILE, at.kl);
-        const int first = p.causal ? max(0, j0 - off) : 0, end = p.window ? min(at.ql, j1 - 1 - off + p.window) : at.ql;
+        const int first = p.causal ? max(0, j0 - off) : 0, last = p.window ? min(at.ql, j1 - 1 - off + p.window) : at.ql;
         lo = first / CAT_TILE;
-        count = end > first ? (end + CAT_TILE - 1) / CAT_TILE - lo : 0;
+        count = last > first ? (last + CAT_TILE - 1) / CAT_TILE - lo : 0;
+        begin = 0;
+        end = count * p.group;
+        if (SPLIT) take_part(begin, end, part, p.k_splits);
     }
-    __device__ __forceinline__ int steps() const { return count * heads; }
-    __device__ __forceinline__ void where(int n, int &head, int &tile) const
+    __device__ __forceinline__ int steps() const { return end - begin; }
+    __device__ __forceinline__ void where(const CatParams &p, int n, int &head, int &tile) const
     {
+        if (SPLIT) n += begin;
         const int h = n / count;
-        head = head0 + h;
+        head = kv_head * p.group + h;
         tile = lo + n - h * count;
     }
 };
@@ -260,9 +263,9 @@ __device__ __forceinline__ void put_rounded(uint32_t taddr, const float (&s)[32]
     tmem_st_wait();
 }
 
-template <bool BF16>
+template <bool BF16, bool SPLIT>
 __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
-                                            const KeyTile &kt, uint32_t &done, uint32_t &items)
+                                            const KeyTile<SPLIT> &kt, uint32_t &done, uint32_t &items)
 {
     const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -270,7 +273,7 @@ __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &
     const f32x2 c2 = pack2(p.scale_log2, p.scale_log2), minus = pack2(-1.0f, -1.0f);
     const int off = at.kl - at.ql, j = kt.j0 + row;
     const int steps = kt.steps();
-    int tile = kt.lo;
+    int tile = kt.count > 0 ? kt.lo + kt.begin % kt.count : 0;
     for (int n = 0; n < steps; ++n, ++done) {
         const uint32_t slot = done % kSlots;
         const uint32_t stats = S.stats + slot * 2 * CAT_TILE * 4 + part * 32 * 4;
@@ -322,20 +325,20 @@ __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &
     const long long token = at.k0 + j, first = token - (threadIdx.x & 31);
     const bool is_dk = part >= 2;
     const int c0 = 32 * p.slices * (part & 1), c1 = min(p.dim, c0 + 32 * p.slices), rows = at.kl - (j & ~31);
-    const long long ld = p.splits > 1 ? static_cast<long long>(p.kv_heads) * p.dim : is_dk ? p.ld_dk : p.ld_dv;
+    const long long ld = SPLIT ? static_cast<long long>(p.kv_heads) * p.dim : is_dk ? p.ld_dk : p.ld_dv;
     uint16_t *out = static_cast<uint16_t *>(is_dk ? p.dk : p.dv) + first * ld + static_cast<long long>(kt.kv_head) * p.dim;
-    float *sum = p.partial + ((2ll * kt.split + is_dk) * p.k_tokens + first) * ld + static_cast<long long>(kt.kv_head) * p.dim;
+    float *sum = p.k_partial + ((2ll * kt.part + is_dk) * p.k_tokens + first) * ld + static_cast<long long>(kt.kv_head) * p.dim;
     if (steps > 0) {
         if (!wait_bar(S.B.out_full, items & 1u, ctl)) return false;
         ++items;
         tc_fence_after();
         const uint32_t taddr = tmem + lanes + kSum + 64u * p.slices * is_dk;
-        if (p.splits > 1) store_rows_f32(taddr, c0, c1, sum, ld, rows);
+        if (SPLIT) store_rows_f32(taddr, c0, c1, 1.0f, sum, ld, rows);
         else store_rows<BF16>(taddr, c0, c1, is_dk ? p.scale : 1.0f, out, ld, rows);
         warp_arrive(S.B.out_empty);
     } else if (j < at.kl) {
         const int lane = threadIdx.x & 31;
-        if (p.splits > 1)
+        if (SPLIT)
             for (int c = c0; c < c1; c += 4) *reinterpret_cast<float4 *>(sum + lane * ld + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         else
             zero_row(out + lane * ld, c0, c1);
@@ -343,7 +346,7 @@ __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &
     return true;
 }
 
-template <bool BF16, int SLICES>
+template <bool BF16, int SLICES, bool SPLIT>
 __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(const __grid_constant__ CatParams p)
 {
     constexpr uint32_t tile_bytes = kSliceBytes * SLICES;
@@ -365,15 +368,15 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
     Item item;
     uint32_t done = 0, items = 0;  // steps, and items that had some
     if (warp == kWarpItems) {
-        run_items(p, S.I, ctl, CAT_TILE, true, p.kv_heads * p.splits);
+        run_items(p, S.I, ctl, CAT_TILE, true, p.kv_heads * p.k_splits);
     } else if (warp == kWarpLoad) {
         const bool leader = elect_one_sync();
         for (int n = 0; next_item(S.I, ctl, n, item); ++n) {
-            const KeyTile kt(p, item);
+            const KeyTile<SPLIT> kt(p, item);
             if (!run_grad_loads(p, S, ctl, leader, kt.steps(), p.tmK, p.tmV, kt.kv_head, item.at.k0 + kt.j0, p.tmQ, p.tmDO, items, done,
                                 [&](int k, int &head, int &token) {
                                     int tile;
-                                    kt.where(k, head, tile);
+                                    kt.where(p, k, head, tile);
                                     token = item.at.q0 + tile * CAT_TILE;
                                 }))
                 break;
@@ -384,11 +387,11 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
         const int lane = threadIdx.x & 31;
         bool ok = true;
         for (int n = 0; ok && next_item(S.I, ctl, n, item); ++n) {
-            const KeyTile kt(p, item);
+            const KeyTile<SPLIT> kt(p, item);
             for (int k = 0; k < kt.steps(); ++k, ++done) {
                 const uint32_t slot = done % kSlots;
                 int head, tile;
-                kt.where(k, head, tile);
+                kt.where(p, k, head, tile);
                 ok = wait_bar(S.B.st_empty0 + 8u * slot, ((done / kSlots) & 1u) ^ 1u, ctl);
                 if (!ok) break;
                 const float2 *src = p.stats + static_cast<long long>(head) * p.q_tokens + item.at.q0;
@@ -407,14 +410,15 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
         const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dv = tm + kSum, dk = dv + 64u * SLICES;
         bool ok = true;
         for (int n = 0; ok && next_item(S.I, ctl, n, item); ++n) {
-            const KeyTile kt(p, item);
-            const int total = uniform(kt.steps()), count = uniform(kt.count), rest = uniform(item.at.ql - kt.lo * CAT_TILE);
+            const KeyTile<SPLIT> kt(p, item);
+            const int total = uniform(kt.steps()), count = uniform(kt.count), begin = uniform(kt.begin);
+            const int rest = uniform(item.at.ql - kt.lo * CAT_TILE);
             if (total == 0) continue;
             // waits for the k-th streamed tile; rows behind the sequence's end become zeros
             auto filled = [&](uint32_t full0, uint32_t ring, int k, uint32_t step) {
                 if (!wait_bar(full0 + 8u * (step % kSlots), (step / kSlots) & 1u, ctl)) return false;
                 tc_fence_after();
-                const int valid = rest - k % count * CAT_TILE;
+                const int valid = rest - (begin + k) % count * CAT_TILE;
                 if (valid < CAT_TILE) zero_rows(ring + (step % kSlots) * tile_bytes, SLICES, valid);
                 return true;
             };
@@ -459,44 +463,34 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
         drain_mmas(p, S, leader);
     } else if (warp < 16) {
         for (int n = 0; next_item(S.I, ctl, n, item); ++n)
-            if (!compute_dkv<BF16>(p, S, ctl, tmem, item.at, KeyTile(p, item), done, items)) break;
+            if (!compute_dkv<BF16, SPLIT>(p, S, ctl, tmem, item.at, KeyTile<SPLIT>(p, item), done, items)) break;
     }
     grad_end(p, S, tmem);
 }
 
-// dk and dv of a tile of keys and a head: the splits' sums, added in order.
-template <bool BF16>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ CatParams p)
-{
-    grid_dep_launch_dependents();
-    grid_dep_wait();
-    const int kv_head = static_cast<int>(blockIdx.x % p.kv_heads);
-    const Place at = find_tile(p, blockIdx.x / p.kv_heads, CAT_TILE, true);
-    if (at.tile < 0) return;
-    const int rows = min(CAT_TILE, at.kl - at.tile * CAT_TILE), vecs = p.dim / 4;
-    const long long ld = static_cast<long long>(p.kv_heads) * p.dim, token0 = at.k0 + at.tile * CAT_TILE;
-    for (int i = threadIdx.x; i < 2 * rows * vecs; i += 256) {
-        const int kind = i / (rows * vecs), r = (i - kind * rows * vecs) / vecs, c = (i - (kind * rows + r) * vecs) * 4;
-        const long long token = token0 + r;
-        const float *src = p.partial + (static_cast<long long>(kind) * p.k_tokens + token) * ld + static_cast<long long>(kv_head) * p.dim + c;
-        float4 v = __ldg(reinterpret_cast<const float4 *>(src));
-        for (int s = 1; s < p.splits; ++s) {
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(src + 2ll * s * p.k_tokens * ld));
-            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-        }
-        const float f = kind ? p.scale : 1.0f;
-        uint16_t *out = kind ? static_cast<uint16_t *>(p.dk) + token * p.ld_dk : static_cast<uint16_t *>(p.dv) + token * p.ld_dv;
-        *reinterpret_cast<uint2 *>(out + static_cast<long long>(kv_head) * p.dim + c) =
-            make_uint2(round2<BF16>(v.x * f, v.y * f), round2<BF16>(v.z * f, v.w * f));
-    }
-}
-
 // ------------------------------------------------------------------ dq
 
-template <bool BF16>
+// An item of dq: 128 queries from i0 of a head, its part [lo, hi) of the steps of keys.
+template <bool SPLIT>
+struct QueryTile {
+    int i0, lo, hi, head, part;
+    __device__ __forceinline__ QueryTile(const CatParams &p, const Item &item)
+    {
+        const Place &at = item.at;
+        head = SPLIT ? item.head / p.q_splits : item.head;
+        part = SPLIT ? item.head - head * p.q_splits : 0;
+        // a sequence's last queries first: under a causal mask they see most keys
+        i0 = ((at.ql + CAT_TILE - 1) / CAT_TILE - 1 - at.tile) * CAT_TILE;
+        key_steps(p, at, i0, min(i0 + CAT_TILE, at.ql), lo, hi);
+        if (SPLIT) take_part(lo, hi, part, p.q_splits);
+    }
+};
+
+template <bool BF16, bool SPLIT>
 __device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
-                                           int i0, int head, int lo, int hi, uint32_t &done, uint32_t &items)
+                                           const QueryTile<SPLIT> &qt, uint32_t &done, uint32_t &items)
 {
+    const int i0 = qt.i0, head = qt.head, lo = qt.lo, hi = qt.hi;
     const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127, i = i0 + row;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t s_col = tmem + lanes + kS + 32u * part, dp_col = tmem + lanes + kDP + 32u * part;
@@ -537,31 +531,28 @@ __device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S
         warp_arrive(S.B.ds_ready);
     }
     uint16_t *out = static_cast<uint16_t *>(p.dq) + (token - (threadIdx.x & 31)) * p.ld_dq + static_cast<long long>(head) * p.dim;
+    const long long width = static_cast<long long>(p.heads) * p.dim;
+    float *sum = p.q_partial + (static_cast<long long>(qt.part) * p.q_tokens + token - (threadIdx.x & 31)) * width + static_cast<long long>(head) * p.dim;
     const int c0 = 32 * part, c1 = min(p.dim, c0 + 32);
     if (hi > lo) {
         if (!wait_bar(S.B.out_full, items & 1u, ctl)) return false;
         ++items;
         tc_fence_after();
-        store_rows<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out, p.ld_dq, at.ql - (i & ~31));
+        const int rows = at.ql - (i & ~31);
+        if (SPLIT) store_rows_f32(tmem + lanes + kSum, c0, c1, 1.0f, sum, width, rows);
+        else store_rows<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out, p.ld_dq, rows);
         warp_arrive(S.B.out_empty);
     } else if (valid) {
-        zero_row(out + (threadIdx.x & 31) * p.ld_dq, c0, c1);
+        const int lane = threadIdx.x & 31;
+        if (SPLIT)
+            for (int c = c0; c < c1; c += 4) *reinterpret_cast<float4 *>(sum + lane * width + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        else
+            zero_row(out + lane * p.ld_dq, c0, c1);
     }
     return true;
 }
 
-// An item of dq: 128 queries from i0 of a head, steps [lo, hi) of keys.
-struct QueryTile {
-    int i0, lo, hi;
-    __device__ __forceinline__ QueryTile(const CatParams &p, const Place &at)
-    {
-        // a sequence's last queries first: under a causal mask they see most keys
-        i0 = ((at.ql + CAT_TILE - 1) / CAT_TILE - 1 - at.tile) * CAT_TILE;
-        key_steps(p, at, i0, min(i0 + CAT_TILE, at.ql), lo, hi);
-    }
-};
-
-template <bool BF16, int SLICES>
+template <bool BF16, int SLICES, bool SPLIT>
 __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const __grid_constant__ CatParams p)
 {
     constexpr uint32_t tile_bytes = kSliceBytes * SLICES;
@@ -580,14 +571,14 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const
     Item item;
     uint32_t done = 0, items = 0;  // steps, and items that had some
     if (warp == kWarpItems) {
-        run_items(p, S.I, ctl, CAT_TILE, false, p.heads);
+        run_items(p, S.I, ctl, CAT_TILE, false, p.heads * p.q_splits);
     } else if (warp == kWarpLoad) {
         const bool leader = elect_one_sync();
         for (int n = 0; next_item(S.I, ctl, n, item); ++n) {
-            const QueryTile qt(p, item.at);
-            if (!run_grad_loads(p, S, ctl, leader, qt.hi - qt.lo, p.tmQ, p.tmDO, item.head, item.at.q0 + qt.i0, p.tmK, p.tmV, items, done,
+            const QueryTile<SPLIT> qt(p, item);
+            if (!run_grad_loads(p, S, ctl, leader, qt.hi - qt.lo, p.tmQ, p.tmDO, qt.head, item.at.q0 + qt.i0, p.tmK, p.tmV, items, done,
                                 [&](int k, int &head, int &token) {
-                                    head = item.head / p.group;
+                                    head = qt.head / p.group;
                                     token = item.at.k0 + (qt.lo + k) * CAT_TILE;
                                 }))
                 break;
@@ -599,7 +590,7 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const
         const uint32_t tm = uniform(tmem), s = tm + kS, dp = tm + kDP, dq = tm + kSum;
         bool ok = true;
         for (int n = 0; ok && next_item(S.I, ctl, n, item); ++n) {
-            const QueryTile qt(p, item.at);
+            const QueryTile<SPLIT> qt(p, item);
             const int total = uniform(qt.hi - qt.lo), rest = uniform(item.at.kl - qt.lo * CAT_TILE);
             if (total <= 0) continue;
             auto scores = [&](int k) {
@@ -646,8 +637,8 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const
         drain_mmas(p, S, leader);
     } else if (warp < 16) {
         for (int n = 0; next_item(S.I, ctl, n, item); ++n) {
-            const QueryTile qt(p, item.at);
-            if (!compute_dq<BF16>(p, S, ctl, tmem, item.at, qt.i0, item.head, qt.lo, qt.hi, done, items)) break;
+            const QueryTile<SPLIT> qt(p, item);
+            if (!compute_dq<BF16, SPLIT>(p, S, ctl, tmem, item.at, qt, done, items)) break;
         }
     }
     grad_end(p, S, tmem);
@@ -656,10 +647,74 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const
     grid_dep_wait();
 }
 
+// Sums of the parts of up to 16 rows of one head, added in order, times f, to 16-bit rows.
+template <bool BF16>
+__device__ __forceinline__ void join_rows(const float *src, long long width, long long part, int parts, float f, uint16_t *out,
+                                          long long ld, int rows, int dim)
+{
+    const int vecs = dim / 4;
+    for (int i = threadIdx.x; i < rows * vecs; i += 128) {
+        const int r = i / vecs, c = (i - r * vecs) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(src + s * part + r * width + c));
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        *reinterpret_cast<uint2 *>(out + r * ld + c) = make_uint2(round2<BF16>(v.x * f, v.y * f), round2<BF16>(v.z * f, v.w * f));
+    }
+}
+
+// CTAs [0, key_items): dk and dv of 16 keys and a head; the others: dq of 16 queries and a head.
+template <bool BF16>
+__global__ void __launch_bounds__(128) attention_grad_join_kernel(const __grid_constant__ CatParams p, unsigned key_items)
+{
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    if (blockIdx.x < key_items) {
+        const int head = static_cast<int>(blockIdx.x % p.kv_heads);
+        const Place at = find_tile(p, blockIdx.x / p.kv_heads, CAT_JOIN_ROWS, true);
+        if (at.tile < 0) return;
+        const int rows = min(CAT_JOIN_ROWS, at.kl - at.tile * CAT_JOIN_ROWS);
+        const long long width = static_cast<long long>(p.kv_heads) * p.dim, token = at.k0 + at.tile * CAT_JOIN_ROWS, kind = p.k_tokens * width,
+                        col = static_cast<long long>(head) * p.dim;
+        const float *src = p.k_partial + token * width + col;
+        join_rows<BF16>(src, width, 2 * kind, p.k_splits, 1.0f, static_cast<uint16_t *>(p.dv) + token * p.ld_dv + col, p.ld_dv, rows, p.dim);
+        join_rows<BF16>(src + kind, width, 2 * kind, p.k_splits, p.scale, static_cast<uint16_t *>(p.dk) + token * p.ld_dk + col, p.ld_dk, rows,
+                        p.dim);
+    } else {
+        const unsigned item = blockIdx.x - key_items;
+        const int head = static_cast<int>(item % p.heads);
+        const Place at = find_tile(p, item / p.heads, CAT_JOIN_ROWS, false);
+        if (at.tile < 0) return;
+        const long long width = static_cast<long long>(p.heads) * p.dim, token = at.q0 + at.tile * CAT_JOIN_ROWS, col = static_cast<long long>(head) * p.dim;
+        join_rows<BF16>(p.q_partial + token * width + col, width, p.q_tokens * width, p.q_splits, p.scale,
+                        static_cast<uint16_t *>(p.dq) + token * p.ld_dq + col, p.ld_dq, min(CAT_JOIN_ROWS, at.ql - at.tile * CAT_JOIN_ROWS), p.dim);
+    }
+}
+
 }  // namespace
 }  // namespace cdg
 
 size_t cat_smem_grad(int slices) { return 1024 + (2 + 2 * cdg::kSlots) * cdg::kSliceBytes * slices + cdg::kSlots * CAT_TILE * 8 + cdg::kGradTail; }
+
+namespace {
+typedef void (*Kernel)(CatParams);
+template <int SLICES, bool SPLIT>
+Kernel dkv_kernel(int bf16) { return bf16 ? cdg::attention_dkv_kernel<true, SLICES, SPLIT> : cdg::attention_dkv_kernel<false, SLICES, SPLIT>; }
+Kernel dkv_kernel(int slices, int bf16, int split)
+{
+    return slices == 2 ? (split ? dkv_kernel<2, true>(bf16) : dkv_kernel<2, false>(bf16))
+                       : (split ? dkv_kernel<1, true>(bf16) : dkv_kernel<1, false>(bf16));
+}
+template <int SLICES, bool SPLIT>
+Kernel dq_kernel(int bf16) { return bf16 ? cdg::attention_dq_kernel<true, SLICES, SPLIT> : cdg::attention_dq_kernel<false, SLICES, SPLIT>; }
+Kernel dq_kernel(int slices, int bf16, int split)
+{
+    return slices == 2 ? (split ? dq_kernel<2, true>(bf16) : dq_kernel<2, false>(bf16))
+                       : (split ? dq_kernel<1, true>(bf16) : dq_kernel<1, false>(bf16));
+}
+}  // namespace
 
 cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
 {
@@ -673,18 +728,19 @@ cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
 cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaStream_t s)
 {
     using namespace cdg;
-    const dim3 grid(static_cast<unsigned>(items * p.splits)), block(CAT_GRAD_THREADS);
+    const dim3 grid(static_cast<unsigned>(items * p.k_splits)), block(CAT_GRAD_THREADS);
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
-    void (*k)(CatParams) = p.slices == 2 ? (bf16 ? attention_dkv_kernel<true, 2> : attention_dkv_kernel<false, 2>)
-                                         : (bf16 ? attention_dkv_kernel<true, 1> : attention_dkv_kernel<false, 1>);
+    const Kernel k = dkv_kernel(p.slices, bf16, p.k_splits > 1);
     return launch_early(k, grid, block, smem, s, p);
 }
 
-cudaError_t cat_launch_join(const CatParams &p, int bf16, long long items, cudaStream_t s)
+cudaError_t cat_launch_grad_join(const CatParams &p, int bf16, long long key_items, long long query_items, cudaStream_t s)
 {
     using namespace cdg;
-    const dim3 grid(static_cast<unsigned>(items)), block(256);
-    return bf16 ? launch_early(attention_join_kernel<true>, grid, block, 0, s, p) : launch_early(attention_join_kernel<false>, grid, block, 0, s, p);
+    const unsigned keys = p.k_splits > 1 ? static_cast<unsigned>(key_items) : 0u, queries = p.q_splits > 1 ? static_cast<unsigned>(query_items) : 0u;
+    if (keys + queries == 0) return cudaSuccess;
+    return bf16 ? launch_early(attention_grad_join_kernel<true>, dim3(keys + queries), dim3(128), 0, s, p, keys)
+                : launch_early(attention_grad_join_kernel<false>, dim3(keys + queries), dim3(128), 0, s, p, keys);
 }
 
 // After cat_launch_dkv on the same stream, beside whose end it begins; without
@@ -692,10 +748,9 @@ cudaError_t cat_launch_join(const CatParams &p, int bf16, long long items, cudaS
 cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStream_t s)
 {
     using namespace cdg;
-    const dim3 grid(static_cast<unsigned>(items)), block(CAT_GRAD_THREADS);
+    const dim3 grid(static_cast<unsigned>(items * p.q_splits)), block(CAT_GRAD_THREADS);
     const int smem = static_cast<int>(cat_smem_grad(p.slices));
-    void (*k)(CatParams) = p.slices == 2 ? (bf16 ? attention_dq_kernel<true, 2> : attention_dq_kernel<false, 2>)
-                                         : (bf16 ? attention_dq_kernel<true, 1> : attention_dq_kernel<false, 1>);
+    const Kernel k = dq_kernel(p.slices, bf16, p.q_splits > 1);
     if (p.k_tokens > 0) return launch_early(k, grid, block, smem, s, p);
     k<<<grid, block, smem, s>>>(p);
     return cudaGetLastError();
@@ -703,10 +758,10 @@ cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStr
 
 cudaError_t cat_prepare_grad()
 {
-    for (auto *k : {cdg::attention_dkv_kernel<true, 1>, cdg::attention_dkv_kernel<false, 1>, cdg::attention_dkv_kernel<true, 2>,
-                    cdg::attention_dkv_kernel<false, 2>, cdg::attention_dq_kernel<true, 1>, cdg::attention_dq_kernel<false, 1>,
-                    cdg::attention_dq_kernel<true, 2>, cdg::attention_dq_kernel<false, 2>}) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CDG_MAX_DYN_SMEM);
+    for (int i = 0; i < 16; ++i) {
+        const int slices = 1 + (i & 1), bf16 = i >> 1 & 1, split = i >> 2 & 1;
+        const cudaError_t e = cudaFuncSetAttribute(i & 8 ? dkv_kernel(slices, bf16, split) : dq_kernel(slices, bf16, split),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, CDG_MAX_DYN_SMEM);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

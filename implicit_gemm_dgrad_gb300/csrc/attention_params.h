@@ -34,8 +34,13 @@ struct CatParams {
     long long ld_oi, ld_do;
     const float *lse_in;
     float2 *stats;
-    int splits;                  // dk and dv: parts of a group's query heads, a CTA each; above 1 their fp32 sums go to
-    float *partial;              // [splits][dk, dv][k_tokens][kv_heads * dim], and are added in order by a kernel of their own
+    // Parts that an item's steps are split into, a CTA each, where items are few.  Above
+    // 1 their fp32 results go to `partial`, and a kernel of its own joins them in order:
+    int q_splits;                // o, or dq: q_partial is [q_splits][q_tokens][heads * dim],
+    float *q_partial;
+    float *lse_partial;          //   of o with each part's own lse, [q_splits][heads][q_tokens]
+    int k_splits;                // dk and dv: k_partial is [k_splits][dv, dk][k_tokens][kv_heads * dim]
+    float *k_partial;
     int *status;
 };
 
@@ -43,9 +48,12 @@ size_t cat_smem_forward(int slices);
 size_t cat_smem_grad(int slices);
 cudaError_t cat_prepare_forward();
 cudaError_t cat_prepare_grad();
-// bf16: 1 for bfloat16, 0 for float16; items: CTAs of a launch (of dk and dv: without the splits)
-cudaError_t cat_launch_forward(const CatParams &p, int bf16, long long items, cudaStream_t s);
+#define CAT_JOIN_ROWS 16  // rows and one head that a CTA of a join takes
+
+// bf16: 1 for bfloat16, 0 for float16; items: CTAs of a launch without the splits
+cudaError_t cat_launch_forward(const CatParams &p, int bf16, long long items, long long join_items, cudaStream_t s);
 cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s);
 cudaError_t cat_launch_dkv(const CatParams &p, int bf16, long long items, cudaStream_t s);
 cudaError_t cat_launch_dq(const CatParams &p, int bf16, long long items, cudaStream_t s);
-cudaError_t cat_launch_join(const CatParams &p, int bf16, long long items, cudaStream_t s);
+// joins what dk and dv, dq, or both have in parts; CTAs for keys' rows and for queries' rows
+cudaError_t cat_launch_grad_join(const CatParams &p, int bf16, long long key_items, long long query_items, cudaStream_t s);

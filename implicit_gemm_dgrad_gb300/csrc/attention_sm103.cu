@@ -37,12 +37,17 @@ struct Range {
 };
 
 // An item's 256 queries of one head: two tiles from query i0, and the steps of
-// keys that each of them and both together see.
+// keys that each of them and both together see (SPLIT: of those, its part).
+template <bool SPLIT>
 struct Steps {
     int i0;
     Range tile[2], all;
-    __device__ __forceinline__ Steps(const CatParams &p, const Place &at)
+    int head, part;
+    __device__ __forceinline__ Steps(const CatParams &p, const Item &item)
     {
+        const Place &at = item.at;
+        head = SPLIT ? item.head / p.q_splits : item.head;
+        part = SPLIT ? item.head - head * p.q_splits : 0;
         // a sequence's last tiles first: under a causal mask they are the longest
         i0 = ((at.ql + 2 * CAT_TILE - 1) / (2 * CAT_TILE) - 1 - at.tile) * 2 * CAT_TILE;
 #pragma unroll
@@ -54,6 +59,14 @@ struct Steps {
         const bool some0 = tile[0].hi > tile[0].lo, some1 = tile[1].hi > tile[1].lo;
         all.lo = some0 && some1 ? min(tile[0].lo, tile[1].lo) : some0 ? tile[0].lo : tile[1].lo;
         all.hi = some0 && some1 ? max(tile[0].hi, tile[1].hi) : some0 ? tile[0].hi : tile[1].hi;
+        if (SPLIT) {
+            take_part(all.lo, all.hi, part, p.q_splits);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                tile[t] = Range{max(tile[t].lo, all.lo), min(tile[t].hi, all.hi)};
+                if (tile[t].hi <= tile[t].lo) tile[t] = Range{all.lo, all.lo};
+            }
+        }
     }
 };
 
@@ -66,9 +79,9 @@ __device__ __forceinline__ void hide(float (&s)[32], int lo, int hi)
 }
 
 // One tile's softmax over one item.  steps, items: what this tile has done before.
-template <bool BF16>
+template <bool BF16, bool SPLIT>
 __device__ __forceinline__ bool run_softmax(const CatParams &p, const FwdBars &B, Ctl ctl, uint32_t tmem, const Place &at,
-                                            int head, int i0, int t, Range range, uint32_t &steps, uint32_t &items)
+                                            int head, int part, int i0, int t, Range range, uint32_t &steps, uint32_t &items)
 {
     const int warp = threadIdx.x / 32, row = threadIdx.x & 127, i = i0 + row;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -151,26 +164,32 @@ __device__ __forceinline__ bool run_softmax(const CatParams &p, const FwdBars &B
         warp_arrive(B.p_ready0 + 8u * t);
     }
     const bool valid = i < at.ql;
-    const long long token = at.q0 + i;
-    uint16_t *out = static_cast<uint16_t *>(p.o) + (token - (threadIdx.x & 31)) * p.ld_o + static_cast<long long>(head) * p.dim;
+    const long long token = at.q0 + i, first = token - (threadIdx.x & 31), width = static_cast<long long>(p.heads) * p.dim;
     // a row that sees nothing (l = 0, m = -inf) answers 0 and -inf
     const bool none = m == -INFINITY && l == 0.0f;
+    float *lse = SPLIT ? p.lse_partial + static_cast<long long>(part) * p.heads * p.q_tokens : p.lse;
     if (valid)
-        p.lse[static_cast<long long>(head) * p.q_tokens + token] =
+        lse[static_cast<long long>(head) * p.q_tokens + token] =
             none ? -INFINITY : (__fmul_rn(m, c) + log2f(l)) * 0.6931471805599453f;
+    uint16_t *out = static_cast<uint16_t *>(p.o) + first * p.ld_o + static_cast<long long>(head) * p.dim;
     if (range.hi > range.lo) {
         if (!wait_bar(B.o_full0 + 8u * t, items & 1u, ctl)) return false;
         ++items;
         tc_fence_after();
-        store_rows<BF16>(o_col, 0, p.dim, none ? 0.0f : 1.0f / l, out, p.ld_o, at.ql - (i & ~31));
+        const float f = none ? 0.0f : 1.0f / l;
+        const int rows = at.ql - (i & ~31);
+        if (SPLIT)
+            store_rows_f32(o_col, 0, p.dim, f, p.q_partial + (static_cast<long long>(part) * p.q_tokens + first) * width + static_cast<long long>(head) * p.dim, width, rows);
+        else
+            store_rows<BF16>(o_col, 0, p.dim, f, out, p.ld_o, rows);
         warp_arrive(B.o_empty0 + 8u * t);
-    } else if (valid) {
+    } else if (valid && !SPLIT) {
         zero_row(out + (threadIdx.x & 31) * p.ld_o, 0, p.dim);
     }
     return true;
 }
 
-template <bool BF16, int SLICES>
+template <bool BF16, int SLICES, bool SPLIT>
 __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_constant__ CatParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -212,7 +231,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_
     const uint32_t tmem = *tmem_slot;
     const Ctl ctl{abort_flag, p.status};
     if (warp == kWarpItems) {
-        run_items(p, I, ctl, 2 * CAT_TILE, false, p.heads);
+        run_items(p, I, ctl, 2 * CAT_TILE, false, p.heads * p.q_splits);
     } else if (warp == kWarpLoad) {
         const bool leader = elect_one_sync();
         Item item;
@@ -221,14 +240,14 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_
         uint32_t parity = 0;
         bool ok = true;
         for (int n = 0; ok && next_item(I, ctl, n, item); ++n) {
-            const Steps st(p, item.at);
+            const Steps<SPLIT> st(p, item);
             auto load_q = [&](int t) {
                 if (st.tile[t].hi <= st.tile[t].lo) return true;
                 if (!wait_bar(B.q_empty0 + 8u * t, (q_loads[t] & 1u) ^ 1u, ctl)) return false;
                 if (leader) {
                     slot_parity[kStages + t] = (q_loads[t] & 1u) | 2u;
                     mbar_arrive_expect_tx(B.q_full0 + 8u * t, tile_bytes);
-                    load_tile(q_smem + t * tile_bytes, p.tmQ, B.q_full0 + 8u * t, SLICES, item.head, item.at.q0 + st.i0 + t * CAT_TILE);
+                    load_tile(q_smem + t * tile_bytes, p.tmQ, B.q_full0 + 8u * t, SLICES, st.head, item.at.q0 + st.i0 + t * CAT_TILE);
                 }
                 __syncwarp();
                 ++q_loads[t];
@@ -243,7 +262,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_
                 if (leader) {
                     slot_parity[stage] = parity | 2u;
                     mbar_arrive_expect_tx(B.full0 + 8u * stage, tile_bytes);
-                    load_tile(ring + stage * tile_bytes, k & 1 ? p.tmV : p.tmK, B.full0 + 8u * stage, SLICES, item.head / p.group,
+                    load_tile(ring + stage * tile_bytes, k & 1 ? p.tmV : p.tmK, B.full0 + 8u * stage, SLICES, st.head / p.group,
                               item.at.k0 + (st.all.lo + k / 2) * CAT_TILE);
                 }
                 __syncwarp();
@@ -269,7 +288,7 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_
         bool ok = true;
         Item item;
         for (int n = 0; ok && next_item(I, ctl, n, item); ++n) {
-            const Steps st(p, item.at);
+            const Steps<SPLIT> st(p, item);
             const int lo = st.all.lo, steps = uniform(st.all.hi - lo), kl = uniform(item.at.kl - lo * CAT_TILE);
             if (steps <= 0) continue;
             // each tile's steps [first, end), counted from lo
@@ -338,9 +357,10 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_
         uint32_t steps = 0, items = 0;
         Item item;
         for (int n = 0; next_item(I, ctl, n, item); ++n) {
-            const Steps st(p, item.at);
+            const Steps<SPLIT> st(p, item);
             if (st.i0 + t * CAT_TILE < item.at.ql &&
-                !run_softmax<BF16>(p, B, ctl, tmem, item.at, item.head, st.i0 + t * CAT_TILE, t, t ? st.tile[1] : st.tile[0], steps, items))
+                !run_softmax<BF16, SPLIT>(p, B, ctl, tmem, item.at, st.head, st.part, st.i0 + t * CAT_TILE, t, t ? st.tile[1] : st.tile[0], steps,
+                                   items))
                 break;
         }
     }
@@ -362,26 +382,83 @@ __global__ void __launch_bounds__(CAT_THREADS, 1) attention_kernel(const __grid_
     }
 }
 
+// o and lse of 16 queries and a head from their parts': lse = log sum exp(lse_s),
+// o = sum exp(lse_s - lse) o_s.  A part that saw nothing (-inf) has left its o
+// unwritten: it is loaded, so that all loads are in flight together, and not used.
+template <bool BF16>
+__global__ void __launch_bounds__(128) attention_join_kernel(const __grid_constant__ CatParams p)
+{
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int head = static_cast<int>(blockIdx.x % p.heads);
+    const Place at = find_tile(p, blockIdx.x / p.heads, CAT_JOIN_ROWS, false);
+    if (at.tile < 0) return;
+    const int rows = min(CAT_JOIN_ROWS, at.ql - at.tile * CAT_JOIN_ROWS), vecs = p.dim / 4;
+    const long long width = static_cast<long long>(p.heads) * p.dim, part = p.q_tokens * width, lse_part = static_cast<long long>(p.heads) * p.q_tokens;
+    for (int i = threadIdx.x; i < rows * vecs; i += 128) {
+        const int r = i / vecs, c = (i - r * vecs) * 4;
+        const long long token = at.q0 + at.tile * CAT_JOIN_ROWS + r;
+        const float *lse = p.lse_partial + static_cast<long long>(head) * p.q_tokens + token;
+        const float *src = p.q_partial + token * width + static_cast<long long>(head) * p.dim + c;
+        float top = -INFINITY;
+#pragma unroll 8
+        for (int s = 0; s < p.q_splits; ++s) top = fmaxf(top, __ldg(lse + s * lse_part));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float total = 0.0f;
+#pragma unroll 4
+        for (int s = 0; s < p.q_splits; ++s) {
+            const float l = __ldg(lse + s * lse_part);
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(src + s * part));
+            const bool seen = l != -INFINITY;
+            const float w = expf(l - ref);
+            total += w;
+            v.x = seen ? fmaf(w, u.x, v.x) : v.x;
+            v.y = seen ? fmaf(w, u.y, v.y) : v.y;
+            v.z = seen ? fmaf(w, u.z, v.z) : v.z;
+            v.w = seen ? fmaf(w, u.w, v.w) : v.w;
+        }
+        const float f = total == 0.0f ? 0.0f : 1.0f / total;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + token * p.ld_o + static_cast<long long>(head) * p.dim + c) =
+            make_uint2(round2<BF16>(v.x * f, v.y * f), round2<BF16>(v.z * f, v.w * f));
+        if (c == 0) p.lse[static_cast<long long>(head) * p.q_tokens + token] = total == 0.0f ? -INFINITY : top + logf(total);
+    }
+}
+
 }  // namespace
 }  // namespace cdg
 
 size_t cat_smem_forward(int slices) { return 1024 + (2 + cdg::kStages) * cdg::kSliceBytes * slices + cdg::kItemBytes + 256; }
 
-cudaError_t cat_launch_forward(const CatParams &p, int bf16, long long items, cudaStream_t s)
+namespace {
+typedef void (*Kernel)(CatParams);
+template <int SLICES, bool SPLIT>
+Kernel forward_kernel(int bf16) { return bf16 ? cdg::attention_kernel<true, SLICES, SPLIT> : cdg::attention_kernel<false, SLICES, SPLIT>; }
+Kernel forward_kernel(int slices, int bf16, int split)
+{
+    return slices == 2 ? (split ? forward_kernel<2, true>(bf16) : forward_kernel<2, false>(bf16))
+                       : (split ? forward_kernel<1, true>(bf16) : forward_kernel<1, false>(bf16));
+}
+}  // namespace
+
+cudaError_t cat_launch_forward(const CatParams &p, int bf16, long long items, long long join_items, cudaStream_t s)
 {
     using namespace cdg;
-    const dim3 grid(static_cast<unsigned>(items)), block(CAT_THREADS);
+    const dim3 grid(static_cast<unsigned>(items * p.q_splits)), block(CAT_THREADS);
     const int smem = static_cast<int>(cat_smem_forward(p.slices));
-    void (*k)(CatParams) = p.slices == 2 ? (bf16 ? attention_kernel<true, 2> : attention_kernel<false, 2>)
-                                         : (bf16 ? attention_kernel<true, 1> : attention_kernel<false, 1>);
-    return launch_early(k, grid, block, smem, s, p);
+    void (*k)(CatParams) = forward_kernel(p.slices, bf16, p.q_splits > 1);
+    const cudaError_t e = launch_early(k, grid, block, smem, s, p);
+    if (e != cudaSuccess || p.q_splits == 1) return e;
+    const dim3 tiles(static_cast<unsigned>(join_items));
+    return bf16 ? launch_early(attention_join_kernel<true>, tiles, dim3(128), 0, s, p)
+                : launch_early(attention_join_kernel<false>, tiles, dim3(128), 0, s, p);
 }
 
 cudaError_t cat_prepare_forward()
 {
-    for (auto *k : {cdg::attention_kernel<true, 1>, cdg::attention_kernel<false, 1>, cdg::attention_kernel<true, 2>,
-                    cdg::attention_kernel<false, 2>}) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, CDG_MAX_DYN_SMEM);
+    for (int i = 0; i < 8; ++i) {
+        const cudaError_t e = cudaFuncSetAttribute(forward_kernel(1 + (i & 1), i >> 1 & 1, i >> 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   CDG_MAX_DYN_SMEM);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
