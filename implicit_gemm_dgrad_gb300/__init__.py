@@ -1063,6 +1063,12 @@ def _check_workspace(t, known: dict, need, *sizes) -> None:
 def _offsets(q_offsets, k_offsets, sequences) -> tuple:
     """Addresses of two offset lists, bytes per number, and the number of
     sequences (of raw addresses, which hold int64 numbers: as given, or one)."""
+    if type(q_offsets) is _tensor and type(k_offsets) is _tensor and sequences is None and q_offsets.dtype is k_offsets.dtype:
+        n = q_offsets.nbytes
+        size = _SIZES.get(_type_names.get(q_offsets.dtype)) if n > 0 else None
+        if size and k_offsets.nbytes >= n and not q_offsets.is_floating_point() and q_offsets.is_contiguous() and \
+                k_offsets.is_contiguous() and q_offsets.get_device() == k_offsets.get_device() == _cuda_device():
+            return q_offsets.data_ptr(), k_offsets.data_ptr(), size, n // size - 1  # as below
     n = sequences
     for t in (q_offsets, k_offsets):
         if n is None and t is not None and not isinstance(t, int):

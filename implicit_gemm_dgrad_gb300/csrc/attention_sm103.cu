@@ -122,27 +122,31 @@ __device__ __forceinline__ bool run_softmax(const CatParams &p, const FwdBars &B
             const f32x2 shift = pack2(-mc, -mc);
             float mx[2] = {-INFINITY, -INFINITY};
             sum[0] = sum[1] = pack2(0.0f, 0.0f);
-            float s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld_32(s_col + 32u * q, s[q]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_wait(s[q]);
-            if (!whole) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) hide(s[q], lo - 32 * q, hi - 32 * q);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
+            auto exponentials = [&](float(&v)[32], int q) {
+                if (!whole) hide(v, lo - 32 * q, hi - 32 * q);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], s[q][e], s[q][e + 1]);
+                    mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v[e], v[e + 1]);
                     float a, b;
-                    unpack2(fma2(pack2(s[q][e], s[q][e + 1]), c2, shift), a, b);
+                    unpack2(fma2(pack2(v[e], v[e + 1]), c2, shift), a, b);
                     a = exp2_approx(a);
                     b = exp2_approx(b);
                     sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(a, b));
                     w[q][e / 2] = round2<BF16>(a, b);
                 }
+            };
+            // (the last quarter is loaded into the first one's registers)
+            float s[3][32];
+#pragma unroll
+            for (int q = 0; q < 3; ++q) tmem_ld_32(s_col + 32u * q, s[q]);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) tmem_wait(s[q]);
+            exponentials(s[0], 0);
+            tmem_ld_32(s_col + 96u, s[0]);
+            exponentials(s[1], 1);
+            exponentials(s[2], 2);
+            tmem_wait(s[0]);
+            exponentials(s[0], 3);
             const float top = fmaxf(mx[0], mx[1]);
             const bool grow = (top - m) * c > 8.0f;  // (false where both are -inf)
             if (!__any_sync(0xFFFFFFFFu, grow)) break;
