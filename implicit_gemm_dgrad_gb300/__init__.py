@@ -1065,9 +1065,9 @@ def _offsets(q_offsets, k_offsets, sequences) -> tuple:
     sequences (of raw addresses, which hold int64 numbers: as given, or one)."""
     if type(q_offsets) is _tensor and type(k_offsets) is _tensor and sequences is None and q_offsets.dtype is k_offsets.dtype:
         n = q_offsets.nbytes
-        size = _SIZES.get(_type_names.get(q_offsets.dtype)) if n > 0 else None
-        if size and k_offsets.nbytes >= n and not q_offsets.is_floating_point() and q_offsets.is_contiguous() and \
-                k_offsets.is_contiguous() and q_offsets.get_device() == k_offsets.get_device() == _cuda_device():
+        size = {"int32": 4, "int64": 8}.get(_type_names.get(q_offsets.dtype), 0)
+        if size and n > 0 and k_offsets.nbytes >= n and q_offsets.is_contiguous() and k_offsets.is_contiguous() and \
+                q_offsets.get_device() == k_offsets.get_device() == _cuda_device():
             return q_offsets.data_ptr(), k_offsets.data_ptr(), size, n // size - 1  # as below
     n = sequences
     for t in (q_offsets, k_offsets):

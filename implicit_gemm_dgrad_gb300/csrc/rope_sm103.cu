@@ -55,6 +55,7 @@ int check_rows(const Rows &r)
 {
     if (r.rows == 0 || r.width == 0) return CDG_OK;
     if (!r.p || r.ld < r.width) return CDG_ERR_INVALID_ARG;
+    if (r.ld >= (1ll << 31)) return CDG_ERR_UNSUPPORTED;
     return aligned_to(r.p, r.esize) ? CDG_OK : CDG_ERR_ALIGNMENT;
 }
 

@@ -725,10 +725,12 @@ int cdg_attention_device_status(cdg_attention_t h, cdg_stream_t stream);
  * turned back: dw = sum over tokens and heads of dz n, dn = dz w,
  * dx = (dn - n mean(dn n)) / sqrt(mean(x^2) + eps); dx = dz without the norm.
  *
- * Matrices are dtype (CDG_F16, CDG_BF16, CDG_F32) with row strides ld_*, aligned
- * to the element; inv_freq, w_q, w_k, dw_q and dw_k are fp32.  Computed in
- * fp32, rounded once; angles are reduced exactly at any position.  Repeated
- * calls give the same bits.
+ * Matrices are dtype (CDG_F16, CDG_BF16, CDG_F32) with row strides ld_* (below
+ * 2^31), aligned to the element; inv_freq, w_q, w_k, dw_q and dw_k are fp32.
+ * Computed in fp32 (a head's sum of squares has to be representable), rounded
+ * once; a frequency is held to 2^-64 of a turn, so that angles are as exact as
+ * fp32 holds them at positions up to 2^38.  16-bit results use cosines and sines
+ * good to 2^-20.  Repeated calls give the same bits.
  *   heads, kv_heads   either may be 0 (that side's pointers are not used)
  *   dim        at most 256;  rot even, 0 .. dim (0: no rotation, inv_freq may be NULL)
  *   positions  int32 or int64 (index_bytes 4, 8), any value; NULL: the token's number

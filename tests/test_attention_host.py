@@ -106,7 +106,7 @@ ROPE = [
     (dict(factor=math.nan), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=math.inf), INVALID),
     (dict(inv_freq=None), INVALID), (dict(norm=False), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
     (dict(ld_q=255), INVALID), (dict(ld_k=100), INVALID), (dict(dim=258), UNSUPPORTED), (dict(tokens=1 << 31), UNSUPPORTED),
-    (dict(heads=70000), UNSUPPORTED), (dict(q=P[0] + 1), ALIGNMENT), (dict(positions=P[2] + 4), ALIGNMENT),
+    (dict(heads=70000), UNSUPPORTED), (dict(ld_q=1 << 31), UNSUPPORTED), (dict(q=P[0] + 1), ALIGNMENT), (dict(positions=P[2] + 4), ALIGNMENT),
     (dict(inv_freq=P[3] + 2), ALIGNMENT), (dict(w_q=P[6] + 1), ALIGNMENT)]
 
 
