@@ -29,35 +29,43 @@ constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpStats = 18;
 constexpr int kSlots = 2;  // steps of each streamed operand in shared memory
 
 // (- lse log2 e, D) of every row and head; a row that saw nothing (lse = -inf)
-// gets -inf there, so that every p of it is 0.  16 lanes a row.
+// gets -inf there, so that every p of it is 0.  16 lanes take kStatRows tokens of
+// a head, all of whose loads are in flight together.
+constexpr int kStatRows = 4;
 template <bool BF16>
 __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_constant__ CatParams p)
 {
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     grid_dep_launch_dependents();
     grid_dep_wait();
     const long long g = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 16;
     const int lane = threadIdx.x & 15;
-    const long long token = g / p.heads;
-    const int head = static_cast<int>(g - token * p.heads);
-    float sum = 0.0f;
-    if (token < p.q_tokens) {
-        const uint4 *a = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.d_o) + token * p.ld_do + static_cast<long long>(head) * p.dim);
-        const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o_in) + token * p.ld_oi + static_cast<long long>(head) * p.dim);
-        if (8 * lane < p.dim) {
-            using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-            float x[8], y[8];
-            widen_vec<T>(__ldg(a + lane), x);
-            widen_vec<T>(__ldg(b + lane), y);
+    const long long block = g / p.heads, token = block * kStatRows;
+    const int head = static_cast<int>(g - block * p.heads);
+    const long long col = static_cast<long long>(head) * p.dim + 8 * lane;
+    uint4 a[kStatRows], b[kStatRows];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
-        }
+    for (int r = 0; r < kStatRows; ++r) {
+        const bool in = token + r < p.q_tokens && 8 * lane < p.dim;
+        a[r] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.d_o) + (token + r) * p.ld_do + col)) : make_uint4(0, 0, 0, 0);
+        b[r] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o_in) + (token + r) * p.ld_oi + col)) : make_uint4(0, 0, 0, 0);
     }
+    float mine = 0.0f;  // lane r: row r's sum
 #pragma unroll
-    for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (lane == 0 && token < p.q_tokens) {
-        const long long at = static_cast<long long>(head) * p.q_tokens + token;
+    for (int r = 0; r < kStatRows; ++r) {
+        float x[8], y[8], sum = 0.0f;
+        widen_vec<T>(a[r], x);
+        widen_vec<T>(b[r], y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+#pragma unroll
+        for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if (lane == r) mine = sum;
+    }
+    if (lane < kStatRows && token + lane < p.q_tokens) {
+        const long long at = static_cast<long long>(head) * p.q_tokens + token + lane;
         const float lse = p.lse_in[at];
-        p.stats[at] = make_float2(lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f, sum);
+        p.stats[at] = make_float2(lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f, mine);
     }
 }
 
@@ -719,8 +727,8 @@ Kernel dq_kernel(int slices, int bf16, int split)
 cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
 {
     using namespace cdg;
-    const long long rows = static_cast<long long>(p.q_tokens) * p.heads;
-    const dim3 grid(static_cast<unsigned>((rows + 15) / 16)), block(256);
+    const long long groups = (p.q_tokens + kStatRows - 1ll) / kStatRows * p.heads;
+    const dim3 grid(static_cast<unsigned>((groups + 15) / 16)), block(256);
     return bf16 ? launch_early(attention_stats_kernel<true>, grid, block, 0, s, p)
                 : launch_early(attention_stats_kernel<false>, grid, block, 0, s, p);
 }
