@@ -189,11 +189,19 @@ struct Place {
     int q0, ql, k0, kl;  // first row and length of the queries and of the keys
     int tile;            // of this sequence; -1: no such tile
 };
-__device__ __forceinline__ Place find_tile(const CatParams &p, long long item, int rows, bool of_keys)
+// Where the search for a tile left off: items of one CTA come in ascending order,
+// and the next one's search goes on there (a search from the first one would read all
+// offsets before it for every item).
+struct Scan {
+    int sequence = 0;
+    long long before = 0;  // tiles of the sequences before it
+};
+__device__ __forceinline__ Place find_tile(const CatParams &p, long long item, int rows, bool of_keys, Scan &scan)
 {
     const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int s0 = 0; s0 < p.sequences; s0 += 32) {
+    if (item < scan.before) scan = Scan{};
+    long long before = scan.before;
+    for (int s0 = scan.sequence; s0 < p.sequences; s0 += 32) {
         const int s = s0 + lane;
         int q0 = 0, ql = 0, k0 = 0, kl = 0;
         if (s < p.sequences) {
@@ -217,12 +225,19 @@ __device__ __forceinline__ Place find_tile(const CatParams &p, long long item, i
             r.ql = __shfl_sync(0xFFFFFFFFu, ql, w);
             r.k0 = __shfl_sync(0xFFFFFFFFu, k0, w);
             r.kl = __shfl_sync(0xFFFFFFFFu, kl, w);
+            scan.sequence = s0;
+            scan.before = before;
             r.tile = static_cast<int>(item - before) - (__shfl_sync(0xFFFFFFFFu, upto, w) - __shfl_sync(0xFFFFFFFFu, n, w));
             return r;
         }
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
     return Place{0, 0, 0, 0, -1};
+}
+__device__ __forceinline__ Place find_tile(const CatParams &p, long long item, int rows, bool of_keys)
+{
+    Scan scan;
+    return find_tile(p, item, rows, of_keys, scan);
 }
 
 // ---------------------------------------------------------------- work items
@@ -248,8 +263,11 @@ __device__ __forceinline__ void run_items(const CatParams &p, const ItemBars &I,
     const int lane = threadIdx.x & 31;
     long long item = blockIdx.x;
     int n = 0;
+    Scan scan;
+    // an item may take longer than a step's wait may; what goes wrong in it ends these waits too
+    ctl.limit = 600000000000ull;
     for (uint32_t asked = 0;; ++asked) {
-        const Place at = find_tile(p, item / heads, rows, of_keys);
+        const Place at = find_tile(p, item / heads, rows, of_keys, scan);
         if (at.tile >= 0) {
             if (!wait_bar(I.empty0 + 8u * (n & 1), ((n >> 1) & 1) ^ 1u, ctl)) return;
             if (lane == 0) {

@@ -3,8 +3,8 @@
 // rope_sm103.cu and rope_grad_sm103.cu).
 //
 // Both read and write every element once and are DRAM-bound.  A warp takes one
-// token's heads of one block (queries or keys, up to kUnroll groups of heads),
-// a group of lanes a head; it keeps its frequencies and weights in registers
+// token's heads of one block (of the queries or of the keys, UNROLL groups of
+// heads at a time), a group of lanes a head; it keeps its frequencies and weights in registers
 // and walks over tokens, and all loads of a token's block are in flight
 // together.  A lane holds, of each vector pair it loads, both values of every
 // rotated pair: vectors i and i + rot / 2 of the half layout, neighbouring
@@ -14,6 +14,10 @@
 // position * frequency, modulo 2^64, is the exact fraction of a turn at any
 // position (in fp32 the product itself is off by 0.06 radians at position 10^6),
 // in integer instructions rather than fp64 ones.
+//
+// Measured (GB300, 32768 tokens, 32 + 8 heads of 128, bf16, with norms): forward 107
+// us, 6.3 TB/s; gradient 168 us, 6.0 TB/s, of which the weights' sums are 4 us.  Copy
+// rate: 6.8 TB/s.
 #pragma once
 
 #include <algorithm>
