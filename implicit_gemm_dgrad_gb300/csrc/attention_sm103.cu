@@ -129,7 +129,6 @@ __device__ __forceinline__ bool run_softmax(const CatParams &p, const FwdBars &B
             float mx[2] = {-INFINITY, -INFINITY};
             sum[0] = sum[1] = pack2(0.0f, 0.0f);
             auto exponentials = [&](float(&v)[32], int q) {
-                if (!whole) hide(v, lo - 32 * q, hi - 32 * q);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v[e], v[e + 1]);
@@ -147,11 +146,16 @@ __device__ __forceinline__ bool run_softmax(const CatParams &p, const FwdBars &B
             for (int q = 0; q < 3; ++q) tmem_ld_32(s_col + 32u * q, s[q]);
 #pragma unroll
             for (int q = 0; q < 3; ++q) tmem_wait(s[q]);
+            if (!whole) {
+#pragma unroll
+                for (int q = 0; q < 3; ++q) hide(s[q], lo - 32 * q, hi - 32 * q);
+            }
             exponentials(s[0], 0);
             tmem_ld_32(s_col + 96u, s[0]);
             exponentials(s[1], 1);
             exponentials(s[2], 2);
             tmem_wait(s[0]);
+            if (!whole) hide(s[0], lo - 96, hi - 96);
             exponentials(s[0], 3);
             const float top = fmaxf(mx[0], mx[1]);
             const bool grow = (top - m) * c > 8.0f;  // (false where both are -inf)
