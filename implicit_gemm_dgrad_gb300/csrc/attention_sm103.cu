@@ -19,7 +19,7 @@
 //
 // Measured (GB300, 8192 causal tokens, 16 heads of 128 over 4, bf16): 189 us, 1450
 // TFLOP/s; packed documents of 1 to 4096 tokens 144 us, 1150; 8192 x 8192 heads of 64
-// 768.  A step of a pair of tiles takes 2.6 thousand cycles, its products
+// 808.  A step of a pair of tiles takes 2.6 thousand cycles, its products
 // 2.05: what bounds it is the chain of one tile, scores -> softmax (1.1 thousand
 // cycles) -> P V -> next scores, which the other tile's products do not quite cover.
 #include "attention_device.cuh"
