@@ -986,8 +986,10 @@ class AttentionPlan:
         if scale is None:
             scale = max(self.dim, 1) ** -0.5
         make = self.lib.cdg_attention_plan_host if host_only else self.lib.cdg_attention_plan
+        # (the C argument is an int: a larger window hides nothing either, and would lose its upper bits)
+        window = max(-1, min(int(window), (1 << 31) - 1))
         h = ctypes.c_void_p()
-        rc = make(self.heads, self.kv_heads, self.dim, _dtype(dtype), int(bool(causal)), int(window), float(scale),
+        rc = make(self.heads, self.kv_heads, self.dim, _dtype(dtype), int(bool(causal)), window, float(scale),
                   ctypes.byref(h))
         if rc != OK:
             raise CdgError(rc, "cdg_attention_plan")

@@ -145,7 +145,9 @@ int common(const cdg_attention_st *h, CatParams &p, long long q_tokens, long lon
     p.slices = (h->dim + 63) / 64;
     p.ksteps = (h->dim + 15) / 16;
     p.causal = h->causal;
-    p.window = h->window;
+    // A window past the call's keys hides none of them: cut there, its sums with rows'
+    // numbers (all below 2^30) stay inside 32 bits.
+    p.window = std::min(h->window, std::max(1, p.k_tokens));
     p.scale = h->scale;
     p.scale_log2 = static_cast<float>(h->scale * 1.4426950408889634);
     // fp32 sums, operands of the type, N, M = 128; B of the second is MN-major (bit 16)

@@ -296,7 +296,7 @@ __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &
         if (++tile == kt.lo + kt.count) tile = kt.lo;
         // columns [lo, hi) of this part see the key
         const bool whole = (!p.causal || kt.j0 + CAT_TILE - 1 <= i0 + off) && (!p.window || kt.j0 > i0 + CAT_TILE - 1 + off - p.window);
-        const int lo = p.causal ? j - off - i0 - 32 * part : 0, hi = p.window ? j - off + p.window - i0 - 32 * part : 32;
+        const int lo = p.causal ? j - off - i0 - 32 * part : 0, hi = p.window ? j - off - i0 - 32 * part + p.window : 32;
         if (!wait_bar(S.B.st_full0 + 8u * slot, (done / kSlots) & 1u, ctl) || !wait_bar(S.B.s_full, done & 1u, ctl)) return false;
         tc_fence_after();
         float s[32];

@@ -687,7 +687,7 @@ int cdg_muon_device_status(cdg_muon_t h, cdg_stream_t stream);
  */
 typedef struct cdg_attention_st *cdg_attention_t;
 
-/* window 0 (none), or > 0 with causal = 1; scale > 0, finite. */
+/* window 0 (none), or > 0 with causal = 1 (one past every key hides nothing); scale > 0, finite. */
 int cdg_attention_plan(int heads, int kv_heads, int dim, int dtype, int causal, int window, float scale,
                        cdg_attention_t *out);
 /* The same without a device: for the checks and sizes. */
