@@ -329,6 +329,8 @@ __global__ void __launch_bounds__(kRopeThreads, !GRAD || !NORM ? 3 : 2) rope_ker
                         if (GRAD) g += __shfl_xor_sync(0xFFFFFFFFu, g, d);
                     }
                 q = rsqrtf(fmaf(q, inv_dim, p.eps));
+                // (a head past the last has x = dz = 0 and, with eps = 0, no finite scale of its own)
+                if (GRAD && !WHOLE && u * groups + group >= left) q = 0.0f;
                 scale = pack2(q, q);
                 if (GRAD) {
                     g = -(q * q * (g * inv_dim));
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kRopeThreads, !GRAD || !NORM ? 3 : 2) rope_ker
                             fa[i][e] = mul2(fa[i][e], mul2(scale, wa[i][e]));
                             fb[i][e] = mul2(fb[i][e], mul2(scale, wb[i][e]));
                         } else {
-                            // (a head past the last has dz = x = 0)
+                            // (a head past the last has dz = x = scale = 0)
                             dwa[i][e] = fma2(ga[i][e], mul2(fa[i][e], scale), dwa[i][e]);
                             dwb[i][e] = fma2(gb[i][e], mul2(fb[i][e], scale), dwb[i][e]);
                             ga[i][e] = mul2(scale, fma2(fa[i][e], back, mul2(ga[i][e], wa[i][e])));
