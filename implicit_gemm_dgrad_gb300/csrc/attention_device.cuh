@@ -264,18 +264,26 @@ struct ItemBars {
 };
 constexpr int kItemBytes = 8 * 6 + 16 + 64;  // barriers, reply, slots
 
+// Waits for the next item, or for one to be taken up, last as long as an item does: millions of
+// steps of a very long sequence, or a list of a million offsets.  What goes wrong
+// inside an item ends these waits too, through the abort flag.
+__device__ __forceinline__ Ctl across_items(Ctl ctl)
+{
+    ctl.limit = 600000000000ull;
+    return ctl;
+}
+
 __device__ __forceinline__ void run_items(const CatParams &p, const ItemBars &I, Ctl ctl, int rows, bool of_keys, int heads)
 {
     const int lane = threadIdx.x & 31;
     long long item = blockIdx.x;
     int n = 0;
     Scan scan;
-    // an item may take longer than a step's wait may; what goes wrong in it ends these waits too
-    ctl.limit = 600000000000ull;
+    const Ctl patient = across_items(ctl);
     for (uint32_t asked = 0;; ++asked) {
         const Place at = find_tile(p, item / heads, rows, of_keys, scan);
         if (at.tile >= 0) {
-            if (!wait_bar(I.empty0 + 8u * (n & 1), ((n >> 1) & 1) ^ 1u, ctl)) return;
+            if (!wait_bar(I.empty0 + 8u * (n & 1), ((n >> 1) & 1) ^ 1u, patient)) return;
             if (lane == 0) {
                 volatile int *v = I.slots + 8 * (n & 1);
                 v[0] = 1; v[1] = static_cast<int>(item % heads);
@@ -283,7 +291,7 @@ __device__ __forceinline__ void run_items(const CatParams &p, const ItemBars &I,
                 mbar_arrive(I.full0 + 8u * (n & 1));
             }
             __syncwarp();
-            if (!wait_bar(I.go, n & 1, ctl)) return;
+            if (!wait_bar(I.go, n & 1, patient)) return;
             ++n;
         }
         if (lane == 0) {
@@ -310,7 +318,7 @@ __device__ __forceinline__ void run_items(const CatParams &p, const ItemBars &I,
         if (!more) break;
         item = x;
     }
-    if (!wait_bar(I.empty0 + 8u * (n & 1), ((n >> 1) & 1) ^ 1u, ctl)) return;
+    if (!wait_bar(I.empty0 + 8u * (n & 1), ((n >> 1) & 1) ^ 1u, patient)) return;
     if (lane == 0) {
         I.slots[8 * (n & 1)] = 0;
         mbar_arrive(I.full0 + 8u * (n & 1));
@@ -320,7 +328,7 @@ __device__ __forceinline__ void run_items(const CatParams &p, const ItemBars &I,
 // The n-th item, for one of the warps that work on items; false after the last.
 __device__ __forceinline__ bool next_item(const ItemBars &I, Ctl ctl, int n, Item &item)
 {
-    if (!wait_bar(I.full0 + 8u * (n & 1), (n >> 1) & 1, ctl)) return false;
+    if (!wait_bar(I.full0 + 8u * (n & 1), (n >> 1) & 1, across_items(ctl))) return false;
     volatile int *v = I.slots + 8 * (n & 1);
     const int some = v[0];
     item.head = v[1];
