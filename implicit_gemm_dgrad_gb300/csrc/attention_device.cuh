@@ -43,6 +43,33 @@ __device__ __forceinline__ uint32_t round2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Loads of what an overlapping launch writes (statistics, parts, the forward's o and
+// lse): past L1, and kept behind this kernel's wait, which read-only loads are not.
+__device__ __forceinline__ float ld_written(const float *p)
+{
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_written(const float2 *p)
+{
+    float2 v;
+    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_written(const float4 *p)
+{
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_written(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 // 32 TMEM lanes x 32 columns into registers; the values are there after tmem_wait.
 __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, float (&r)[32])
 {

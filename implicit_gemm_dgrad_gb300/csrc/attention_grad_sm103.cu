@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_const
 #pragma unroll
     for (int r = 0; r < kStatRows; ++r) {
         const bool in = token + r < p.q_tokens && 8 * lane < p.dim;
-        a[r] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.d_o) + (token + r) * p.ld_do + col)) : make_uint4(0, 0, 0, 0);
-        b[r] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o_in) + (token + r) * p.ld_oi + col)) : make_uint4(0, 0, 0, 0);
+        a[r] = in ? ld_written(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.d_o) + (token + r) * p.ld_do + col)) : make_uint4(0, 0, 0, 0);
+        b[r] = in ? ld_written(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o_in) + (token + r) * p.ld_oi + col)) : make_uint4(0, 0, 0, 0);
     }
     float mine = 0.0f;  // lane r: row r's sum
 #pragma unroll
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_const
     }
     if (lane < kStatRows && token + lane < p.q_tokens) {
         const long long at = static_cast<long long>(head) * p.q_tokens + token + lane;
-        const float lse = p.lse_in[at];
+        const float lse = ld_written(p.lse_in + at);
         p.stats[at] = make_float2(lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f, mine);
     }
 }
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = 32 * e + lane, i = tile * CAT_TILE + c;
-                    const float2 v = i < item.at.ql ? __ldg(src + i) : make_float2(-INFINITY, 0.0f);
+                    const float2 v = i < item.at.ql ? ld_written(src + i) : make_float2(-INFINITY, 0.0f);
                     st_shared_f32(S.stats + (slot * 2 * CAT_TILE + c) * 4u, v.x);
                     st_shared_f32(S.stats + ((slot * 2 + 1) * CAT_TILE + c) * 4u, v.y);
                 }
@@ -513,7 +513,7 @@ __device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S
     const int r_first = i0 + at.kl - at.ql, r = r_first + row;
     const long long token = at.q0 + i;
     const bool valid = i < at.ql;
-    const float2 st = valid ? __ldg(p.stats + static_cast<long long>(head) * p.q_tokens + token) : make_float2(-INFINITY, 0.0f);
+    const float2 st = valid ? ld_written(p.stats + static_cast<long long>(head) * p.q_tokens + token) : make_float2(-INFINITY, 0.0f);
     const f32x2 shift = pack2(st.x, st.x), minus_d = pack2(-st.y, -st.y);
     for (int j = lo; j < hi; ++j, ++done) {
         const int k0 = j * CAT_TILE;
@@ -673,7 +673,7 @@ __device__ __forceinline__ void join_rows(const float *src, long long width, lon
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
         for (int s = 0; s < parts; ++s) {
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(src + s * part + r * width + c));
+            const float4 u = ld_written(reinterpret_cast<const float4 *>(src + s * part + r * width + c));
             v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
         }
         *reinterpret_cast<uint2 *>(out + r * ld + c) = make_uint2(round2<BF16>(v.x * f, v.y * f), round2<BF16>(v.z * f, v.w * f));

@@ -416,14 +416,14 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
         const float *src = p.q_partial + token * width + static_cast<long long>(head) * p.dim + c;
         float top = -INFINITY;
 #pragma unroll 8
-        for (int s = 0; s < p.q_splits; ++s) top = fmaxf(top, __ldg(lse + s * lse_part));
+        for (int s = 0; s < p.q_splits; ++s) top = fmaxf(top, ld_written(lse + s * lse_part));
         const float ref = top == -INFINITY ? 0.0f : top;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float total = 0.0f;
 #pragma unroll 4
         for (int s = 0; s < p.q_splits; ++s) {
-            const float l = __ldg(lse + s * lse_part);
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(src + s * part));
+            const float l = ld_written(lse + s * lse_part);
+            const float4 u = ld_written(reinterpret_cast<const float4 *>(src + s * part));
             const bool seen = l != -INFINITY;
             const float w = expf(l - ref);
             total += w;
