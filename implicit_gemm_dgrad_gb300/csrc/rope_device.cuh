@@ -222,6 +222,9 @@ __global__ void __launch_bounds__(kRopeThreads, !GRAD || !NORM ? 3 : 2) rope_ker
     int at_a[R], at_b[R];
     bool has_a[R], has_b[R], turned[R];
     uint64_t freq[R][V];
+    // An infinite or NaN frequency is no number of turns, and its angles are NaN: carried by the
+    // factor, that reaches all of this lane's pairs (a check of every pair of every token cost 3 %).
+    float factor = p.factor;
     f32x2 wa[R][N], wb[R][N], dwa[R][N], dwb[R][N];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -235,7 +238,9 @@ __global__ void __launch_bounds__(kRopeThreads, !GRAD || !NORM ? 3 : 2) rope_ker
         for (int e = 0; e < V; ++e) {
             // rotated pairs' numbers: those of the vector pair; past the rotated part the angle is 0
             const int k = interleaved ? v.a / 2 + e : v.a + e;
-            freq[i][e] = turned[i] && 2 * k < p.rot ? turns_of(__ldg(p.inv_freq + k)) : 0;
+            const float f = turned[i] && 2 * k < p.rot ? __ldg(p.inv_freq + k) : 0.0f;
+            freq[i][e] = turns_of(f);
+            if (!isfinite(f)) factor = __int_as_float(0x7FC00000);
         }
 #pragma unroll
         for (int e = 0; e < N; ++e) {
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(kRopeThreads, !GRAD || !NORM ? 3 : 2) rope_ker
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const int k = interleaved ? at_a[i] / 2 + e : at_a[i] + e;
-                    if (all_turned || (turned[i] && 2 * k < p.rot)) cos_sin<T>(pos * freq[i][e], p.factor, c[i][e], s[i][e]);
+                    if (all_turned || (turned[i] && 2 * k < p.rot)) cos_sin<T>(pos * freq[i][e], factor, c[i][e], s[i][e]);
                     else c[i][e] = 1.0f, s[i][e] = 0.0f;
                     if (GRAD) s[i][e] = -s[i][e];  // back
                 }

@@ -729,7 +729,8 @@ int cdg_attention_device_status(cdg_attention_t h, cdg_stream_t stream);
  * 2^31), aligned to the element; inv_freq, w_q, w_k, dw_q and dw_k are fp32.
  * Computed in fp32 (a head's sum of squares has to be representable), rounded
  * once; a frequency is held to 2^-64 of a turn, so that angles are as exact as
- * fp32 holds them at positions up to 2^38.  16-bit results use cosines and sines
+ * fp32 holds them at positions up to 2^38.  An infinite or NaN frequency makes its
+ * pairs NaN, and may others of the rotated part.  16-bit results use cosines and sines
  * good to 2^-20.  Repeated calls give the same bits.
  *   heads, kv_heads   either may be 0 (that side's pointers are not used)
  *   dim        at most 256;  rot even, 0 .. dim (0: no rotation, inv_freq may be NULL)
