@@ -197,15 +197,19 @@ struct Workspace {
     }
 };
 
-// The gradient's: the rows' statistics, then the sums of the parts of dq, and of dk and dv.
+// The gradient's: the rows' statistics, fp16's sizes, then the sums of the parts of dq, and of dk and dv.
 struct GradWorkspace {
     int q_parts, k_parts;
-    size_t dq, dkv, bytes;
+    long long stat_ctas, size_ctas;
+    size_t sizes, dq, dkv, bytes;
     GradWorkspace(const cdg_attention_st *h, long long q_tokens, long long k_tokens, int sequences)
     {
         q_parts = parts_of(items(q_tokens, sequences, CAT_TILE, h->heads), steps_of(h, k_tokens, sequences), h->sms);
         k_parts = parts_of(items(k_tokens, sequences, CAT_TILE, h->kv_heads), h->heads / h->kv_heads * steps_of(h, q_tokens, sequences), h->sms);
-        dq = up256(static_cast<size_t>(q_tokens) * h->heads * sizeof(float2));
+        sizes = up256(static_cast<size_t>(q_tokens) * h->heads * sizeof(float2));
+        stat_ctas = cat_stat_ctas(q_tokens, h->heads, h->dtype == CDG_BF16);
+        size_ctas = h->dtype == CDG_F16 ? cat_stat_ctas(k_tokens, h->kv_heads, 0) : 0;
+        dq = sizes + (h->dtype == CDG_F16 ? up256(static_cast<size_t>(stat_ctas + size_ctas) * sizeof(uint4)) : 0);
         dkv = dq + (q_parts > 1 ? up256(static_cast<size_t>(q_parts) * q_tokens * h->heads * h->dim * 4) : 0);
         bytes = dkv + (k_parts > 1 ? up256(2ull * k_parts * k_tokens * h->kv_heads * h->dim * 4) : 0);
         bytes = std::max<size_t>(256, bytes);
@@ -335,6 +339,10 @@ int cdg_attention_grad(cdg_attention_t h, const void *q, long long ld_q, const v
     p.lse_in = lse;
     const GradWorkspace ws(h, q_tokens, k_tokens, sequences);
     p.stats = static_cast<float2 *>(workspace);
+    p.v_in = v; p.ld_v = ld_v;
+    p.sizes = reinterpret_cast<uint4 *>(static_cast<char *>(workspace) + ws.sizes);
+    p.stat_ctas = static_cast<int>(ws.stat_ctas);
+    p.size_ctas = static_cast<int>(ws.size_ctas);
     p.q_splits = ws.q_parts;
     p.k_splits = ws.k_parts;
     p.q_partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.dq);

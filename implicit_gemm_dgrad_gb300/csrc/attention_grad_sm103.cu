@@ -13,7 +13,8 @@
 // For dk and dv the scores are computed transposed (a thread a key, columns
 // queries), so that P^T and dS^T lie as those products need them.
 //
-// p and ds are rounded to 16 bits as operands of the products that sum them.
+// p and ds are rounded to 16 bits as operands of the products that sum them; fp16's
+// at a power of two times their value (DsScale).
 //
 // Each kernel's warps (640 threads): 0-15 compute (128 rows x 32 columns a
 // warpgroup), 16 loads by TMA, 17 issues MMAs, 18 fetches the queries'
@@ -27,6 +28,8 @@
 // documents 452 us.  A step's phases wait for one another: scores complete, p of all
 // sixteen warps 1.4 thousand cycles, two products 1.3.  Eight warps of 64 columns
 // took 725 us where sixteen of 32 took 663.
+#include <algorithm>
+
 #include "attention_device.cuh"
 
 namespace cdg {
@@ -38,43 +41,132 @@ constexpr int kSlots = 2;  // steps of each streamed operand in shared memory
 // (- lse log2 e, D) of every row and head; a row that saw nothing (lse = -inf)
 // gets -inf there, so that every p of it is 0.  16 lanes take kStatRows tokens of
 // a head, all of whose loads are in flight together.
+//
+// fp16: the largest sizes beside them (CatParams::sizes), and those of v's rows by CTAs of their
+// own, from which dS's power of two comes (DsScale).  Rows that are not finite, or in
+// no sequence, have none.
 constexpr int kStatRows = 4;
+constexpr int kStatThreads = 256, kStatGroups = kStatThreads / 16;
+constexpr int kSizeCtas = 304;  // fp16, of each side: two on each of 152 SMs
+
+__device__ __forceinline__ uint32_t finite_size(float v) { return isfinite(v) ? __float_as_uint(fabsf(v)) : 0u; }
+__device__ __forceinline__ uint4 larger(uint4 a, uint4 b) { return make_uint4(max(a.x, b.x), max(a.y, b.y), max(a.z, b.z), 0u); }
+// (sizes are not negative: their bits compare as they do)
+__device__ __forceinline__ uint4 warp_largest(uint4 v)
+{
+    return make_uint4(__reduce_max_sync(0xFFFFFFFFu, v.x), __reduce_max_sync(0xFFFFFFFFu, v.y), __reduce_max_sync(0xFFFFFFFFu, v.z), 0u);
+}
+
+// The sum over 16 lanes of 8 products each.
+__device__ __forceinline__ float dot16(const float (&x)[8], const float (&y)[8])
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+#pragma unroll
+    for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    return sum;
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_constant__ CatParams p)
+__global__ void __launch_bounds__(kStatThreads) attention_stats_kernel(const __grid_constant__ CatParams p)
 {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     grid_dep_launch_dependents();
     grid_dep_wait();
-    const long long g = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 16;
-    const int lane = threadIdx.x & 15;
-    const long long block = g / p.heads, token = block * kStatRows;
-    const int head = static_cast<int>(g - block * p.heads);
-    const long long col = static_cast<long long>(head) * p.dim + 8 * lane;
-    uint4 a[kStatRows], b[kStatRows];
-#pragma unroll
-    for (int r = 0; r < kStatRows; ++r) {
-        const bool in = token + r < p.q_tokens && 8 * lane < p.dim;
-        a[r] = in ? ld_written(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.d_o) + (token + r) * p.ld_do + col)) : make_uint4(0, 0, 0, 0);
-        b[r] = in ? ld_written(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o_in) + (token + r) * p.ld_oi + col)) : make_uint4(0, 0, 0, 0);
+    const bool of_v = !BF16 && static_cast<int>(blockIdx.x) >= p.stat_ctas;
+    const int cta = of_v ? blockIdx.x - p.stat_ctas : blockIdx.x, ctas = of_v ? p.size_ctas : p.stat_ctas;
+    const int tokens = of_v ? p.k_tokens : p.q_tokens, heads = of_v ? p.kv_heads : p.heads, lane = threadIdx.x & 15;
+    int lo = 0, hi = 0;  // the rows that sequences hold
+    if (!BF16) {
+        const void *offsets = of_v ? p.k_offsets : p.q_offsets;
+        lo = offset_at(offsets, p.index_bytes, 0, tokens);
+        hi = offset_at(offsets, p.index_bytes, p.sequences, tokens);
     }
-    float mine = 0.0f;  // lane r: row r's sum
+    uint4 top = make_uint4(0, 0, 0, 0);
+    const long long groups = (tokens + kStatRows - 1ll) / kStatRows * heads;
+    // (a warp's two groups go round together)
+    for (long long g0 = static_cast<long long>(cta) * kStatGroups + threadIdx.x / 32 * 2; g0 < groups; g0 += static_cast<long long>(ctas) * kStatGroups) {
+        const long long g = g0 + ((threadIdx.x >> 4) & 1), block = g / heads, token = block * kStatRows;
+        const int head = static_cast<int>(g - block * heads);
+        const long long col = static_cast<long long>(head) * p.dim + 8 * lane;
+        uint4 a[kStatRows], b[kStatRows];
+        float x[8], y[8];
+        if (of_v) {
 #pragma unroll
-    for (int r = 0; r < kStatRows; ++r) {
-        float x[8], y[8], sum = 0.0f;
-        widen_vec<T>(a[r], x);
-        widen_vec<T>(b[r], y);
+            for (int r = 0; r < kStatRows; ++r)
+                a[r] = token + r >= lo && token + r < hi && 8 * lane < p.dim
+                           ? ld_written(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v_in) + (token + r) * p.ld_v + col))
+                           : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+            for (int r = 0; r < kStatRows; ++r) {
+                widen_vec<T>(a[r], x);
+                top.y = max(top.y, finite_size(dot16(x, x)));
+            }
+            continue;
+        }
 #pragma unroll
-        for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (lane == r) mine = sum;
+        for (int r = 0; r < kStatRows; ++r) {
+            const bool in = token + r < tokens && 8 * lane < p.dim;
+            a[r] = in ? ld_written(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.d_o) + (token + r) * p.ld_do + col)) : make_uint4(0, 0, 0, 0);
+            b[r] = in ? ld_written(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o_in) + (token + r) * p.ld_oi + col)) : make_uint4(0, 0, 0, 0);
+        }
+        float mine = 0.0f, square = 0.0f;  // lane r: row r's sums
+#pragma unroll
+        for (int r = 0; r < kStatRows; ++r) {
+            widen_vec<T>(a[r], x);
+            widen_vec<T>(b[r], y);
+            const float sum = dot16(x, y);
+            if (lane == r) mine = sum;
+            if (!BF16) {
+                const float sq = dot16(x, x);
+                if (lane == r) square = sq;
+            }
+        }
+        if (lane < kStatRows && token + lane < tokens) {
+            const long long at = static_cast<long long>(head) * p.q_tokens + token + lane;
+            const float lse = ld_written(p.lse_in + at);
+            p.stats[at] = make_float2(lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f, mine);
+            if (!BF16 && token + lane >= lo && token + lane < hi) top = larger(top, make_uint4(finite_size(square), 0u, finite_size(mine), 0u));
+        }
     }
-    if (lane < kStatRows && token + lane < p.q_tokens) {
-        const long long at = static_cast<long long>(head) * p.q_tokens + token + lane;
-        const float lse = ld_written(p.lse_in + at);
-        p.stats[at] = make_float2(lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f, mine);
+    if constexpr (!BF16) {
+        __shared__ uint4 red[kStatThreads / 32];
+        top = warp_largest(top);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = top;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int w = 1; w < kStatThreads / 32; ++w) top = larger(top, red[w]);
+            p.sizes[blockIdx.x] = top;
+        }
     }
 }
+
+// fp16 holds p of 1 / n of many keys, and ds, which is smaller still, below its smallest normal
+// number (2^-14), where its steps are 2^-24.  Both are therefore rounded at a power of
+// two times their value, exactly undone where the sums are stored: p at 2^11 (dk and dv's
+// alone: dq's stays fp32), ds at the 2^k >= 1 that brings max |do| max |v| + max |do o|, which
+// |dp - D| is never above, to between 2^10 and 2^11.  With the forward's lse p is at most 1; the
+// 2^5 that is left is for an lse that is not.  bf16 has fp32's range, and scales nothing.
+constexpr int kPScale = 11;
+template <bool BF16>
+struct DsScale {
+    float up = 1.0f, down = 1.0f;  // 2^k, 2^-k
+    // (a converged warp, in fp16; each warp that needs it reads the sizes for itself, beneath the first loads)
+    __device__ __forceinline__ explicit DsScale(const CatParams &p)
+    {
+        if constexpr (!BF16) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            for (int i = threadIdx.x & 31; i < p.stat_ctas + p.size_ctas; i += 32) v = larger(v, ld_written(p.sizes + i));
+            v = warp_largest(v);
+            const float bound = sqrtf(__uint_as_float(v.x)) * sqrtf(__uint_as_float(v.y)) + __uint_as_float(v.z);
+            const int k = bound > 0.0f ? max(0, kPScale - 1 - ilogbf(bound)) : 0;
+            up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);  // (fp16's smallest numbers: k is below 64)
+            down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        }
+    }
+};
 
 constexpr int kWarpItems = 19;
 
@@ -280,12 +372,14 @@ __device__ __forceinline__ void put_rounded(uint32_t taddr, const float (&s)[32]
 
 template <bool BF16, bool SPLIT>
 __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
-                                            const KeyTile<SPLIT> &kt, uint32_t &done, uint32_t &items)
+                                            const KeyTile<SPLIT> &kt, const DsScale<BF16> &scale, uint32_t &done, uint32_t &items)
 {
     const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t s_col = tmem + lanes + kS + 32u * part, dp_col = tmem + lanes + kDP + 32u * part;
-    const f32x2 c2 = pack2(p.scale_log2, p.scale_log2), minus = pack2(-1.0f, -1.0f);
+    // (p is at 2^kPScale in fp16)
+    const float of_p = BF16 ? 1.0f : scale.up * (1.0f / (1 << kPScale)), p_down = BF16 ? 1.0f : 1.0f / (1 << kPScale);
+    const f32x2 c2 = pack2(p.scale_log2, p.scale_log2), of_p2 = pack2(of_p, of_p);
     const int off = at.kl - at.ql, j = kt.j0 + row;
     const int steps = kt.steps();
     int tile = kt.count > 0 ? kt.lo + kt.begin % kt.count : 0;
@@ -328,7 +422,7 @@ __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &
             ld_shared_4(stats + (CAT_TILE + e) * 4u, d);
 #pragma unroll
             for (int f = 0; f < 4; f += 2)
-                unpack2(mul2(pack2(s[e + f], s[e + f + 1]), fma2(pack2(d[f], d[f + 1]), minus, pack2(dp[e + f], dp[e + f + 1]))),
+                unpack2(mul2(pack2(s[e + f], s[e + f + 1]), fma2(pack2(dp[e + f], dp[e + f + 1]), of_p2, pack2(d[f], d[f + 1]))),
                         dp[e + f], dp[e + f + 1]);
         }
         if (!whole) hide(dp, lo, hi);  // (dP of an unseen pair may be anything)
@@ -348,8 +442,9 @@ __device__ __forceinline__ bool compute_dkv(const CatParams &p, const GradSmem &
         ++items;
         tc_fence_after();
         const uint32_t taddr = tmem + lanes + kSum + 64u * p.slices * is_dk;
-        if (SPLIT) store_rows_f32(taddr, c0, c1, 1.0f, sum, ld, rows);
-        else store_rows<BF16>(taddr, c0, c1, is_dk ? p.scale : 1.0f, out, ld, rows);
+        const float down = is_dk ? scale.down : p_down;
+        if (SPLIT) store_rows_f32(taddr, c0, c1, down, sum, ld, rows);
+        else store_rows<BF16>(taddr, c0, c1, is_dk ? p.scale * down : down, out, ld, rows);
         warp_arrive(S.B.out_empty);
     } else if (j < at.kl) {
         const int lane = threadIdx.x & 31;
@@ -400,6 +495,8 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
         }
     } else if (warp == kWarpStats) {
         const int lane = threadIdx.x & 31;
+        // as the computing warps add them: fp16's p and ds are scaled
+        const float p_up = BF16 ? 0.0f : kPScale, minus = BF16 ? -1.0f : DsScale<BF16>(p).up * (-1.0f / (1 << kPScale));
         bool ok = true;
         for (int n = 0; ok && next_item(S.I, ctl, n, item); ++n) {
             const KeyTile<SPLIT> kt(p, item);
@@ -414,8 +511,8 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
                 for (int e = 0; e < 4; ++e) {
                     const int c = 32 * e + lane, i = tile * CAT_TILE + c;
                     const float2 v = i < item.at.ql ? ld_written(src + i) : make_float2(-INFINITY, 0.0f);
-                    st_shared_f32(S.stats + (slot * 2 * CAT_TILE + c) * 4u, v.x);
-                    st_shared_f32(S.stats + ((slot * 2 + 1) * CAT_TILE + c) * 4u, v.y);
+                    st_shared_f32(S.stats + (slot * 2 * CAT_TILE + c) * 4u, BF16 ? v.x : v.x + p_up);
+                    st_shared_f32(S.stats + ((slot * 2 + 1) * CAT_TILE + c) * 4u, v.y * minus);
                 }
                 mbar_arrive(S.B.st_full0 + 8u * slot);
             }
@@ -477,8 +574,9 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dkv_kernel(cons
         }
         drain_mmas(p, S, leader);
     } else if (warp < 16) {
+        const DsScale<BF16> scale(p);
         for (int n = 0; next_item(S.I, ctl, n, item); ++n)
-            if (!compute_dkv<BF16, SPLIT>(p, S, ctl, tmem, item.at, KeyTile<SPLIT>(p, item), done, items)) break;
+            if (!compute_dkv<BF16, SPLIT>(p, S, ctl, tmem, item.at, KeyTile<SPLIT>(p, item), scale, done, items)) break;
     }
     grad_end(p, S, tmem);
 }
@@ -503,7 +601,7 @@ struct QueryTile {
 
 template <bool BF16, bool SPLIT>
 __device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S, Ctl ctl, uint32_t tmem, const Place &at,
-                                           const QueryTile<SPLIT> &qt, uint32_t &done, uint32_t &items)
+                                           const QueryTile<SPLIT> &qt, const DsScale<BF16> &scale, uint32_t &done, uint32_t &items)
 {
     const int i0 = qt.i0, head = qt.head, lo = qt.lo, hi = qt.hi;
     const int warp = threadIdx.x / 32, part = warp / 4, row = threadIdx.x & 127, i = i0 + row;
@@ -514,7 +612,8 @@ __device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S
     const long long token = at.q0 + i;
     const bool valid = i < at.ql;
     const float2 st = valid ? ld_written(p.stats + static_cast<long long>(head) * p.q_tokens + token) : make_float2(-INFINITY, 0.0f);
-    const f32x2 shift = pack2(st.x, st.x), minus_d = pack2(-st.y, -st.y);
+    const float d = -st.y * scale.up;
+    const f32x2 shift = pack2(st.x, st.x), minus_d = pack2(d, d), up2 = pack2(scale.up, scale.up);
     for (int j = lo; j < hi; ++j, ++done) {
         const int k0 = j * CAT_TILE;
         const bool whole = k0 + CAT_TILE <= at.kl && (!p.causal || k0 + CAT_TILE - 1 <= r_first) &&
@@ -539,7 +638,7 @@ __device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S
         tmem_wait(dp);
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
-            unpack2(mul2(pack2(s[e], s[e + 1]), add2(pack2(dp[e], dp[e + 1]), minus_d)), dp[e], dp[e + 1]);
+            unpack2(mul2(pack2(s[e], s[e + 1]), fma2(pack2(dp[e], dp[e + 1]), up2, minus_d)), dp[e], dp[e + 1]);
         if (!whole)  // (scores and dP of an unseen pair may be anything)
             hide(dp, p.window ? r - p.window + 1 - k0 - 32 * part : 0, min(at.kl, p.causal ? r + 1 : at.kl) - k0 - 32 * part);
         put_rounded<BF16>(dp_col, dp);
@@ -554,8 +653,8 @@ __device__ __forceinline__ bool compute_dq(const CatParams &p, const GradSmem &S
         ++items;
         tc_fence_after();
         const int rows = at.ql - (i & ~31);
-        if (SPLIT) store_rows_f32(tmem + lanes + kSum, c0, c1, 1.0f, sum, width, rows);
-        else store_rows<BF16>(tmem + lanes + kSum, c0, c1, p.scale, out, p.ld_dq, rows);
+        if (SPLIT) store_rows_f32(tmem + lanes + kSum, c0, c1, scale.down, sum, width, rows);
+        else store_rows<BF16>(tmem + lanes + kSum, c0, c1, p.scale * scale.down, out, p.ld_dq, rows);
         warp_arrive(S.B.out_empty);
     } else if (valid) {
         const int lane = threadIdx.x & 31;
@@ -651,9 +750,10 @@ __global__ void __launch_bounds__(CAT_GRAD_THREADS, 1) attention_dq_kernel(const
         }
         drain_mmas(p, S, leader);
     } else if (warp < 16) {
+        const DsScale<BF16> scale(p);
         for (int n = 0; next_item(S.I, ctl, n, item); ++n) {
             const QueryTile<SPLIT> qt(p, item);
-            if (!compute_dq<BF16, SPLIT>(p, S, ctl, tmem, item.at, qt, done, items)) break;
+            if (!compute_dq<BF16, SPLIT>(p, S, ctl, tmem, item.at, qt, scale, done, items)) break;
         }
     }
     grad_end(p, S, tmem);
@@ -731,11 +831,16 @@ Kernel dq_kernel(int slices, int bf16, int split)
 }
 }  // namespace
 
+long long cat_stat_ctas(long long tokens, int heads, int bf16)
+{
+    const long long n = ((tokens + cdg::kStatRows - 1) / cdg::kStatRows * heads + cdg::kStatGroups - 1) / cdg::kStatGroups;
+    return bf16 ? n : std::min<long long>(n, cdg::kSizeCtas);
+}
+
 cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s)
 {
     using namespace cdg;
-    const long long groups = (p.q_tokens + kStatRows - 1ll) / kStatRows * p.heads;
-    const dim3 grid(static_cast<unsigned>((groups + 15) / 16)), block(256);
+    const dim3 grid(static_cast<unsigned>(p.stat_ctas + p.size_ctas)), block(kStatThreads);
     return bf16 ? launch_early(attention_stats_kernel<true>, grid, block, 0, s, p)
                 : launch_early(attention_stats_kernel<false>, grid, block, 0, s, p);
 }

@@ -34,6 +34,13 @@ struct CatParams {
     long long ld_oi, ld_do;
     const float *lse_in;
     float2 *stats;
+    // fp16: what scales ds.  Of each CTA of the statistics (stat_ctas over the queries' rows,
+    // then size_ctas over v's), the largest |do|^2 or |v|^2 of a row's head, and |do o|, of its finite
+    // rows that a sequence holds:
+    const void *v_in;
+    long long ld_v;
+    uint4 *sizes;
+    int stat_ctas, size_ctas;
     // Parts that an item's steps are split into, a CTA each, where items are few.  Above
     // 1 their fp32 results go to `partial`, and a kernel of its own joins them in order:
     int q_splits;                // o, or dq: q_partial is [q_splits][q_tokens][heads * dim],
@@ -50,6 +57,9 @@ cudaError_t cat_prepare_forward();
 cudaError_t cat_prepare_grad();
 #define CAT_JOIN_ROWS 16  // rows and one head that a CTA of a join takes
 
+// CTAs of the statistics, over the queries' rows (bf16 != 0) or, in fp16, over rows of either side:
+// so few that the next kernels have not many sizes to read.
+long long cat_stat_ctas(long long tokens, int heads, int bf16);
 // bf16: 1 for bfloat16, 0 for float16; items: CTAs of a launch without the splits
 cudaError_t cat_launch_forward(const CatParams &p, int bf16, long long items, long long join_items, cudaStream_t s);
 cudaError_t cat_launch_stats(const CatParams &p, int bf16, cudaStream_t s);

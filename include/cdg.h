@@ -662,7 +662,12 @@ int cdg_muon_device_status(cdg_muon_t h, cdg_stream_t stream);
  *
  * All matrices are dtype (CDG_F16 or CDG_BF16); products have fp32 sums, p and
  * ds are rounded to dtype as their operands; row sums, lse (heads x q_tokens,
- * natural log) and do . o are fp32.  Repeated calls give the same bits.
+ * natural log) and do . o are fp32.  Repeated calls give the same bits.  The
+ * gradient rounds fp16's p and ds at powers of two times their value, so that
+ * those of many keys or small do keep their bits: p is held to 2^-36 or 2^-11 of
+ * itself, ds to 2^-35 of max |do| max |v| + max |do . o| over the call's heads and
+ * rows that are finite and a sequence's, or 2^-11 of itself.  It therefore takes
+ * an lse for which p stays below 2^5 (the forward's: 1).
  * A NaN or an infinity in a row of a sequence may reach other results of that
  * sequence and head, masked or not, and none of another sequence or head
  * (group of heads, for k and v).
