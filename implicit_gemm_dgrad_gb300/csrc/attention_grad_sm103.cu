@@ -22,10 +22,11 @@
 // overlap two products of the tensor cores: dk and dv run
 //   p(i) | dS^T(i-1) Q, dP^T(i)      then      ds(i) | P^T(i) dO, S^T(i+1)
 //
-// Measured (GB300, 8192 causal tokens, 16 heads of 128 over 4, bf16): 603 us, 1140
-// TFLOP/s of the five products that the gradient needs, 1600 of the seven made (dk and
-// dv 3.0 thousand cycles a step for products of 2.05, dq 2.3 for 1.54); packed
-// documents 452 us.  A step's phases wait for one another: scores complete, p of all
+// Measured (GB300, 8192 causal tokens, 16 heads of 128 over 4, bf16): 647 us, 1060
+// TFLOP/s of the five products that the gradient needs, 1490 of the seven made, call after
+// call, where the power limit lowers the SM clock (609 us for ten; dk and dv 3.0 thousand
+// cycles a step for products of 2.05, dq 2.3 for 1.54); packed documents 474 us (454); fp16
+// 660 for ten, 2 % more than bf16 at the same clock.  A step's phases wait for one another: scores complete, p of all
 // sixteen warps 1.4 thousand cycles, two products 1.3.  Eight warps of 64 columns
 // took 725 us where sixteen of 32 took 663.
 #include <algorithm>

@@ -17,9 +17,10 @@
 // Roles (384 threads): warps 0-3 and 4-7 the tiles' softmax, warp 8 TMA loads
 // (Q once an item, K and V steps through a ring), warp 9 MMA issue, warp 10 items.
 //
-// Measured (GB300, 8192 causal tokens, 16 heads of 128 over 4, bf16): 189 us, 1450
-// TFLOP/s; packed documents of 1 to 4096 tokens 144 us, 1150; 8192 x 8192 heads of 64
-// 808.  A step of a pair of tiles takes 2.6 thousand cycles, its products
+// Measured (GB300, 8192 causal tokens, 16 heads of 128 over 4, bf16): 198 us, 1390
+// TFLOP/s call after call, where the power limit lowers the SM clock (189 us for ten at 2.07
+// GHz); packed documents of 1 to 4096 tokens 150 us, 1100 (145); 8192 x 8192 heads of 64
+// 814 TFLOP/s.  A step of a pair of tiles takes 2.6 thousand cycles, its products
 // 2.05: what bounds it is the chain of one tile, scores -> softmax (1.1 thousand
 // cycles) -> P V -> next scores, which the other tile's products do not quite cover.
 #include "attention_device.cuh"
